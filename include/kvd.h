@@ -482,6 +482,161 @@ KVD_API kvd_status rswa_verify_i8(const float *q, const float *draft_k, const fl
 /* Device error word kept in an R-SWA workspace (see kvd_layer_device_error). */
 KVD_API kvd_status rswa_device_error(const void *workspace, int32_t clear, uint32_t *word_out);
 
+/* ---- Paged serving: K and V rows in pages that requests take from one
+ * pool, so that a request holds memory for the rows it has and not for the
+ * rows it may ever have.  The pages have no counterpart for this part.
+ *
+ * One step is kv_paged_plan (where do the new rows go), then per layer
+ * kv_paged_append (rotate q and k, write k and v) and paged_attention (attend
+ * the new rows over everything their request holds).  Lengths, tables and
+ * slots live on the device and no call reads them back, so a step can be
+ * captured into a CUDA graph and replayed while the lengths go on.
+ *
+ *   k_pages, v_pages   [n_pages][n_kv][page_size][head_dim], f16 or bf16,
+ *                      16-byte aligned; page_size 16, 32, 64 or 128;
+ *   block_table        int32 [n_seq][max_pages]: row p of request b is row
+ *                      p % page_size of page block_table[b][p / page_size];
+ *   seq_len            int32 [n_seq], rows that a request holds;
+ *   free_pages, n_free int32 [n_pages] and int32 [1]: a stack of the pages
+ *                      that no request holds, its height and top at n_free;
+ *   slot               page * page_size + row in page, one number for a row.
+ * The new rows of a step are packed: request b's are rows cu_new[b] ..
+ * cu_new[b + 1] - 1 of q, k, v, positions, slots and out.  Row contents that
+ * no request holds (the rest of a last page, free pages) are never used,
+ * whatever they are; rows that a request holds must be finite.
+ *
+ * `err` is the device error word (uint32, caller-owned, zeroed once): bit 0 a
+ * bounded wait gave up, bit 1 metadata out of range (the access is skipped),
+ * bit 2 a plan did not fit.  kv_paged_device_error reads it. */
+typedef enum { KVD_T_F32 = 0, KVD_T_F16 = 1, KVD_T_BF16 = 2 } kvd_dtype;
+
+/* Rows [token][head][head_dim] inside a larger array: strides in elements,
+ * head_dim contiguous.  q, k and v may so be slices of one projection. */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} kvd_rows;
+
+/* Rotary positions.  Pair i < rot_dim / 2 of a head is turned by the angle
+ * position * f_i, (a, b) -> (a cos - b sin, b cos + a sin), with f_i = base^(-2 i /
+ * rot_dim) before scaling; channels from rot_dim on are left alone.
+ *   layout   KVD_ROPE_INTERLEAVED: pair i is channels 2 i, 2 i + 1;
+ *            KVD_ROPE_HALF: channels i, i + rot_dim / 2;
+ *   scaling  KVD_ROPE_NONE;
+ *            KVD_ROPE_LINEAR: f_i / factor;
+ *            KVD_ROPE_NTK: base * factor^(rot_dim / (rot_dim - 2)) for base;
+ *            KVD_ROPE_YARN: between f_i and f_i / factor by a ramp over i,
+ *              from the pair that turns beta_fast times in original_len
+ *              positions (rounded down) to the one that turns beta_slow times
+ *              (rounded up);
+ *            KVD_ROPE_BANDS: with w_i = original_len f_i / 2 pi turns, f_i for
+ *              w_i >= high_freq_factor, f_i / factor for w_i <=
+ *              low_freq_factor, linear in w_i between;
+ *   attention_factor  multiplies cos and sin; 0 = 1, or 0.1 ln(factor) + 1
+ *              for KVD_ROPE_YARN.
+ * Fields that a scaling does not name are not read. */
+enum { KVD_ROPE_INTERLEAVED = 0, KVD_ROPE_HALF = 1 };
+enum { KVD_ROPE_NONE = 0, KVD_ROPE_LINEAR = 1, KVD_ROPE_NTK = 2, KVD_ROPE_YARN = 3, KVD_ROPE_BANDS = 4 };
+typedef struct {
+    int32_t rot_dim, layout, scaling, pad;
+    double base, factor, original_len, beta_fast, beta_slow, low_freq_factor, high_freq_factor;
+    double attention_factor;
+} kvd_rope_config;
+
+/* Frequencies of a config.  Host memory, plain bytes, filled by
+ * kvd_rope_init; calls copy it, so it may be freed once they return. */
+typedef struct kvd_rope {
+    uint64_t opaque[264];
+} kvd_rope;
+
+/* Fill R (host only).  KVD_EINVAL for an odd rot_dim or one outside 2 .. 512,
+ * a base <= 1, a factor < 1, a scaling's other fields outside their range
+ * (original_len >= 1, beta_fast > beta_slow > 0, high_freq_factor >
+ * low_freq_factor >= 0), NTK with rot_dim 2, or anything not finite. */
+KVD_API kvd_status kvd_rope_init(kvd_rope *R, const kvd_rope_config *config);
+
+/* Rotate the rows of q [n_tokens][n_q] and k [n_tokens][n_kv] (either may be
+ * NULL with its output) into q_out and k_out, which may be the same rows (same
+ * pointer and strides; outputs must not overlap inputs otherwise).  f32, f16
+ * or bf16; the products are taken in f32 and rounded once.  The angle is held
+ * as a 64-bit fraction of a turn, so it is as exact at position 2^31 - 1 as at
+ * 1.  positions: device int32 [n_tokens]; a negative one leaves its output
+ * rows as they were.  Any head_dim from rot_dim to 512. */
+KVD_API kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const kvd_rows *q_out, int32_t n_q,
+                                  const kvd_rows *k, const kvd_rows *k_out, int32_t n_kv, int32_t head_dim,
+                                  int32_t dtype, const int32_t *positions, int64_t n_tokens, void *stream);
+
+/* One scheduling step: shorten requests, then make room for new rows.  Request
+ * b first keeps keep_len[b] <= seq_len[b] rows (NULL: all of them; 0 drops a
+ * finished request, and the same step may start another in its place), then
+ * grows by new_len[b] >= 0.  Pages past its new end go back on the stack (in
+ * order of requests, then of pages), after which missing pages are taken off
+ * its top (same order).  Device arrays, all int32:
+ *   in      seq_len, new_len, keep_len [n_seq], n_free [1];
+ *   in/out  block_table, free_pages;
+ *   out     seq_len_out [n_seq], n_free_out [1] (may be seq_len and n_free:
+ *           the step then takes effect in place.  Apart, they leave the old
+ *           state standing and the same step may be planned again),
+ *           cu_new [n_seq + 1], positions and slots [n_tokens] of the packed
+ *           new rows, -1 in the places behind the last one.
+ * n_tokens is the room for new rows.  A step that does not fit (pages, table
+ * width, n_tokens) sets bit 2 of the error word, one with malformed numbers
+ * (negative, keep_len > seq_len, n_free out of range) bit 1, and neither
+ * changes anything: seq_len_out and n_free_out repeat the inputs, cu_new is 0,
+ * positions and slots are -1, so the rest of the step does nothing.  Table
+ * places past a request's pages and the stack above n_free_out hold nothing.
+ * n_seq <= 8192. */
+KVD_API kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_len, const int32_t *new_len,
+                                 int32_t n_seq, int64_t n_pages, int32_t page_size, int32_t *block_table,
+                                 int32_t max_pages, int32_t *free_pages, const int32_t *n_free,
+                                 int32_t *seq_len_out, int32_t *n_free_out, int32_t *cu_new,
+                                 int32_t *positions, int32_t *slots, int64_t n_tokens, uint32_t *err,
+                                 void *stream);
+
+/* Write the new rows k, v [n_tokens][n_kv] to their slots, k rotated, and
+ * rotate q [n_tokens][n_q] into q_out (both NULL: k and v only).  R NULL: no
+ * rotation (q is then copied).  in_dtype is f32 or page_dtype; k_pages,
+ * v_pages and q_out have page_dtype, one rounding.  A negative slot leaves the
+ * pages alone, a negative position q_out's rows; a slot past the pool sets bit
+ * 1 of the error word and is skipped.  Slots must differ: which of two rows
+ * with one slot stays is not said.  n_pages * page_size < 2^31.  q_out may be
+ * q (same strides and type); it must not overlap k or v. */
+KVD_API kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, const kvd_rows *q_out, int32_t n_q,
+                                   const kvd_rows *k, const kvd_rows *v, int32_t n_kv, int32_t head_dim,
+                                   int32_t in_dtype, int32_t page_dtype, const int32_t *positions,
+                                   const int32_t *slots, int64_t n_tokens, void *k_pages, void *v_pages,
+                                   int64_t n_pages, int32_t page_size, uint32_t *err, void *stream);
+
+/* Workspace bytes paged_attention needs (no initialisation). */
+KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv,
+                                                   int32_t head_dim, int64_t *bytes_out);
+
+/* Attention of each request's new rows over the rows it holds, causal: request
+ * b holds L_b = seq_len[b] rows, the last n_b = cu_new[b + 1] - cu_new[b] of
+ * them new and already appended; new row i stands at position P = L_b - n_b + i
+ * and attends rows [max(0, P - window + 1), P] (window 0: [0, P]); query head
+ * h reads KV head h / (n_q / n_kv).  softcap and sinks as decode_attention_ex.
+ *   q, out     [n_tokens][n_q][head_dim], dtype f16 or bf16 like the pages,
+ *              16-byte aligned with strides of multiples of 8 elements;
+ *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0.
+ * Scores, the softmax's maximum and sum and the output are accumulated in f32;
+ * the weights are rounded once to dtype for the value product.  Rows of `out`
+ * behind cu_new[n_seq] are left as they were; a row whose position is negative
+ * (n_b > L_b) sees nothing and becomes zeros.  Metadata out of range (a
+ * negative or oversized length, rows past n_tokens, a page past n_pages) sets
+ * bit 1 of the error word: such a request is skipped, such a page reads as
+ * zeros.  Calls that overlap on the GPU need a workspace each. */
+KVD_API kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q,
+                                   int32_t n_kv, int32_t head_dim, int32_t dtype, const void *k_pages,
+                                   const void *v_pages, int64_t n_pages, int32_t page_size,
+                                   const int32_t *block_table, int32_t max_pages, const int32_t *cu_new,
+                                   const int32_t *seq_len, int32_t n_seq, float scale, int64_t window,
+                                   float softcap, const float *sinks, void *workspace,
+                                   int64_t workspace_bytes, uint32_t *err, void *stream);
+
+/* The device error word of the paged calls (see kvd_layer_device_error). */
+KVD_API kvd_status kv_paged_device_error(uint32_t *err, int32_t clear, uint32_t *word_out);
+
 /* Short English description of a status code (static storage). */
 KVD_API const char *kvd_status_string(int32_t status);
 

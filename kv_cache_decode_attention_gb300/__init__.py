@@ -24,3 +24,13 @@ from .api import (  # noqa: F401
     rswa_ring_write,
     rswa_verify,
 )
+from .paged import (  # noqa: F401
+    PagedKvCache,
+    PagedPlan,
+    RopeTable,
+    paged_append,
+    paged_attention,
+    paged_attention_workspace,
+    paged_plan,
+    rope,
+)

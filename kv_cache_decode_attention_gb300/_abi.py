@@ -41,6 +41,20 @@ class rswa_checkpoint(C.Structure):
                 ("pad", C.c_int32)]
 
 
+class kvd_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class kvd_rope_config(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32), ("pad", C.c_int32)] + \
+        [(n, C.c_double) for n in ("base", "factor", "original_len", "beta_fast", "beta_slow", "low_freq_factor",
+                                   "high_freq_factor", "attention_factor")]
+
+
+class kvd_rope(C.Structure):
+    _fields_ = [("opaque", C.c_uint64 * 264)]
+
+
 class KvdError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__("%s failed: %s (%d)" % (fn, msg, status))
@@ -92,6 +106,16 @@ _SIGS = {
     "rswa_verify_i8": [_vp, _vp, _vp, _i32, _P(rswa_i8_mirror), _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i32,
                        _f32, _vp, _vp, _i64, _vp],
     "rswa_device_error": [_vp, _i32, _P(C.c_uint32)],
+    "kvd_rope_init": [_P(kvd_rope), _P(kvd_rope_config)],
+    "kvd_rope_apply": [_P(kvd_rope), _P(kvd_rows), _P(kvd_rows), _i32, _P(kvd_rows), _P(kvd_rows), _i32, _i32, _i32,
+                       _vp, _i64, _vp],
+    "kv_paged_plan": [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
+    "kv_paged_append": [_P(kvd_rope), _P(kvd_rows), _P(kvd_rows), _i32, _P(kvd_rows), _P(kvd_rows), _i32, _i32, _i32,
+                        _i32, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _vp],
+    "paged_attention_workspace_bytes": [_i64, _i32, _i32, _i32, _P(_i64)],
+    "paged_attention": [_P(kvd_rows), _P(kvd_rows), _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i32, _vp,
+                        _vp, _i32, _f32, _i64, _f32, _vp, _vp, _i64, _vp, _vp],
+    "kv_paged_device_error": [_vp, _i32, _P(C.c_uint32)],
     "kvd_status_string": [_i32],
 }
 

@@ -28,6 +28,7 @@ constexpr int kSlice = 256;     // sequences/streams described per launch (kerne
 // Device error-word bits.
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrBounds = 2u;
+constexpr uint32_t kErrPages = 4u;  // a paged plan did not fit
 
 inline bool quant_k(int mode) { return mode == KVD_Q8 || mode == KVD_Q8K; }
 

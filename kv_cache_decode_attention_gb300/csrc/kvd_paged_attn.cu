@@ -1,0 +1,160 @@
+// kvd_paged_attn.cu -- the entry points of paged_attention: checks, tensor
+// maps, workspace and launches.  Kernels: kvd_paged_attn.cuh, compiled per head
+// size in kvd_paged_attn64.cu and kvd_paged_attn128.cu.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "kvd_paged_attn.cuh"
+
+namespace kvd {
+
+cudaError_t launch_paged_attention_64(const PaArgs &a, bool bf16, bool cap, cudaStream_t st);
+cudaError_t launch_paged_attention_128(const PaArgs &a, bool bf16, bool cap, cudaStream_t st);
+
+namespace {
+
+// The driver's encoder, looked up once; nullptr if it is missing.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *m, bool bf16, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return fn != nullptr &&
+           fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(base),
+              dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool pow2_page(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+// Rows of one piece in the workspace.
+int32_t piece_rows(int64_t n_tokens, int32_t group) {
+    const int32_t tile_tok = kPaTile / group;
+    return n_tokens > tile_tok ? kPaMaxRows : int32_t(round_up(n_tokens * group, 8));
+}
+
+struct WsLayout {
+    int64_t meta, ml, o, total;
+};
+WsLayout ws_layout(int64_t n_tokens, int32_t group, int32_t hd) {
+    WsLayout w;
+    const int64_t rows = int64_t(2) * kPaCtas * piece_rows(n_tokens, group);
+    w.meta = 0;
+    w.ml = round_up(int64_t(kPaCtas) * 8 * 4, 256);
+    w.o = w.ml + round_up(rows * 8, 256);
+    w.total = w.o + rows * hd * 4;
+    return w;
+}
+
+bool shape_ok(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t hd) {
+    return n_tokens >= 0 && n_tokens <= (int64_t(1) << 30) && n_kv >= 1 && n_kv <= 1024 && n_q >= n_kv &&
+           n_q % n_kv == 0 && n_q / n_kv <= kMaxHpk && (hd == 64 || hd == 128);
+}
+
+// A [tokens][heads][hd] view whose rows a 16-byte access may touch.
+bool view_ok(const kvd_rows *r, int64_t tokens) {
+    const int64_t lim = int64_t(1) << 38;
+    return r != nullptr && (r->data != nullptr || tokens == 0) && (reinterpret_cast<uintptr_t>(r->data) & 15) == 0 && r->token_stride >= 0 &&
+           r->head_stride >= 0 && r->token_stride < lim && r->head_stride < lim && r->token_stride % 8 == 0 &&
+           r->head_stride % 8 == 0;
+}
+
+}  // namespace
+}  // namespace kvd
+
+using namespace kvd;
+
+extern "C" kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t head_dim,
+                                                      int64_t *bytes_out) {
+    if (bytes_out == nullptr || !shape_ok(n_tokens, n_q, n_kv, head_dim)) return KVD_EINVAL;
+    *bytes_out = ws_layout(n_tokens, n_q / n_kv, head_dim).total;
+    return KVD_OK;
+}
+
+extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q, int32_t n_kv,
+                                      int32_t head_dim, int32_t dtype, const void *k_pages, const void *v_pages,
+                                      int64_t n_pages, int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                      const int32_t *cu_new, const int32_t *seq_len, int32_t n_seq, float scale,
+                                      int64_t window, float softcap, const float *sinks, void *workspace,
+                                      int64_t workspace_bytes, uint32_t *err, void *stream) {
+    KVD_NVTX_RANGE("paged_attention");
+    if (!shape_ok(n_tokens, n_q, n_kv, head_dim) || (dtype != KVD_T_F16 && dtype != KVD_T_BF16)) return KVD_EINVAL;
+    if (!view_ok(q, n_tokens) || !view_ok(out, n_tokens) || (q->data == out->data && n_tokens > 0)) return KVD_EINVAL;
+    if (k_pages == nullptr || v_pages == nullptr ||
+        ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15) != 0)
+        return KVD_EINVAL;
+    if (!pow2_page(page_size) || n_pages < 1 || n_pages * page_size >= (int64_t(1) << 31) ||
+        n_pages >= (int64_t(1) << 31) || n_pages * page_size * n_kv >= (int64_t(1) << 31))
+        return KVD_EINVAL;
+    if (block_table == nullptr || cu_new == nullptr || seq_len == nullptr || err == nullptr || n_seq < 1 || max_pages < 1 ||
+        int64_t(max_pages) * page_size >= (int64_t(1) << 31))
+        return KVD_EINVAL;
+    if (!std::isfinite(scale) || scale <= 0.0f || window < 0 || !std::isfinite(softcap) || softcap < 0.0f) return KVD_EINVAL;
+    if (sinks != nullptr && (reinterpret_cast<uintptr_t>(sinks) & 3) != 0) return KVD_EINVAL;
+    const int32_t group = n_q / n_kv;
+    const WsLayout ws = ws_layout(n_tokens, group, head_dim);
+    if (n_tokens == 0) return KVD_OK;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < ws.total)
+        return KVD_EINVAL;
+
+    PaArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const bool bf16 = dtype == KVD_T_BF16;
+    a.tile_tok = kPaTile / group;
+    {
+        const cuuint64_t dims[4] = {cuuint64_t(head_dim), cuuint64_t(group), cuuint64_t(n_kv), cuuint64_t(n_tokens)};
+        // strides of axes that have one entry are never used; give them a legal value
+        const int64_t hs = n_q > 1 ? q->head_stride : head_dim, ts = n_tokens > 1 ? q->token_stride : hs * n_q;
+        const cuuint64_t strides[3] = {cuuint64_t(hs) * 2, cuuint64_t(hs) * 2 * group, cuuint64_t(ts) * 2};
+        const cuuint32_t box[4] = {64, cuuint32_t(group), 1, cuuint32_t(a.tile_tok)};
+        if (!encode(&a.q, bf16, 4, q->data, dims, strides, box)) return KVD_EINVAL;
+        const cuuint64_t kdims[2] = {cuuint64_t(head_dim), cuuint64_t(n_pages * page_size * n_kv)};
+        const cuuint64_t kstrides[1] = {cuuint64_t(head_dim) * 2};
+        const cuuint32_t kbox[2] = {64, cuuint32_t(page_size)};
+        if (!encode(&a.k, bf16, 2, k_pages, kdims, kstrides, kbox) || !encode(&a.v, bf16, 2, v_pages, kdims, kstrides, kbox))
+            return KVD_EINVAL;
+    }
+    char *w = static_cast<char *>(workspace);
+    a.meta = reinterpret_cast<int32_t *>(w + ws.meta);
+    a.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
+    a.part_o = reinterpret_cast<float *>(w + ws.o);
+    a.part_rows = piece_rows(n_tokens, group);
+    a.block_table = block_table;
+    a.cu_new = cu_new;
+    a.seq_len = seq_len;
+    a.out = out->data;
+    a.out_tok = out->token_stride;
+    a.out_head = out->head_stride;
+    a.sinks = sinks;
+    a.err = err;
+    a.window = window;
+    a.n_seq = n_seq;
+    a.n_tokens = int32_t(n_tokens);
+    a.n_kv = n_kv;
+    a.group = group;
+    a.max_pages = max_pages;
+    a.n_pages = int32_t(n_pages);
+    a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    a.pool_rows = int32_t(n_pages * page_size * n_kv);
+    const float log2e = 1.4426950408889634f;
+    a.scale_log2 = (softcap > 0.0f ? softcap : scale) * log2e;
+    a.cap_in = softcap > 0.0f ? 2.0f * scale * log2e / softcap : 0.0f;
+    const cudaError_t e = head_dim == 64 ? launch_paged_attention_64(a, bf16, softcap > 0.0f, as_stream(stream))
+                                         : launch_paged_attention_128(a, bf16, softcap > 0.0f, as_stream(stream));
+    return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
+}
