@@ -19,9 +19,12 @@
 //
 // One CTA per SM:
 //   warps 0-3, 4-7  softmax of stream 0 and 1, a thread per query row;
-//   warp 8          TMA loads: Q, and K / V tiles of 128 rows into a ring, page
-//                   by page (a page that does not exist reads as zeros);
-//   warp 9          the MMAs: S = Q K^T and O += P V, P read from TMEM.
+//   warps 8, 12     TMA loads of Q and K, and of V: tiles of 128 rows into one
+//                   ring, page by page (a page that does not exist reads as
+//                   zeros); small pages take many copies, hence two warps;
+//   warp 9          issues the MMAs: S = Q K^T and O += P V, P from TMEM;
+//   warp 10         clears the rows of V behind a request's last one;
+//   warp 11         walks the CTA's share of the work and hands the items on.
 // TMEM: S0 S1 (128 columns each; P overwrites the first 64) O0 O1.
 // MMAs of one thread run in order, so S of a stream's next tile may be issued
 // behind P V of its last one without a wait, and S being complete says that P V
@@ -34,15 +37,17 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kvd_internal.cuh"
 
 namespace kvd {
 
 constexpr int kPaCtas = 152;       // one per SM; also fixes the cut of the work
-constexpr int kPaThreads = 384;    // warps 10 and 11 only fill their warpgroup
-// Registers a thread: the launch gives 384 x 168; the softmax warpgroups trade up.
-constexpr int kPaRegs = 168, kPaSoftRegs = 208, kPaLoadRegs = 88;
-static_assert(2 * kPaSoftRegs + kPaLoadRegs <= 3 * kPaRegs, "setmaxnreg shares");
+constexpr int kPaThreads = 512;    // warps 13 to 15 only fill their warpgroup
+// Registers a thread: the launch gives 512 x 128; the softmax warpgroups trade up.
+constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
+static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
 constexpr int kPaQBytes = 2 * kPaTile * 256;
 constexpr int kPaMaxRows = 2 * kPaTile;
@@ -89,61 +94,55 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, float *r) {
           "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
+
 
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]),
-        "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]),
-        "f"(r[17]), "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]),
-        "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]) : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle.  K-major operands: sbo =
-// bytes between groups of eight rows.  MN-major: lbo = bytes between runs of 64
-// MN elements, sbo = bytes between groups of eight K rows.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
 // Instruction descriptor of kind::f16: f32 accumulator, M x N, B MN-major or not.
 __host__ __device__ constexpr uint32_t tc_idesc(bool bf16, int m, int n, bool b_mn) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
            (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
+// One lane of a converged warp; always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// The MMAs are issued by a whole warp that elects a lane for each: their
+// operands are uniform registers, which converged code holds anyway, while a
+// branch for one lane around all of them fills them anew for each instruction
+// (measured: 53 against 67 cycles an instruction, and slower still between batches).
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    if (elect_one())
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    if (elect_one())
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
 }
-// Arrive once on bar when every MMA this thread has issued so far is complete.
+// Arrive once on bar when every MMA the elected lane has issued so far is complete.
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
 }
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void pa_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -207,6 +206,25 @@ __device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, volatile
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *stop = 1;
     return ok;
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool pa_wait_one(uint64_t *bar, uint32_t parity, volatile int *stop) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (*stop != 0 || global_ns() - t0 > 2000000000ull) {
+            *stop = 1;
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // ---------------------------------------------------------------- the work
@@ -347,11 +365,24 @@ struct PaShape {
     static constexpr int kTiles = 2 * kQTileBytes + kStages * kStageBytes;
 };
 
+// One item as the other warps see it; n = 0 ends the work.
+struct PaJob {
+    int32_t n;                 // KV tiles of this CTA's part of it
+    int32_t tile0;             // the first of them
+    int32_t tail;              // which of them holds the request's short last page, or -1
+    int32_t dual, head, whole; // two query tiles; begins here; begins and ends here
+    int32_t seq, kv_head, tok; // request, KV head, first token in its new rows
+    int32_t q0, fresh, len;    // as PaSeq
+};
+constexpr int kPaJobs = 4;
+
 struct PaShared {
+    uint64_t job_full[kPaJobs], job_empty[kPaJobs];
+    PaJob job[kPaJobs];
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2];
-    uint64_t ml_full[2], drain;
+    uint64_t ml_full[2], tail_go, tail_ready, drain;
     PaStart start;
     int64_t warp_sums[kPaThreads / 32];
     uint32_t tmem;
@@ -381,6 +412,61 @@ __device__ __forceinline__ PaPart pa_part(const PaItem &it, int32_t unit, int64_
     return p;
 }
 
+// What the MMA thread keeps: the ring's cursor (loads are used in their order,
+// dual K0 V0 K1 V1 .., single K0 K1 V0 K2 V1 ..) and the operands' bases.
+template <int HD, bool BF16>
+struct PaIssue {
+    using S = PaShape<HD>;
+    PaShared &sh;
+    const uint32_t tmem, q, kv;
+    volatile int *stop;
+    uint32_t stage = 0, phase = 0;
+    __device__ PaIssue(PaShared &s, uint32_t q_smem, uint32_t kv_smem, uint32_t t, volatile int *st)
+        : sh(s), tmem(uni(t)), q(uni((q_smem & 0x3ffffu) >> 4)), kv(uni((kv_smem & 0x3ffffu) >> 4)), stop(st) {}
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) { return pa_wait(bar, parity, stop); }
+    __device__ __forceinline__ bool wait_stage() { return pa_wait(&sh.kv_full[stage], phase, stop); }
+    __device__ __forceinline__ uint32_t take() {
+        const uint32_t at = stage;
+        if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        return at;
+    }
+    // Shared-memory matrix descriptor, 128-byte swizzle, groups of eight rows
+    // 1024 bytes apart; for MN-major operands lbo = bytes between runs of 64.
+    static __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t lbo) {
+        constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+        return (uint64_t(hi) << 32) | (uint64_t(lbo >> 4) << 16) | lo;
+    }
+    // S of stream d = Q tile qt x K in stage k
+    __device__ __forceinline__ void score(int d, int qt, uint32_t k) const {
+        constexpr uint32_t id = tc_idesc(BF16, 128, 128, false);
+        const uint64_t qd = desc(q + qt * (S::kQTileBytes >> 4), 16), kd = desc(kv + k * (S::kStageBytes >> 4), 16);
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+            constexpr uint32_t kHalf = kPaTile * 128 >> 4;
+            const uint32_t off = (kk / 4) * kHalf + (kk % 4) * 2;
+            tc_mma_ss(tmem + d * 128, qd + off, kd + off, id, kk != 0);
+        }
+    }
+    // O of stream d (+)= P x V in stage v
+    __device__ __forceinline__ void value(int d, uint32_t v, bool more) const {
+        constexpr uint32_t id = tc_idesc(BF16, 128, HD, true);
+        const uint64_t vd = desc(kv + v * (S::kStageBytes >> 4), kPaTile * 128);
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < kPaTile / 16; ++kk)
+            tc_mma_ts(tmem + 256 + d * HD, tmem + d * 128 + kk * 8, vd + kk * (2048 >> 4), id, more || kk != 0);
+    }
+};
+// The part's tile in which the request's last page ends short, or -1.
+__device__ __forceinline__ int32_t pa_tail_tile(const PaArgs &a, const PaSeq &s, const PaItem &it, const PaPart &pt) {
+    const int32_t t = s.len / kPaTile - it.tile0 - pt.first;
+    return t >= 0 && t < pt.n && (s.len & ((1 << a.page_log2) - 1)) != 0 ? t : -1;
+}
+
 template <int HD, bool BF16, bool CAP>
 __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __grid_constant__ PaArgs a) {
     using S = PaShape<HD>;
@@ -406,6 +492,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             mbar_init(&sh.o_empty[i], 4);
             mbar_init(&sh.ml_full[i], 4);
         }
+        for (int i = 0; i < kPaJobs; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], 12);  // two of loads, MMAs, ends of V, eight softmax warps
+        }
+        mbar_init(&sh.tail_go, 1);
+        mbar_init(&sh.tail_ready, 1);
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.stop = 0;
@@ -426,195 +518,224 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
     const PaStart st = sh.start;
-    int32_t issued = 0;  // loader: ring entries issued, for the clean-up below
+    uint32_t loaded = 0, parity = 0;  // loads: stages filled and their last parities, for the clean-up below
 
-    if (threadIdx.x == 0) {
+    if (warp == 11 && lane == 0) {
         int32_t *m = a.meta + blockIdx.x * 8;
         m[kPmTail] = 0;
         m[kPmFirst] = st.units == 0 ? 3 : st.unit == 0 ? 0 : 2;
     }
     if (st.units > 0) {
-        PaWalk w;
-        w.b = st.b;
-        w.h = st.h;
-        w.tok = st.tok;
-        w.s = pa_seq(a, w.b, false);
-        int32_t unit = st.unit;
-        int64_t left = st.units;
+        // the next item: its record, read in place until job_empty is told
+        uint32_t job_at = 0;
+        auto next_job = [&](bool &ok) -> const PaJob & {
+            ok = pa_wait(&sh.job_full[job_at % kPaJobs], job_at / kPaJobs & 1, stop);
+            return sh.job[job_at++ % kPaJobs];
+        };
+        auto done_job = [&]() {
+            __syncwarp();
+            if (lane == 0) pa_arrive(&sh.job_empty[(job_at - 1) % kPaJobs]);
+        };
 
         if (warp >= 8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLoadRegs));
-            if (warp == 8) {
+            if (warp == 8 || warp == 12) {
                 // ------------------------------------------------------ loads
                 const int ppt = kPaTile >> a.page_log2;          // pages of a tile
-                const uint32_t box = (128u << a.page_log2);      // bytes of one page's half
-                uint32_t items = 0;
+                const uint32_t box = 128u << a.page_log2;        // bytes of one page's half
+                const bool v_warp = warp == 12;
+                const CUtensorMap *map = v_warp ? &a.v : &a.k;
+                uint32_t items = 0, ring = 0;
                 bool ok = true;
-                while (ok && left > 0) {
-                    const PaItem it = pa_item(a, w.s, w.tok);
-                    const PaPart pt = pa_part(it, unit, left);
-                    const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
-                    const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
+                for (;;) {
+                    const PaJob &job = next_job(ok);
+                    if (!ok || job.n == 0) break;
+                    const int32_t n = job.n, t0 = job.tile0, h = job.kv_head;
+                    const bool dual = job.dual != 0;
+                    const int32_t held = (job.len + (1 << a.page_log2) - 1) >> a.page_log2, q_row = job.q0 + job.tok;
+                    const int32_t *table = a.block_table + int64_t(job.seq) * a.max_pages;
+                    done_job();
                     // the tensor-map row of lane's page of a tile; past the pool = zeros
                     auto page_row = [&](int32_t tile) {
                         const int32_t p = tile * ppt + lane;
                         int32_t row = a.pool_rows;
                         if (lane < ppt && p < held) {
                             const int32_t page = table[p];
-                            if (uint32_t(page) < uint32_t(a.n_pages)) row = (page * a.n_kv + w.h) << a.page_log2;
+                            if (uint32_t(page) < uint32_t(a.n_pages)) row = (page * a.n_kv + h) << a.page_log2;
                             else set_error(a.err, kErrBounds);
                         }
                         return row;
                     };
-                    auto load = [&](const CUtensorMap *map, int32_t row) {
-                        const int stage = issued % S::kStages;
-                        if (issued >= S::kStages) ok = pa_wait(&sh.kv_empty[stage], ((issued / S::kStages) & 1) ^ 1, stop);
-                        if (!ok) return;
+                    // places in the ring, in the order the MMAs use them: dual K0 V0 K1
+                    // V1 .., single K0 K1 V0 K2 V1 .. (K runs one tile further ahead)
+                    int32_t row = page_row(t0);
+                    for (int32_t t = 0; t < n; ++t) {
+                        const int32_t now = row;
+                        if (t + 1 < n) row = page_row(t0 + t + 1);  // looked up while this one waits
+                        const uint32_t at = ring + uint32_t(v_warp ? (dual ? 2 * t + 1 : t < n - 1 ? 2 * t + 2 : 2 * n - 1)
+                                                                   : (dual ? 2 * t : t < 2 ? t : 2 * t - 1));
+                        const uint32_t stage = at % S::kStages, turn = at / S::kStages;
+                        if (turn > 0) ok = pa_wait(&sh.kv_empty[stage], (turn & 1) ^ 1, stop);
+                        if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[stage], S::kStageBytes);
                         __syncwarp();
                         if (lane < ppt) {
                             const uint32_t dst = kv_smem + stage * S::kStageBytes + lane * box;
 #pragma unroll
                             for (int i = 0; i < S::kHalves; ++i)
-                                tma_2d(dst + i * (kPaTile * 128), map, i * 64, row, &sh.kv_full[stage]);
+                                tma_2d(dst + i * (kPaTile * 128), map, i * 64, now, &sh.kv_full[stage]);
                         }
-                        ++issued;
-                    };
-                    const int32_t t0 = it.tile0 + pt.first;
-                    // Q once the MMAs of the item before have read theirs
-                    if (items > 0) ok = pa_wait(&sh.q_empty, (items - 1) & 1, stop);
+                        loaded |= 1u << stage;
+                        parity = (parity & ~(1u << stage)) | (turn & 1) << stage;
+                        if (t == 0 && !v_warp) {
+                            // Q once the MMAs of the item before have read theirs
+                            if (items > 0) ok = pa_wait(&sh.q_empty, (items - 1) & 1, stop);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                const uint32_t bytes = uint32_t(a.tile_tok * a.group) * 128u * S::kHalves;
+                                mbar_arrive_expect_tx(&sh.q_full, dual ? 2 * bytes : bytes);
+                                for (int d = 0; d < (dual ? 2 : 1); ++d)
+#pragma unroll
+                                    for (int i = 0; i < S::kHalves; ++i)
+                                        tma_4d(q_smem + d * S::kQTileBytes + i * (kPaTile * 128), &a.q, i * 64, 0, h,
+                                               q_row + d * a.tile_tok, &sh.q_full);
+                            }
+                            __syncwarp();
+                            ++items;
+                        }
+                    }
+                    ring += 2 * n;
                     if (!ok) break;
-                    if (lane == 0) {
-                        const uint32_t bytes = uint32_t(a.tile_tok * a.group) * 128u * S::kHalves;
-                        mbar_arrive_expect_tx(&sh.q_full, it.dual ? 2 * bytes : bytes);
-                        for (int d = 0; d < (it.dual ? 2 : 1); ++d)
-                            for (int i = 0; i < S::kHalves; ++i)
-                                tma_4d(q_smem + d * S::kQTileBytes + i * (kPaTile * 128), &a.q, i * 64, 0, w.h,
-                                       w.s.q0 + w.tok + d * a.tile_tok, &sh.q_full);
-                    }
-                    __syncwarp();
-                    ++items;
-                    // K and V in the order the MMAs use them: dual K0 V0 K1 V1 ..,
-                    // single K0 K1 V0 K2 V1 .. (K runs one tile further ahead)
-                    const int ahead = it.dual ? 1 : 2;
-                    int32_t row_k = page_row(t0), row_v = row_k;
-                    load(&a.k, row_k);
-                    int32_t row_k1 = 0;
-                    if (ahead == 2 && pt.n > 1) {
-                        row_k1 = page_row(t0 + 1);
-                        if (ok) load(&a.k, row_k1);
-                    }
-                    for (int32_t i = 0; ok && i < pt.n; ++i) {
-                        const int32_t next = i + ahead;
-                        const int32_t row_n = next < pt.n ? page_row(t0 + next) : 0;
-                        load(&a.v, row_v);
-                        if (ok && next < pt.n) load(&a.k, row_n);
-                        if (ahead == 1) {
-                            row_v = row_n;
-                        } else {
-                            row_v = row_k1;
-                            row_k1 = row_n;
-                        }
-                    }
-                    left -= it.units - unit < left ? it.units - unit : left;
-                    unit = 0;
-                    if (left > 0) pa_next(a, w);
                 }
             } else if (warp == 9) {
                 // ------------------------------------------------------ MMAs
-                constexpr uint32_t id_s = tc_idesc(BF16, 128, 128, false), id_o = tc_idesc(BF16, 128, HD, true);
-                uint32_t items = 0, ring = 0, p_phase[2] = {0, 0}, o_items[2] = {0, 0};
+                // The tensor cores wait for this warp's instructions between two
+                // batches: the ring is a cursor, a batch's descriptors differ by
+                // constants, and both streams' steps are written out.
+                PaIssue<HD, BF16> mma(sh, q_smem, kv_smem, tmem, stop);
+                uint32_t items = 0, tails = 0, p_phase = 0;
                 bool ok = true;
-                auto stage_full = [&](uint32_t at) {
-                    return pa_wait(&sh.kv_full[at % S::kStages], (at / S::kStages) & 1, stop);
-                };
-                while (ok && left > 0) {
-                    const PaItem it = pa_item(a, w.s, w.tok);
-                    const PaPart pt = pa_part(it, unit, left);
-                    const int32_t steps = it.dual ? 2 * pt.n : pt.n;
-                    auto at_k = [&](int32_t t) {
-                        return ring + uint32_t(it.dual ? 2 * t : t < 2 ? t : 2 * t - 1);
-                    };
-                    auto at_v = [&](int32_t t) {
-                        return ring + uint32_t(it.dual ? 2 * t + 1 : t < pt.n - 1 ? 2 * t + 2 : 2 * pt.n - 1);
-                    };
-                    // the last rows of the last page hold nothing the request wrote:
-                    // rows [cut0, cut1) of that tile are cleared in V before use
-                    const int32_t end_tile = w.s.len / kPaTile;
-                    const int32_t cut0 = w.s.len % kPaTile;
-                    const int32_t cut1 = ((cut0 + (1 << a.page_log2) - 1) >> a.page_log2) << a.page_log2;
-                    auto issue_s = [&](int32_t j) {  // S of step j
-                        const int d = j & 1;
-                        const int32_t t = it.dual ? j >> 1 : j;
-                        const uint32_t at = at_k(t);
-                        ok = stage_full(at);
-                        if (!ok) return;
-                        tc_after();
-                        if (lane == 0) {
-                            const uint32_t qa = q_smem + (it.dual ? d : 0) * S::kQTileBytes;
-                            const uint32_t ka = kv_smem + (at % S::kStages) * S::kStageBytes;
-#pragma unroll
-                            for (int kk = 0; kk < HD / 16; ++kk) {
-                                const uint32_t off = (kk / 4) * (kPaTile * 128) + (kk % 4) * 32;
-                                tc_mma_ss(tmem + d * 128, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), id_s,
-                                          kk != 0);
-                            }
-                            if (!it.dual || d == 1) tc_commit(&sh.kv_empty[at % S::kStages]);
-                            tc_commit(&sh.s_full[d]);
-                            if (j == steps - 1) tc_commit(&sh.q_empty);
-                        }
-                        __syncwarp();
-                    };
-                    ok = pa_wait(&sh.q_full, items & 1, stop);
+                for (;;) {
+                    ok = mma.wait(&sh.job_full[job_at % kPaJobs], job_at / kPaJobs & 1);
                     if (!ok) break;
-                    ++items;
-                    issue_s(0);
-                    if (ok && steps > 1) issue_s(1);
-                    for (int32_t j = 0; ok && j < steps; ++j) {
-                        const int d = j & 1;
-                        const int32_t t = it.dual ? j >> 1 : j;
-                        const uint32_t at = at_v(t);
-                        ok = stage_full(at);
-                        if (!ok) break;
-                        if (it.tile0 + pt.first + t == end_tile && cut0 < cut1 && (!it.dual || d == 0)) {
-                            const uint32_t va = kv_smem + (at % S::kStages) * S::kStageBytes;
-                            const int32_t pieces = (cut1 - cut0) * 8;
-                            for (int h = 0; h < S::kHalves; ++h)
-                                for (int32_t i = lane; i < pieces; i += 32)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(va + h * (kPaTile * 128) + cut0 * 128 + i * 16),
-                                                 "r"(0)
-                                                 : "memory");
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                        }
-                        ok = pa_wait(&sh.p_ready[d], p_phase[d], stop);
-                        if (!ok) break;
-                        p_phase[d] ^= 1;
-                        if (j < 2) {  // the first write to O of this item: the one before must have been read
-                            if (o_items[d] > 0) ok = pa_wait(&sh.o_empty[d], (o_items[d] - 1) & 1, stop);
-                            if (!ok) break;
-                        }
-                        tc_after();
-                        if (lane == 0) {
-                            const uint32_t va = kv_smem + (at % S::kStages) * S::kStageBytes;
-#pragma unroll
-                            for (int kk = 0; kk < kPaTile / 16; ++kk)
-                                tc_mma_ts(tmem + kO + d * HD, tmem + d * 128 + kk * 8,
-                                          tc_desc(va + kk * 2048, kPaTile * 128, 1024), id_o, j >= 2 || kk != 0);
-                            if (!it.dual || d == 1) tc_commit(&sh.kv_empty[at % S::kStages]);
+                    const PaJob &job = sh.job[job_at % kPaJobs];
+                    const int32_t n = uni(job.n), tail = uni(job.tail);
+                    const bool dual = uni(job.dual) != 0;
+                    ++job_at;
+                    done_job();
+                    if (n == 0) break;
+                    ok = mma.wait(&sh.q_full, items & 1);
+                    if (!ok) break;
+                    // step j: P V of stream j & 1, then its S two steps on.  A dual
+                    // item's K and V tile serves both streams, a single one's one.
+                    const int32_t steps = dual ? 2 * n : n;
+                    uint32_t k = 0, v = 0;
+                    // (written out for both streams: what differs are constants)
+                    auto step = [&](int32_t j, auto stream) {
+                        constexpr int d = decltype(stream)::value;
+                        const bool second = !dual || d == 1;  // the tiles' last use
+                        if (j >= 0) {
+                            if (!dual || d == 0) {
+                                ok = mma.wait_stage();
+                                if (ok && (dual ? j >> 1 : j) == tail) {  // it ends short: cleared first
+                                    if (elect_one()) pa_arrive(&sh.tail_go);
+                                    ok = mma.wait(&sh.tail_ready, tails++ & 1);
+                                }
+                                v = mma.take();
+                            }
+                            // before the first write to O the last item's must have been read
+                            if (ok && j < 2 && items > 0) ok = mma.wait(&sh.o_empty[d], (items - 1) & 1);
+                            if (ok) ok = mma.wait(&sh.p_ready[d], p_phase >> d & 1);
+                            if (!ok) return;
+                            p_phase ^= 1u << d;
+                            mma.value(d, v, j >= 2);
                             if (j + 2 >= steps) tc_commit(&sh.o_full[d]);
                         }
-                        __syncwarp();
-                        if (j + 2 < steps) issue_s(j + 2);
+                        if (j + 2 < steps) {
+                            if (!dual || d == 0) {
+                                ok = mma.wait_stage();
+                                if (!ok) return;
+                                k = mma.take();
+                            }
+                            mma.score(d, dual ? d : 0, k);
+                            tc_commit(&sh.s_full[d]);
+                            if (second) tc_commit(&sh.kv_empty[k]);
+                            if (j + 3 == steps) tc_commit(&sh.q_empty);
+                        }
+                        if (j >= 0 && second) tc_commit(&sh.kv_empty[v]);
+                    };
+                    for (int32_t j = -2; ok && j < steps; j += 2) {
+                        step(j, std::integral_constant<int, 0>());
+                        if (ok && j + 1 < steps) step(j + 1, std::integral_constant<int, 1>());
                     }
-                    ++o_items[0];
-                    ++o_items[1];
-                    ring += 2 * pt.n;
-                    left -= it.units - unit < left ? it.units - unit : left;
+                    if (!ok) break;
+                    ++items;
+                }
+                if (!ok) tc_commit(&sh.drain);
+            } else if (warp == 10) {
+                // ------------------------------------------------------ ends of V
+                // Rows of a request's last page behind its last row hold nothing;
+                // their weights are zero, but zero times NaN is not: they are
+                // cleared after the copy and before the MMA, whose thread says when.
+                uint32_t ring = 0, tails = 0;
+                bool ok = true;
+                for (;;) {
+                    const PaJob &job = next_job(ok);
+                    if (!ok || job.n == 0) break;
+                    const int32_t t = job.tail, n = job.n, row0 = job.len % kPaTile;
+                    const bool dual = job.dual != 0;
+                    done_job();
+                    if (t >= 0) {
+                        ok = pa_wait(&sh.tail_go, tails++ & 1, stop);
+                        if (!ok) break;
+                        const uint32_t stage = (ring + uint32_t(dual ? 2 * t + 1 : t < n - 1 ? 2 * t + 2 : 2 * n - 1)) % S::kStages;
+                        const int32_t row1 = ((row0 + (1 << a.page_log2) - 1) >> a.page_log2) << a.page_log2;
+                        const uint32_t va = kv_smem + stage * S::kStageBytes + row0 * 128;
+                        for (int h = 0; h < S::kHalves; ++h)
+                            for (int32_t i = lane; i < (row1 - row0) * 8; i += 32)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(va + h * (kPaTile * 128) + i * 16), "r"(0)
+                                             : "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) pa_arrive(&sh.tail_ready);
+                    }
+                    ring += 2 * n;
+                }
+            } else if (warp == 11 && lane == 0) {
+                // ------------------------------------------------------ items
+                PaWalk w = {st.b, st.h, st.tok, pa_seq(a, st.b, false)};
+                int32_t unit = st.unit;
+                int64_t left = st.units;
+                bool ok = true;
+                for (;; ++job_at) {
+                    const uint32_t slot = job_at % kPaJobs;
+                    if (job_at >= kPaJobs) ok = pa_wait_one(&sh.job_empty[slot], (job_at / kPaJobs & 1) ^ 1, stop);
+                    if (!ok) break;
+                    PaJob &job = sh.job[slot];
+                    job.n = 0;
+                    int64_t step = 0;
+                    if (left > 0) {
+                        const PaItem it = pa_item(a, w.s, w.tok);
+                        const PaPart pt = pa_part(it, unit, left);
+                        job = PaJob{pt.n, it.tile0 + pt.first, pa_tail_tile(a, w.s, it, pt), it.dual, pt.head, pt.head && pt.tail,
+                                    w.b, w.h, w.tok, w.s.q0, w.s.fresh, w.s.len};
+                        // pieces of items that were cut, for the kernel that joins them
+                        int32_t *m = a.meta + blockIdx.x * 8;
+                        if (pt.head && !pt.tail) {
+                            m[kPmTail] = 1;
+                            m[kPmSeq] = w.b;
+                            m[kPmHead] = w.h;
+                            m[kPmTok] = w.tok;
+                        }
+                        if (!pt.head && pt.tail) m[kPmFirst] = 1;
+                        step = it.units - unit;
+                    }
+                    pa_arrive(&sh.job_full[slot]);
+                    if (left <= 0) break;
+                    left -= step;
                     unit = 0;
                     if (left > 0) pa_next(a, w);
                 }
-                if (!ok && lane == 0) tc_commit(&sh.drain);
             }
         } else {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftRegs));
@@ -630,56 +751,68 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             const bool in_tile = rtok < a.tile_tok;
             uint32_t s_phase = 0, o_phase[2] = {0, 0}, ml_phase = 0, ml_items = 0;
             bool ok = true;
-            while (ok && left > 0) {
-                const PaItem it = pa_item(a, w.s, w.tok);
-                const PaPart pt = pa_part(it, unit, left);
-                const int32_t tok = w.tok + (it.dual ? d * a.tile_tok : 0) + rtok;  // of the request
-                const bool valid = in_tile && tok < w.s.fresh;
-                const int32_t pos = w.s.len - w.s.fresh + tok;
+            for (;;) {
+                const PaJob &job = next_job(ok);
+                if (!ok || job.n == 0) break;
+                const bool dual = job.dual != 0;
+                const int32_t tok = job.tok + (dual ? d * a.tile_tok : 0) + rtok;  // of the request
+                const bool valid = in_tile && tok < job.fresh;
+                const int32_t pos = job.len - job.fresh + tok;
                 int64_t lo64 = a.window > 0 ? int64_t(pos) - a.window + 1 : 0;
                 const int32_t lo = lo64 > 0 ? int32_t(lo64) : 0;
                 const bool busy = __any_sync(0xffffffffu, valid);
-                const int32_t n = it.dual ? pt.n : (pt.n - d + 1) / 2;  // tiles of this stream
+                const int32_t n = dual ? job.n : (job.n - d + 1) / 2;  // tiles of this stream
+                const int32_t step = dual ? kPaTile : 2 * kPaTile;
+                int32_t key0 = (job.tile0 + (dual ? 0 : d)) * kPaTile;
                 float ref = -INFINITY;  // reference maximum, log2 units, less kLift
                 float2 sum2 = make_float2(0.0f, 0.0f);
-                for (int32_t i = 0; i < n; ++i) {
-                    const int32_t t = it.tile0 + pt.first + (it.dual ? i : 2 * i + d);
+                for (int32_t i = 0; i < n; ++i, key0 += step) {
                     ok = pa_wait(&sh.s_full[d], s_phase, stop);
                     if (!ok) break;
                     s_phase ^= 1;
                     if (busy) {
                         tc_after();
-                        float x[128];
+                        // first pass: the maximum, 64 scores at a time; capped and
+                        // masked ones go back to TMEM so that the second finds them
+                        float m0 = -INFINITY, m1 = -INFINITY;
+                        const int32_t hi_c = pos - key0, lo_c = lo - key0;
+                        const bool edge = __any_sync(0xffffffffu, hi_c < kPaTile - 1 || lo_c > 0);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kPaTile; c0 += 64) {
+                            float x[64];
+                            tc_ld32(t_s + c0, x);
+                            tc_ld32(t_s + c0 + 32, x + 32);
+                            tc_wait_ld();
+                            if (CAP) {
+                                // softcap * tanh(s / softcap), with tanh(y) = 1 - 2 / (e^2y + 1)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tc_ld32(t_s + c * 32, x + c * 32);
-                        tc_wait_ld();
-                        if (CAP) {
-                            // softcap * tanh(s / softcap), with tanh(y) = 1 - 2 / (e^2y + 1)
+                                for (int c = 0; c < 64; ++c) x[c] = 1.0f - __fdividef(2.0f, ex2(x[c] * a.cap_in) + 1.0f);
+                            }
+                            if (edge) {
+                                const int32_t hi = hi_c - c0, low = lo_c - c0;
 #pragma unroll
-                            for (int c = 0; c < 128; ++c) x[c] = 1.0f - __fdividef(2.0f, ex2(x[c] * a.cap_in) + 1.0f);
+                                for (int c = 0; c < 64; ++c) x[c] = c <= hi && c >= low ? x[c] : -INFINITY;
+                            }
+                            if (CAP || edge) {
+                                tc_st32(t_s + c0, x);
+                                tc_st32(t_s + c0 + 32, x + 32);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 64; c += 4) {
+                                m0 = max3(m0, x[c], x[c + 1]);
+                                m1 = max3(m1, x[c + 2], x[c + 3]);
+                            }
                         }
-                        const int32_t key0 = t * kPaTile, hi_c = pos - key0, lo_c = lo - key0;
-                        if (__any_sync(0xffffffffu, hi_c < kPaTile - 1 || lo_c > 0)) {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c) x[c] = c <= hi_c && c >= lo_c ? x[c] : -INFINITY;
-                        }
-                        float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]), m2 = fmaxf(x[4], x[5]), m3 = fmaxf(x[6], x[7]);
-#pragma unroll
-                        for (int c = 8; c < 128; c += 8) {
-                            m0 = fmaxf(m0, fmaxf(x[c], x[c + 1]));
-                            m1 = fmaxf(m1, fmaxf(x[c + 2], x[c + 3]));
-                            m2 = fmaxf(m2, fmaxf(x[c + 4], x[c + 5]));
-                            m3 = fmaxf(m3, fmaxf(x[c + 6], x[c + 7]));
-                        }
-                        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * a.scale_log2 - kLift;
+                        if (CAP || edge) tc_wait_st();
+                        const float top = fmaxf(m0, m1) * a.scale_log2 - kLift;
                         // move the reference when a row grew past the slack
                         if (__any_sync(0xffffffffu, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
                             const float now = fmaxf(ref, top);
                             if (i > 0) {
                                 const float f = now == -INFINITY ? 1.0f : ex2(ref - now);
-                                const float2 f2 = make_float2(f, f), z2 = make_float2(0.0f, 0.0f);
-                                sum2 = fma2(sum2, f2, z2);
-#pragma unroll
+                                sum2.x *= f;
+                                sum2.y *= f;
+#pragma unroll 1
                                 for (int c = 0; c < HD; c += 32) {
                                     float o[32];
                                     tc_ld32(t_row + kO + d * HD + c, o);
@@ -691,23 +824,30 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             }
                             ref = now;
                         }
+                        // second pass: the weights, 32 at a time, the next scores on
+                        // their way; P takes the place of scores already read
                         const float base = ref == -INFINITY ? 0.0f : ref;
                         const float2 sc = make_float2(a.scale_log2, a.scale_log2), nb = make_float2(-base, -base);
-                        float2 acc[4] = {sum2, make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                        float2 acc = make_float2(0.0f, 0.0f);
+                        float x[4][32];
+                        tc_ld32(t_s, x[0]);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t p[32];
+                        for (int q = 0; q < 4; ++q) {
+                            tc_wait_ld();
+                            if (q < 3) tc_ld32(t_s + (q + 1) * 32, x[q + 1]);
+                            float p[16];
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                float2 v = fma2(make_float2(x[half * 64 + 2 * c], x[half * 64 + 2 * c + 1]), sc, nb);
+                            for (int c = 0; c < 16; ++c) {
+                                float2 v = fma2(make_float2(x[q][2 * c], x[q][2 * c + 1]), sc, nb);
                                 v.x = ex2(v.x);
                                 v.y = ex2(v.y);
-                                acc[c & 3] = add2(acc[c & 3], v);
-                                p[c] = pack2<BF16>(v.x, v.y);
+                                if (c & 1) acc = add2(acc, v);
+                                else sum2 = add2(sum2, v);
+                                p[c] = __uint_as_float(pack2<BF16>(v.x, v.y));
                             }
-                            tc_st32(t_s + half * 32, p);
+                            tc_st16(t_s + q * 16, p);
                         }
-                        sum2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                        sum2 = add2(sum2, acc);
                         tc_wait_st();
                         tc_before();
                     }
@@ -719,7 +859,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
 
                 // ---- the end of the item, or of this CTA's piece of it
                 float other_ref = -INFINITY, other_sum = 0.0f;
-                const bool two = !it.dual && pt.n > 1;  // a single item with a second stream
+                const bool two = !dual && job.n > 1;  // a single item with a second stream
                 if (two) {
                     if (d == 1) {
                         sh.ml[ml_items & 1][row] = make_float2(ref, sum);
@@ -735,7 +875,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     }
                     ++ml_items;
                 }
-                if (it.dual || d == 0) {
+                if (dual || d == 0) {
                     ok = pa_wait(&sh.o_full[d], o_phase[d], stop);
                     if (!ok) break;
                     if (two) {
@@ -747,11 +887,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         const float top = fmaxf(ref, other_ref), base = top == -INFINITY ? 0.0f : top;
                         float f0 = ex2(ref - base), f1 = two ? ex2(other_ref - base) : 0.0f;
                         sum = sum * f0 + other_sum * f1;
-                        const bool whole = pt.head && pt.tail;
+                        const bool whole = job.whole != 0;
                         if (whole) {
                             if (a.sinks != nullptr && valid) {
                                 // the sink joins the maximum and the sum (a row without rows stays zero)
-                                const float sink = a.sinks[w.h * a.group + rhead] * 1.4426950408889634f;
+                                const float sink = a.sinks[job.kv_head * a.group + rhead] * 1.4426950408889634f;
                                 const float all = fmaxf(top, sink), g = ex2(base - all);
                                 if (top != -INFINITY) {
                                     sum = sum * g + ex2(sink - all);
@@ -763,13 +903,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             f0 *= inv;
                             f1 *= inv;
                         }
-                        const int32_t slot = blockIdx.x * 2 + (pt.head ? 1 : 0);
-                        const int32_t prow = (it.dual ? d * a.tile_tok * a.group : 0) + row;
+                        const int32_t slot = blockIdx.x * 2 + job.head;
+                        const int32_t prow = (dual ? d * a.tile_tok * a.group : 0) + row;
                         if (!whole && valid) a.part_ml[int64_t(slot) * a.part_rows + prow] = make_float2(top, sum);
                         uint8_t *dst = static_cast<uint8_t *>(a.out) +
-                                       ((int64_t(w.s.q0) + tok) * a.out_tok + int64_t(w.h * a.group + rhead) * a.out_head) * 2;
+                                       ((int64_t(job.q0) + tok) * a.out_tok + int64_t(job.kv_head * a.group + rhead) * a.out_head) * 2;
                         float *pdst = a.part_o + (int64_t(slot) * a.part_rows + prow) * HD;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < HD; c += 32) {
                             float y[32];
                             __syncwarp();
@@ -802,25 +942,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     __syncwarp();
                     if (lane == 0) {
                         // O1 first: the MMA warp takes O0 of a single item as a sign for both
-                        if (!it.dual) pa_arrive(&sh.o_empty[1]);
+                        if (!dual) pa_arrive(&sh.o_empty[1]);
                         pa_arrive(&sh.o_empty[d]);
-                    }
-                    if (threadIdx.x == 0) {
-                        int32_t *m = a.meta + blockIdx.x * 8;
-                        if (pt.head && !pt.tail) {
-                            m[kPmTail] = 1;
-                            m[kPmSeq] = w.b;
-                            m[kPmHead] = w.h;
-                            m[kPmTok] = w.tok;
-                        }
-                        if (!pt.head && pt.tail) m[kPmFirst] = 1;
                     }
                 }
                 o_phase[0] ^= 1;
-                if (it.dual || two) o_phase[1] ^= 1;
-                left -= it.units - unit < left ? it.units - unit : left;
-                unit = 0;
-                if (left > 0) pa_next(a, w);
+                if (dual || two) o_phase[1] ^= 1;
+                done_job();
             }
         }
     }
@@ -828,9 +956,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     __syncwarp();
     if (*stop != 0) {
         if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
-        if (warp == 8)
-            for (int32_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-                mbar_wait_bounded(&sh.kv_full[i % S::kStages], (i / S::kStages) & 1, 500000000ull);
+        for (int i = 0; i < S::kStages; ++i)
+            if (loaded >> i & 1) mbar_wait_bounded(&sh.kv_full[i], parity >> i & 1, 500000000ull);
         if (warp == 9) mbar_wait_bounded(&sh.drain, 0, 500000000ull);
     }
     tc_before();
