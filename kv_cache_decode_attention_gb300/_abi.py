@@ -106,14 +106,13 @@ _SIGS = {
     "rswa_verify_i8": [_vp, _vp, _vp, _i32, _P(rswa_i8_mirror), _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i32,
                        _f32, _vp, _vp, _i64, _vp],
     "rswa_device_error": [_vp, _i32, _P(C.c_uint32)],
-    "kvd_rope_init": [_P(kvd_rope), _P(kvd_rope_config)],
-    "kvd_rope_apply": [_P(kvd_rope), _P(kvd_rows), _P(kvd_rows), _i32, _P(kvd_rows), _P(kvd_rows), _i32, _i32, _i32,
-                       _vp, _i64, _vp],
+    # kvd_rows and kvd_rope_config are taken as any buffer of their layout (packed bytes, or byref of the structs)
+    "kvd_rope_init": [_P(kvd_rope), _vp],
+    "kvd_rope_apply": [_P(kvd_rope), _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp],
     "kv_paged_plan": [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
-    "kv_paged_append": [_P(kvd_rope), _P(kvd_rows), _P(kvd_rows), _i32, _P(kvd_rows), _P(kvd_rows), _i32, _i32, _i32,
-                        _i32, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _vp],
+    "kv_paged_append": [_P(kvd_rope), _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _vp],
     "paged_attention_workspace_bytes": [_i64, _i32, _i32, _i32, _P(_i64)],
-    "paged_attention": [_P(kvd_rows), _P(kvd_rows), _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i32, _vp,
+    "paged_attention": [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i32, _vp,
                         _vp, _i32, _f32, _i64, _f32, _vp, _vp, _i64, _vp, _vp],
     "kv_paged_device_error": [_vp, _i32, _P(C.c_uint32)],
     "kvd_status_string": [_i32],

@@ -24,7 +24,8 @@
 //                   zeros); small pages take many copies, hence two warps;
 //   warp 9          issues the MMAs: S = Q K^T and O += P V, P from TMEM;
 //   warp 10         clears the rows of V behind a request's last one;
-//   warp 11         walks the CTA's share of the work and hands the items on.
+//   warp 11         walks the CTA's share of the work and hands the items on;
+//   warp 13         ends every wait if the CTA stops making steps.
 // TMEM: S0 S1 (128 columns each; P overwrites the first 64) O0 O1.
 // MMAs of one thread run in order, so S of a stream's next tile may be issued
 // behind P V of its last one without a wait, and S being complete says that P V
@@ -44,7 +45,7 @@
 namespace kvd {
 
 constexpr int kPaCtas = 152;       // one per SM; also fixes the cut of the work
-constexpr int kPaThreads = 512;    // warps 13 to 15 only fill their warpgroup
+constexpr int kPaThreads = 512;    // warps 14 and 15 only fill their warpgroup
 // Registers a thread: the launch gives 512 x 128; the softmax warpgroups trade up.
 constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
 static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
@@ -116,25 +117,19 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-// The MMAs are issued by a whole warp that elects a lane for each: their
-// operands are uniform registers, which converged code holds anyway, while a
-// branch for one lane around all of them fills them anew for each instruction
-// (measured: 53 against 67 cycles an instruction, and slower still between batches).
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    if (elect_one())
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    if (elect_one())
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
 // Arrive once on bar when every MMA the elected lane has issued so far is complete.
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
@@ -191,40 +186,49 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// A wait that gives up: bounded in time, and ended early once another warp of
-// the CTA has given up.  The whole warp gets one answer.
-__device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, volatile int *stop) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-        if (!ok) {
-            const uint64_t t0 = global_ns();
-            while (!(ok = mbar_try_wait(bar, parity)))
-                if (*stop != 0 || global_ns() - t0 > 2000000000ull) break;
-        }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) *stop = 1;
-    return ok;
-}
-
-// The same for one thread.
+// A wait that gives up once *stop is set, which the watching warp does when the
+// CTA has made no step for two seconds.  Small on purpose: it stands in twenty
+// places, and code that does not stay in the instruction caches is paid again
+// for every item.
 __device__ __forceinline__ bool pa_wait_one(uint64_t *bar, uint32_t parity, volatile int *stop) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
+#pragma unroll 1
     while (!mbar_try_wait(bar, parity))
-        if (*stop != 0 || global_ns() - t0 > 2000000000ull) {
-            *stop = 1;
-            return false;
-        }
+        if (*stop != 0) return false;
     return true;
+}
+// Looks at three barriers at once; a bit for each whose phase is over.  While the tensor
+// cores read both operands from shared memory they leave little of its
+// bandwidth, and one such look takes some 200 cycles: the MMA warp takes its
+// looks together.
+__device__ __forceinline__ uint32_t pa_test3(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b, c;\n\t.reg .b32 x, y, z;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 a, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 b, [%3], %4;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 c, [%5], %6;\n\t"
+        "selp.u32 x, 1, 0, a;\n\tselp.u32 y, 2, 0, b;\n\tselp.u32 z, 4, 0, c;\n\t"
+        "or.b32 x, x, y;\n\tor.b32 %0, x, z;\n\t}"
+        : "=r"(r)
+        : "r"(smem_addr(b0)), "r"(p0), "r"(smem_addr(b1)), "r"(p1), "r"(smem_addr(b2)), "r"(p2)
+        : "memory");
+    return __reduce_and_sync(0xffffffffu, r);
+}
+// A wait with one answer for a whole warp.
+__device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, volatile int *stop) {
+    return __all_sync(0xffffffffu, pa_wait_one(bar, parity, stop));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// Bits lo .. hi of 32 (none if lo > hi or both lie outside): the columns a row sees.
+__device__ __forceinline__ uint32_t pa_seen(int32_t lo, int32_t hi) {
+    const uint32_t to = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+    const uint32_t from = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+    return to & from;
 }
 
 // ---------------------------------------------------------------- the work
@@ -290,66 +294,72 @@ __device__ __forceinline__ void pa_next(const PaArgs &a, PaWalk &w) {
 
 struct PaStart {
     int32_t b, h, tok, unit;  // first item and the unit in it
+    PaSeq s;                  // its request
     int64_t units;            // units of this CTA
 };
 
-// The cut: CTA c of n takes units [c W / n, (c + 1) W / n) of the W there are.
-// All threads; the result is in shared memory.
+// The cut: CTA c of kPaCtas takes units [c W / kPaCtas, (c + 1) W / kPaCtas) of
+// the W there are.  All threads; the result is in shared memory.
 __device__ __forceinline__ void pa_cut(const PaArgs &a, PaStart *out, int64_t *warp_sums) {
     const int per = (a.n_seq + kPaThreads - 1) / kPaThreads;
     const int b0 = threadIdx.x * per < a.n_seq ? threadIdx.x * per : a.n_seq;
     const int b1 = b0 + per < a.n_seq ? b0 + per : a.n_seq;
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const PaSeq s = pa_seq(a, b, blockIdx.x == 0);
-        int64_t u = 0;
-        for (int32_t tok = 0; tok < s.fresh; tok += 2 * a.tile_tok) u += pa_item(a, s, tok).units;
-        mine += u * a.n_kv;
-    }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int64_t x = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) warp_sums[w] = x;
-    if (threadIdx.x == 0) out->units = 0;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < kPaThreads / 32; ++i) {
-        const int64_t v = warp_sums[i];
-        before += i < w ? v : 0;
-        total += v;
-    }
-    before += x - mine;
-    const int64_t from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
-    if (from < to && before <= from && from < before + mine) {
-        int64_t off = from - before;
+    // first turn: this thread's units; second, for the thread whose requests
+    // hold the CTA's first unit: where it is in them
+    int64_t mine = 0, off = 0, u = 0, from = 0, to = 0;
+    PaSeq s = {0, 0, 0};
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
         int b = b0;
-        PaSeq s;
-        int64_t u;
-        for (;; ++b) {
-            s = pa_seq(a, b, false);
-            u = 0;
-            for (int32_t tok = 0; tok < s.fresh; tok += 2 * a.tile_tok) u += pa_item(a, s, tok).units;
-            if (off < u * a.n_kv) break;
-            off -= u * a.n_kv;
+        if (turn == 0 || per > 1) {  // a thread's only request is still at hand
+#pragma unroll 1
+            for (; b < b1; ++b) {
+                s = pa_seq(a, b, turn == 0 && blockIdx.x == 0);
+                u = 0;
+#pragma unroll 1
+                for (int32_t tok = 0; tok < s.fresh; tok += 2 * a.tile_tok) u += pa_item(a, s, tok).units;
+                if (turn == 0) mine += u * a.n_kv;
+                else if (off < u * a.n_kv) break;
+                else off -= u * a.n_kv;
+            }
         }
-        const int32_t h = int32_t(off / u);
-        off -= h * u;
-        int32_t tok = 0;
-        for (;; tok += 2 * a.tile_tok) {
-            const int32_t n = pa_item(a, s, tok).units;
-            if (off < n) break;
-            off -= n;
+        if (turn == 1) {
+            int32_t h = 0, tok = 0;
+#pragma unroll 1
+            for (; off >= u; off -= u) ++h;
+#pragma unroll 1
+            for (;; tok += 2 * a.tile_tok) {
+                const int32_t n = pa_item(a, s, tok).units;
+                if (off < n) break;
+                off -= n;
+            }
+            *out = PaStart{b, h, tok, int32_t(off), s, to - from};
+            break;
         }
-        out->b = b;
-        out->h = h;
-        out->tok = tok;
-        out->unit = int32_t(off);
-        out->units = to - from;
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) warp_sums[w] = x;
+        if (threadIdx.x == 0) out->units = 0;
+        __syncthreads();
+        constexpr int kWarps = kPaThreads / 32;
+        int64_t before = lane < kWarps ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < kWarps; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += y;
+        }
+        const uint64_t total = __shfl_sync(0xffffffffu, before, kWarps - 1);
+        before = __shfl_sync(0xffffffffu, before, w > 0 ? w - 1 : 0);
+        before = (w > 0 ? before : 0) + x - mine;
+        from = total * blockIdx.x / kPaCtas;
+        to = total * (blockIdx.x + 1) / kPaCtas;
+        off = from - before;
+        if (from >= to || off < 0 || off >= mine) break;
     }
     __syncthreads();
 }
@@ -382,11 +392,11 @@ struct PaShared {
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2];
-    uint64_t ml_full[2], tail_go, tail_ready, drain;
+    uint64_t ml_full[2], tail_go, tail_ready, all_done, drain;
     PaStart start;
     int64_t warp_sums[kPaThreads / 32];
     uint32_t tmem;
-    int stop;
+    int stop, steps;  // the watch: give up; changes with every K tile that is loaded
     float2 ml[2][kPaTile];  // stream 1's maximum and sum of a single item, by item parity
 };
 
@@ -433,6 +443,9 @@ struct PaIssue {
         }
         return at;
     }
+    // the stage after the next one
+    __device__ __forceinline__ uint32_t after() const { return stage + 1 == S::kStages ? 0 : stage + 1; }
+    __device__ __forceinline__ uint32_t phase_after() const { return stage + 1 == S::kStages ? phase ^ 1 : phase; }
     // Shared-memory matrix descriptor, 128-byte swizzle, groups of eight rows
     // 1024 bytes apart; for MN-major operands lbo = bytes between runs of 64.
     static __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t lbo) {
@@ -442,8 +455,9 @@ struct PaIssue {
     // S of stream d = Q tile qt x K in stage k
     __device__ __forceinline__ void score(int d, int qt, uint32_t k) const {
         constexpr uint32_t id = tc_idesc(BF16, 128, 128, false);
-        const uint64_t qd = desc(q + qt * (S::kQTileBytes >> 4), 16), kd = desc(kv + k * (S::kStageBytes >> 4), 16);
+        const uint64_t qd = desc(uni(q + qt * (S::kQTileBytes >> 4)), 16), kd = desc(uni(kv + k * (S::kStageBytes >> 4)), 16);
         tc_after();
+        if (!elect_one()) return;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
             constexpr uint32_t kHalf = kPaTile * 128 >> 4;
@@ -454,8 +468,9 @@ struct PaIssue {
     // O of stream d (+)= P x V in stage v
     __device__ __forceinline__ void value(int d, uint32_t v, bool more) const {
         constexpr uint32_t id = tc_idesc(BF16, 128, HD, true);
-        const uint64_t vd = desc(kv + v * (S::kStageBytes >> 4), kPaTile * 128);
+        const uint64_t vd = desc(uni(kv + v * (S::kStageBytes >> 4)), kPaTile * 128);
         tc_after();
+        if (!elect_one()) return;
 #pragma unroll
         for (int kk = 0; kk < kPaTile / 16; ++kk)
             tc_mma_ts(tmem + 256 + d * HD, tmem + d * 128 + kk * 8, vd + kk * (2048 >> 4), id, more || kk != 0);
@@ -497,10 +512,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             mbar_init(&sh.job_empty[i], 12);  // two of loads, MMAs, ends of V, eight softmax warps
         }
         mbar_init(&sh.tail_go, 1);
+        mbar_init(&sh.all_done, 8);
         mbar_init(&sh.tail_ready, 1);
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.stop = 0;
+        sh.steps = 0;
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
@@ -581,11 +598,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         __syncwarp();
                         if (lane < ppt) {
                             const uint32_t dst = kv_smem + stage * S::kStageBytes + lane * box;
-#pragma unroll
+#pragma unroll 1
                             for (int i = 0; i < S::kHalves; ++i)
                                 tma_2d(dst + i * (kPaTile * 128), map, i * 64, now, &sh.kv_full[stage]);
                         }
                         loaded |= 1u << stage;
+                        if (lane == 0 && !v_warp) *static_cast<volatile int *>(&sh.steps) = int(ring) + t;
                         parity = (parity & ~(1u << stage)) | (turn & 1) << stage;
                         if (t == 0 && !v_warp) {
                             // Q once the MMAs of the item before have read theirs
@@ -594,11 +612,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             if (lane == 0) {
                                 const uint32_t bytes = uint32_t(a.tile_tok * a.group) * 128u * S::kHalves;
                                 mbar_arrive_expect_tx(&sh.q_full, dual ? 2 * bytes : bytes);
-                                for (int d = 0; d < (dual ? 2 : 1); ++d)
-#pragma unroll
-                                    for (int i = 0; i < S::kHalves; ++i)
-                                        tma_4d(q_smem + d * S::kQTileBytes + i * (kPaTile * 128), &a.q, i * 64, 0, h,
-                                               q_row + d * a.tile_tok, &sh.q_full);
+#pragma unroll 1
+                                for (int i = 0; i < (dual ? 2 * S::kHalves : S::kHalves); ++i)
+                                    tma_4d(q_smem + i * (kPaTile * 128), &a.q, i % S::kHalves * 64, 0, h,
+                                           q_row + i / S::kHalves * a.tile_tok, &sh.q_full);
                             }
                             __syncwarp();
                             ++items;
@@ -633,10 +650,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     // (written out for both streams: what differs are constants)
                     auto step = [&](int32_t j, auto stream) {
                         constexpr int d = decltype(stream)::value;
-                        const bool second = !dual || d == 1;  // the tiles' last use
+                        const bool first = !dual || d == 0, second = !dual || d == 1;  // the tiles' first and last use
+                        const bool ahead = j + 2 < steps;
+                        uint32_t is = 0;  // bits: V there, P there, next K there
                         if (j >= 0) {
-                            if (!dual || d == 0) {
-                                ok = mma.wait_stage();
+                            if (first) {
+                                is = pa_test3(&sh.kv_full[mma.stage], mma.phase, &sh.p_ready[d], p_phase >> d & 1, &sh.kv_full[mma.after()], mma.phase_after());
+                                if ((is & 1) == 0) ok = mma.wait_stage();
                                 if (ok && (dual ? j >> 1 : j) == tail) {  // it ends short: cleared first
                                     if (elect_one()) pa_arrive(&sh.tail_go);
                                     ok = mma.wait(&sh.tail_ready, tails++ & 1);
@@ -645,15 +665,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             }
                             // before the first write to O the last item's must have been read
                             if (ok && j < 2 && items > 0) ok = mma.wait(&sh.o_empty[d], (items - 1) & 1);
-                            if (ok) ok = mma.wait(&sh.p_ready[d], p_phase >> d & 1);
+                            if (ok && (is & 2) == 0) ok = mma.wait(&sh.p_ready[d], p_phase >> d & 1);
                             if (!ok) return;
                             p_phase ^= 1u << d;
                             mma.value(d, v, j >= 2);
-                            if (j + 2 >= steps) tc_commit(&sh.o_full[d]);
+                            if (!ahead) tc_commit(&sh.o_full[d]);
                         }
-                        if (j + 2 < steps) {
-                            if (!dual || d == 0) {
-                                ok = mma.wait_stage();
+                        if (ahead) {
+                            if (first) {
+                                if ((is & 4) == 0) ok = mma.wait_stage();
                                 if (!ok) return;
                                 k = mma.take();
                             }
@@ -701,9 +721,24 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     }
                     ring += 2 * n;
                 }
+            } else if (warp == 13 && lane == 0) {
+                // ------------------------------------------------------ watch
+                volatile int *steps = &sh.steps;
+                int last = 0;
+                uint64_t since = global_ns();
+                while (!mbar_try_wait(&sh.all_done, 0)) {
+                    const uint64_t now = global_ns();
+                    if (*steps != last) {
+                        last = *steps;
+                        since = now;
+                    } else if (now - since > 2000000000ull) {
+                        *stop = 1;
+                        break;
+                    }
+                }
             } else if (warp == 11 && lane == 0) {
                 // ------------------------------------------------------ items
-                PaWalk w = {st.b, st.h, st.tok, pa_seq(a, st.b, false)};
+                PaWalk w = {st.b, st.h, st.tok, st.s};
                 int32_t unit = st.unit;
                 int64_t left = st.units;
                 bool ok = true;
@@ -789,9 +824,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 for (int c = 0; c < 64; ++c) x[c] = 1.0f - __fdividef(2.0f, ex2(x[c] * a.cap_in) + 1.0f);
                             }
                             if (edge) {
-                                const int32_t hi = hi_c - c0, low = lo_c - c0;
 #pragma unroll
-                                for (int c = 0; c < 64; ++c) x[c] = c <= hi && c >= low ? x[c] : -INFINITY;
+                                for (int e = 0; e < 64; e += 32) {
+                                    const uint32_t seen = pa_seen(lo_c - c0 - e, hi_c - c0 - e);
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
+                                }
                             }
                             if (CAP || edge) {
                                 tc_st32(t_s + c0, x);
@@ -911,19 +949,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         float *pdst = a.part_o + (int64_t(slot) * a.part_rows + prow) * HD;
 #pragma unroll 1
                         for (int c = 0; c < HD; c += 32) {
-                            float y[32];
+                            float y[32], z[32];
                             __syncwarp();
                             tc_ld32(t_row + kO + d * HD + c, y);
+                            if (two) tc_ld32(t_row + kO + HD + c, z);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] *= f0;
-                            if (two) {
-                                float z[32];
-                                tc_ld32(t_row + kO + HD + c, z);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] += z[e] * f1;
-                            }
+                            for (int e = 0; e < 32; ++e) y[e] = two ? y[e] * f0 + z[e] * f1 : y[e] * f0;
                             if (valid && whole) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 8)
@@ -950,12 +982,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 if (dual || two) o_phase[1] ^= 1;
                 done_job();
             }
+            __syncwarp();
+            if (lane == 0) pa_arrive(&sh.all_done);
         }
     }
     // ---- the end: nothing may still be in flight into this CTA's memory
     __syncwarp();
     if (*stop != 0) {
         if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
+#pragma unroll 1
         for (int i = 0; i < S::kStages; ++i)
             if (loaded >> i & 1) mbar_wait_bounded(&sh.kv_full[i], parity >> i & 1, 500000000ull);
         if (warp == 9) mbar_wait_bounded(&sh.drain, 0, 500000000ull);

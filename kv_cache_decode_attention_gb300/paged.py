@@ -14,60 +14,56 @@ allocates buffers, marshals pointers and raises on a non-OK status.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
+import struct
 
 import torch
 
 from . import _abi
-from .api import _ptr, _stream
 
+_I32, _F32 = torch.int32, torch.float32
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
+# A step makes four calls a layer, so what the binding costs a call counts: the
+# structs of the ABI are packed as bytes, checks read each attribute once, and
+# the current device and stream are asked for without building objects.
+_pack_rows = struct.Struct("Pqq").pack          # kvd_rows
+_pack_config = struct.Struct("iiii8d").pack     # kvd_rope_config
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-def _i32(t, name, numel=None, device=None):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()):
-        raise ValueError("%s must be a contiguous int32 CUDA tensor" % name)
+
+def _stream(index, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _i32(t, name, numel, device):
+    """A contiguous int32 tensor of so many numbers on the device; its pointer."""
+    if not (t.dtype is _I32 and t.device == device and t.is_contiguous()):
+        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
     if numel is not None and t.numel() != numel:
         raise ValueError("%s must hold %d numbers, has %d" % (name, numel, t.numel()))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    return t
+    return t.data_ptr()
 
 
-def _rows(t, name, heads_dim, device):
+def _rows(t, name, shape, device):
     """kvd_rows of a [tokens, heads, head_dim] view (head_dim contiguous)."""
-    if not (t.is_cuda and t.device == device):
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
-    if t.dim() != 3 or (heads_dim is not None and t.shape[2] != heads_dim) or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError("%s must be [tokens, heads, head_dim] with head_dim contiguous" % name)
-    return _abi.kvd_rows(t.data_ptr(), t.stride(0), t.stride(1))
+    stride = t.stride()
+    if t.shape != shape or t.device != device or (stride[2] != 1 and shape[2] > 1):
+        raise ValueError("%s must be %s on %s with head_dim contiguous" % (name, list(shape), device))
+    return _pack_rows(t.data_ptr(), stride[0], stride[1])
 
 
-class _on:
-    """Makes `device` current for the launches inside (nothing to do when it is)."""
-
-    __slots__ = ("device", "before")
-
-    def __init__(self, device):
-        self.device = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.device is not None and self.before != self.device:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *a):
-        if self.device is not None and self.before != self.device:
-            torch.cuda.set_device(self.before)
-
-
-def _own(t, stream):
-    """A tensor allocated here and used on a stream of the caller's choice."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _cuda(device):
+    """The index of a CUDA device."""
+    if device.type != "cuda":
+        raise ValueError("the paged calls take CUDA tensors, got one on %s" % device)
+    return device.index if device.index is not None else _device()
 
 
 class RopeTable:
@@ -79,7 +75,7 @@ class RopeTable:
     attention_factor multiplies cos and sin (None: 1, for yarn 0.1 ln(factor) + 1).
     """
 
-    __slots__ = ("rot_dim", "layout", "scaling", "R", "_ref")
+    __slots__ = ("rot_dim", "layout", "scaling", "R")
 
     def __init__(self, rot_dim: int, layout: str = "half", scaling: str = "none", base: float = 10000.0,
                  factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
@@ -89,12 +85,12 @@ class RopeTable:
         if scaling not in _SCALINGS:
             raise ValueError("scaling must be one of %s" % ", ".join(sorted(_SCALINGS)))
         self.rot_dim, self.layout, self.scaling = int(rot_dim), layout, scaling
-        cfg = _abi.kvd_rope_config(self.rot_dim, _LAYOUTS[layout], _SCALINGS[scaling], 0, base, factor, original_len,
-                                   beta_fast, beta_slow, low_freq_factor, high_freq_factor,
-                                   0.0 if attention_factor is None else attention_factor)
         self.R = _abi.kvd_rope()
-        self._ref = C.byref(self.R)
-        _abi.call("kvd_rope_init", self._ref, C.byref(cfg))
+        st = _abi.lib().kvd_rope_init(self.R, _pack_config(
+            self.rot_dim, _LAYOUTS[layout], _SCALINGS[scaling], 0, base, factor, original_len, beta_fast, beta_slow,
+            low_freq_factor, high_freq_factor, 0.0 if attention_factor is None else attention_factor))
+        if st:
+            _abi.check("kvd_rope_init", st)
 
 
 def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, table: RopeTable,
@@ -107,33 +103,49 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor
     some = q if q is not None else k
     if some is None:
         raise ValueError("rope needs q or k")
-    dev, tokens, hd = some.device, some.shape[0], some.shape[-1]
-    if some.dtype not in _DTYPES:
+    dev, dtype = some.device, some.dtype
+    index = _cuda(dev)
+    if _device() != index:
+        with torch.cuda.device(dev):
+            return rope(q, k, positions, table, q_out, k_out, stream)
+    if dtype not in _DTYPES:
         raise ValueError("rope takes float32, float16 or bfloat16")
-    if not some.is_cuda:
-        raise ValueError("rope takes CUDA tensors")
-    _i32(positions, "positions", tokens, dev)
-    args = []
-    outs = []
-    with _on(dev):
-        for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if t is None:
-                if o is not None:
-                    raise ValueError("%s_out without %s" % (name, name))
-                args += [None, None, 0]
-                outs.append(None)
-                continue
-            if t.dtype != some.dtype or t.shape[0] != tokens:
-                raise ValueError("q and k must have one dtype and as many tokens")
-            if o is None:
-                o = _own(torch.empty(t.shape, dtype=t.dtype, device=dev), stream)
-            elif o.dtype != t.dtype or o.shape != t.shape:
-                raise ValueError("%s_out must have the shape and dtype of %s" % (name, name))
-            args += [_rows(t, name, hd, dev), _rows(o, name + "_out", hd, dev), t.shape[1]]
-            outs.append(o)
-        _abi.call("kvd_rope_apply", table._ref, *args, hd, _DTYPES[some.dtype], positions.data_ptr(), tokens,
-                  _stream(stream))
-    return outs[0], outs[1]
+    if some.dim() != 3:
+        raise ValueError("rope takes [tokens, heads, head_dim]")
+    tokens, _, hd = some.shape
+    pos = _i32(positions, "positions", tokens, dev)
+    qi = qo = ki = ko = None
+    n_q = n_k = 0
+    if q is not None:
+        n_q = q.shape[1]
+        qi = _rows(q, "q", (tokens, n_q, hd), dev)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+            if stream is not None:
+                q_out.record_stream(stream)
+        elif q_out.dtype is not dtype:
+            raise ValueError("q_out must have q's dtype")
+        qo = _rows(q_out, "q_out", (tokens, n_q, hd), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        if k.dtype is not dtype or k.dim() != 3:
+            raise ValueError("q and k must have one dtype and be [tokens, heads, head_dim]")
+        n_k = k.shape[1]
+        ki = _rows(k, "k", (tokens, n_k, hd), dev)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+            if stream is not None:
+                k_out.record_stream(stream)
+        elif k_out.dtype is not dtype:
+            raise ValueError("k_out must have k's dtype")
+        ko = _rows(k_out, "k_out", (tokens, n_k, hd), dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    st = _abi.lib().kvd_rope_apply(table.R, qi, qo, n_q, ki, ko, n_k, hd, _DTYPES[dtype], pos, tokens, _stream(index, stream))
+    if st:
+        _abi.check("kvd_rope_apply", st)
+    return q_out, k_out
 
 
 class PagedKvCache:
@@ -146,7 +158,7 @@ class PagedKvCache:
     """
 
     __slots__ = ("k", "v", "block_table", "seq_len", "free_pages", "n_free", "error", "page_size", "n_pages", "n_kv",
-                 "head_dim", "n_seq", "max_pages", "dtype", "device")
+                 "head_dim", "n_seq", "max_pages", "dtype", "device", "index")
 
     def __init__(self, n_pages: int, page_size: int, n_kv: int, head_dim: int, n_seq: int, max_pages: int,
                  dtype=torch.bfloat16, device="cuda"):
@@ -175,41 +187,45 @@ class PagedKvCache:
                                self.free_pages, self.n_free, self.error)
 
     def _bind(self, k, v, block_table, seq_len, free_pages, n_free, error, page_size):
+        dev = block_table.device
+        self.index = _cuda(dev)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [n_seq, max_pages]")
-        dev = block_table.device
-        self.n_seq, self.max_pages = block_table.shape
-        _i32(block_table, "block_table")
-        _i32(seq_len, "seq_len", self.n_seq, dev)
+        n, self.max_pages = block_table.shape
+        self.n_seq, self.device = n, dev
+        _i32(block_table, "block_table", None, dev)
+        _i32(seq_len, "seq_len", n, dev)
         if k is not None:
-            for t, name in ((k, "k"), (v, "v")):
-                if not (t is not None and t.is_cuda and t.device == dev and t.dim() == 4 and t.is_contiguous()):
-                    raise ValueError("%s must be contiguous pages [n_pages, n_kv, page_size, head_dim] on %s" % (name, dev))
-            if k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.float16, torch.bfloat16):
+            dtype, shape = k.dtype, k.shape
+            if v is None or v.dtype is not dtype or v.shape != shape or (dtype is not torch.bfloat16 and dtype is not torch.float16):
                 raise ValueError("k and v must have one shape and be float16 or bfloat16")
-            self.n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
+            if not (len(shape) == 4 and k.device == dev and v.device == dev and k.is_contiguous() and v.is_contiguous()):
+                raise ValueError("k and v must be contiguous pages [n_pages, n_kv, page_size, head_dim] on %s" % dev)
+            self.n_pages, self.n_kv, self.page_size, self.head_dim = shape
             if page_size is not None and page_size != self.page_size:
                 raise ValueError("page_size is not that of the pages")
-            self.dtype = k.dtype
+            self.dtype = dtype
         else:
             if page_size is None or free_pages is None or v is not None:
                 raise ValueError("a cache without k and v needs page_size and free_pages")
             self.n_pages, self.n_kv, self.page_size, self.head_dim, self.dtype = free_pages.numel(), 0, int(page_size), 0, None
         if free_pages is not None:
+            if n_free is None:
+                raise ValueError("free_pages without n_free")
             _i32(free_pages, "free_pages", self.n_pages, dev)
             _i32(n_free, "n_free", 1, dev)
         if error is None:
-            error = torch.zeros(1, dtype=torch.int32, device=dev)
+            error = torch.zeros(1, dtype=_I32, device=dev)
         _i32(error, "error", 1, dev)
         self.k, self.v, self.block_table, self.seq_len = k, v, block_table, seq_len
-        self.free_pages, self.n_free, self.error, self.device = free_pages, n_free, error, dev
+        self.free_pages, self.n_free, self.error = free_pages, n_free, error
 
     def device_error(self, clear: bool = True) -> int:
         """The error word (synchronises): bit 0 a bounded wait gave up, bit 1
         metadata out of range, bit 2 a plan did not fit."""
         w = C.c_uint32(0)
-        with _on(self.device):
-            st = _abi.lib().kv_paged_device_error(_ptr(self.error), int(clear), C.byref(w))
+        with torch.cuda.device(self.device):
+            st = _abi.lib().kv_paged_device_error(self.error.data_ptr(), int(clear), C.byref(w))
         if st not in (_abi.OK, _abi.EDEVICE):
             _abi.check("kv_paged_device_error", st)
         return int(w.value)
@@ -236,37 +252,43 @@ def paged_plan(cache: PagedKvCache, new_len: torch.Tensor, n_tokens: int, keep_l
     stay (the plan holds the new ones), and the step may be planned again.
     plan: buffers of an earlier plan to fill again, as a captured graph needs.
     A step that does not fit changes nothing and sets the error word's bit 2."""
-    if cache.free_pages is None:
+    free = cache.free_pages
+    if free is None:
         raise ValueError("the cache has no free pages to plan with")
-    dev, n = cache.device, cache.n_seq
-    _i32(new_len, "new_len", n, dev)
-    if keep_len is not None:
-        _i32(keep_len, "keep_len", n, dev)
+    dev, n, index = cache.device, cache.n_seq, cache.index
+    if _device() != index:
+        with torch.cuda.device(dev):
+            return paged_plan(cache, new_len, n_tokens, keep_len, advance, plan, stream)
+    new = _i32(new_len, "new_len", n, dev)
+    keep = None if keep_len is None else _i32(keep_len, "keep_len", n, dev)
     n_tokens = int(n_tokens)
-    with _on(dev):
-        if plan is None:
-            if n_tokens < 0:
-                raise ValueError("n_tokens must not be negative")
-            # one allocation, cut into the step's arrays
-            sizes = [n + 1, n_tokens, n_tokens] + ([] if advance else [n, 1])
-            parts = _own(torch.empty(sum(sizes), dtype=torch.int32, device=dev), stream).split(sizes)
-            plan = PagedPlan(parts[0], cache.seq_len if advance else parts[3], cache.n_free if advance else parts[4],
-                             parts[1], parts[2])
-        else:
-            _i32(plan.cu_new, "plan.cu_new", n + 1, dev)
-            _i32(plan.positions, "plan.positions", n_tokens, dev)
-            _i32(plan.slots, "plan.slots", n_tokens, dev)
-            if advance:
-                plan.seq_len, plan.n_free = cache.seq_len, cache.n_free
-            _i32(plan.seq_len, "plan.seq_len", n, dev)
-            _i32(plan.n_free, "plan.n_free", 1, dev)
-            if not advance and (plan.seq_len is cache.seq_len or plan.n_free is cache.n_free):
-                raise ValueError("plan holds the cache's own state: pass advance=True, or a plan made with advance=False")
-        _abi.call("kv_paged_plan", cache.seq_len.data_ptr(), None if keep_len is None else keep_len.data_ptr(),
-                  new_len.data_ptr(), n, cache.n_pages, cache.page_size, cache.block_table.data_ptr(), cache.max_pages,
-                  cache.free_pages.data_ptr(), cache.n_free.data_ptr(), plan.seq_len.data_ptr(), plan.n_free.data_ptr(),
-                  plan.cu_new.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(), n_tokens,
-                  cache.error.data_ptr(), _stream(stream))
+    if plan is None:
+        if n_tokens < 0:
+            raise ValueError("n_tokens must not be negative")
+        empty = torch.empty
+        plan = PagedPlan(empty(n + 1, dtype=_I32, device=dev), cache.seq_len if advance else empty(n, dtype=_I32, device=dev),
+                         cache.n_free if advance else empty(1, dtype=_I32, device=dev),
+                         empty(n_tokens, dtype=_I32, device=dev), empty(n_tokens, dtype=_I32, device=dev))
+        if stream is not None:
+            for t in (plan.cu_new, plan.seq_len, plan.n_free, plan.positions, plan.slots):
+                t.record_stream(stream)
+        cu, pos, slots = plan.cu_new.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr()
+    else:
+        cu = _i32(plan.cu_new, "plan.cu_new", n + 1, dev)
+        pos = _i32(plan.positions, "plan.positions", n_tokens, dev)
+        slots = _i32(plan.slots, "plan.slots", n_tokens, dev)
+        if advance:
+            plan.seq_len, plan.n_free = cache.seq_len, cache.n_free
+        _i32(plan.seq_len, "plan.seq_len", n, dev)
+        _i32(plan.n_free, "plan.n_free", 1, dev)
+        if not advance and (plan.seq_len is cache.seq_len or plan.n_free is cache.n_free):
+            raise ValueError("plan holds the cache's own state: pass advance=True, or a plan made with advance=False")
+    st = _abi.lib().kv_paged_plan(
+        cache.seq_len.data_ptr(), keep, new, n, cache.n_pages, cache.page_size, cache.block_table.data_ptr(),
+        cache.max_pages, free.data_ptr(), cache.n_free.data_ptr(), plan.seq_len.data_ptr(), plan.n_free.data_ptr(), cu, pos,
+        slots, n_tokens, cache.error.data_ptr(), _stream(index, stream))
+    if st:
+        _abi.check("kv_paged_plan", st)
     return plan
 
 
@@ -280,32 +302,46 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
         raise ValueError("the cache has no pages")
     if plan.positions is None or plan.slots is None:
         raise ValueError("the plan has no positions and slots")
-    dev, hd, tokens = cache.device, cache.head_dim, k.shape[0]
-    _i32(plan.positions, "plan.positions", tokens, dev)
-    _i32(plan.slots, "plan.slots", tokens, dev)
-    if k.dtype not in _DTYPES or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise ValueError("q, k and v must have one dtype")
-    if k.shape != (tokens, cache.n_kv, hd) or v.shape != k.shape:
+    dev, hd, n_kv, index = cache.device, cache.head_dim, cache.n_kv, cache.index
+    if _device() != index:
+        with torch.cuda.device(dev):
+            return paged_append(cache, plan, k, v, q, q_out, rope, stream)
+    tokens, dtype = k.shape[0], k.dtype
+    pos = _i32(plan.positions, "plan.positions", tokens, dev)
+    slots = _i32(plan.slots, "plan.slots", tokens, dev)
+    if dtype not in _DTYPES or v.dtype is not dtype:
+        raise ValueError("q, k and v must have one dtype: float32 or the pages'")
+    shape = (tokens, n_kv, hd)
+    if k.dim() != 3 or v.dim() != 3:
         raise ValueError("k and v must be [tokens, n_kv, head_dim]")
-    with _on(dev):
-        args = [None, None, 0]
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != tokens:
-                raise ValueError("q must be [tokens, n_q, head_dim]")
-            if q_out is None:
-                q_out = _own(torch.empty(q.shape, dtype=cache.dtype, device=dev), stream)
-            elif q_out.dtype != cache.dtype or q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape and the pages' dtype")
-            args = [_rows(q, "q", hd, dev), _rows(q_out, "q_out", hd, dev), q.shape[1]]
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        _abi.call("kv_paged_append", None if rope is None else rope._ref, *args, _rows(k, "k", hd, dev), _rows(v, "v", hd, dev),
-                  cache.n_kv, hd, _DTYPES[k.dtype], _DTYPES[cache.dtype], plan.positions.data_ptr(), plan.slots.data_ptr(),
-                  tokens, cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size, cache.error.data_ptr(),
-                  _stream(stream))
+    ki, vi = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+    qi = qo = None
+    n_q = 0
+    if q is not None:
+        if q.dim() != 3 or q.dtype is not dtype:
+            raise ValueError("q must be [tokens, n_q, head_dim] of k's dtype")
+        n_q = q.shape[1]
+        shape = (tokens, n_q, hd)
+        qi = _rows(q, "q", shape, dev)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=cache.dtype, device=dev)
+            if stream is not None:
+                q_out.record_stream(stream)
+        elif q_out.dtype is not cache.dtype:
+            raise ValueError("q_out must have the pages' dtype")
+        qo = _rows(q_out, "q_out", shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = _abi.lib().kv_paged_append(
+        None if rope is None else rope.R, qi, qo, n_q, ki, vi, n_kv, hd, _DTYPES[dtype], _DTYPES[cache.dtype], pos, slots,
+        tokens, cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size, cache.error.data_ptr(),
+        _stream(index, stream))
+    if st:
+        _abi.check("kv_paged_append", st)
     return q_out
 
 
+@functools.lru_cache(maxsize=None)
 def paged_attention_workspace(n_tokens: int, n_q: int, n_kv: int, head_dim: int) -> int:
     """Bytes of workspace that paged_attention needs for up to n_tokens new rows."""
     n = C.c_int64(0)
@@ -320,29 +356,44 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
     over all rows their requests hold; out has q's shape and dtype (rows behind
     the last new one are left as they were).
     window, softcap and sinks as in decode_attention."""
-    if cache.k is None:
+    k = cache.k
+    if k is None:
         raise ValueError("the cache has no pages")
-    dev, hd, n_kv = cache.device, cache.head_dim, cache.n_kv
-    if q.dim() != 3 or q.shape[2] != hd or q.dtype != cache.dtype:
+    dev, hd, n_kv, index, dtype = cache.device, cache.head_dim, cache.n_kv, cache.index, cache.dtype
+    if _device() != index:
+        with torch.cuda.device(dev):
+            return paged_attention(q, cache, plan, out, scale, window, softcap, sinks, workspace, stream)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != hd or q.dtype is not dtype:
         raise ValueError("q must be [tokens, n_q, head_dim] in the pages' dtype")
-    tokens, n_q = q.shape[0], q.shape[1]
-    _i32(plan.cu_new, "plan.cu_new", cache.n_seq + 1, dev)
-    _i32(plan.seq_len, "plan.seq_len", cache.n_seq, dev)
-    if sinks is not None and not (sinks.is_cuda and sinks.dtype == torch.float32 and sinks.is_contiguous() and
-                                  sinks.numel() == n_q and sinks.device == dev):
-        raise ValueError("sinks must be contiguous float32 [n_q] on %s" % dev)
-    with _on(dev):
-        if out is None:
-            out = _own(torch.empty(q.shape, dtype=q.dtype, device=dev), stream)
-        elif out.dtype != q.dtype or out.shape != q.shape:
-            raise ValueError("out must have q's shape and dtype")
-        if workspace is None:
-            workspace = _own(torch.empty(paged_attention_workspace(tokens, n_q, n_kv, hd), dtype=torch.uint8, device=dev), stream)
-        elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous CUDA tensor on %s" % dev)
-        _abi.call("paged_attention", _rows(q, "q", hd, dev), _rows(out, "out", hd, dev), tokens, n_q, n_kv, hd,
-                  _DTYPES[q.dtype], cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
-                  cache.block_table.data_ptr(), cache.max_pages, plan.cu_new.data_ptr(), plan.seq_len.data_ptr(), cache.n_seq,
-                  1.0 / math.sqrt(hd) if scale is None else scale, window, softcap, None if sinks is None else sinks.data_ptr(),
-                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), cache.error.data_ptr(), _stream(stream))
+    tokens, n_q, _ = shape
+    cu = _i32(plan.cu_new, "plan.cu_new", cache.n_seq + 1, dev)
+    lens = _i32(plan.seq_len, "plan.seq_len", cache.n_seq, dev)
+    if sinks is not None:
+        if not (sinks.dtype is _F32 and sinks.device == dev and sinks.is_contiguous() and sinks.numel() == n_q):
+            raise ValueError("sinks must be contiguous float32 [n_q] on %s" % dev)
+        sinks = sinks.data_ptr()
+    qi = _rows(q, "q", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        if stream is not None:
+            out.record_stream(stream)
+    elif out.dtype is not dtype:
+        raise ValueError("out must have q's dtype")
+    oi = _rows(out, "out", shape, dev)
+    if workspace is None:
+        size = paged_attention_workspace(tokens, n_q, n_kv, hd)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    st = _abi.lib().paged_attention(
+        qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
+        cache.block_table.data_ptr(), cache.max_pages, cu, lens, cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale,
+        window, softcap, sinks, workspace.data_ptr(), size, cache.error.data_ptr(), _stream(index, stream))
+    if st:
+        _abi.check("paged_attention", st)
     return out
