@@ -163,6 +163,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Two f32 operations in one issue slot.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -819,9 +824,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             tc_ld32(t_s + c0 + 32, x + 32);
                             tc_wait_ld();
                             if (CAP) {
-                                // softcap * tanh(s / softcap), with tanh(y) = 1 - 2 / (e^2y + 1)
+                                // softcap * tanh(s / softcap), with tanh(y) = 1 - 2 / (e^2y + 1);
+                                // two special-function instructions a score, which bound it
+                                const float2 in = make_float2(a.cap_in, a.cap_in), one = make_float2(1.0f, 1.0f);
+                                const float2 zero = make_float2(0.0f, 0.0f), two = make_float2(-2.0f, -2.0f);
 #pragma unroll
-                                for (int c = 0; c < 64; ++c) x[c] = 1.0f - __fdividef(2.0f, ex2(x[c] * a.cap_in) + 1.0f);
+                                for (int c = 0; c < 64; c += 2) {
+                                    float2 v = fma2(make_float2(x[c], x[c + 1]), in, zero);
+                                    v = add2(make_float2(ex2(v.x), ex2(v.y)), one);
+                                    v = fma2(make_float2(rcp(v.x), rcp(v.y)), two, one);
+                                    x[c] = v.x;
+                                    x[c + 1] = v.y;
+                                }
                             }
                             if (edge) {
 #pragma unroll

@@ -107,12 +107,17 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
 
 // cos and sin of the CTA's tokens into cs[token][pair].
 __device__ __forceinline__ void fill_angles(const RopeArgs &a, float2 *cs, int64_t tok0, int n_tok) {
+    // The table lies in the kernel's parameters.  Read through a plain pointer:
+    // a load that the compiler knows to be of constant memory takes a turn for
+    // every different address of a warp, an ordinary one takes the line at once.
+    const uint64_t *turns = a.turns;
+    asm volatile("" : "+l"(turns));
     for (int i = threadIdx.x; i < n_tok * a.pairs; i += blockDim.x) {
         const int t = i / a.pairs, p = i - t * a.pairs;
         const int32_t pos = a.positions[tok0 + t];
         float s = 0.0f, c = 1.0f;
         if (pos >= 0) {
-            const uint64_t frac = uint64_t(pos) * a.turns[p];
+            const uint64_t frac = uint64_t(pos) * turns[p];
             // signed top 32 bits: the turn in [-1/2, 1/2), as half turns for sincospi
             sincospif(float(int32_t(frac >> 32)) * 4.656612873077393e-10f, &s, &c);
         }
@@ -215,6 +220,65 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     }
 }
 
+// A rot_dim that is no multiple of 16, in rows that allow 16-byte accesses: a
+// thread owns eight neighbouring channels.  Interleaved partners are its own;
+// the other layout's lie in other threads of the row, which is one warp's
+// (head_dim 64, 128 or 256), and come through shared memory.
+template <typename TI, typename TO, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads) rope_part_kernel(const __grid_constant__ RopeArgs a, int tok_per_cta) {
+    extern __shared__ __align__(16) float2 cs[];
+    __shared__ float row[HALF ? kRopeThreads : 1][9];  // 9: a thread's eight values start in another bank
+    pdl_wait();
+    const int64_t tok0 = int64_t(blockIdx.x) * tok_per_cta;
+    const int n_tok = int(a.n_tokens - tok0 < tok_per_cta ? a.n_tokens - tok0 : tok_per_cta);
+    fill_angles(a, cs, tok0, n_tok);
+    __syncthreads();
+    const int chunks = a.hd / 8, lanes = kRopeThreads / chunks;
+    const int chunk = threadIdx.x % chunks, lane = threadIdx.x / chunks, base = threadIdx.x - chunk;
+    const int total = a.g[0].heads + a.g[1].heads + a.g[2].heads, rot = 2 * a.pairs;
+    for (int t = 0; t < n_tok; ++t) {
+        const int64_t tok = tok0 + t;
+        const Place place = place_of(a, tok);
+        const float2 *angle = cs + t * a.pairs;
+        for (int h0 = 0; h0 < total; h0 += lanes) {
+            int gi = 0, head = h0 + lane;
+            const bool there = head < total;
+            if (head >= a.g[0].heads) head -= a.g[0].heads, gi = 1;
+            if (gi == 1 && head >= a.g[1].heads) head -= a.g[1].heads, gi = 2;
+            if (!there) gi = 0, head = 0;
+            const Group &g = a.g[gi];
+            TO *out = there ? row_out<TO>(a, gi, tok, head, place) : nullptr;
+            float x[8], y[8];
+            if (out != nullptr) load8<TI>(static_cast<const TI *>(g.in) + tok * g.in_tok + head * g.in_head + chunk * 8, x);
+            const bool turn = gi < 2 && chunk * 8 < rot;
+            if (HALF) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row[threadIdx.x][i] = x[i];
+                __syncwarp();
+            }
+            if (out == nullptr) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int ch = chunk * 8 + i;
+                y[i] = x[i];
+                if (!turn || ch >= rot) continue;
+                if (HALF) {
+                    const bool low = ch < a.pairs;
+                    const int other = low ? ch + a.pairs : ch - a.pairs;
+                    const float2 v = angle[low ? ch : other];
+                    const float z = row[base + other / 8][other % 8];
+                    y[i] = low ? x[i] * v.x - z * v.y : x[i] * v.x + z * v.y;
+                } else {
+                    const float2 v = angle[ch / 2];
+                    y[i] = i % 2 == 0 ? x[i] * v.x - x[i | 1] * v.y : x[i] * v.x + x[i & 6] * v.y;
+                }
+            }
+            store8<TO>(out + chunk * 8, y);
+        }
+    }
+}
+
 // Any other size, stride or alignment: one thread per pair or plain channel.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeArgs a, int interleaved) {
@@ -265,7 +329,15 @@ bool aligned16(const Group &g, bool paged_out, int in_bytes, int out_bytes) {
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_rope(const RopeArgs &a, bool vec, int layout, cudaStream_t st) {
+cudaError_t launch_rope(const RopeArgs &a, bool aligned, int layout, cudaStream_t st) {
+    const bool vec = aligned && a.hd % 16 == 0 && a.pairs % 8 == 0;
+    if (!vec && aligned && (a.hd == 64 || a.hd == 128 || a.hd == 256)) {
+        const int tok = a.n_tokens >= 152 * 2 * kMaxTok ? kMaxTok : a.n_tokens >= 152 * 4 ? 2 : 1;
+        const dim3 grid(unsigned(ceil_div(a.n_tokens, tok)));
+        const size_t smem = sizeof(float2) * size_t(a.pairs) * tok;
+        return layout == KVD_ROPE_HALF ? launch_pdl(rope_part_kernel<TI, TO, true>, grid, dim3(kRopeThreads), smem, st, a, tok)
+                                       : launch_pdl(rope_part_kernel<TI, TO, false>, grid, dim3(kRopeThreads), smem, st, a, tok);
+    }
     if (!vec) {
         const size_t smem = sizeof(float2) * size_t(a.pairs);
         // positions are walked one CTA per token in launches of at most 2^30
@@ -391,7 +463,7 @@ extern "C" kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const
         return KVD_EINVAL;
     RopeArgs a;
     std::memset(&a, 0, sizeof(a));
-    bool vec = head_dim % 16 == 0 && r->rot_dim % 16 == 0;
+    bool aligned = true;
     const kvd_rows *in[2] = {q, k}, *out[2] = {q_out, k_out};
     const int32_t heads[2] = {n_q, n_kv};
     for (int i = 0; i < 2; ++i) {
@@ -400,16 +472,16 @@ extern "C" kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const
         if (!rows_ok(in[i], n_tokens, heads[i], bytes) || !rows_ok(out[i], n_tokens, heads[i], bytes)) return KVD_EINVAL;
         if (!in_place_ok(in[i], out[i])) return KVD_EINVAL;
         a.g[i] = group_of(in[i], out[i], heads[i]);
-        vec = vec && aligned16(a.g[i], false, bytes, bytes);
+        aligned = aligned && aligned16(a.g[i], false, bytes, bytes);
     }
     if (n_tokens == 0) return KVD_OK;
     set_rope(&a, r, head_dim);
     a.positions = positions;
     a.n_tokens = n_tokens;
     cudaStream_t st = as_stream(stream);
-    const cudaError_t e = dtype == KVD_T_F32   ? launch_rope<float, float>(a, vec, r->layout, st)
-                          : dtype == KVD_T_F16 ? launch_rope<__half, __half>(a, vec, r->layout, st)
-                                               : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, vec, r->layout, st);
+    const cudaError_t e = dtype == KVD_T_F32   ? launch_rope<float, float>(a, aligned, r->layout, st)
+                          : dtype == KVD_T_F16 ? launch_rope<__half, __half>(a, aligned, r->layout, st)
+                                               : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, aligned, r->layout, st);
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }
 
@@ -435,18 +507,18 @@ extern "C" kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, cons
     if (!rows_ok(k, n_tokens, n_kv, ib) || !rows_ok(v, n_tokens, n_kv, ib)) return KVD_EINVAL;
     RopeArgs a;
     std::memset(&a, 0, sizeof(a));
-    bool vec = r == nullptr || r->rot_dim % 16 == 0;
+    bool aligned = true;
     if (q != nullptr) {
         if (n_q < 1 || n_q > 1024 || !rows_ok(q, n_tokens, n_q, ib) || !rows_ok(q_out, n_tokens, n_q, ob)) return KVD_EINVAL;
         if (q->data != nullptr && q->data == q_out->data && ib != ob) return KVD_EINVAL;
         if (!in_place_ok(q, q_out)) return KVD_EINVAL;
         a.g[0] = group_of(q, q_out, n_q);
-        vec = vec && aligned16(a.g[0], false, ib, ob);
+        aligned = aligned16(a.g[0], false, ib, ob);
     }
     const kvd_rows kp = {k_pages, 0, 0}, vp = {v_pages, 0, 0};
     a.g[1] = group_of(k, &kp, n_kv);
     a.g[2] = group_of(v, &vp, n_kv);
-    vec = vec && aligned16(a.g[1], true, ib, ob) && aligned16(a.g[2], true, ib, ob);
+    aligned = aligned && aligned16(a.g[1], true, ib, ob) && aligned16(a.g[2], true, ib, ob);
     if (n_tokens == 0) return KVD_OK;
     set_rope(&a, r, head_dim);
     a.paged = 1;
@@ -461,10 +533,10 @@ extern "C" kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, cons
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
     if (page_dtype == KVD_T_F16)
-        e = in_dtype == KVD_T_F32 ? launch_rope<float, __half>(a, vec, layout, st)
-                                  : launch_rope<__half, __half>(a, vec, layout, st);
+        e = in_dtype == KVD_T_F32 ? launch_rope<float, __half>(a, aligned, layout, st)
+                                  : launch_rope<__half, __half>(a, aligned, layout, st);
     else
-        e = in_dtype == KVD_T_F32 ? launch_rope<float, __nv_bfloat16>(a, vec, layout, st)
-                                  : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, vec, layout, st);
+        e = in_dtype == KVD_T_F32 ? launch_rope<float, __nv_bfloat16>(a, aligned, layout, st)
+                                  : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, aligned, layout, st);
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }

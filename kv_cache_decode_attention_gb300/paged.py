@@ -34,6 +34,11 @@ _pack_rows = struct.Struct("Pqq").pack          # kvd_rows
 _pack_config = struct.Struct("iiii8d").pack     # kvd_rope_config
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# A workspace of one call is taken from torch's allocator by pointer and given
+# back once the launches are in: it is bound to the call's stream, so the next
+# taker on that stream comes after them.  (A tensor in its place costs some 4 us.)
+_take = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_give = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _stream(index, stream):
@@ -381,19 +386,30 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
     elif out.dtype is not dtype:
         raise ValueError("out must have q's dtype")
     oi = _rows(out, "out", shape, dev)
+    on = _stream(index, stream)
+    taken = None
     if workspace is None:
         size = paged_attention_workspace(tokens, n_q, n_kv, hd)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        if _take is not None and _give is not None:
+            ws = taken = _take(size, on)
+        else:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+            ws = workspace.data_ptr()
     else:
         size = workspace.numel() * workspace.element_size()
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-    st = _abi.lib().paged_attention(
-        qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
-        cache.block_table.data_ptr(), cache.max_pages, cu, lens, cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale,
-        window, softcap, sinks, workspace.data_ptr(), size, cache.error.data_ptr(), _stream(index, stream))
+        ws = workspace.data_ptr()
+    try:
+        st = _abi.lib().paged_attention(
+            qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
+            cache.block_table.data_ptr(), cache.max_pages, cu, lens, cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale,
+            window, softcap, sinks, ws, size, cache.error.data_ptr(), on)
+    finally:
+        if taken is not None:
+            _give(taken)
     if st:
         _abi.check("paged_attention", st)
     return out
