@@ -49,13 +49,13 @@ int32_t piece_rows(int64_t n_tokens, int32_t group) {
 }
 
 struct WsLayout {
-    int64_t meta, ml, o, total;
+    int64_t tickets, ml, o, total;
 };
 WsLayout ws_layout(int64_t n_tokens, int32_t group, int32_t hd) {
     WsLayout w;
     const int64_t rows = int64_t(2) * kPaCtas * piece_rows(n_tokens, group);
-    w.meta = 0;
-    w.ml = round_up(int64_t(kPaCtas) * 8 * 4, 256);
+    w.tickets = 0;
+    w.ml = round_up(int64_t(kPaCtas) * 8, 256);
     w.o = w.ml + round_up(rows * 8, 256);
     w.total = w.o + rows * hd * 4;
     return w;
@@ -130,7 +130,9 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
             return KVD_EINVAL;
     }
     char *w = static_cast<char *>(workspace);
-    a.meta = reinterpret_cast<int32_t *>(w + ws.meta);
+    a.tickets = reinterpret_cast<uint64_t *>(w + ws.tickets);
+    static std::atomic<uint64_t> launches{0x9e3779b97f4a7cull};  // any start will do; 2^56 launches wrap
+    a.nonce = launches.fetch_add(1, std::memory_order_relaxed) & ((uint64_t(1) << 56) - 1);
     a.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
     a.part_o = reinterpret_cast<float *>(w + ws.o);
     a.part_rows = piece_rows(n_tokens, group);

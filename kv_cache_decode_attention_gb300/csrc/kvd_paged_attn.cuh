@@ -15,7 +15,8 @@
 // Work is cut into units (one KV tile of a dual item, two of a single one) and
 // every CTA gets the same number of consecutive units, however long the
 // requests are; an item that is cut leaves its pieces (unnormalised output,
-// maximum, sum) in the workspace and paged_merge_kernel joins them.
+// maximum, sum) in the workspace, and the CTA that finishes the last of them
+// joins them: nobody waits for another CTA, and there is no second launch.
 //
 // One CTA per SM:
 //   warps 0-3, 4-7  softmax of stream 0 and 1, a thread per query row;
@@ -61,7 +62,8 @@ struct PaArgs {
     const float *sinks;
     float *part_o;     // [2 * kPaCtas][part_rows][hd]
     float2 *part_ml;   // [2 * kPaCtas][part_rows]: reference maximum (log2 units), sum
-    int32_t *meta;     // [kPaCtas][8]
+    uint64_t *tickets; // [kPaCtas]: of the cut item that begins in the CTA, nonce << 8 | pieces done
+    uint64_t nonce;    // of the launch, below 2^56
     uint32_t *err;
     int64_t window;    // 0 = none
     int32_t n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2;
@@ -70,12 +72,10 @@ struct PaArgs {
     float cap_in;      // softcap > 0: 2 * scale * log2 e / softcap
 };
 
-// Piece records in PaArgs::meta.
-enum { kPmTail = 0, kPmSeq = 1, kPmHead = 2, kPmTok = 3, kPmFirst = 4 };
-// kPmTail: 1 = this CTA holds the head piece of a cut item (slot 2 c + 1).
-// kPmFirst: 0 = starts on an item boundary, 1 = its first piece continues the
-// item of the CTA before and ends it, 2 = continues and does not end it,
-// 3 = this CTA has no work.
+// A ticket that carries another nonce counts as zero, so the workspace needs no
+// initialisation; whoever joins the pieces sets it to 0 for a graph's next
+// replay, which comes with the same nonce.  A piece of CTA c is kept in slot
+// 2 c + 1 if it begins its item, else in slot 2 c.
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -140,6 +140,10 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 __device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void pa_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void pa_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar) {
@@ -301,6 +305,7 @@ struct PaStart {
     int32_t b, h, tok, unit;  // first item and the unit in it
     PaSeq s;                  // its request
     int64_t units;            // units of this CTA
+    int64_t from, total;      // its first unit, and all units
 };
 
 // The cut: CTA c of kPaCtas takes units [c W / kPaCtas, (c + 1) W / kPaCtas) of
@@ -313,6 +318,7 @@ __device__ __forceinline__ void pa_cut(const PaArgs &a, PaStart *out, int64_t *w
     // first turn: this thread's units; second, for the thread whose requests
     // hold the CTA's first unit: where it is in them
     int64_t mine = 0, off = 0, u = 0, from = 0, to = 0;
+    uint64_t total = 0;
     PaSeq s = {0, 0, 0};
 #pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
@@ -339,7 +345,7 @@ __device__ __forceinline__ void pa_cut(const PaArgs &a, PaStart *out, int64_t *w
                 if (off < n) break;
                 off -= n;
             }
-            *out = PaStart{b, h, tok, int32_t(off), s, to - from};
+            *out = PaStart{b, h, tok, int32_t(off), s, to - from, from, int64_t(total)};
             break;
         }
         int64_t x = mine;
@@ -358,7 +364,7 @@ __device__ __forceinline__ void pa_cut(const PaArgs &a, PaStart *out, int64_t *w
             const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
             if (lane >= d) before += y;
         }
-        const uint64_t total = __shfl_sync(0xffffffffu, before, kWarps - 1);
+        total = __shfl_sync(0xffffffffu, before, kWarps - 1);
         before = __shfl_sync(0xffffffffu, before, w > 0 ? w - 1 : 0);
         before = (w > 0 ? before : 0) + x - mine;
         from = total * blockIdx.x / kPaCtas;
@@ -388,6 +394,8 @@ struct PaJob {
     int32_t dual, head, whole; // two query tiles; begins here; begins and ends here
     int32_t seq, kv_head, tok; // request, KV head, first token in its new rows
     int32_t q0, fresh, len;    // as PaSeq
+    int32_t count, units;      // tokens and units of the whole item
+    int64_t unit0;             // its first unit of all
 };
 constexpr int kPaJobs = 4;
 
@@ -397,10 +405,11 @@ struct PaShared {
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2];
-    uint64_t ml_full[2], tail_go, tail_ready, all_done, drain;
+    uint64_t ml_full[2], tail_go, tail_ready, piece_done, verdict, all_done, drain;
     PaStart start;
     int64_t warp_sums[kPaThreads / 32];
     uint32_t tmem;
+    int join;         // the verdict: this CTA joins the pieces
     int stop, steps;  // the watch: give up; changes with every K tile that is loaded
     float2 ml[2][kPaTile];  // stream 1's maximum and sum of a single item, by item parity
 };
@@ -487,6 +496,107 @@ __device__ __forceinline__ int32_t pa_tail_tile(const PaArgs &a, const PaSeq &s,
     return t >= 0 && t < pt.n && (s.len & ((1 << a.page_log2) - 1)) != 0 ? t : -1;
 }
 
+// The CTAs that hold pieces of a cut item.  With W units in all, unit u lies in
+// CTA ceil((u + 1) kPaCtas / W) - 1; with fewer units than CTAs every unit has
+// one of its own, else every CTA between the first and the last has a piece.
+struct PaPieces {
+    int64_t unit0, total;
+    int32_t first, n;
+    __device__ __forceinline__ PaPieces(const PaJob &job, int64_t total_) : unit0(job.unit0), total(total_) {
+        first = cta_of(unit0);
+        n = total < kPaCtas ? job.units : cta_of(unit0 + job.units - 1) - first + 1;
+    }
+    __device__ __forceinline__ int32_t cta_of(int64_t u) const {
+        return int32_t((uint64_t(u + 1) * kPaCtas + total - 1) / uint64_t(total)) - 1;
+    }
+    __device__ __forceinline__ int64_t slot(int32_t i) const {
+        return i == 0 ? 2 * first + 1 : 2 * int64_t(total < kPaCtas ? cta_of(unit0 + i) : first + i);
+    }
+};
+
+// One more piece of the item is done: whether it was the last.
+static __device__ __noinline__ bool pa_ticket(const PaArgs &a, const PaPieces &p) {
+    unsigned long long *word = reinterpret_cast<unsigned long long *>(a.tickets) + p.first;
+    __threadfence();
+    unsigned long long old = *static_cast<volatile unsigned long long *>(word), now;
+    for (;;) {
+        now = (old >> 8 == a.nonce ? old : a.nonce << 8) + 1;
+        // n <= 152 pieces fit the low byte; the last one leaves 0 for a replay
+        const unsigned long long got = atomicCAS(word, old, int32_t(now & 255u) == p.n ? 0ull : now);
+        if (got == old) break;
+        old = got;
+    }
+    __threadfence();
+    return int32_t(now & 255u) == p.n;
+}
+
+// Rows r0 .. r0 + 7 of a cut item from its pieces, by a warp.  For the pieces'
+// maxima and weights lane 8 i + e stands for piece i (of four at a time) and row
+// e; for the output the lanes stand for columns and eight rows are under way.
+template <int HD, bool BF16>
+static __device__ __noinline__ void pa_join_rows(const PaArgs &a, const PaJob &job, const PaPieces &pieces, int32_t r0) {
+    constexpr int kPer = HD / 32;
+    const int lane = threadIdx.x & 31, e = lane & 7;
+    const int32_t rows = job.count * a.group, r = r0 + e;
+    auto ml_of = [&](int32_t i) {
+        return i < pieces.n && r < rows ? __ldcg(&a.part_ml[pieces.slot(i) * a.part_rows + r]) : make_float2(-INFINITY, 0.0f);
+    };
+    const float2 mine = ml_of(lane >> 3);  // up to four pieces are at hand, more are read again
+    float top = mine.x;
+    for (int32_t i = 4 + (lane >> 3); i < pieces.n; i += 4) top = fmaxf(top, ml_of(i).x);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, o[8][kPer] = {};
+#pragma unroll 1
+    for (int32_t i0 = 0; i0 < pieces.n; i0 += 4) {
+        const float2 ml = i0 == 0 ? mine : ml_of(i0 + (lane >> 3));
+        const float w = ex2(ml.x - base);
+        sum += ml.y * w;
+#pragma unroll 2
+        for (int32_t i = i0; i < i0 + 4 && i < pieces.n; ++i) {
+            const float *p = a.part_o + (pieces.slot(i) * a.part_rows + r0) * HD + lane * kPer;
+            float v[8][kPer];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (r0 + q >= rows) continue;
+                if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[q]) = __ldcg(reinterpret_cast<const float4 *>(p + q * HD));
+                else *reinterpret_cast<float2 *>(v[q]) = __ldcg(reinterpret_cast<const float2 *>(p + q * HD));
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float f = __shfl_sync(0xffffffffu, w, (i - i0) * 8 + q);
+                if (r0 + q >= rows) continue;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) o[q][c] += v[q][c] * f;
+            }
+        }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    const int32_t rtok = r / a.group, rhead = r - rtok * a.group;
+    float g = 1.0f;
+    if (a.sinks != nullptr && top != -INFINITY && r < rows) {
+        const float sink = a.sinks[job.kv_head * a.group + rhead] * 1.4426950408889634f;
+        const float all = fmaxf(top, sink);
+        g = ex2(base - all);
+        sum = sum * g + ex2(sink - all);
+    }
+    g *= sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t to = (int64_t(job.q0) + job.tok + rtok) * a.out_tok + int64_t(job.kv_head * a.group + rhead) * a.out_head;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float f = __shfl_sync(0xffffffffu, g, q);
+        const int64_t at = __shfl_sync(0xffffffffu, to, q);
+        if (r0 + q >= rows) continue;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.out) + (at + lane * kPer) * 2);
+        if constexpr (kPer == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF16>(o[q][0] * f, o[q][1] * f), pack2<BF16>(o[q][2] * f, o[q][3] * f));
+        else
+            *dst = pack2<BF16>(o[q][0] * f, o[q][1] * f);
+    }
+}
+
 template <int HD, bool BF16, bool CAP>
 __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __grid_constant__ PaArgs a) {
     using S = PaShape<HD>;
@@ -517,6 +627,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             mbar_init(&sh.job_empty[i], 12);  // two of loads, MMAs, ends of V, eight softmax warps
         }
         mbar_init(&sh.tail_go, 1);
+        mbar_init(&sh.piece_done, 8);
+        mbar_init(&sh.verdict, 1);
         mbar_init(&sh.all_done, 8);
         mbar_init(&sh.tail_ready, 1);
         mbar_init(&sh.drain, 1);
@@ -542,11 +654,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     const PaStart st = sh.start;
     uint32_t loaded = 0, parity = 0;  // loads: stages filled and their last parities, for the clean-up below
 
-    if (warp == 11 && lane == 0) {
-        int32_t *m = a.meta + blockIdx.x * 8;
-        m[kPmTail] = 0;
-        m[kPmFirst] = st.units == 0 ? 3 : st.unit == 0 ? 0 : 2;
-    }
     if (st.units > 0) {
         // the next item: its record, read in place until job_empty is told
         uint32_t job_at = 0;
@@ -758,16 +865,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         const PaItem it = pa_item(a, w.s, w.tok);
                         const PaPart pt = pa_part(it, unit, left);
                         job = PaJob{pt.n, it.tile0 + pt.first, pa_tail_tile(a, w.s, it, pt), it.dual, pt.head, pt.head && pt.tail,
-                                    w.b, w.h, w.tok, w.s.q0, w.s.fresh, w.s.len};
-                        // pieces of items that were cut, for the kernel that joins them
-                        int32_t *m = a.meta + blockIdx.x * 8;
-                        if (pt.head && !pt.tail) {
-                            m[kPmTail] = 1;
-                            m[kPmSeq] = w.b;
-                            m[kPmHead] = w.h;
-                            m[kPmTok] = w.tok;
-                        }
-                        if (!pt.head && pt.tail) m[kPmFirst] = 1;
+                                    w.b, w.h, w.tok, w.s.q0, w.s.fresh, w.s.len,
+                                    it.count, it.units, st.from + (st.units - left) - unit};
                         step = it.units - unit;
                     }
                     pa_arrive(&sh.job_full[slot]);
@@ -789,7 +888,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             constexpr float kLift = BF16 ? 0.0f : 8.0f, kSlack = BF16 ? 8.0f : 4.0f;
             const int32_t rtok = row / a.group, rhead = row - rtok * a.group;
             const bool in_tile = rtok < a.tile_tok;
-            uint32_t s_phase = 0, o_phase[2] = {0, 0}, ml_phase = 0, ml_items = 0;
+            uint32_t s_phase = 0, o_phase[2] = {0, 0}, ml_phase = 0, ml_items = 0, cuts = 0;
             bool ok = true;
             for (;;) {
                 const PaJob &job = next_job(ok);
@@ -994,6 +1093,27 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 }
                 o_phase[0] ^= 1;
                 if (dual || two) o_phase[1] ^= 1;
+                if (job.whole == 0 && (dual || d == 0)) {
+                    // this CTA's piece is in the workspace once all its warps say so
+                    // (the four of a single item say it twice); then one thread
+                    // takes a ticket, and the holder of the last one has them joined
+                    __syncwarp();
+                    if (lane == 0) pa_arrive_n(&sh.piece_done, dual ? 1 : 2);
+                    const PaPieces pieces(job, st.total);
+                    if (warp == 0) {
+                        ok = pa_wait(&sh.piece_done, cuts & 1, stop);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            sh.join = pa_ticket(a, pieces) ? 1 : 0;
+                            pa_arrive(&sh.verdict);
+                        }
+                    }
+                    ok = pa_wait(&sh.verdict, cuts & 1, stop);
+                    if (!ok) break;
+                    if (sh.join != 0)
+                        for (int32_t r = warp * 8; r < job.count * a.group; r += dual ? 64 : 32) pa_join_rows<HD, BF16>(a, job, pieces, r);
+                }
+                cuts += job.whole == 0 ? 1 : 0;
                 done_job();
             }
             __syncwarp();
@@ -1016,74 +1136,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the pieces of a cut item: CTA (c, y) those of the item whose head piece
-// CTA c of the attention left, a warp per query row.
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PaArgs a) {
-    pdl_wait();
-    const int c0 = blockIdx.x;
-    const int32_t *m = a.meta + c0 * 8;
-    if (m[kPmTail] == 0) return;
-    const PaSeq s = pa_seq(a, m[kPmSeq], false);
-    const int32_t h = m[kPmHead], tok0 = m[kPmTok];
-    const PaItem it = pa_item(a, s, tok0);
-    const int32_t rows = it.count * a.group;
-    // slots of its pieces, in the order of the CTAs up to the one that ends it
-    __shared__ int32_t slots[kPaCtas];
-    __shared__ int32_t n_slots, last;
-    const int32_t c = threadIdx.x;
-    const int32_t first = c < kPaCtas ? a.meta[c * 8 + kPmFirst] : 3;
-    if (c == 0) last = kPaCtas - 1;
-    __syncthreads();
-    if (c > c0 && first == 1) atomicMin(&last, c);
-    __syncthreads();
-    const bool mine = c == c0 || (c > c0 && c <= last && first != 3);
-    __shared__ int32_t counts[8];
-    const uint32_t vote = __ballot_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = __popc(vote);
-    __syncthreads();
-    int32_t rank = __popc(vote & ((1u << (threadIdx.x & 31)) - 1u));
-    for (int i = 0; i < (threadIdx.x >> 5); ++i) rank += counts[i];
-    if (mine) slots[rank] = c == c0 ? 2 * c + 1 : 2 * c;
-    if (c == last) n_slots = rank + 1;
-    __syncthreads();
-    const int32_t n = n_slots;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kPer = HD / 32;
-    for (int32_t r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        float top = -INFINITY;
-        for (int32_t i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[int64_t(slots[i]) * a.part_rows + r].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f, o[kPer] = {};
-#pragma unroll 4
-        for (int32_t i = 0; i < n; ++i) {
-            const int64_t at = int64_t(slots[i]) * a.part_rows + r;
-            const float2 ml = a.part_ml[at];
-            const float f = ex2(ml.x - base);
-            sum += ml.y * f;
-            const float *p = a.part_o + at * HD + lane * kPer;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) o[e] += p[e] * f;
-        }
-        const int32_t rtok = r / a.group, rhead = r - rtok * a.group;
-        float g = 1.0f;
-        if (a.sinks != nullptr && top != -INFINITY) {
-            const float sink = a.sinks[h * a.group + rhead] * 1.4426950408889634f;
-            const float all = fmaxf(top, sink);
-            g = ex2(base - all);
-            sum = sum * g + ex2(sink - all);
-        }
-        g *= sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(
-            static_cast<uint8_t *>(a.out) +
-            ((int64_t(s.q0) + tok0 + rtok) * a.out_tok + int64_t(h * a.group + rhead) * a.out_head + lane * kPer) * 2);
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) dst[i / 2] = pack2<BF16>(o[i] * g, o[i + 1] * g);
-    }
-}
-
 template <int HD, bool BF16, bool CAP>
 cudaError_t launch_paged_one(const PaArgs &a, cudaStream_t st) {
     constexpr int smem = PaShape<HD>::kTiles + int(sizeof(PaShared));
@@ -1091,9 +1143,7 @@ cudaError_t launch_paged_one(const PaArgs &a, cudaStream_t st) {
     const auto kern = paged_attention_kernel<HD, BF16, CAP>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(kPaCtas), dim3(kPaThreads), smem, st, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(paged_merge_kernel<HD, BF16>, dim3(kPaCtas, unsigned(ceil_div(a.part_rows, 64))), dim3(256), 0, st, a);
+    return launch_pdl(kern, dim3(kPaCtas), dim3(kPaThreads), smem, st, a);
 }
 
 template <int HD>

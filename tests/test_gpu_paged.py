@@ -696,7 +696,7 @@ def test_a_failed_launch_is_reported(env):
     x = torch.ones(1, 1, 64, device="cuda", dtype=torch.bfloat16)
     plan = kvd.PagedPlan(_i32(torch, [0, 1]), cache.seq_len, positions=_i32(torch, [0]), slots=_i32(torch, [-1]))
     calls = [(lambda: kvd.rope(x, None, plan.positions, kvd.RopeTable(64)), 1), (lambda: kvd.paged_plan(cache, _i32(torch, [0]), 0), 1),
-             (lambda: kvd.paged_append(cache, plan, x, x), 1), (lambda: kvd.paged_attention(x, cache, plan), 2)]
+             (lambda: kvd.paged_append(cache, plan, x, x), 1), (lambda: kvd.paged_attention(x, cache, plan), 1)]
     try:
         for call, launches in calls:
             for n in range(launches):
