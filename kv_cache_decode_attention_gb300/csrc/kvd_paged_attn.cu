@@ -49,13 +49,14 @@ int32_t piece_rows(int64_t n_tokens, int32_t group) {
 }
 
 struct WsLayout {
-    int64_t tickets, ml, o, total;
+    int64_t tickets, cut, ml, o, total;
 };
 WsLayout ws_layout(int64_t n_tokens, int32_t group, int32_t hd) {
     WsLayout w;
     const int64_t rows = int64_t(2) * kPaCtas * piece_rows(n_tokens, group);
     w.tickets = 0;
-    w.ml = round_up(int64_t(kPaCtas) * 8, 256);
+    w.cut = round_up(int64_t(kPaCtas) * 8, 256);
+    w.ml = w.cut + round_up(int64_t(kPaCtas) * int64_t(sizeof(PaPiecesOf)), 256);
     w.o = w.ml + round_up(rows * 8, 256);
     w.total = w.o + rows * hd * 4;
     return w;
@@ -130,6 +131,8 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
             return KVD_EINVAL;
     }
     char *w = static_cast<char *>(workspace);
+    a.cut = reinterpret_cast<PaPiecesOf *>(w + ws.cut);
+    a.join_here = n_tokens * group <= kPaJoinRows ? 1 : 0;
     a.tickets = reinterpret_cast<uint64_t *>(w + ws.tickets);
     static std::atomic<uint64_t> launches{0x9e3779b97f4a7cull};  // any start will do; 2^56 launches wrap
     a.nonce = launches.fetch_add(1, std::memory_order_relaxed) & ((uint64_t(1) << 56) - 1);

@@ -15,8 +15,10 @@
 // Work is cut into units (one KV tile of a dual item, two of a single one) and
 // every CTA gets the same number of consecutive units, however long the
 // requests are; an item that is cut leaves its pieces (unnormalised output,
-// maximum, sum) in the workspace, and the CTA that finishes the last of them
-// joins them: nobody waits for another CTA, and there is no second launch.
+// maximum, sum) in the workspace.  A call of at most kPaJoinRows query rows a KV
+// head has them joined by the CTA that finishes the last of them (nobody waits
+// for another CTA, and there is no second launch); larger calls, whose joins
+// are work for more than one CTA, by paged_join_kernel.
 //
 // One CTA per SM:
 //   warps 0-3, 4-7  softmax of stream 0 and 1, a thread per query row;
@@ -53,6 +55,15 @@ static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shar
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
 constexpr int kPaQBytes = 2 * kPaTile * 256;
 constexpr int kPaMaxRows = 2 * kPaTile;
+// Joining 16 rows of 19 pieces takes one CTA some 3 us, as long as a second
+// launch; 256 rows of 2 pieces took it 20 us, and the kernel 3.
+constexpr int kPaJoinRows = 16;
+
+// A cut item as paged_join_kernel finds it; n = 0: none.
+struct PaPiecesOf {
+    int64_t unit0, total;
+    int32_t units, rows, q_row, kv_head, n, pad;
+};
 
 struct PaArgs {
     CUtensorMap q, k, v;
@@ -64,6 +75,8 @@ struct PaArgs {
     float2 *part_ml;   // [2 * kPaCtas][part_rows]: reference maximum (log2 units), sum
     uint64_t *tickets; // [kPaCtas]: of the cut item that begins in the CTA, nonce << 8 | pieces done
     uint64_t nonce;    // of the launch, below 2^56
+    PaPiecesOf *cut;   // [kPaCtas]: the cut item that begins in each CTA
+    int32_t join_here; // by the last finisher
     uint32_t *err;
     int64_t window;    // 0 = none
     int32_t n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2;
@@ -140,10 +153,6 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 __device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void pa_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ void pa_arrive_n(uint64_t *bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar) {
@@ -499,102 +508,101 @@ __device__ __forceinline__ int32_t pa_tail_tile(const PaArgs &a, const PaSeq &s,
 // The CTAs that hold pieces of a cut item.  With W units in all, unit u lies in
 // CTA ceil((u + 1) kPaCtas / W) - 1; with fewer units than CTAs every unit has
 // one of its own, else every CTA between the first and the last has a piece.
+static __device__ __noinline__ int32_t pa_cta_of(int64_t u, int64_t total) {
+    return int32_t((uint64_t(u + 1) * kPaCtas + total - 1) / uint64_t(total)) - 1;
+}
 struct PaPieces {
-    int64_t unit0, total;
-    int32_t first, n;
-    __device__ __forceinline__ PaPieces(const PaJob &job, int64_t total_) : unit0(job.unit0), total(total_) {
-        first = cta_of(unit0);
-        n = total < kPaCtas ? job.units : cta_of(unit0 + job.units - 1) - first + 1;
-    }
-    __device__ __forceinline__ int32_t cta_of(int64_t u) const {
-        return int32_t((uint64_t(u + 1) * kPaCtas + total - 1) / uint64_t(total)) - 1;
+    int32_t first, n, sparse, unit0;  // sparse = units in all, if fewer than CTAs, else 0
+    __device__ __forceinline__ PaPieces(int64_t unit0_, int32_t units, int64_t total) {
+        first = pa_cta_of(unit0_, total);
+        sparse = total < kPaCtas ? int32_t(total) : 0;
+        unit0 = int32_t(unit0_);
+        n = sparse != 0 ? units : pa_cta_of(unit0_ + units - 1, total) - first + 1;
     }
     __device__ __forceinline__ int64_t slot(int32_t i) const {
-        return i == 0 ? 2 * first + 1 : 2 * int64_t(total < kPaCtas ? cta_of(unit0 + i) : first + i);
+        if (i == 0) return 2 * first + 1;
+        const int32_t c = sparse != 0 ? (uint32_t(unit0 + i + 1) * kPaCtas + sparse - 1) / uint32_t(sparse) - 1 : first + i;
+        return 2 * c;
     }
 };
 
-// One more piece of the item is done: whether it was the last.
-static __device__ __noinline__ bool pa_ticket(const PaArgs &a, const PaPieces &p) {
-    unsigned long long *word = reinterpret_cast<unsigned long long *>(a.tickets) + p.first;
-    __threadfence();
-    unsigned long long old = *static_cast<volatile unsigned long long *>(word), now;
+// One more piece of the item is done: whether it was the last.  `old` is what
+// the ticket was a while ago; a wrong guess costs one more turn.
+static __device__ __noinline__ bool pa_ticket(uint64_t *word, uint64_t nonce, int32_t n, uint64_t old) {
+    uint64_t now;
     for (;;) {
-        now = (old >> 8 == a.nonce ? old : a.nonce << 8) + 1;
+        now = (old >> 8 == nonce ? old : nonce << 8) + 1;
         // n <= 152 pieces fit the low byte; the last one leaves 0 for a replay
-        const unsigned long long got = atomicCAS(word, old, int32_t(now & 255u) == p.n ? 0ull : now);
+        uint64_t got;
+        asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                     : "=l"(got)
+                     : "l"(word), "l"(old), "l"(int32_t(now & 255u) == n ? uint64_t(0) : now)
+                     : "memory");
         if (got == old) break;
         old = got;
     }
-    __threadfence();
-    return int32_t(now & 255u) == p.n;
+    return int32_t(now & 255u) == n;
 }
 
-// Rows r0 .. r0 + 7 of a cut item from its pieces, by a warp.  For the pieces'
-// maxima and weights lane 8 i + e stands for piece i (of four at a time) and row
-// e; for the output the lanes stand for columns and eight rows are under way.
+// Row r of a cut item from its pieces, by a warp whose lanes stand for columns,
+// four pieces under way at a time.
 template <int HD, bool BF16>
-static __device__ __noinline__ void pa_join_rows(const PaArgs &a, const PaJob &job, const PaPieces &pieces, int32_t r0) {
+__device__ __forceinline__ void pa_join_row(const PaArgs &a, const PaPieces &pieces, int32_t r, int32_t q_row, int32_t kv_head) {
     constexpr int kPer = HD / 32;
-    const int lane = threadIdx.x & 31, e = lane & 7;
-    const int32_t rows = job.count * a.group, r = r0 + e;
-    auto ml_of = [&](int32_t i) {
-        return i < pieces.n && r < rows ? __ldcg(&a.part_ml[pieces.slot(i) * a.part_rows + r]) : make_float2(-INFINITY, 0.0f);
-    };
-    const float2 mine = ml_of(lane >> 3);  // up to four pieces are at hand, more are read again
-    float top = mine.x;
-    for (int32_t i = 4 + (lane >> 3); i < pieces.n; i += 4) top = fmaxf(top, ml_of(i).x);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, o[8][kPer] = {};
+    const int32_t col = int32_t(threadIdx.x & 31) * kPer;
+    float top = -INFINITY, sum = 0.0f, o[kPer] = {};
 #pragma unroll 1
     for (int32_t i0 = 0; i0 < pieces.n; i0 += 4) {
-        const float2 ml = i0 == 0 ? mine : ml_of(i0 + (lane >> 3));
-        const float w = ex2(ml.x - base);
-        sum += ml.y * w;
-#pragma unroll 2
-        for (int32_t i = i0; i < i0 + 4 && i < pieces.n; ++i) {
-            const float *p = a.part_o + (pieces.slot(i) * a.part_rows + r0) * HD + lane * kPer;
-            float v[8][kPer];
+        float2 ml[4];
+        float v[4][kPer] = {};
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (r0 + q >= rows) continue;
-                if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[q]) = __ldcg(reinterpret_cast<const float4 *>(p + q * HD));
-                else *reinterpret_cast<float2 *>(v[q]) = __ldcg(reinterpret_cast<const float2 *>(p + q * HD));
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float f = __shfl_sync(0xffffffffu, w, (i - i0) * 8 + q);
-                if (r0 + q >= rows) continue;
-#pragma unroll
-                for (int c = 0; c < kPer; ++c) o[q][c] += v[q][c] * f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            if (i0 + i >= pieces.n) continue;
+            const int64_t at = pieces.slot(i0 + i) * a.part_rows + r;
+            ml[i] = __ldcg(&a.part_ml[at]);
+            const float *p = a.part_o + at * HD + col;
+            if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[i]) = __ldcg(reinterpret_cast<const float4 *>(p));
+            else *reinterpret_cast<float2 *>(v[i]) = __ldcg(reinterpret_cast<const float2 *>(p));
         }
+        const float now = fmaxf(max3(top, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), base = now == -INFINITY ? 0.0f : now;
+        const float f0 = ex2(top - base);
+        sum *= f0;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] *= f0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = ex2(ml[i].x - base);
+            sum += ml[i].y * f;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[c] += v[i][c] * f;
+        }
+        top = now;
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-    const int32_t rtok = r / a.group, rhead = r - rtok * a.group;
+    const int32_t rtok = r / a.group, head = kv_head * a.group + r - rtok * a.group;
     float g = 1.0f;
-    if (a.sinks != nullptr && top != -INFINITY && r < rows) {
-        const float sink = a.sinks[job.kv_head * a.group + rhead] * 1.4426950408889634f;
-        const float all = fmaxf(top, sink);
-        g = ex2(base - all);
+    if (a.sinks != nullptr && top != -INFINITY) {
+        const float sink = a.sinks[head] * 1.4426950408889634f, all = fmaxf(top, sink);
+        g = ex2(top - all);
         sum = sum * g + ex2(sink - all);
     }
     g *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t to = (int64_t(job.q0) + job.tok + rtok) * a.out_tok + int64_t(job.kv_head * a.group + rhead) * a.out_head;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float f = __shfl_sync(0xffffffffu, g, q);
-        const int64_t at = __shfl_sync(0xffffffffu, to, q);
-        if (r0 + q >= rows) continue;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.out) + (at + lane * kPer) * 2);
-        if constexpr (kPer == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF16>(o[q][0] * f, o[q][1] * f), pack2<BF16>(o[q][2] * f, o[q][3] * f));
-        else
-            *dst = pack2<BF16>(o[q][0] * f, o[q][1] * f);
-    }
+    uint8_t *dst = static_cast<uint8_t *>(a.out) + ((int64_t(q_row) + rtok) * a.out_tok + int64_t(head) * a.out_head + col) * 2;
+    if constexpr (kPer == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF16>(o[0] * g, o[1] * g), pack2<BF16>(o[2] * g, o[3] * g));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack2<BF16>(o[0] * g, o[1] * g);
+}
+
+// CTA (c, y) joins rows of the cut item that begins in CTA c.
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PaArgs a) {
+    pdl_wait();
+    const PaPiecesOf cut = a.cut[blockIdx.x];
+    if (cut.n == 0) return;
+    const PaPieces pieces(cut.unit0, cut.units, cut.total);
+    for (int32_t r = blockIdx.y * 8 + (threadIdx.x >> 5); r < cut.rows; r += gridDim.y * 8)
+        pa_join_row<HD, BF16>(a, pieces, r, cut.q_row, cut.kv_head);
 }
 
 template <int HD, bool BF16, bool CAP>
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             mbar_init(&sh.job_empty[i], 12);  // two of loads, MMAs, ends of V, eight softmax warps
         }
         mbar_init(&sh.tail_go, 1);
-        mbar_init(&sh.piece_done, 8);
+        mbar_init(&sh.piece_done, 4);
         mbar_init(&sh.verdict, 1);
         mbar_init(&sh.all_done, 8);
         mbar_init(&sh.tail_ready, 1);
@@ -654,6 +662,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     const PaStart st = sh.start;
     uint32_t loaded = 0, parity = 0;  // loads: stages filled and their last parities, for the clean-up below
 
+    if (a.join_here == 0 && warp == 11 && lane == 0) a.cut[blockIdx.x].n = 0;
     if (st.units > 0) {
         // the next item: its record, read in place until job_empty is told
         uint32_t job_at = 0;
@@ -868,6 +877,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                     w.b, w.h, w.tok, w.s.q0, w.s.fresh, w.s.len,
                                     it.count, it.units, st.from + (st.units - left) - unit};
                         step = it.units - unit;
+                        if (a.join_here == 0 && pt.head && !pt.tail)
+                            a.cut[blockIdx.x] = PaPiecesOf{job.unit0, st.total, it.units, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
                     }
                     pa_arrive(&sh.job_full[slot]);
                     if (left <= 0) break;
@@ -1093,27 +1104,31 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 }
                 o_phase[0] ^= 1;
                 if (dual || two) o_phase[1] ^= 1;
-                if (job.whole == 0 && (dual || d == 0)) {
-                    // this CTA's piece is in the workspace once all its warps say so
-                    // (the four of a single item say it twice); then one thread
-                    // takes a ticket, and the holder of the last one has them joined
+                if (a.join_here != 0 && job.whole == 0 && d == 0) {
+                    // (a call so small has single items only.)  The CTA's piece is in
+                    // the workspace once its four warps say so; then one thread takes a
+                    // ticket, and the holder of the last one has the pieces joined.
                     __syncwarp();
-                    if (lane == 0) pa_arrive_n(&sh.piece_done, dual ? 1 : 2);
-                    const PaPieces pieces(job, st.total);
+                    if (lane == 0) pa_arrive(&sh.piece_done);
+                    const PaPieces pieces(job.unit0, job.units, st.total);
                     if (warp == 0) {
+                        uint64_t *word = a.tickets + pieces.first;
+                        const uint64_t old = *static_cast<volatile uint64_t *>(word);
                         ok = pa_wait(&sh.piece_done, cuts & 1, stop);
                         if (!ok) break;
                         if (lane == 0) {
-                            sh.join = pa_ticket(a, pieces) ? 1 : 0;
+                            sh.join = pa_ticket(word, a.nonce, pieces.n, old) ? 1 : 0;
                             pa_arrive(&sh.verdict);
                         }
                     }
                     ok = pa_wait(&sh.verdict, cuts & 1, stop);
                     if (!ok) break;
-                    if (sh.join != 0)
-                        for (int32_t r = warp * 8; r < job.count * a.group; r += dual ? 64 : 32) pa_join_rows<HD, BF16>(a, job, pieces, r);
+                    ++cuts;
+                    if (sh.join != 0) {
+                        const int32_t rows = job.count * a.group;
+                        for (int32_t r = warp; r < rows; r += 4) pa_join_row<HD, BF16>(a, pieces, r, job.q0 + job.tok, job.kv_head);
+                    }
                 }
-                cuts += job.whole == 0 ? 1 : 0;
                 done_job();
             }
             __syncwarp();
@@ -1143,7 +1158,9 @@ cudaError_t launch_paged_one(const PaArgs &a, cudaStream_t st) {
     const auto kern = paged_attention_kernel<HD, BF16, CAP>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(kPaCtas), dim3(kPaThreads), smem, st, a);
+    e = launch_pdl(kern, dim3(kPaCtas), dim3(kPaThreads), smem, st, a);
+    if (e != cudaSuccess || a.join_here != 0) return e;
+    return launch_pdl(paged_join_kernel<HD, BF16>, dim3(kPaCtas, unsigned(ceil_div(a.part_rows, 32))), dim3(256), 0, st, a);
 }
 
 template <int HD>
