@@ -158,7 +158,18 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     a.pool_rows = int32_t(n_pages * page_size * n_kv);
     const float log2e = 1.4426950408889634f;
     a.scale_log2 = (softcap > 0.0f ? softcap : scale) * log2e;
-    a.cap_in = softcap > 0.0f ? 2.0f * scale * log2e / softcap : 0.0f;
+    if (softcap > 0.0f) {
+        a.cap_in = 2.0f * scale * log2e / softcap;
+        a.cap_mul = scale * log2e;
+        // tanh(y) / y in powers of y^2 up to |y| = 1/2, fitted to a relative error
+        // of 1.3e-8; the kernel has it in powers of the score s = y softcap / scale.
+        // (A scale so small that s^2 leaves the f32 range does without.)
+        const double k = double(scale) / softcap, fit[4] = {-0.3333306908607483, 0.13324779272079468, -0.05298607423901558,
+                                                            0.017135001718997955};
+        double power = 1.0;
+        for (int i = 0; i < 4; ++i) a.cap_c[i] = float(fit[i] * (power *= k * k));
+        a.cap_near = k > 1e-15 ? float(0.5 / k) : -1.0f;
+    }
     const cudaError_t e = head_dim == 64 ? launch_paged_attention_64(a, bf16, softcap > 0.0f, as_stream(stream))
                                          : launch_paged_attention_128(a, bf16, softcap > 0.0f, as_stream(stream));
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;

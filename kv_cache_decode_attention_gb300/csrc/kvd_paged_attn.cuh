@@ -83,6 +83,9 @@ struct PaArgs {
     int32_t part_rows, pool_rows;
     float scale_log2;  // scale * log2 e (softcap 0), or softcap * log2 e
     float cap_in;      // softcap > 0: 2 * scale * log2 e / softcap
+    float cap_mul;     // scale * log2 e
+    float cap_near;    // below it in size, a score's tanh is the polynomial
+    float cap_c[4];    // its coefficients, in powers of the score
 };
 
 // A ticket that carries another nonce counts as zero, so the workspace needs no
@@ -181,6 +184,9 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// tanh(y) of x = 2 y log2 e, as 1 - 2 / (e^2y + 1): two special-function
+// instructions, right to some 2^-23 of 1.
+__device__ __forceinline__ float pa_tanh(float x) { return fmaf(rcp(ex2(x) + 1.0f), -2.0f, 1.0f); }
 // Two f32 operations in one issue slot.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -922,9 +928,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     s_phase ^= 1;
                     if (busy) {
                         tc_after();
-                        // first pass: the maximum, 64 scores at a time; capped and
-                        // masked ones go back to TMEM so that the second finds them
-                        float m0 = -INFINITY, m1 = -INFINITY;
+                        // first pass: the maximum, 64 scores at a time; masked ones go
+                        // back to TMEM as such, so that the second finds them.  Capping
+                        // keeps the order, so it is left to the second pass.
+                        float m0 = -INFINITY, m1 = -INFINITY, a0 = 0.0f, a1 = 0.0f;
                         const int32_t hi_c = pos - key0, lo_c = lo - key0;
                         const bool edge = __any_sync(0xffffffffu, hi_c < kPaTile - 1 || lo_c > 0);
 #pragma unroll 1
@@ -934,17 +941,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             tc_ld32(t_s + c0 + 32, x + 32);
                             tc_wait_ld();
                             if (CAP) {
-                                // softcap * tanh(s / softcap), with tanh(y) = 1 - 2 / (e^2y + 1);
-                                // two special-function instructions a score, which bound it
-                                const float2 in = make_float2(a.cap_in, a.cap_in), one = make_float2(1.0f, 1.0f);
-                                const float2 zero = make_float2(0.0f, 0.0f), two = make_float2(-2.0f, -2.0f);
 #pragma unroll
-                                for (int c = 0; c < 64; c += 2) {
-                                    float2 v = fma2(make_float2(x[c], x[c + 1]), in, zero);
-                                    v = add2(make_float2(ex2(v.x), ex2(v.y)), one);
-                                    v = fma2(make_float2(rcp(v.x), rcp(v.y)), two, one);
-                                    x[c] = v.x;
-                                    x[c + 1] = v.y;
+                                for (int c = 0; c < 64; c += 4) {
+                                    a0 = max3(a0, fabsf(x[c]), fabsf(x[c + 1]));
+                                    a1 = max3(a1, fabsf(x[c + 2]), fabsf(x[c + 3]));
                                 }
                             }
                             if (edge) {
@@ -954,10 +954,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
 #pragma unroll
                                     for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
                                 }
-                            }
-                            if (CAP || edge) {
-                                tc_st32(t_s + c0, x);
-                                tc_st32(t_s + c0 + 32, x + 32);
+                                if (!CAP) {
+                                    tc_st32(t_s + c0, x);
+                                    tc_st32(t_s + c0 + 32, x + 32);
+                                }
                             }
 #pragma unroll
                             for (int c = 0; c < 64; c += 4) {
@@ -965,8 +965,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 m1 = max3(m1, x[c + 2], x[c + 3]);
                             }
                         }
-                        if (CAP || edge) tc_wait_st();
-                        const float top = fmaxf(m0, m1) * a.scale_log2 - kLift;
+                        if (!CAP && edge) tc_wait_st();
+                        float top = fmaxf(m0, m1);
+                        bool near = false;  // all of the warp's scores are small beside the cap
+                        if (CAP) {
+                            near = __all_sync(0xffffffffu, fmaxf(a0, a1) <= a.cap_near);
+                            const bool some = hi_c >= 0 && lo_c < kPaTile && lo_c <= hi_c;
+                            top = some ? pa_tanh(top * a.cap_in) : -INFINITY;
+                        }
+                        top = top * a.scale_log2 - kLift;
                         // move the reference when a row grew past the slack
                         if (__any_sync(0xffffffffu, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
                             const float now = fmaxf(ref, top);
@@ -991,23 +998,57 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         const float base = ref == -INFINITY ? 0.0f : ref;
                         const float2 sc = make_float2(a.scale_log2, a.scale_log2), nb = make_float2(-base, -base);
                         float2 acc = make_float2(0.0f, 0.0f);
-                        float x[4][32];
-                        tc_ld32(t_s, x[0]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tc_wait_ld();
-                            if (q < 3) tc_ld32(t_s + (q + 1) * 32, x[q + 1]);
+                        // weights of 32 scores from their exponents, and P
+                        auto weigh = [&](const float *x, int q, auto exponent, uint32_t seen) {
                             float p[16];
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
-                                float2 v = fma2(make_float2(x[q][2 * c], x[q][2 * c + 1]), sc, nb);
+                                float2 v = exponent(make_float2(x[2 * c], x[2 * c + 1]));
                                 v.x = ex2(v.x);
                                 v.y = ex2(v.y);
+                                if (seen != ~0u) {  // known to be ~0 where nothing is masked
+                                    v.x = (seen >> (2 * c) & 1u) != 0 ? v.x : 0.0f;
+                                    v.y = (seen >> (2 * c + 1) & 1u) != 0 ? v.y : 0.0f;
+                                }
                                 if (c & 1) acc = add2(acc, v);
                                 else sum2 = add2(sum2, v);
                                 p[c] = __uint_as_float(pack2<BF16>(v.x, v.y));
                             }
                             tc_st16(t_s + q * 16, p);
+                        };
+                        // tanh(y) = y (1 + c1 y^2 + .. + c4 y^8), in powers of the score
+                        auto near_cap = [&](float2 v) {
+                            const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
+                            const float2 z = fma2(v, v, zero);
+                            float2 t = fma2(z, make_float2(a.cap_c[3], a.cap_c[3]), make_float2(a.cap_c[2], a.cap_c[2]));
+                            t = fma2(t, z, make_float2(a.cap_c[1], a.cap_c[1]));
+                            t = fma2(t, z, make_float2(a.cap_c[0], a.cap_c[0]));
+                            t = fma2(t, z, one);
+                            return fma2(t, fma2(v, make_float2(a.cap_mul, a.cap_mul), zero), nb);
+                        };
+                        if (!CAP || (near && !edge)) {
+                            float x[4][32];
+                            tc_ld32(t_s, x[0]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                tc_wait_ld();
+                                if (q < 3) tc_ld32(t_s + (q + 1) * 32, x[q + 1]);
+                                if constexpr (CAP) weigh(x[q], q, near_cap, ~0u);
+                                else weigh(x[q], q, [&](float2 v) { return fma2(v, sc, nb); }, ~0u);
+                            }
+                        } else {
+                            // a capped tile at an edge, or one with large scores: rare, and small code
+#pragma unroll 1
+                            for (int q = 0; q < 4; ++q) {
+                                float x[32];
+                                tc_ld32(t_s + q * 32, x);
+                                tc_wait_ld();
+                                const uint32_t seen = pa_seen(lo_c - q * 32, hi_c - q * 32);
+                                if (near) weigh(x, q, near_cap, seen);
+                                else weigh(x, q, [&](float2 v) {
+                                    return fma2(make_float2(pa_tanh(v.x * a.cap_in), pa_tanh(v.y * a.cap_in)), sc, nb);
+                                }, seen);
+                            }
                         }
                         sum2 = add2(sum2, acc);
                         tc_wait_st();
