@@ -242,6 +242,11 @@ __device__ __forceinline__ uint32_t pa_test3(uint64_t *b0, uint32_t p0, uint64_t
 __device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, volatile int *stop) {
     return __all_sync(0xffffffffu, pa_wait_one(bar, parity, stop));
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -930,8 +935,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         tc_after();
                         // first pass: the maximum, 64 scores at a time; masked ones go
                         // back to TMEM as such, so that the second finds them.  Capping
-                        // keeps the order, so it is left to the second pass.
-                        float m0 = -INFINITY, m1 = -INFINITY, a0 = 0.0f, a1 = 0.0f;
+                        // keeps the order, so it is left to the second pass; there a
+                        // masked score is one so low that its polynomial is lower still.
+                        float m0 = -INFINITY, m1 = -INFINITY, low0 = INFINITY, low1 = INFINITY;
+                        const float hidden = CAP ? -1e4f * a.cap_near : -INFINITY;
                         const int32_t hi_c = pos - key0, lo_c = lo - key0;
                         const bool edge = __any_sync(0xffffffffu, hi_c < kPaTile - 1 || lo_c > 0);
 #pragma unroll 1
@@ -943,8 +950,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             if (CAP) {
 #pragma unroll
                                 for (int c = 0; c < 64; c += 4) {
-                                    a0 = max3(a0, fabsf(x[c]), fabsf(x[c + 1]));
-                                    a1 = max3(a1, fabsf(x[c + 2]), fabsf(x[c + 3]));
+                                    low0 = min3(low0, x[c], x[c + 1]);
+                                    low1 = min3(low1, x[c + 2], x[c + 3]);
                                 }
                             }
                             if (edge) {
@@ -952,12 +959,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 for (int e = 0; e < 64; e += 32) {
                                     const uint32_t seen = pa_seen(lo_c - c0 - e, hi_c - c0 - e);
 #pragma unroll
-                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
+                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : hidden;
                                 }
-                                if (!CAP) {
-                                    tc_st32(t_s + c0, x);
-                                    tc_st32(t_s + c0 + 32, x + 32);
-                                }
+                                tc_st32(t_s + c0, x);
+                                tc_st32(t_s + c0 + 32, x + 32);
                             }
 #pragma unroll
                             for (int c = 0; c < 64; c += 4) {
@@ -965,11 +970,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 m1 = max3(m1, x[c + 2], x[c + 3]);
                             }
                         }
-                        if (!CAP && edge) tc_wait_st();
+                        if (edge) tc_wait_st();
                         float top = fmaxf(m0, m1);
                         bool near = false;  // all of the warp's scores are small beside the cap
                         if (CAP) {
-                            near = __all_sync(0xffffffffu, fmaxf(a0, a1) <= a.cap_near);
+                            near = __all_sync(0xffffffffu, top <= a.cap_near && fminf(low0, low1) >= -a.cap_near);
                             const bool some = hi_c >= 0 && lo_c < kPaTile && lo_c <= hi_c;
                             top = some ? pa_tanh(top * a.cap_in) : -INFINITY;
                         }
@@ -1026,7 +1031,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             t = fma2(t, z, one);
                             return fma2(t, fma2(v, make_float2(a.cap_mul, a.cap_mul), zero), nb);
                         };
-                        if (!CAP || (near && !edge)) {
+                        if (!CAP || near) {
                             float x[4][32];
                             tc_ld32(t_s, x[0]);
 #pragma unroll
@@ -1037,15 +1042,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 else weigh(x[q], q, [&](float2 v) { return fma2(v, sc, nb); }, ~0u);
                             }
                         } else {
-                            // a capped tile at an edge, or one with large scores: rare, and small code
+                            // scores that come near the cap: rare, and small code
 #pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
                                 float x[32];
                                 tc_ld32(t_s + q * 32, x);
                                 tc_wait_ld();
                                 const uint32_t seen = pa_seen(lo_c - q * 32, hi_c - q * 32);
-                                if (near) weigh(x, q, near_cap, seen);
-                                else weigh(x, q, [&](float2 v) {
+                                weigh(x, q, [&](float2 v) {
                                     return fma2(make_float2(pa_tanh(v.x * a.cap_in), pa_tanh(v.y * a.cap_in)), sc, nb);
                                 }, seen);
                             }
