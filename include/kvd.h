@@ -503,7 +503,9 @@ KVD_API kvd_status rswa_device_error(const void *workspace, int32_t clear, uint3
  * The new rows of a step are packed: request b's are rows cu_new[b] ..
  * cu_new[b + 1] - 1 of q, k, v, positions, slots and out.  Row contents that
  * no request holds (the rest of a last page, free pages) are never used,
- * whatever they are; rows that a request holds must be finite.
+ * whatever they are; rows that a request holds must be finite (a NaN or an
+ * infinity in one may reach every new row of its request, those that do not
+ * see it too, but no other request).  max_pages * page_size <= 2^31 - 1024.
  *
  * `err` is the device error word (uint32, caller-owned, zeroed once): bit 0 a
  * bounded wait gave up, bit 1 metadata out of range (the access is skipped),
@@ -582,8 +584,8 @@ KVD_API kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const kv
  * n_tokens is the room for new rows.  A step that does not fit (pages, table
  * width, n_tokens) sets bit 2 of the error word, one with malformed numbers
  * (negative, keep_len > seq_len, n_free out of range) bit 1, and neither
- * changes anything: seq_len_out and n_free_out repeat the inputs, cu_new is 0,
- * positions and slots are -1, so the rest of the step does nothing.  Table
+ * changes anything that counts: seq_len_out and n_free_out repeat the inputs,
+ * cu_new is 0, positions and slots are -1, so the rest of the step does nothing.  Table
  * places past a request's pages and the stack above n_free_out hold nothing.
  * n_seq <= 8192. */
 KVD_API kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_len, const int32_t *new_len,
@@ -607,7 +609,8 @@ KVD_API kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, const k
                                    const int32_t *slots, int64_t n_tokens, void *k_pages, void *v_pages,
                                    int64_t n_pages, int32_t page_size, uint32_t *err, void *stream);
 
-/* Workspace bytes paged_attention needs (no initialisation). */
+/* Workspace bytes paged_attention needs (no initialisation; one block serves
+ * every call of at most so many tokens, one call at a time). */
 KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv,
                                                    int32_t head_dim, int64_t *bytes_out);
 

@@ -67,12 +67,16 @@ bool shape_ok(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t hd) {
            n_q % n_kv == 0 && n_q / n_kv <= kMaxHpk && (hd == 64 || hd == 128);
 }
 
-// A [tokens][heads][hd] view whose rows a 16-byte access may touch.
-bool view_ok(const kvd_rows *r, int64_t tokens) {
+// A [tokens][heads][hd] view whose rows a 16-byte access may touch (the stride of
+// an axis with one entry is never used); the rows of `out` may not lie on one another.
+bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads, bool out) {
     const int64_t lim = int64_t(1) << 38;
-    return r != nullptr && (r->data != nullptr || tokens == 0) && (reinterpret_cast<uintptr_t>(r->data) & 15) == 0 && r->token_stride >= 0 &&
-           r->head_stride >= 0 && r->token_stride < lim && r->head_stride < lim && r->token_stride % 8 == 0 &&
-           r->head_stride % 8 == 0;
+    if (r == nullptr || (r->data == nullptr && tokens > 0) || (reinterpret_cast<uintptr_t>(r->data) & 15) != 0) return false;
+    if (tokens == 0) return true;
+    auto ok = [&](int64_t entries, int64_t stride) {
+        return entries <= 1 || (stride >= (out ? 8 : 0) && stride < lim && stride % 8 == 0);
+    };
+    return ok(tokens, r->token_stride) && ok(heads, r->head_stride);
 }
 
 }  // namespace
@@ -95,7 +99,7 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
                                       int64_t workspace_bytes, uint32_t *err, void *stream) {
     KVD_NVTX_RANGE("paged_attention");
     if (!shape_ok(n_tokens, n_q, n_kv, head_dim) || (dtype != KVD_T_F16 && dtype != KVD_T_BF16)) return KVD_EINVAL;
-    if (!view_ok(q, n_tokens) || !view_ok(out, n_tokens) || (q->data == out->data && n_tokens > 0)) return KVD_EINVAL;
+    if (!view_ok(q, n_tokens, n_q, false) || !view_ok(out, n_tokens, n_q, true) || (q->data == out->data && n_tokens > 0)) return KVD_EINVAL;
     if (k_pages == nullptr || v_pages == nullptr ||
         ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15) != 0)
         return KVD_EINVAL;
@@ -103,9 +107,12 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
         n_pages >= (int64_t(1) << 31) || n_pages * page_size * n_kv >= (int64_t(1) << 31))
         return KVD_EINVAL;
     if (block_table == nullptr || cu_new == nullptr || seq_len == nullptr || err == nullptr || n_seq < 1 || max_pages < 1 ||
-        int64_t(max_pages) * page_size >= (int64_t(1) << 31))
+        int64_t(max_pages) * page_size > (int64_t(1) << 31) - 1024)
         return KVD_EINVAL;
     if (!std::isfinite(scale) || scale <= 0.0f || window < 0 || !std::isfinite(softcap) || softcap < 0.0f) return KVD_EINVAL;
+    const float log2e = 1.4426950408889634f;
+    if (!std::isfinite(scale * log2e) || (softcap > 0.0f && (!std::isfinite(softcap * log2e) || !std::isfinite(2.0f * scale * log2e / softcap))))
+        return KVD_EINVAL;
     if (sinks != nullptr && (reinterpret_cast<uintptr_t>(sinks) & 3) != 0) return KVD_EINVAL;
     const int32_t group = n_q / n_kv;
     const WsLayout ws = ws_layout(n_tokens, group, head_dim);
@@ -156,7 +163,6 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     a.n_pages = int32_t(n_pages);
     a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     a.pool_rows = int32_t(n_pages * page_size * n_kv);
-    const float log2e = 1.4426950408889634f;
     a.scale_log2 = (softcap > 0.0f ? softcap : scale) * log2e;
     if (softcap > 0.0f) {
         a.cap_in = 2.0f * scale * log2e / softcap;

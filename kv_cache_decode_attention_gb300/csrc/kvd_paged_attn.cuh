@@ -53,7 +53,6 @@ constexpr int kPaThreads = 512;    // warps 14 and 15 only fill their warpgroup
 constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
 static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
-constexpr int kPaQBytes = 2 * kPaTile * 256;
 constexpr int kPaMaxRows = 2 * kPaTile;
 // Joining 16 rows of 19 pieces takes one CTA some 3 us, as long as a second
 // launch; 256 rows of 2 pieces took it 20 us, and the kernel 3.
@@ -947,22 +946,24 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             tc_ld32(t_s + c0, x);
                             tc_ld32(t_s + c0 + 32, x + 32);
                             tc_wait_ld();
-                            if (CAP) {
-#pragma unroll
-                                for (int c = 0; c < 64; c += 4) {
-                                    low0 = min3(low0, x[c], x[c + 1]);
-                                    low1 = min3(low1, x[c + 2], x[c + 3]);
-                                }
-                            }
                             if (edge) {
 #pragma unroll
                                 for (int e = 0; e < 64; e += 32) {
                                     const uint32_t seen = pa_seen(lo_c - c0 - e, hi_c - c0 - e);
 #pragma unroll
-                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : hidden;
+                                    for (int c = 0; c < 32; ++c) {
+                                        if (CAP) low0 = fminf(low0, (seen >> c & 1u) != 0 ? x[e + c] : INFINITY);
+                                        x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : hidden;
+                                    }
                                 }
                                 tc_st32(t_s + c0, x);
                                 tc_st32(t_s + c0 + 32, x + 32);
+                            } else if (CAP) {
+#pragma unroll
+                                for (int c = 0; c < 64; c += 4) {
+                                    low0 = min3(low0, x[c], x[c + 1]);
+                                    low1 = min3(low1, x[c + 2], x[c + 3]);
+                                }
                             }
 #pragma unroll
                             for (int c = 0; c < 64; c += 4) {
@@ -972,13 +973,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         }
                         if (edge) tc_wait_st();
                         float top = fmaxf(m0, m1);
+                        // (Rows that are no row of the request have no say in what its
+                        // rows do, nor have scores that no row sees: the same bits come
+                        // out whatever lies there.)
                         bool near = false;  // all of the warp's scores are small beside the cap
                         if (CAP) {
-                            near = __all_sync(0xffffffffu, top <= a.cap_near && fminf(low0, low1) >= -a.cap_near);
+                            near = __all_sync(0xffffffffu, !valid || (top <= a.cap_near && fminf(low0, low1) >= -a.cap_near));
                             const bool some = hi_c >= 0 && lo_c < kPaTile && lo_c <= hi_c;
                             top = some ? pa_tanh(top * a.cap_in) : -INFINITY;
                         }
-                        top = top * a.scale_log2 - kLift;
+                        top = valid ? top * a.scale_log2 - kLift : -INFINITY;
                         // move the reference when a row grew past the slack
                         if (__any_sync(0xffffffffu, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
                             const float now = fmaxf(ref, top);

@@ -194,7 +194,7 @@ extern "C" kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_
     if (n_tokens > 0 && (positions == nullptr || slots == nullptr)) return KVD_EINVAL;
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return KVD_EINVAL;
     if (n_pages < 1 || n_pages >= (int64_t(1) << 31) || n_pages * page_size >= (int64_t(1) << 31)) return KVD_EINVAL;
-    if (int64_t(max_pages) * page_size >= (int64_t(1) << 31)) return KVD_EINVAL;
+    if (int64_t(max_pages) * page_size > (int64_t(1) << 31) - 1024) return KVD_EINVAL;
     PlanArgs a = {};
     a.seq_len = seq_len;
     a.keep_len = keep_len;

@@ -383,8 +383,10 @@ Group group_of(const kvd_rows *in, const kvd_rows *out, int32_t heads) {
     return g;
 }
 
-// In place is fine row by row; any other way of sharing a buffer is not.
-bool in_place_ok(const kvd_rows *in, const kvd_rows *out) {
+// In place is fine row by row; any other way of sharing a buffer is not, nor are
+// output rows that lie on one another.
+bool out_ok(const kvd_rows *in, const kvd_rows *out, int64_t tokens, int32_t heads) {
+    if ((tokens > 1 && out->token_stride == 0) || (tokens > 0 && heads > 1 && out->head_stride == 0)) return false;
     return in->data != out->data || in->data == nullptr || (in->token_stride == out->token_stride && in->head_stride == out->head_stride);
 }
 
@@ -470,7 +472,7 @@ extern "C" kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const
         if (in[i] == nullptr) continue;
         if (heads[i] < 1 || heads[i] > 1024) return KVD_EINVAL;
         if (!rows_ok(in[i], n_tokens, heads[i], bytes) || !rows_ok(out[i], n_tokens, heads[i], bytes)) return KVD_EINVAL;
-        if (!in_place_ok(in[i], out[i])) return KVD_EINVAL;
+        if (!out_ok(in[i], out[i], n_tokens, heads[i])) return KVD_EINVAL;
         a.g[i] = group_of(in[i], out[i], heads[i]);
         aligned = aligned && aligned16(a.g[i], false, bytes, bytes);
     }
@@ -511,7 +513,7 @@ extern "C" kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, cons
     if (q != nullptr) {
         if (n_q < 1 || n_q > 1024 || !rows_ok(q, n_tokens, n_q, ib) || !rows_ok(q_out, n_tokens, n_q, ob)) return KVD_EINVAL;
         if (q->data != nullptr && q->data == q_out->data && ib != ob) return KVD_EINVAL;
-        if (!in_place_ok(q, q_out)) return KVD_EINVAL;
+        if (!out_ok(q, q_out, n_tokens, n_q)) return KVD_EINVAL;
         a.g[0] = group_of(q, q_out, n_q);
         aligned = aligned16(a.g[0], false, ib, ob);
     }

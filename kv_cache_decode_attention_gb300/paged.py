@@ -346,7 +346,7 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
     return q_out
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def paged_attention_workspace(n_tokens: int, n_q: int, n_kv: int, head_dim: int) -> int:
     """Bytes of workspace that paged_attention needs for up to n_tokens new rows."""
     n = C.c_int64(0)

@@ -207,7 +207,8 @@ def _same_state(cache, model):
         assert table[b, : len(p)].tolist() == p, b
 
 
-@pytest.mark.parametrize("n_seq,page,width,n_pages,most", [(1, 16, 8, 8, 60), (7, 16, 10, 40, 40), (33, 32, 6, 120, 90), (1500, 16, 3, 3000, 20), (1500, 16, 12, 12000, 20), (5, 128, 50, 200, 2500)])
+@pytest.mark.parametrize("n_seq,page,width,n_pages,most", [(1, 16, 8, 8, 60), (7, 16, 10, 40, 40), (33, 32, 6, 120, 90), (1500, 16, 3, 3000, 20), (1500, 16, 12, 12000, 20), (5, 128, 50, 200, 2500),
+                                                            (8192, 16, 4, 20000, 12)])
 def test_plan_follows_a_simple_allocator(env, n_seq, page, width, n_pages, most):
     torch, kvd = env
     r = np.random.default_rng(n_seq)
@@ -668,6 +669,72 @@ def test_a_captured_step_replays_while_lengths_go_on(env):
         assert graph.caches[0].seq_len.tolist() == now and graph.caches[0].device_error() == 0
 
 
+def test_capture_without_a_workspace(env):
+    """A workspace taken by the call itself lives as long as the graph that captured it; small calls (joined in the kernel) and larger
+    ones, replayed between eager calls."""
+    torch, kvd = env
+    for lens, new in (([9000], [1]), ([700, 3000], [40, 90])):
+        cache, _ = _poisoned(torch, kvd, lens, 2, 128, 16, torch.bfloat16, 3)
+        q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).bfloat16()
+        plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+        want = kvd.paged_attention(q, cache, plan)
+        torch.cuda.synchronize()
+        graphs = []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                out = kvd.paged_attention(q, cache, plan)
+            graphs.append((g, out))
+        for _ in range(4):
+            for g, out in graphs:
+                out.zero_()
+                g.replay()
+                assert torch.equal(kvd.paged_attention(q, cache, plan), want)
+                assert torch.equal(out, want)
+        assert cache.device_error() == 0
+
+
+def test_a_workspace_of_any_contents(env):
+    """No initialisation: zeros, ones and what an earlier call of other sizes left give the same bits."""
+    torch, kvd = env
+    ws = torch.empty(kvd.paged_attention_workspace(300, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    first = {}
+    for fill in (0, 255, 1, None, None):
+        for lens, new in (([9000], [1]), ([700, 3000], [40, 90]), ([20, 30000, 5], [1, 2, 1]), ([2500], [300])):
+            cache, _ = _poisoned(torch, kvd, lens, 2, 128, 16, torch.bfloat16, 3)
+            q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).bfloat16()
+            plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+            if fill is not None:
+                ws.fill_(fill)
+            out = kvd.paged_attention(q, cache, plan, workspace=ws)
+            assert cache.device_error() == 0
+            assert torch.equal(out, first.setdefault(str(lens), out))
+
+
+@pytest.mark.parametrize("softcap,scale", [(0.0, 0.09), (30.0, 0.09), (30.0, 9.0)])
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f16", 64)])
+def test_what_nobody_holds_leaves_no_trace(env, dtype, hd, softcap, scale):
+    """Rows of pages behind a request's last one and rows of q behind the last request: the same bits whatever they are (they share
+    tiles, and warps, with rows that count)."""
+    torch, kvd = env
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    for lens, new in (([2001, 77], [1, 1]), ([530, 1000], [3, 150]), ([40], [40])):
+        cache, _ = _poisoned(torch, kvd, lens, 2, hd, 64, dt, 11)
+        t = sum(new)
+        q = torch.randn(t + 5, 10, hd, device="cuda", generator=torch.Generator(device="cuda").manual_seed(12)).to(dt)
+        plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+        free = torch.isnan(cache.k)
+        outs = []
+        for junk in (0.0, float("nan"), float("inf"), -float("inf"), 60000.0, -60000.0):
+            for x in (cache.k, cache.v):
+                x.masked_fill_(free, junk)
+            q[t:] = junk
+            outs.append(kvd.paged_attention(q, cache, plan, scale=scale, softcap=softcap)[:t])
+        assert cache.device_error() == 0
+        assert not bool(torch.isnan(outs[0]).any())
+        assert all(torch.equal(outs[0], x) for x in outs)
+
+
 def test_two_streams_and_repeats_give_the_same_bits(env):
     torch, kvd = env
     cases = []
@@ -696,7 +763,8 @@ def test_a_failed_launch_is_reported(env):
     x = torch.ones(1, 1, 64, device="cuda", dtype=torch.bfloat16)
     plan = kvd.PagedPlan(_i32(torch, [0, 1]), cache.seq_len, positions=_i32(torch, [0]), slots=_i32(torch, [-1]))
     calls = [(lambda: kvd.rope(x, None, plan.positions, kvd.RopeTable(64)), 1), (lambda: kvd.paged_plan(cache, _i32(torch, [0]), 0), 1),
-             (lambda: kvd.paged_append(cache, plan, x, x), 1), (lambda: kvd.paged_attention(x, cache, plan), 1)]
+             (lambda: kvd.paged_append(cache, plan, x, x), 1), (lambda: kvd.paged_attention(x, cache, plan), 1),
+             (lambda: kvd.paged_attention(x.expand(20, 1, 64), cache, plan), 2)]
     try:
         for call, launches in calls:
             for n in range(launches):

@@ -100,7 +100,8 @@ def test_rope_apply_refusals(abi):
     assert call(n=0) == abi.OK  # nothing to do, nothing launched
     for bad in (dict(R=None), dict(R=C.byref(abi.kvd_rope())), dict(q=None), dict(qo=None), dict(q=None, qo=None, k=None, ko=None), dict(n_q=0),
                 dict(n_kv=1025), dict(hd=64), dict(hd=520), dict(dtype=3), dict(pos=None), dict(n=-1), dict(n=1 << 31), dict(q=_rows(abi, 0)),
-                dict(q=_rows(abi, FAKE + 1)), dict(qo=_rows(abi, tok=2048)), dict(q=_rows(abi, tok=-1024)), dict(k=_rows(abi, head=-1))):
+                dict(q=_rows(abi, FAKE + 1)), dict(qo=_rows(abi, tok=2048)), dict(q=_rows(abi, tok=-1024)), dict(k=_rows(abi, head=-1)),
+                dict(qo=_rows(abi, 2 * FAKE, tok=0)), dict(ko=_rows(abi, 2 * FAKE, head=0))):
         assert call(**bad) == abi.EINVAL, bad
 
 
@@ -116,7 +117,7 @@ def test_plan_refusals(abi):
     for bad in (dict(seq_len=None), dict(new_len=None), dict(table=None), dict(free=None), dict(n_free=None), dict(len_out=None), dict(free_out=None),
                 dict(cu=None), dict(positions=None), dict(slots=None), dict(err=None), dict(n_seq=0), dict(n_seq=8193), dict(n_pages=0),
                 dict(n_pages=1 << 27), dict(page_size=8), dict(page_size=48), dict(page_size=256), dict(max_pages=0), dict(max_pages=1 << 27),
-                dict(n_tokens=-1), dict(n_tokens=1 << 31)):
+                dict(max_pages=(1 << 27) - 63), dict(n_tokens=-1), dict(n_tokens=1 << 31)):
         assert call(**bad) == abi.EINVAL, bad
 
 
@@ -154,11 +155,13 @@ def test_attention_refusals(abi):
         return L.paged_attention(q, out, n, n_q, n_kv, hd, dt, kp, vp, n_pages, page, table, width, cu, lens, n_seq, scale, window, softcap, sinks, w, wb, err, None)
 
     assert call(n=0) == abi.OK
+    assert call(n=0, q=_rows(abi, 0, tok=3, head=128)) == abi.OK  # the stride of an axis with one entry is not looked at
     inf, nan = float("inf"), float("nan")
     for bad in (dict(q=None), dict(out=None), dict(out=_rows(abi)), dict(q=_rows(abi, FAKE + 8)), dict(q=_rows(abi, tok=1028)), dict(out=_rows(abi, 2 * FAKE, head=132)),
                 dict(q=_rows(abi, tok=-1024)), dict(n=-1), dict(n_q=12), dict(n_q=136), dict(n_kv=0), dict(hd=32), dict(dt=0), dict(dt=7), dict(kp=None), dict(vp=FAKE + 8),
-                dict(n_pages=0), dict(n_pages=1 << 24), dict(page=12), dict(page=256), dict(table=None), dict(width=0), dict(width=1 << 27), dict(cu=None), dict(lens=None),
-                dict(n_seq=0), dict(scale=0.0), dict(scale=-0.1), dict(scale=nan), dict(scale=inf), dict(window=-1), dict(softcap=-1.0), dict(softcap=nan), dict(sinks=FAKE + 2),
+                dict(n_pages=0), dict(n_pages=1 << 24), dict(page=12), dict(page=256), dict(table=None), dict(width=0), dict(width=1 << 27),
+                dict(width=(1 << 27) - 63), dict(out=_rows(abi, 2 * FAKE, tok=0)), dict(out=_rows(abi, 2 * FAKE, head=0)), dict(scale=3e38), dict(softcap=3e38),
+                dict(softcap=1e-38, scale=10.0), dict(cu=None), dict(lens=None), dict(n_seq=0), dict(scale=0.0), dict(scale=-0.1), dict(scale=nan), dict(scale=inf), dict(window=-1), dict(softcap=-1.0), dict(softcap=nan), dict(sinks=FAKE + 2),
                 dict(w=None), dict(w=FAKE + 16), dict(wb=1024), dict(err=None)):
         assert call(**bad) == abi.EINVAL, bad
     assert L.kv_paged_device_error(None, 0, None) == abi.EINVAL
