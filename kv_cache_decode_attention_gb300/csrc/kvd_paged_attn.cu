@@ -172,7 +172,7 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
         // (A scale so small that s^2 leaves the f32 range does without.)
         const double k = double(scale) / softcap, fit[4] = {-0.3333306908607483, 0.13324779272079468, -0.05298607423901558,
                                                             0.017135001718997955};
-        double power = 1.0;
+        double power = double(scale) * log2e;
         for (int i = 0; i < 4; ++i) a.cap_c[i] = float(fit[i] * (power *= k * k));
         a.cap_near = k > 1e-15 ? float(0.5 / k) : -1.0f;
     }

@@ -25,7 +25,8 @@
 //   warps 8, 12     TMA loads of Q and K, and of V: tiles of 128 rows into one
 //                   ring, page by page (a page that does not exist reads as
 //                   zeros); small pages take many copies, hence two warps;
-//   warp 9          issues the MMAs: S = Q K^T and O += P V, P from TMEM;
+//   warps 9, 14     issue the MMAs of stream 0 and 1: S = Q K^T and O += P V, P
+//                   from TMEM;
 //   warp 10         clears the rows of V behind a request's last one;
 //   warp 11         walks the CTA's share of the work and hands the items on;
 //   warp 13         ends every wait if the CTA stops making steps.
@@ -48,7 +49,7 @@
 namespace kvd {
 
 constexpr int kPaCtas = 152;       // one per SM; also fixes the cut of the work
-constexpr int kPaThreads = 512;    // warps 14 and 15 only fill their warpgroup
+constexpr int kPaThreads = 512;    // warp 15 only fills its warpgroup
 // Registers a thread: the launch gives 512 x 128; the softmax warpgroups trade up.
 constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
 static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
@@ -82,9 +83,9 @@ struct PaArgs {
     int32_t part_rows, pool_rows;
     float scale_log2;  // scale * log2 e (softcap 0), or softcap * log2 e
     float cap_in;      // softcap > 0: 2 * scale * log2 e / softcap
-    float cap_mul;     // scale * log2 e
+    float cap_mul;     // scale * log2 e: the polynomial's first coefficient
     float cap_near;    // below it in size, a score's tanh is the polynomial
-    float cap_c[4];    // its coefficients, in powers of the score
+    float cap_c[4];    // its other coefficients, in powers of the score
 };
 
 // A ticket that carries another nonce counts as zero, so the workspace needs no
@@ -221,7 +222,7 @@ __device__ __forceinline__ bool pa_wait_one(uint64_t *bar, uint32_t parity, vola
 }
 // Looks at three barriers at once; a bit for each whose phase is over.  While the tensor
 // cores read both operands from shared memory they leave little of its
-// bandwidth, and one such look takes some 200 cycles: the MMA warp takes its
+// bandwidth, and one such look takes some 200 cycles: the MMA warps take their
 // looks together.
 __device__ __forceinline__ uint32_t pa_test3(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2) {
     uint32_t r;
@@ -424,7 +425,7 @@ struct PaShared {
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2];
-    uint64_t ml_full[2], tail_go, tail_ready, piece_done, verdict, all_done, drain;
+    uint64_t ml_full[2], tail_go[2], tail_ready[2], pace[2], piece_done, verdict, all_done, drain[2];
     PaStart start;
     int64_t warp_sums[kPaThreads / 32];
     uint32_t tmem;
@@ -475,6 +476,13 @@ struct PaIssue {
             phase ^= 1;
         }
         return at;
+    }
+    // a tile of the other stream's
+    __device__ __forceinline__ bool skip() {
+        if (!wait_stage()) return false;
+        const uint32_t at = take();
+        if (elect_one()) pa_arrive(&sh.kv_empty[at]);
+        return true;
     }
     // the stage after the next one
     __device__ __forceinline__ uint32_t after() const { return stage + 1 == S::kStages ? 0 : stage + 1; }
@@ -628,10 +636,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
 
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.q_empty, 2);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&sh.kv_full[i], 1);
-            mbar_init(&sh.kv_empty[i], 1);
+            mbar_init(&sh.kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -639,17 +647,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_empty[i], 4);
             mbar_init(&sh.ml_full[i], 4);
+            mbar_init(&sh.tail_go[i], 1);
+            mbar_init(&sh.pace[i], 1);
+            mbar_init(&sh.tail_ready[i], 1);
+            mbar_init(&sh.drain[i], 1);
         }
         for (int i = 0; i < kPaJobs; ++i) {
             mbar_init(&sh.job_full[i], 1);
-            mbar_init(&sh.job_empty[i], 12);  // two of loads, MMAs, ends of V, eight softmax warps
+            mbar_init(&sh.job_empty[i], 13);  // two of loads, two of MMAs, ends of V, eight softmax warps
         }
-        mbar_init(&sh.tail_go, 1);
         mbar_init(&sh.piece_done, 4);
         mbar_init(&sh.verdict, 1);
         mbar_init(&sh.all_done, 8);
-        mbar_init(&sh.tail_ready, 1);
-        mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.stop = 0;
         sh.steps = 0;
@@ -755,13 +764,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     ring += 2 * n;
                     if (!ok) break;
                 }
-            } else if (warp == 9) {
+            } else if (warp == 9 || warp == 14) {
                 // ------------------------------------------------------ MMAs
-                // The tensor cores wait for this warp's instructions between two
-                // batches: the ring is a cursor, a batch's descriptors differ by
-                // constants, and both streams' steps are written out.
+                // A warp for each stream.  Between two batches of MMAs come looks at
+                // barriers, which queue up behind the batch: the other warp's batches
+                // fill that time.
                 PaIssue<HD, BF16> mma(sh, q_smem, kv_smem, tmem, stop);
-                uint32_t items = 0, tails = 0, p_phase = 0;
+                const uint32_t d = uni(warp == 14 ? 1 : 0);
+                uint32_t items = 0, tails = 0, p_phase = 0, pairs = 0;
                 bool ok = true;
                 for (;;) {
                     ok = mma.wait(&sh.job_full[job_at % kPaJobs], job_at / kPaJobs & 1);
@@ -774,61 +784,67 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     if (n == 0) break;
                     ok = mma.wait(&sh.q_full, items & 1);
                     if (!ok) break;
-                    // step j: P V of stream j & 1, then its S two steps on.  A dual
-                    // item's K and V tile serves both streams, a single one's one.
-                    const int32_t steps = dual ? 2 * n : n;
-                    uint32_t k = 0, v = 0;
-                    // (written out for both streams: what differs are constants)
-                    auto step = [&](int32_t j, auto stream) {
-                        constexpr int d = decltype(stream)::value;
-                        const bool first = !dual || d == 0, second = !dual || d == 1;  // the tiles' first and last use
-                        const bool ahead = j + 2 < steps;
-                        uint32_t is = 0;  // bits: V there, P there, next K there
-                        if (j >= 0) {
-                            if (first) {
-                                is = pa_test3(&sh.kv_full[mma.stage], mma.phase, &sh.p_ready[d], p_phase >> d & 1, &sh.kv_full[mma.after()], mma.phase_after());
-                                if ((is & 1) == 0) ok = mma.wait_stage();
-                                if (ok && (dual ? j >> 1 : j) == tail) {  // it ends short: cleared first
-                                    if (elect_one()) pa_arrive(&sh.tail_go);
-                                    ok = mma.wait(&sh.tail_ready, tails++ & 1);
-                                }
-                                v = mma.take();
-                            }
-                            // before the first write to O the last item's must have been read
-                            if (ok && j < 2 && items > 0) ok = mma.wait(&sh.o_empty[d], (items - 1) & 1);
-                            if (ok && (is & 2) == 0) ok = mma.wait(&sh.p_ready[d], p_phase >> d & 1);
-                            if (!ok) return;
-                            p_phase ^= 1u << d;
-                            mma.value(d, v, j >= 2);
-                            if (!ahead) tc_commit(&sh.o_full[d]);
+                    // Step j: P V of tile j, then S of this stream's next tile.  Of a single
+                    // item's tiles a stream uses every other one; it waits for the rest and
+                    // lets go of them, so that it sees every turn of the ring.
+                    const int32_t next = dual ? 1 : 2;
+                    for (int32_t j = -next; j < n; ++j) {
+                        const bool more = j + next < n;
+                        if (!dual && (uint32_t(j) & 1) != d) {
+                            if (j >= 0) ok = mma.skip();
+                            if (ok && more) ok = mma.skip();
+                            if (!ok) break;
+                            continue;
                         }
-                        if (ahead) {
-                            if (first) {
-                                if ((is & 4) == 0) ok = mma.wait_stage();
-                                if (!ok) return;
-                                k = mma.take();
+                        uint32_t is = 0, v = 0;  // bits: V there, P there, next K there
+                        if (j >= 0) {
+                            is = pa_test3(&sh.kv_full[mma.stage], mma.phase, &sh.p_ready[d], p_phase, &sh.kv_full[mma.after()], mma.phase_after());
+                            if ((is & 1) == 0) ok = mma.wait_stage();
+                            if (ok && j == tail) {  // it ends short: cleared first
+                                if ((!dual || d == 0) && elect_one()) pa_arrive(&sh.tail_go[d]);
+                                ok = mma.wait(&sh.tail_ready[d], tails++ & 1);
                             }
+                            v = mma.take();
+                            // before the first write to O the last item's must have been read
+                            if (ok && j < next && items > 0) ok = mma.wait(&sh.o_empty[d], (items - 1) & 1);
+                            if (ok && (is & 2) == 0) ok = mma.wait(&sh.p_ready[d], p_phase);
+                            // the streams of a dual item take turns: one that ran ahead would
+                            // leave the other to end the item alone
+                            if (ok && dual && (d == 1 || pairs > 0)) ok = mma.wait(&sh.pace[d ^ 1], (pairs - (d ^ 1)) & 1);
+                            if (!ok) break;
+                            p_phase ^= 1;
+                            mma.value(d, v, j >= next);
+                            if (!more) tc_commit(&sh.o_full[d]);
+                        }
+                        if (more) {
+                            if ((is & 4) == 0) ok = mma.wait_stage();
+                            if (!ok) break;
+                            const uint32_t k = mma.take();
                             mma.score(d, dual ? d : 0, k);
                             tc_commit(&sh.s_full[d]);
-                            if (second) tc_commit(&sh.kv_empty[k]);
-                            if (j + 3 == steps) tc_commit(&sh.q_empty);
+                            tc_commit(&sh.kv_empty[k]);
+                            if (j + 2 * next >= n) tc_commit(&sh.q_empty);
                         }
-                        if (j >= 0 && second) tc_commit(&sh.kv_empty[v]);
-                    };
-                    for (int32_t j = -2; ok && j < steps; j += 2) {
-                        step(j, std::integral_constant<int, 0>());
-                        if (ok && j + 1 < steps) step(j + 1, std::integral_constant<int, 1>());
+                        if (j >= 0) tc_commit(&sh.kv_empty[v]);
+                        if (dual && j >= 0) {
+                            if (elect_one()) pa_arrive(&sh.pace[d]);
+                            ++pairs;
+                        }
+                    }
+                    if (ok && !dual && n == 1 && d == 1) {  // no tile for this stream
+                        if (items > 0) ok = mma.wait(&sh.o_empty[1], (items - 1) & 1);
+                        if (ok && elect_one()) pa_arrive(&sh.q_empty);
                     }
                     if (!ok) break;
                     ++items;
                 }
-                if (!ok) tc_commit(&sh.drain);
+                if (!ok) tc_commit(&sh.drain[d]);
             } else if (warp == 10) {
                 // ------------------------------------------------------ ends of V
                 // Rows of a request's last page behind its last row hold nothing;
                 // their weights are zero, but zero times NaN is not: they are
                 // cleared after the copy and before the MMA, whose thread says when.
-                uint32_t ring = 0, tails = 0;
+                uint32_t ring = 0, tails = 0;  // bits: parity of each stream's next one
                 bool ok = true;
                 for (;;) {
                     const PaJob &job = next_job(ok);
@@ -837,8 +853,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     const bool dual = job.dual != 0;
                     done_job();
                     if (t >= 0) {
-                        ok = pa_wait(&sh.tail_go, tails++ & 1, stop);
+                        const int s = dual ? 0 : t & 1;
+                        ok = pa_wait(&sh.tail_go[s], tails >> s & 1, stop);
                         if (!ok) break;
+                        tails ^= 1u << s;
                         const uint32_t stage = (ring + uint32_t(dual ? 2 * t + 1 : t < n - 1 ? 2 * t + 2 : 2 * n - 1)) % S::kStages;
                         const int32_t row1 = ((row0 + (1 << a.page_log2) - 1) >> a.page_log2) << a.page_log2;
                         const uint32_t va = kv_smem + stage * S::kStageBytes + row0 * 128;
@@ -848,7 +866,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                              : "memory");
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                        if (lane == 0) pa_arrive(&sh.tail_ready);
+                        if (lane == 0) pa_arrive(&sh.tail_ready[s]);
+                        if (lane == 0 && dual) pa_arrive(&sh.tail_ready[1]);
                     }
                     ring += 2 * n;
                 }
@@ -1025,15 +1044,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             }
                             tc_st16(t_s + q * 16, p);
                         };
-                        // tanh(y) = y (1 + c1 y^2 + .. + c4 y^8), in powers of the score
+                        // tanh(y) = y (1 + c1 y^2 + .. + c4 y^8), in powers of the score and
+                        // log2 units
                         auto near_cap = [&](float2 v) {
-                            const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
+                            const float2 zero = make_float2(0.0f, 0.0f);
                             const float2 z = fma2(v, v, zero);
                             float2 t = fma2(z, make_float2(a.cap_c[3], a.cap_c[3]), make_float2(a.cap_c[2], a.cap_c[2]));
                             t = fma2(t, z, make_float2(a.cap_c[1], a.cap_c[1]));
                             t = fma2(t, z, make_float2(a.cap_c[0], a.cap_c[0]));
-                            t = fma2(t, z, one);
-                            return fma2(t, fma2(v, make_float2(a.cap_mul, a.cap_mul), zero), nb);
+                            t = fma2(t, z, make_float2(a.cap_mul, a.cap_mul));
+                            return fma2(t, v, nb);
                         };
                         if (!CAP || near) {
                             float x[4][32];
@@ -1191,7 +1211,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
 #pragma unroll 1
         for (int i = 0; i < S::kStages; ++i)
             if (loaded >> i & 1) mbar_wait_bounded(&sh.kv_full[i], parity >> i & 1, 500000000ull);
-        if (warp == 9) mbar_wait_bounded(&sh.drain, 0, 500000000ull);
+        if (warp == 9 || warp == 14) mbar_wait_bounded(&sh.drain[warp == 9 ? 0 : 1], 0, 500000000ull);
     }
     tc_before();
     __syncthreads();
