@@ -12,6 +12,11 @@
 // fills crosses CTAs, and the cluster's hardware barrier carries those.  The
 // fills walk flat ranges of pages and rows with a binary search over the
 // prefix sums, so one long prompt spreads over all threads like many short ones.
+//
+// Measured: one token for each of 256 requests 6.5 us, 500 requests with up to 256
+// new rows each 11.8 us, 8000 requests of one row 20 us.  An empty launch takes 2;
+// the rest is a chain of dependent steps (lengths, three block scans, two cluster
+// barriers, table, slots).  Separate kernels would pay a launch for each barrier.
 
 #include "kvd_internal.cuh"
 
@@ -73,6 +78,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int
     return before + x - v;
 }
 
+template <int RUN>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int64_t warp_sums[32];
@@ -159,19 +165,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         for (int b = threadIdx.x; b <= n; b += kPlanThreads) a.cu_new[b] = ok ? cu[b] : 0;
     }
-    // slots: neighbouring threads write neighbouring rows
+    // slots: a thread takes the rows t .. t + RUN - 1, one after another
     const int32_t mask = (1 << a.page_log2) - 1;
-    for (int t = tid; t < a.n_tokens; t += n_thr) {
-        int32_t pos = -1, slot = -1;
-        if (ok && t < n_rows) {
-            const int b = owner_of(cu, n, t);
-            pos = keep[b] + (t - cu[b]);
-            const int32_t page = a.block_table[int64_t(b) * a.max_pages + (pos >> a.page_log2)];
+    for (int64_t t = int64_t(tid) * RUN; t < a.n_tokens; t += int64_t(n_thr) * RUN) {
+        int32_t pos[RUN], slot[RUN], b = 0, end = 0;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            pos[i] = slot[i] = -1;
+            if (!ok || t + i >= n_rows) continue;
+            if (t + i >= end) {
+                b = owner_of(cu, n, int32_t(t) + i);
+                end = cu[b + 1];
+            }
+            pos[i] = keep[b] + (int32_t(t) + i - cu[b]);
+            const int32_t page = a.block_table[int64_t(b) * a.max_pages + (pos[i] >> a.page_log2)];
             if (page < 0 || page >= a.n_pages) set_error(a.err, kErrBounds);
-            else slot = (page << a.page_log2) + (pos & mask);
+            else slot[i] = (page << a.page_log2) + (pos[i] & mask);
         }
-        a.positions[t] = pos;
-        a.slots[t] = slot;
+        if (RUN == 4 && t + RUN <= a.n_tokens) {
+            *reinterpret_cast<int4 *>(a.positions + t) = *reinterpret_cast<int4 *>(pos);
+            *reinterpret_cast<int4 *>(a.slots + t) = *reinterpret_cast<int4 *>(slot);
+        } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                if (t + i >= a.n_tokens) break;
+                a.positions[t + i] = pos[i];
+                a.slots[t + i] = slot[i];
+            }
+        }
     }
 }
 
@@ -213,9 +234,15 @@ extern "C" kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_
     a.positions = positions;
     a.slots = slots;
     a.err = err;
+    // With more rows than threads and runs of rows that one request owns, a thread
+    // takes four neighbours at a time: one search and one wide store for them.
+    // (500 requests of some 128 new rows: 11.8 us, one by one 13.8; 8000 of three:
+    // 23.7 and 21.2.)
+    const bool four = n_tokens > kPlanCtas * kPlanThreads && n_tokens >= 8 * int64_t(n_seq) &&
+                      ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
+    const auto kern = four ? plan_kernel<4> : plan_kernel<1>;
     const size_t smem = (5 * size_t(n_seq) + 3) * 4;
-    if (smem > 40 * 1024 &&
-        set_smem_once(reinterpret_cast<const void *>(plan_kernel), (5 * kPlanMaxSeq + 3) * 4) != cudaSuccess)
+    if (smem > 40 * 1024 && set_smem_once(reinterpret_cast<const void *>(kern), (5 * kPlanMaxSeq + 3) * 4) != cudaSuccess)
         return KVD_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kPlanCtas);
@@ -231,7 +258,7 @@ extern "C" kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     return e == cudaSuccess && !fault_fires() ? KVD_OK : KVD_ECUDA;
 }
 

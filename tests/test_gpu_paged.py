@@ -247,6 +247,23 @@ def test_plan_follows_a_simple_allocator(env, n_seq, page, width, n_pages, most)
     assert steps >= 2 and steps + refused == 12
 
 
+def test_plan_fills_buffers_at_any_offset(env):
+    """Rows in runs of four where the buffers allow it, one by one where they do not: the same plan."""
+    torch, kvd = env
+    cache = kvd.PagedKvCache(2000, 16, 1, 64, 7, 800)
+    new = _i32(torch, [9001, 3, 0, 1200, 5, 0, 4000])
+    room = 14221
+    want = kvd.paged_plan(cache, new, room, advance=False)
+    for off in (0, 1, 2, 3):
+        pos, slots = (torch.full((room + 8,), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+        plan = kvd.PagedPlan(torch.empty_like(want.cu_new), torch.empty_like(want.seq_len), torch.empty_like(want.n_free), pos[off:off + room], slots[off:off + room])
+        kvd.paged_plan(cache, new, room, advance=False, plan=plan)
+        assert torch.equal(plan.positions, want.positions) and torch.equal(plan.slots, want.slots)
+        for x in (pos, slots):
+            assert bool((x[:off] == 77).all()) and bool((x[off + room:] == 77).all())
+    assert cache.device_error() == 0
+
+
 def test_plan_refuses_what_does_not_fit_or_is_malformed(env):
     torch, kvd = env
     cache = kvd.PagedKvCache(6, 16, 1, 64, 3, 4)
