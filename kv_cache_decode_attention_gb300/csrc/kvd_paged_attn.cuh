@@ -36,6 +36,33 @@
 // before it is: the softmax group may then rescale O in place.  It does so only
 // when a row's maximum grew by more than 2^kSlack; until then the old one is
 // as good a reference.
+//
+// Roundings.  Scores, maxima, sums, weights and O are f32.  The weights are
+// rounded once to the pages' type, because the second product's operands have one
+// type; the sum is taken of the weights before that, so each row's error is that
+// of independent half steps.  f16 weights are held 2^8 higher: without that a
+// weight below 2^-14 of the largest would lose bits.
+//
+// Bounds, and what was measured (GPU time on one GB300; a copy runs at 6.69 TB/s, a
+// large bf16 product at 1934 TFLOP/s, 1753 after seconds at the power limit):
+//   one new row for each of 64 requests of up to 16384 rows, 32 heads over 8: HBM;
+//     346-350 us for 2.31 GB, 6.6-6.7 TB/s.  4 of 131072, 128 heads over 8: 306-311
+//     us, 6.9-7.0 TB/s.  64 KB tiles, five 32 KB stages and equal shares of units
+//     are what that takes: any two of K, V and the next K are under way.
+//   4096 new rows of a prompt over 32768, 32 heads over 8: tensor cores; 1405-1420
+//     us, 1450-1467 TFLOP/s, at the power limit (1510 us in passes that go on for
+//     seconds).  A unit takes 1.8 us where its MMAs
+//     alone need 1.1: a warp's looks at barriers and the hand-over of P are what is
+//     left between them.  Head size 64 takes 1.6 us a unit for half the MMAs.
+//   short requests: an item costs some 3 us beside its copies (the chain of copy, S,
+//     softmax, P V, epilogue), a call some 8 before the first item and 4 more where
+//     a second kernel joins.  One row over 1023 rows takes 14 us, one for each of 256
+//     requests of 300 rows 75.
+// Measured and not taken: two softmax groups for each stream, half a tile each
+// (prompts -5%, drafts +7%, windows +11%); P handed over in halves (prompts +6%); a
+// third buffer for S at head size 64 (long requests -1%, windows +4%); short items
+// each on one stream (one-tile items -24%, drafts +2%, windows and prompts of 2000
+// +2%); one warp for both streams' MMAs (short requests +12%, windows -1%).
 #pragma once
 
 #include <cuda.h>
@@ -56,7 +83,7 @@ static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shar
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
 constexpr int kPaMaxRows = 2 * kPaTile;
 // Joining 16 rows of 19 pieces takes one CTA some 3 us, as long as a second
-// launch; 256 rows of 2 pieces took it 20 us, and the kernel 3.
+// launch; 256 rows of 2 pieces took it 20 us, and the kernel 3 to 4.
 constexpr int kPaJoinRows = 16;
 
 // A cut item as paged_join_kernel finds it; n = 0: none.
@@ -1066,7 +1093,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                 else weigh(x[q], q, [&](float2 v) { return fma2(v, sc, nb); }, ~0u);
                             }
                         } else {
-                            // scores that come near the cap: rare, and small code
+                            // scores that come near the cap: rare, and small code.  (Seven
+                            // chunks with a window: special functions throughout 60 us, the
+                            // polynomial 51.)
 #pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
                                 float x[32];

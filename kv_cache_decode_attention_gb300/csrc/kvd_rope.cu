@@ -10,6 +10,10 @@
 // and sin of its tokens once into shared memory and each thread keeps the
 // eight pairs of its place in the head in registers while it walks the heads,
 // so the trigonometry is paid once per (token, pair) and not per head.
+//
+// Measured: 8192 tokens of 40 bf16 heads of 128 30.5 us, 5.5 TB/s (a copy runs at
+// 6.7); an append of 7800 tokens, f32 in, f16 pages, 31.1 us, 5.8 TB/s; of 256
+// tokens 3.2 us and one token 2.8, where an empty launch takes 2.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -280,6 +284,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_part_kernel(const __grid_co
 }
 
 // Any other size, stride or alignment: one thread per pair or plain channel.
+// (8192 tokens of 40 heads of 128, 70 rotated channels: 120 us, rope_part_kernel 69;
+// 256 tokens: 8.7 and 4.8.)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeArgs a, int interleaved) {
     extern __shared__ float2 cs[];
@@ -340,12 +346,13 @@ cudaError_t launch_rope(const RopeArgs &a, bool aligned, int layout, cudaStream_
     }
     if (!vec) {
         const size_t smem = sizeof(float2) * size_t(a.pairs);
-        // positions are walked one CTA per token in launches of at most 2^30
         return launch_pdl(rope_any_kernel<TI, TO>, dim3(unsigned(a.n_tokens)), dim3(kRopeThreads), smem, st, a,
                           layout == KVD_ROPE_INTERLEAVED ? 1 : 0);
     }
     // Several tokens to a CTA amortise its prologue once there are CTAs enough
-    // for every SM twice over; fewer tokens than that spread wider.
+    // for every SM twice over; fewer tokens than that spread wider.  (8192 tokens of
+    // 40 heads: four to a CTA 30.4 us, one 41.3; 1500: four 6.1, one 7.3; 64: four
+    // 4.0, one 2.5.)
     const int lanes = kRopeThreads / a.n_tasks;
     int tok = a.n_tokens >= 152 * 2 * kMaxTok ? kMaxTok : a.n_tokens >= 152 * 4 ? 2 : 1;
     while (tok > lanes) tok >>= 1;
