@@ -506,6 +506,9 @@ KVD_API kvd_status rswa_device_error(const void *workspace, int32_t clear, uint3
  * whatever they are; rows that a request holds must be finite (a NaN or an
  * infinity in one may reach every new row of its request, those that do not
  * see it too, but no other request).  max_pages * page_size <= 2^31 - 1024.
+ * Tables may name a page several times to be read (a beginning that requests
+ * share); kv_paged_plan takes every page for its request's own, and gives it
+ * back with it.
  *
  * `err` is the device error word (uint32, caller-owned, zeroed once): bit 0 a
  * bounded wait gave up, bit 1 metadata out of range (the access is skipped),

@@ -321,6 +321,33 @@ def test_append_rotates_and_places_rows(env, given, pages, hd, rot, layout):
         assert bool(torch.isnan(t.transpose(1, 2).reshape(20 * page, -1)[~held.cuda()]).all())
 
 
+def test_append_in_place_captured_and_with_a_slot_twice(env):
+    torch, kvd = env
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache, other = kvd.PagedKvCache(8, 16, 2, 64, 2, 4), kvd.PagedKvCache(8, 16, 2, 64, 2, 4)
+    plan = kvd.paged_plan(cache, _i32(torch, [20, 9]), 33)
+    x = torch.randn(33, 10, 64, device="cuda", generator=g).bfloat16()
+    table = kvd.RopeTable(64, "half")
+    for c in (cache, other):
+        c.k.zero_()
+        c.v.zero_()
+    want = kvd.paged_append(cache, plan, x[:, 6:8], x[:, 8:], q=x[:, :6], rope=table)
+    y = x.clone()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        assert kvd.paged_append(other, plan, y[:, 6:8], y[:, 8:], q=y[:, :6], q_out=y[:, :6], rope=table).data_ptr() == y.data_ptr()
+    for _ in range(2):
+        y.copy_(x)
+        graph.replay()
+        assert torch.equal(y[:29, :6], want[:29]) and torch.equal(y[29:], x[29:]) and torch.equal(y[:, 6:], x[:, 6:])
+        assert torch.equal(other.k, cache.k) and torch.equal(other.v, cache.v)
+    twice = kvd.PagedPlan(None, None, positions=_i32(torch, [0, 1]), slots=_i32(torch, [5, 5]))
+    kvd.paged_append(other, twice, x[:2, 6:8], x[:2, 8:])
+    got = other.v.transpose(1, 2).reshape(-1, 2, 64)[5]
+    assert bool(((got == x[0, 8:]) | (got == x[1, 8:])).all())
+    assert other.device_error() == 0 and cache.device_error() == 0
+
+
 def test_append_skips_bad_slots(env):
     torch, kvd = env
     cache = kvd.PagedKvCache(2, 16, 2, 64, 1, 2)
@@ -485,6 +512,42 @@ def test_attention_of_many_requests(env):
     _run_attend(torch, kvd, lens, new, 1, 2, 64, 16, torch.bfloat16, 31, sample=set(range(0, 1100, 13)) | {0, 1, 1098, 1099})
     none = _run_attend(torch, kvd, [5, 7], [0, 0], 1, 2, 64, 16, torch.bfloat16, 31)
     assert none.shape[0] == 3
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_attention_of_mixed_batches(env, seed):
+    """Prompts, drafts, single tokens, requests without new rows and without rows, in any order and length: items of two query tiles and
+    of one, whole and cut, with and without a short last page, follow one another in a CTA."""
+    torch, kvd = env
+    r = np.random.default_rng(900 + seed)
+    hd, dt = (64, 128)[seed % 2], (torch.bfloat16, torch.float16)[seed // 2 % 2]
+    group, page, n_kv = int(r.choice([1, 2, 4, 8])), int(r.choice([16, 32, 64, 128])), int(r.choice([1, 3, 8]))
+    lens, new = [], []
+    for _ in range(int(r.integers(20, 120))):
+        kind = r.random()
+        n = 1 if kind < 0.4 else int(r.integers(2, 9)) if kind < 0.6 else int(r.integers(9, 400)) if kind < 0.85 else 0
+        past = int(r.integers(0, 300)) if r.random() < 0.6 else int(r.integers(0, 3000))
+        new.append(n)
+        lens.append(n + past)
+    sample = set(r.choice(len(lens), 25).tolist())
+    _run_attend(torch, kvd, lens, new, n_kv, group, hd, page, dt, 900 + seed, window=int(r.choice([0, 0, 200])), softcap=float(r.choice([0.0, 0.0, 20.0])),
+                sinks=bool(r.random() < 0.3), sample=sample)
+
+
+def test_requests_may_share_pages_and_rows_may_be_broadcast(env):
+    """A common beginning held once; one query row for all tokens or heads (strides of zero)."""
+    torch, kvd = env
+    cache, rows = _poisoned(torch, kvd, [700, 700], 2, 128, 32, torch.bfloat16, 5)
+    cache.block_table[1, :20] = cache.block_table[0, :20]  # rows 0 .. 639
+    k1, v1 = (torch.cat([a[:640], b[640:]]) for a, b in zip(rows[0], rows[1]))
+    q = torch.randn(1, 1, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).bfloat16()
+    plan = kvd.PagedPlan(_i32(torch, [0, 30, 60]), cache.seq_len)
+    for wide in (q.expand(60, 8, 128), q.expand(60, 1, 128).contiguous().expand(60, 8, 128), q.expand(1, 8, 128).contiguous().expand(60, 8, 128)):
+        out = kvd.paged_attention(wide, cache, plan)
+        assert out.is_contiguous() and torch.equal(out, kvd.paged_attention(wide.contiguous(), cache, plan))
+        for at, (k, v) in ((0, rows[0]), (30, (k1, v1))):
+            _check_attend(torch, out[at:at + 30], *_attend(torch, wide[at:at + 30], k, v, 700, 128 ** -0.5), torch.bfloat16, float(v.abs().max()))
+    assert cache.device_error() == 0
 
 
 @pytest.mark.parametrize("scale", [1e-6, 1.0, 20.0])
