@@ -504,11 +504,11 @@ struct PaIssue {
         }
         return at;
     }
-    // a tile of the other stream's
+    // A tile of the other stream's: let go of behind this one's own, so that stages
+    // become empty in the ring's order, which the loading warps count on.
     __device__ __forceinline__ bool skip() {
         if (!wait_stage()) return false;
-        const uint32_t at = take();
-        if (elect_one()) pa_arrive(&sh.kv_empty[at]);
+        tc_commit(&sh.kv_empty[take()]);
         return true;
     }
     // the stage after the next one
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
         }
         mbar_init(&sh.piece_done, 4);
         mbar_init(&sh.verdict, 1);
-        mbar_init(&sh.all_done, 8);
+        mbar_init(&sh.all_done, 14);  // every warp but 13 and 15
         fence_mbar_init();
         sh.stop = 0;
         sh.steps = 0;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 // fill that time.
                 PaIssue<HD, BF16> mma(sh, q_smem, kv_smem, tmem, stop);
                 const uint32_t d = uni(warp == 14 ? 1 : 0);
-                uint32_t items = 0, tails = 0, p_phase = 0, pairs = 0;
+                uint32_t items = 0, uses = 0, tails = 0, p_phase = 0, pairs = 0;  // uses: items with a tile for this stream
                 bool ok = true;
                 for (;;) {
                     ok = mma.wait(&sh.job_full[job_at % kPaJobs], job_at / kPaJobs & 1);
@@ -828,12 +828,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             is = pa_test3(&sh.kv_full[mma.stage], mma.phase, &sh.p_ready[d], p_phase, &sh.kv_full[mma.after()], mma.phase_after());
                             if ((is & 1) == 0) ok = mma.wait_stage();
                             if (ok && j == tail) {  // it ends short: cleared first
-                                if ((!dual || d == 0) && elect_one()) pa_arrive(&sh.tail_go[d]);
+                                if (elect_one()) pa_arrive(&sh.tail_go[d]);
                                 ok = mma.wait(&sh.tail_ready[d], tails++ & 1);
                             }
                             v = mma.take();
                             // before the first write to O the last item's must have been read
-                            if (ok && j < next && items > 0) ok = mma.wait(&sh.o_empty[d], (items - 1) & 1);
+                            if (ok && j < next && uses > 0) ok = mma.wait(&sh.o_empty[d], (uses - 1) & 1);
                             if (ok && (is & 2) == 0) ok = mma.wait(&sh.p_ready[d], p_phase);
                             // the streams of a dual item take turns: one that ran ahead would
                             // leave the other to end the item alone
@@ -858,11 +858,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             ++pairs;
                         }
                     }
-                    if (ok && !dual && n == 1 && d == 1) {  // no tile for this stream
-                        if (items > 0) ok = mma.wait(&sh.o_empty[1], (items - 1) & 1);
-                        if (ok && elect_one()) pa_arrive(&sh.q_empty);
-                    }
                     if (!ok) break;
+                    if (!dual && n == 1 && d == 1) {  // no tile for this stream
+                        if (elect_one()) pa_arrive(&sh.q_empty);
+                    } else {
+                        ++uses;
+                    }
                     ++items;
                 }
                 if (!ok) tc_commit(&sh.drain[d]);
@@ -882,8 +883,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     if (t >= 0) {
                         const int s = dual ? 0 : t & 1;
                         ok = pa_wait(&sh.tail_go[s], tails >> s & 1, stop);
+                        if (ok && dual) ok = pa_wait(&sh.tail_go[1], tails >> 1 & 1, stop);
                         if (!ok) break;
-                        tails ^= 1u << s;
+                        tails ^= dual ? 3u : 1u << s;
                         const uint32_t stage = (ring + uint32_t(dual ? 2 * t + 1 : t < n - 1 ? 2 * t + 2 : 2 * n - 1)) % S::kStages;
                         const int32_t row1 = ((row0 + (1 << a.page_log2) - 1) >> a.page_log2) << a.page_log2;
                         const uint32_t va = kv_smem + stage * S::kStageBytes + row0 * 128;
@@ -1195,8 +1197,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        // O1 first: the MMA warp takes O0 of a single item as a sign for both
-                        if (!dual) pa_arrive(&sh.o_empty[1]);
+                        if (two) pa_arrive(&sh.o_empty[1]);
                         pa_arrive(&sh.o_empty[d]);
                     }
                 }
@@ -1229,9 +1230,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 }
                 done_job();
             }
-            __syncwarp();
-            if (lane == 0) pa_arrive(&sh.all_done);
         }
+        // (13 goes on watching until every warp is here)
+        __syncwarp();
+        if (lane == 0 && warp != 13 && warp != 15) pa_arrive(&sh.all_done);
     }
     // ---- the end: nothing may still be in flight into this CTA's memory
     __syncwarp();

@@ -534,6 +534,45 @@ def test_attention_of_mixed_batches(env, seed):
                 sinks=bool(r.random() < 0.3), sample=sample)
 
 
+def test_attention_over_many_batches(env):
+    """Hundreds of drawn batches, each computed three times beside copies on another stream: the same bits, no wait that gave up, no row
+    left out, and one request of each against 64 bits."""
+    torch, kvd = env
+    r = np.random.default_rng(77)
+    side = torch.cuda.Stream()
+    src, dst = (torch.zeros(1 << 26, device="cuda", dtype=torch.uint8) for _ in range(2))
+    for i in range(400):
+        hd, page, dt = int(r.choice([64, 64, 128])), int(r.choice([16, 32, 64, 128])), (torch.bfloat16, torch.float16)[i % 2]
+        n_kv, group, n_seq = int(r.choice([1, 2, 8])), int(r.choice([1, 2, 4, 5, 8, 16])), int(2 ** r.uniform(0, 9))
+        kind, room = r.random(n_seq), 2 ** r.uniform(3, 12)
+        new = np.where(kind < 0.5, 1, np.where(kind < 0.7, r.integers(0, 9, n_seq), (2 ** r.uniform(3, 9, n_seq)).astype(int)))
+        lens = new + (r.random(n_seq) * room).astype(int)
+        has = -(-lens // page)
+        table = np.full((n_seq, has.max() + 1), -1, dtype=np.int32)
+        order, at = r.permutation(int(has.sum()) + 1).astype(np.int32), 0
+        for b in range(n_seq):
+            table[b, : has[b]] = order[at:at + has[b]]
+            at += has[b]
+        k, v = (torch.randn(len(order), n_kv, page, hd, device="cuda").to(dt) for _ in range(2))
+        cache = kvd.PagedKvCache.of(k, v, torch.from_numpy(table).cuda(), _i32(torch, lens.tolist()))
+        cu = np.concatenate([[0], np.cumsum(new)])
+        plan = kvd.PagedPlan(_i32(torch, cu.tolist()), cache.seq_len)
+        q = torch.randn(int(cu[-1]), n_kv * group, hd, device="cuda").to(dt)
+        window, cap = int(r.choice([0, 0, 100, 1000])), float(r.choice([0.0, 0.0, 20.0]))
+        outs = []
+        for _ in range(3):
+            with torch.cuda.stream(side):
+                dst.copy_(src)
+            outs.append(kvd.paged_attention(q, cache, plan, out=torch.full_like(q, float("nan")), window=window, softcap=cap))
+        assert cache.device_error() == 0, i
+        assert not bool(torch.isnan(outs[0]).any()) and all(torch.equal(outs[0], x) for x in outs), i
+        b = int(r.integers(n_seq))
+        if new[b] and new[b] * lens[b] * n_kv * group < 1 << 22:
+            kk, vv = (x[cache.block_table[b, : has[b]].long()].transpose(1, 2).reshape(-1, n_kv, hd)[: lens[b]] for x in (k, v))
+            part = slice(int(cu[b]), int(cu[b + 1]))
+            _check_attend(torch, outs[0][part], *_attend(torch, q[part], kk, vv, int(lens[b]), hd ** -0.5, window, cap), dt, float(vv.abs().max()))
+
+
 def test_requests_may_share_pages_and_rows_may_be_broadcast(env):
     """A common beginning held once; one query row for all tokens or heads (strides of zero)."""
     torch, kvd = env
