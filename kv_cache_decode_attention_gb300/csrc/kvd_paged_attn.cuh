@@ -827,7 +827,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         if (j >= 0) {
                             is = pa_test3(&sh.kv_full[mma.stage], mma.phase, &sh.p_ready[d], p_phase, &sh.kv_full[mma.after()], mma.phase_after());
                             if ((is & 1) == 0) ok = mma.wait_stage();
-                            if (ok && j == tail) {  // it ends short: cleared first
+                            // it ends short: cleared first.  (Of a dual item at stream 0's wish,
+                            // after whose turn stream 1's comes.)
+                            if (ok && j == tail && (!dual || d == 0)) {
                                 if (elect_one()) pa_arrive(&sh.tail_go[d]);
                                 ok = mma.wait(&sh.tail_ready[d], tails++ & 1);
                             }
@@ -883,9 +885,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     if (t >= 0) {
                         const int s = dual ? 0 : t & 1;
                         ok = pa_wait(&sh.tail_go[s], tails >> s & 1, stop);
-                        if (ok && dual) ok = pa_wait(&sh.tail_go[1], tails >> 1 & 1, stop);
                         if (!ok) break;
-                        tails ^= dual ? 3u : 1u << s;
+                        tails ^= 1u << s;
                         const uint32_t stage = (ring + uint32_t(dual ? 2 * t + 1 : t < n - 1 ? 2 * t + 2 : 2 * n - 1)) % S::kStages;
                         const int32_t row1 = ((row0 + (1 << a.page_log2) - 1) >> a.page_log2) << a.page_log2;
                         const uint32_t va = kv_smem + stage * S::kStageBytes + row0 * 128;
@@ -896,7 +897,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) pa_arrive(&sh.tail_ready[s]);
-                        if (lane == 0 && dual) pa_arrive(&sh.tail_ready[1]);
                     }
                     ring += 2 * n;
                 }
