@@ -57,12 +57,13 @@
 //   short requests: an item costs some 3 us beside its copies (the chain of copy, S,
 //     softmax, P V, epilogue), a call some 8 before the first item and 4 more where
 //     a second kernel joins.  One row over 1023 rows takes 14 us, one for each of 256
-//     requests of 300 rows 75.
+//     requests of 300 rows 73.
 // Measured and not taken: two softmax groups for each stream, half a tile each
 // (prompts -5%, drafts +7%, windows +11%); P handed over in halves (prompts +6%); a
 // third buffer for S at head size 64 (long requests -1%, windows +4%); short items
 // each on one stream (one-tile items -24%, drafts +2%, windows and prompts of 2000
-// +2%); one warp for both streams' MMAs (short requests +12%, windows -1%).
+// +2%); one warp for both streams' MMAs (300-row requests +16%, mixed prompts +3%,
+// windows -1%, 2000-row prompts at head size 64 -2%).
 #pragma once
 
 #include <cuda.h>
