@@ -626,7 +626,10 @@ KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q
  *              16-byte aligned with strides of multiples of 8 elements;
  *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0.
  * Scores, the softmax's maximum and sum and the output are accumulated in f32;
- * the weights are rounded once to dtype for the value product.  Rows of `out`
+ * the weights are rounded once to dtype for the value product.  Capped scores
+ * are right to 2^-19 of themselves, or to 2^-20 of the cap where scores beside
+ * them come to half of it; a cap that no score below 10^34 before scaling would
+ * feel (scale / softcap below the normal f32 numbers) is none.  Rows of `out`
  * behind cu_new[n_seq] are left as they were; a row whose position is negative
  * (n_b > L_b) sees nothing and becomes zeros.  Metadata out of range (a
  * negative or oversized length, rows past n_tokens, a page past n_pages) sets

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -77,6 +78,27 @@ bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads, bool out) {
         return entries <= 1 || (stride >= (out ? 8 : 0) && stride < lim && stride % 8 == 0);
     };
     return ok(tokens, r->token_stride) && ok(heads, r->head_stride);
+}
+
+// The capped score softcap tanh(y), y = score scale / softcap, in log2 units as a
+// polynomial of the raw score.  Masked scores of such a tile become -10^4 cap_near,
+// y = -5000, where the last term, softcap 0.017 y^9, leads by far and gives a
+// weight of zero.  That holds only where f32 has every coefficient to full
+// precision (one that fell to zero would leave the lead to one of the other sign)
+// and the cap itself is no speck; a call without goes through pa_tanh throughout.
+void set_cap(PaArgs *a, float scale, float softcap) {
+    const double log2e = 1.4426950408889634, k = double(scale) / softcap;
+    a->cap_in = float(2.0 * log2e * k);
+    a->cap_mul = float(scale * log2e);
+    bool whole = softcap >= 1e-20f;
+    double power = scale * log2e;
+    for (int i = 0; i < 4; ++i) {
+        const double c = kPaTanh[i] * (power *= k * k);
+        whole = whole && std::fabs(c) >= FLT_MIN && std::fabs(c) <= FLT_MAX;
+        a->cap_c[i] = whole ? float(c) : 0.0f;
+    }
+    a->cap_near = whole ? float(0.5 / k) : -1.0f;
+    a->cap_hidden = whole ? -1e4f * a->cap_near : -INFINITY;
 }
 
 }  // namespace
@@ -163,20 +185,12 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     a.n_pages = int32_t(n_pages);
     a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     a.pool_rows = int32_t(n_pages * page_size * n_kv);
-    a.scale_log2 = (softcap > 0.0f ? softcap : scale) * log2e;
-    if (softcap > 0.0f) {
-        a.cap_in = 2.0f * scale * log2e / softcap;
-        a.cap_mul = scale * log2e;
-        // tanh(y) / y in powers of y^2 up to |y| = 1/2, fitted to a relative error
-        // of 1.3e-8; the kernel has it in powers of the score s = y softcap / scale.
-        // (A scale so small that s^2 leaves the f32 range does without.)
-        const double k = double(scale) / softcap, fit[4] = {-0.3333306908607483, 0.13324779272079468, -0.05298607423901558,
-                                                            0.017135001718997955};
-        double power = double(scale) * log2e;
-        for (int i = 0; i < 4; ++i) a.cap_c[i] = float(fit[i] * (power *= k * k));
-        a.cap_near = k > 1e-15 ? float(0.5 / k) : -1.0f;
-    }
-    const cudaError_t e = head_dim == 64 ? launch_paged_attention_64(a, bf16, softcap > 0.0f, as_stream(stream))
-                                         : launch_paged_attention_128(a, bf16, softcap > 0.0f, as_stream(stream));
+    // A cap so far above the scale that their quotient is no normal number (a raw
+    // score would have to pass 10^34 to feel it) is none.
+    const bool cap = softcap > 0.0f && scale / softcap >= FLT_MIN;
+    a.scale_log2 = (cap ? softcap : scale) * log2e;
+    if (cap) set_cap(&a, scale, softcap);
+    const cudaError_t e = head_dim == 64 ? launch_paged_attention_64(a, bf16, cap, as_stream(stream))
+                                         : launch_paged_attention_128(a, bf16, cap, as_stream(stream));
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }

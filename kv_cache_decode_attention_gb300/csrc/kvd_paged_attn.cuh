@@ -112,7 +112,8 @@ struct PaArgs {
     float scale_log2;  // scale * log2 e (softcap 0), or softcap * log2 e
     float cap_in;      // softcap > 0: 2 * scale * log2 e / softcap
     float cap_mul;     // scale * log2 e: the polynomial's first coefficient
-    float cap_near;    // below it in size, a score's tanh is the polynomial
+    float cap_near;    // below it in size, a score's tanh is the polynomial (negative: never)
+    float cap_hidden;  // what a masked score becomes before it is capped
     float cap_c[4];    // its other coefficients, in powers of the score
 };
 
@@ -212,9 +213,19 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// tanh(y) / y in powers of y^2, fitted to a relative error of 1.3e-8 up to |y| = 1/2.
+constexpr double kPaTanh[4] = {-0.3333306908607483, 0.13324779272079468, -0.05298607423901558, 0.017135001718997955};
+
 // tanh(y) of x = 2 y log2 e, as 1 - 2 / (e^2y + 1): two special-function
 // instructions, right to some 2^-23 of 1.
 __device__ __forceinline__ float pa_tanh(float x) { return fmaf(rcp(ex2(x) + 1.0f), -2.0f, 1.0f); }
+// The same to some 2^-21 of the result: the polynomial where y is small.  (As all
+// scores are to a cap far out of reach, of which 2^-23 is more than they are.)
+__device__ __forceinline__ float pa_tanh_of_any(float x) {
+    const float y = x * 0.34657359027997264f, z = y * y;
+    const float p = fmaf(fmaf(fmaf(fmaf(float(kPaTanh[3]), z, float(kPaTanh[2])), z, float(kPaTanh[1])), z, float(kPaTanh[0])), z, 1.0f) * y;
+    return fabsf(y) < 0.5f ? p : pa_tanh(x);
+}
 // Two f32 operations in one issue slot.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -984,9 +995,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         // first pass: the maximum, 64 scores at a time; masked ones go
                         // back to TMEM as such, so that the second finds them.  Capping
                         // keeps the order, so it is left to the second pass; there a
-                        // masked score is one so low that its polynomial is lower still.
+                        // masked score is one so low that its polynomial is lower still
+                        // (and -infinity in a call that has no polynomial).
                         float m0 = -INFINITY, m1 = -INFINITY, low0 = INFINITY, low1 = INFINITY;
-                        const float hidden = CAP ? -1e4f * a.cap_near : -INFINITY;
+                        const float hidden = CAP ? a.cap_hidden : -INFINITY;
                         const int32_t hi_c = pos - key0, lo_c = lo - key0;
                         const bool edge = __any_sync(0xffffffffu, hi_c < kPaTile - 1 || lo_c > 0);
 #pragma unroll 1
@@ -1027,9 +1039,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         // out whatever lies there.)
                         bool near = false;  // all of the warp's scores are small beside the cap
                         if (CAP) {
-                            near = __all_sync(0xffffffffu, !valid || (top <= a.cap_near && fminf(low0, low1) >= -a.cap_near));
+                            near = a.cap_near > 0.0f && __all_sync(0xffffffffu, !valid || (top <= a.cap_near && fminf(low0, low1) >= -a.cap_near));
                             const bool some = hi_c >= 0 && lo_c < kPaTile && lo_c <= hi_c;
-                            top = some ? pa_tanh(top * a.cap_in) : -INFINITY;
+                            top = some ? pa_tanh_of_any(top * a.cap_in) : -INFINITY;
                         }
                         top = valid ? top * a.scale_log2 - kLift : -INFINITY;
                         // move the reference when a row grew past the slack
@@ -1097,17 +1109,22 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                             }
                         } else {
                             // scores that come near the cap: rare, and small code.  (Seven
-                            // chunks with a window: special functions throughout 60 us, the
-                            // polynomial 51.)
+                            // chunks with a window: special functions throughout 64 us, with
+                            // the care for small scores 72, the polynomial 51.)
 #pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
                                 float x[32];
                                 tc_ld32(t_s + q * 32, x);
                                 tc_wait_ld();
                                 const uint32_t seen = pa_seen(lo_c - q * 32, hi_c - q * 32);
-                                weigh(x, q, [&](float2 v) {
-                                    return fma2(make_float2(pa_tanh(v.x * a.cap_in), pa_tanh(v.y * a.cap_in)), sc, nb);
-                                }, seen);
+                                if (a.cap_near > 0.0f)
+                                    weigh(x, q, [&](float2 v) {
+                                        return fma2(make_float2(pa_tanh(v.x * a.cap_in), pa_tanh(v.y * a.cap_in)), sc, nb);
+                                    }, seen);
+                                else
+                                    weigh(x, q, [&](float2 v) {
+                                        return fma2(make_float2(pa_tanh_of_any(v.x * a.cap_in), pa_tanh_of_any(v.y * a.cap_in)), sc, nb);
+                                    }, seen);
                             }
                         }
                         sum2 = add2(sum2, acc);

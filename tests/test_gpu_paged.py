@@ -950,3 +950,49 @@ def test_lengths_past_31_bits_of_offsets(env):
     assert cache.device_error() == 0
     for a, e in ((0, 300), (300, 302)):
         _check_attend(torch, out[a:e], *_attend(torch, q[a:e], rows[a:e, :n_kv], rows[a:e, n_kv:], e - a, hd ** -0.5), torch.bfloat16, 6.0)
+
+
+# Caps far above the scores, where tanh(y) is y to the last bit; around them, where the coefficients of its polynomial in powers of the score
+# leave the f32 range one by one; and below the scores, where it saturates.
+CAPS = [(1e3, None), (1e4, None), (2e4, None), (5e4, None), (1e6, None), (1e10, None), (1e15, None), (1e30, None), (2e38, None), (30.0, 1e-4), (120.0, 1e-3),
+        (1.2e3, 1 / 128), (30.0, 9.0), (100.0, 9.0), (5.0, 2.0), (1e-3, 0.1), (1e-22, 1e-23), (1e20, 1e-19)]
+
+
+@pytest.mark.parametrize("softcap,scale", CAPS)
+@pytest.mark.parametrize("hd,dtype", [(64, "f16"), (128, "bf16")])
+def test_attention_with_a_cap_of_any_size(env, hd, dtype, softcap, scale):
+    """Single tokens, prompts and chunks, with and without a window.  tanh moves a score's error by no more than itself and adds, with
+    the products and sums in log2 units behind it, 2^-19 of the capped score (2^-21 of the special functions' form from |y| = 1/2 on,
+    2^-22 of the polynomial below, 2^-23 each of the argument, the product with the cap and the difference to the maximum)."""
+    torch, kvd = env
+    dt = _dt(torch, dtype)
+    scale = hd ** -0.5 if scale is None else scale
+    for window in (0, 100):
+        for lens, new in (([900, 1, 130, 2000, 64], [1, 1, 130, 300, 3]), ([77], [1])):
+            cache, rows = _poisoned(torch, kvd, lens, 2, hd, 16, dt, 81)
+            q = (torch.randn(sum(new), 8, hd, device="cuda", generator=torch.Generator(device="cuda").manual_seed(82)) * 1.5).to(dt)
+            plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+            out = kvd.paged_attention(q, cache, plan, scale=scale, window=window, softcap=softcap)
+            assert cache.device_error() == 0
+            at = 0
+            for (kk, vv), total, n in zip(rows, lens, new):
+                x = q[at:at + n]
+                # the definition without the cap's own slack, and that of the capped scores in its place
+                want, size, _ = _attend(torch, x, kk, vv, total, scale, window, softcap)
+                raw = torch.einsum("nhd,thd->hnt", x.double(), kk.repeat_interleave(4, 1).double()) * scale
+                moved = hd * 2.0 ** -24 * scale * torch.einsum("nhd,thd->hnt", x.double().abs(), kk.repeat_interleave(4, 1).double().abs())
+                slack = 2 * (moved + 2.0 ** -19 * (softcap * torch.tanh(raw / softcap)).abs()).amax(-1).T[..., None] + 2.0 ** -20
+                _check_attend(torch, out[at:at + n], want, size, slack, dt, float(vv.abs().max()))
+                at += n
+
+
+def test_attention_with_a_cap_below_the_scale_and_scores_of_zero(env):
+    """Coefficients past the f32 range: a score of zero stays one."""
+    torch, kvd = env
+    cache, rows = _poisoned(torch, kvd, [300, 40], 2, 64, 16, torch.bfloat16, 83)
+    plan = kvd.PagedPlan(_i32(torch, [0, 30, 31]), cache.seq_len)
+    q = torch.zeros(31, 4, 64, device="cuda", dtype=torch.bfloat16)
+    out = kvd.paged_attention(q, cache, plan, scale=1e10, softcap=1.0)
+    assert cache.device_error() == 0
+    for (a, e), (kk, vv) in zip(((0, 30), (30, 31)), rows):
+        _check_attend(torch, out[a:e], *_attend(torch, q[a:e], kk, vv, kk.shape[0], 1.0), torch.bfloat16, float(vv.abs().max()))
