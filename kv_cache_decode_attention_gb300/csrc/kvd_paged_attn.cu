@@ -176,7 +176,9 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     a.out_head = out->head_stride;
     a.sinks = sinks;
     a.err = err;
-    a.window = window;
+    // every position is below 2^31, so a window from there on hides nothing; as it
+    // stands it would leave the 64-bit range below a negative position
+    a.window = window < (int64_t(1) << 31) ? window : 0;
     a.n_seq = n_seq;
     a.n_tokens = int32_t(n_tokens);
     a.n_kv = n_kv;

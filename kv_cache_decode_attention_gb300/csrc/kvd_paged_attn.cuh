@@ -106,7 +106,7 @@ struct PaArgs {
     PaPiecesOf *cut;   // [kPaCtas]: the cut item that begins in each CTA
     int32_t join_here; // by the last finisher
     uint32_t *err;
-    int64_t window;    // 0 = none
+    int64_t window;    // below 2^31; 0 = none
     int32_t n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2;
     int32_t part_rows, pool_rows;
     float scale_log2;  // scale * log2 e (softcap 0), or softcap * log2 e

@@ -996,3 +996,11 @@ def test_attention_with_a_cap_below_the_scale_and_scores_of_zero(env):
     assert cache.device_error() == 0
     for (a, e), (kk, vv) in zip(((0, 30), (30, 31)), rows):
         _check_attend(torch, out[a:e], *_attend(torch, q[a:e], kk, vv, kk.shape[0], 1.0), torch.bfloat16, float(vv.abs().max()))
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+def test_a_window_wider_than_any_cache_is_none(env, window):
+    """Also where the first new rows stand before the start of their request."""
+    torch, kvd = env
+    lens, new = [3, 0, 130, 0, 700], [5, 2, 400, 1, 1]
+    assert torch.equal(*(_run_attend(torch, kvd, lens, new, 2, 4, 128, 16, torch.bfloat16, 91, window=w)[: sum(new)] for w in (window, 0)))
