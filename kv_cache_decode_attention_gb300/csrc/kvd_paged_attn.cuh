@@ -718,7 +718,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
     const PaStart st = sh.start;
-    uint32_t loaded = 0, parity = 0;  // loads: stages filled and their last parities, for the clean-up below
+    // copies asked for, for the clean-up below: bits of the stages (bit 16: Q) and the parities of their last ones
+    uint32_t loaded = 0, parity = 0;
 
     if (a.join_here == 0 && warp == 11 && lane == 0) a.cut[blockIdx.x].n = 0;
     if (st.units > 0) {
@@ -797,6 +798,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                                            q_row + i / S::kHalves * a.tile_tok, &sh.q_full);
                             }
                             __syncwarp();
+                            loaded |= 1u << 16;
+                            parity = (parity & ~(1u << 16)) | (items & 1) << 16;
                             ++items;
                         }
                     }
@@ -880,7 +883,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                     }
                     ++items;
                 }
-                if (!ok) tc_commit(&sh.drain[d]);
             } else if (warp == 10) {
                 // ------------------------------------------------------ ends of V
                 // Rows of a request's last page behind its last row hold nothing;
@@ -1253,18 +1255,27 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
         __syncwarp();
         if (lane == 0 && warp != 13 && warp != 15) pa_arrive(&sh.all_done);
     }
-    // ---- the end: nothing may still be in flight into this CTA's memory
-    __syncwarp();
-    if (*stop != 0) {
-        if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
-#pragma unroll 1
-        for (int i = 0; i < S::kStages; ++i)
-            if (loaded >> i & 1) mbar_wait_bounded(&sh.kv_full[i], parity >> i & 1, 500000000ull);
-        if (warp == 9 || warp == 14) mbar_wait_bounded(&sh.drain[warp == 9 ? 0 : 1], 0, 500000000ull);
-    }
     tc_before();
     __syncthreads();
     tc_after();
+    if (*stop != 0) {
+        // Given up, and every warp knows: nothing may still be in flight into this
+        // CTA's memory.  Of the copies each stage's last may be, and Q's last.  (Of
+        // the two loading warps' last ones for a stage the newer counts; the wait for
+        // the older may run out, its parity having come round again.)
+        if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
+        if (warp == 9 || warp == 14) {
+            uint64_t *drain = &sh.drain[warp == 9 ? 0 : 1];
+            tc_commit(drain);
+            mbar_wait_bounded(drain, 0, 500000000ull);
+        }
+#pragma unroll 1
+        for (int i = 0; i <= 16; ++i)
+            if (loaded >> i & 1) mbar_wait_bounded(i < 16 ? &sh.kv_full[i] : &sh.q_full, parity >> i & 1, 50000000ull);
+        tc_before();
+        __syncthreads();
+        tc_after();
+    }
     pdl_trigger();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }

@@ -291,3 +291,108 @@ def test_the_model_sees_a_mistake(mistake):
                 n = rng.choice([1, 1, 2, 3, 4, 5])
                 jobs.append({"n": n, "dual": rng.random() < 0.4, "tail": rng.choice([-1, n - 1, rng.randrange(n)])})
             Wrong(jobs, 5, rng).run()
+
+
+class Abandoned(Model):
+    """A run that is given up: every role goes on until it has to wait and leaves there, and then, with all of them at the kernel's end, the
+    copies and MMAs still under way are waited for.  mistake: what that end forgets."""
+
+    mistake = None
+
+    def __init__(self, *args):
+        super().__init__(*args)
+        self.kv_loads, self.q_loads, self.left_early = [0] * self.stages, 0, set()
+
+    def loader(self, is_v):
+        role = super().loader(is_v)
+        list_of, q_of = self.later["V" if is_v else "K"], self.later["Q"]
+        seen, seen_q = 0, 0
+
+        class Counted(list):  # what the loading warps note as they ask for a copy
+            def append(inner, event):
+                stage, at = event.__defaults__
+                self.kv_loads[stage] = at // self.stages + 1
+                list.append(inner, event)
+
+        class CountedQ(list):
+            def append(inner, event):
+                self.q_loads += 1
+                list.append(inner, event)
+
+        if not isinstance(list_of, Counted):
+            self.later["V" if is_v else "K"] = Counted(list_of)
+        if not is_v and not isinstance(q_of, CountedQ):
+            self.later["Q"] = CountedQ(q_of)
+        return role
+
+    def happen(self, name):
+        events = self.later[name]
+        events.pop(0 if name.startswith("MMA") else self.rng.randrange(len(events)))()
+
+    def run(self, moves):
+        roles = {"scheduler": self.scheduler(), "K": self.loader(False), "V": self.loader(True), "MMA0": self.mma(0), "MMA1": self.mma(1),
+                 "ends": self.ends_of_v(), "soft0": self.softmax(0), "soft1": self.softmax(1)}
+        waits = dict.fromkeys(roles)
+
+        def move(k):
+            try:
+                waits[k] = next(roles[k])
+            except StopIteration:
+                del roles[k]
+
+        able = lambda: [k for k in roles if waits[k] is None or waits[k][0].over(waits[k][1])]  # noqa: E731
+        for _ in range(moves):
+            choice = able() + ["later " + k for k, events in self.later.items() if events]
+            if not choice:
+                break
+            k = self.rng.choice(choice)
+            self.happen(k[6:]) if k.startswith("later ") else move(k)
+        self.left_early = {"K", "V"} - set(roles)
+        while True:  # given up
+            k = self.rng.choice(able() or [None])
+            if k is None:
+                break
+            move(k)
+
+        def wait_for(bar, phases, names):
+            while bar.done < phases:
+                names = [n for n in names if self.later[n]]
+                assert names, "the end waits for a copy that nobody asked for"
+                self.happen(self.rng.choice(names))
+
+        wait_for_mmas = [n for n in ("MMA0", "MMA1") if self.mistake != "mmas"]
+        for n in wait_for_mmas:
+            while self.later[n]:
+                self.happen(n)
+        if not (self.mistake == "loads done" and self.left_early):
+            for stage, n in enumerate(self.kv_loads):
+                wait_for(self.kv_full[stage], n, ["K", "V"])
+        if self.mistake != "q":
+            wait_for(self.q_full, self.q_loads, ["Q"])
+        assert not any(self.later.values()), "still under way at the end: %s" % {k: len(v) for k, v in self.later.items() if v}
+
+
+def _drawn_jobs(rng, most):
+    jobs = []
+    for _ in range(rng.randint(1, most)):
+        n = rng.choice([1, 1, 2, 3, 4, 5, 9])
+        jobs.append({"n": n, "dual": rng.random() < 0.4, "tail": rng.choice([-1, n - 1, rng.randrange(n)])})
+    return jobs
+
+
+@pytest.mark.parametrize("stages", [5, 10])
+def test_nothing_is_under_way_when_a_run_is_given_up(stages):
+    for seed in range(600):
+        rng = random.Random(seed)
+        Abandoned(_drawn_jobs(rng, 12), stages, rng).run(int(2 ** rng.uniform(0, 10)))
+
+
+@pytest.mark.parametrize("mistake", ["q", "mmas", "loads done"])
+def test_the_model_sees_what_an_end_forgets(mistake):
+    """Q's copy; MMAs; the copies of a loading warp that was through when the run was given up."""
+    with pytest.raises(AssertionError, match="still under way"):
+        for seed in range(600):
+            rng = random.Random(seed)
+            run = Abandoned(_drawn_jobs(rng, 3), 10, rng)
+            run.mistake = mistake
+            run.run(int(2 ** rng.uniform(0, 10)))
