@@ -643,6 +643,14 @@ KVD_API kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64
                                    float softcap, const float *sinks, void *workspace,
                                    int64_t workspace_bytes, uint32_t *err, void *stream);
 
+/* The bounded waits of paged_attention, run on purpose (for tests).  While armed
+ * with 0 <= cta < 152, that thread block of every launch gives up after_ns (0 ..
+ * 10^9) nanoseconds after it began, if it is not done by then: as after the two
+ * seconds without a step that it has otherwise, every wait of the block ends, bit 0
+ * of the error word is set, the rows it had to do are undefined, and the kernel
+ * exits normally.  cta < 0 disarms.  Process-wide. */
+KVD_API kvd_status kvd_test_give_up(int32_t cta, int64_t after_ns);
+
 /* The device error word of the paged calls (see kvd_layer_device_error). */
 KVD_API kvd_status kv_paged_device_error(uint32_t *err, int32_t clear, uint32_t *word_out);
 

@@ -114,6 +114,7 @@ _SIGS = {
     "paged_attention_workspace_bytes": [_i64, _i32, _i32, _i32, _P(_i64)],
     "paged_attention": [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i32, _vp,
                         _vp, _i32, _f32, _i64, _f32, _vp, _vp, _i64, _vp, _vp],
+    "kvd_test_give_up": [_i32, _i64],
     "kv_paged_device_error": [_vp, _i32, _P(C.c_uint32)],
     "kvd_status_string": [_i32],
 }

@@ -18,6 +18,8 @@ cudaError_t launch_paged_attention_128(const PaArgs &a, bool bf16, bool cap, cud
 
 namespace {
 
+std::atomic<int64_t> g_give_up{-1};  // kvd_test_give_up: CTA << 32 | ns
+
 // The driver's encoder, looked up once; nullptr if it is missing.
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -162,6 +164,9 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     char *w = static_cast<char *>(workspace);
     a.cut = reinterpret_cast<PaPiecesOf *>(w + ws.cut);
     a.join_here = n_tokens * group <= kPaJoinRows ? 1 : 0;
+    const int64_t armed = g_give_up.load(std::memory_order_relaxed);
+    a.give_up = armed < 0 ? -1 : int32_t(armed >> 32);
+    a.give_up_ns = uint32_t(armed);
     a.tickets = reinterpret_cast<uint64_t *>(w + ws.tickets);
     static std::atomic<uint64_t> launches{0x9e3779b97f4a7cull};  // any start will do; 2^56 launches wrap
     a.nonce = launches.fetch_add(1, std::memory_order_relaxed) & ((uint64_t(1) << 56) - 1);
@@ -195,4 +200,10 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     const cudaError_t e = head_dim == 64 ? launch_paged_attention_64(a, bf16, cap, as_stream(stream))
                                          : launch_paged_attention_128(a, bf16, cap, as_stream(stream));
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
+}
+
+extern "C" kvd_status kvd_test_give_up(int32_t cta, int64_t after_ns) {
+    if (cta >= kPaCtas || after_ns < 0 || after_ns > 1000000000) return KVD_EINVAL;
+    g_give_up.store(cta < 0 ? -1 : int64_t(cta) << 32 | after_ns);
+    return KVD_OK;
 }

@@ -105,6 +105,8 @@ struct PaArgs {
     uint64_t nonce;    // of the launch, below 2^56
     PaPiecesOf *cut;   // [kPaCtas]: the cut item that begins in each CTA
     int32_t join_here; // by the last finisher
+    int32_t give_up;   // for tests: the CTA whose watch gives up so many ns after it began, or -1
+    uint32_t give_up_ns;
     uint32_t *err;
     int64_t window;    // below 2^31; 0 = none
     int32_t n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2;
@@ -119,8 +121,9 @@ struct PaArgs {
 
 // A ticket that carries another nonce counts as zero, so the workspace needs no
 // initialisation; whoever joins the pieces sets it to 0 for a graph's next
-// replay, which comes with the same nonce.  A piece of CTA c is kept in slot
-// 2 c + 1 if it begins its item, else in slot 2 c.
+// replay, which comes with the same nonce.  (So every piece has its ticket taken,
+// those of a CTA that gave up too.)  A piece of CTA c is kept in slot 2 c + 1 if it
+// begins its item, else in slot 2 c.
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -469,6 +472,7 @@ struct PaShared {
     int64_t warp_sums[kPaThreads / 32];
     uint32_t tmem;
     int join;         // the verdict: this CTA joins the pieces
+    int tickets;      // that the CTA has taken
     int stop, steps;  // the watch: give up; changes with every K tile that is loaded
     float2 ml[2][kPaTile];  // stream 1's maximum and sum of a single item, by item parity
 };
@@ -601,6 +605,24 @@ static __device__ __noinline__ bool pa_ticket(uint64_t *word, uint64_t nonce, in
     return int32_t(now & 255u) == n;
 }
 
+// Take the tickets that a CTA that gave up still owes, all but its first `taken`:
+// nobody joins for it (the error word tells), but the words come to their 0.
+static __device__ __noinline__ void pa_owed_tickets(const PaArgs &a, const PaStart &st, int32_t taken) {
+    PaWalk w = {st.b, st.h, st.tok, st.s};
+    int32_t unit = st.unit;
+    for (int64_t left = st.units; left > 0;) {
+        const PaItem it = pa_item(a, w.s, w.tok);
+        const PaPart pt = pa_part(it, unit, left);
+        if (!(pt.head && pt.tail) && --taken < 0) {
+            const PaPieces pieces(st.from + (st.units - left) - unit, it.units, st.total);
+            pa_ticket(a.tickets + pieces.first, a.nonce, pieces.n, 0);
+        }
+        left -= it.units - unit;
+        unit = 0;
+        if (left > 0) pa_next(a, w);
+    }
+}
+
 // Row r of a cut item from its pieces, by a warp whose lanes stand for columns,
 // four pieces under way at a time.
 template <int HD, bool BF16>
@@ -701,6 +723,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
         fence_mbar_init();
         sh.stop = 0;
         sh.steps = 0;
+        sh.tickets = 0;
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
@@ -919,12 +942,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 volatile int *steps = &sh.steps;
                 int last = 0;
                 uint64_t since = global_ns();
+                const uint64_t end = a.give_up == int32_t(blockIdx.x) ? since + a.give_up_ns : ~0ull;
                 while (!mbar_try_wait(&sh.all_done, 0)) {
                     const uint64_t now = global_ns();
                     if (*steps != last) {
                         last = *steps;
                         since = now;
-                    } else if (now - since > 2000000000ull) {
+                    }
+                    if (now - since > 2000000000ull || now >= end) {
                         *stop = 1;
                         break;
                     }
@@ -1237,6 +1262,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                         if (!ok) break;
                         if (lane == 0) {
                             sh.join = pa_ticket(word, a.nonce, pieces.n, old) ? 1 : 0;
+                            sh.tickets = int(cuts) + 1;
                             pa_arrive(&sh.verdict);
                         }
                     }
@@ -1250,6 +1276,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 }
                 done_job();
             }
+            if (!ok && a.join_here != 0 && threadIdx.x == 0) pa_owed_tickets(a, sh.start, sh.tickets);
         }
         // (13 goes on watching until every warp is here)
         __syncwarp();
@@ -1271,7 +1298,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
         }
 #pragma unroll 1
         for (int i = 0; i <= 16; ++i)
-            if (loaded >> i & 1) mbar_wait_bounded(i < 16 ? &sh.kv_full[i] : &sh.q_full, parity >> i & 1, 50000000ull);
+            if (loaded >> i & 1) mbar_wait_bounded(i < 16 ? &sh.kv_full[i] : &sh.q_full, parity >> i & 1, 5000000ull);
         tc_before();
         __syncthreads();
         tc_after();

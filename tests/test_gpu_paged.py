@@ -1004,3 +1004,41 @@ def test_a_window_wider_than_any_cache_is_none(env, window):
     torch, kvd = env
     lens, new = [3, 0, 130, 0, 700], [5, 2, 400, 1, 1]
     assert torch.equal(*(_run_attend(torch, kvd, lens, new, 2, 4, 128, 16, torch.bfloat16, 91, window=w)[: sum(new)] for w in (window, 0)))
+
+
+@pytest.mark.parametrize("lens,new", [([9000], [1]), ([60000, 300], [1, 1]), ([20, 30000, 5], [1, 2, 1]), ([2500, 900], [300, 100])])
+def test_a_launch_given_up_leaves_no_trace(env, lens, new):
+    """One CTA's waits end early, at one moment or another: the error bit, every ticket of the workspace back at zero, and the next calls and
+    replays right.  A graph's replays all come with the same tickets."""
+    torch, kvd = env
+    from kv_cache_decode_attention_gb300 import _abi
+
+    cache, _ = _poisoned(torch, kvd, lens, 2, 128, 16, torch.bfloat16, 3)
+    q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).bfloat16()
+    plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+    ws = torch.zeros(kvd.paged_attention_workspace(sum(new), 8, 2, 128), dtype=torch.uint8, device="cuda")
+    counts = ws[: 152 * 8].view(torch.int64)
+    want, out = kvd.paged_attention(q, cache, plan, workspace=ws), torch.empty_like(q)
+    assert cache.device_error() == 0
+    gave_up = 0
+    try:
+        for cta in (0, 37, 75, 76, 151):
+            for after in (0, 2000, 5000, 9000):
+                assert _abi.lib().kvd_test_give_up(cta, after) == 0
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    kvd.paged_attention(q, cache, plan, out=out, workspace=ws)
+                _abi.lib().kvd_test_give_up(-1, 0)
+                for _ in range(4):
+                    out.fill_(float("nan"))
+                    graph.replay()
+                    error = cache.device_error()
+                    assert error in (0, 1)
+                    gave_up += error
+                    assert not bool((counts & 255).any()), (cta, after)
+                    assert error == 1 or torch.equal(out, want)
+                assert torch.equal(kvd.paged_attention(q, cache, plan, out=out, workspace=ws), want) and cache.device_error() == 0
+    finally:
+        _abi.lib().kvd_test_give_up(-1, 0)
+    assert gave_up >= 4

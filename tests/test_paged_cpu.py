@@ -175,3 +175,10 @@ def test_calls_without_rows_do_nothing(abi):
     assert L.kvd_rope_apply(C.byref(R), null(), null(), 8, None, None, 0, 128, 2, None, 0, None) == abi.OK
     assert L.kv_paged_append(C.byref(R), null(), null(), 8, null(), null(), 8, 128, 0, 2, None, None, 0, FAKE, FAKE, 64, 16, FAKE, None) == abi.OK
     assert L.paged_attention(null(), null(), 0, 8, 8, 128, 2, FAKE, FAKE, 64, 16, FAKE, 8, FAKE, FAKE, 4, 0.1, 0, 0.0, None, None, 0, FAKE, None) == abi.OK
+
+
+def test_give_up_refusals(abi):
+    L = abi.lib()
+    assert L.kvd_test_give_up(-1, 0) == abi.OK
+    for bad in ((152, 0), (0, -1), (0, 10 ** 9 + 1)):
+        assert L.kvd_test_give_up(*bad) == abi.EINVAL, bad
