@@ -4,6 +4,9 @@ One step of a server is ``paged_plan`` (pages, slots and positions of the new
 rows, from request lengths on the device), then per layer ``paged_append``
 (rotate q and k, write k and v to their slots) and ``paged_attention``.  Nothing
 is read back, so a step can be captured into a CUDA graph and replayed.
+A call goes to the current stream, or to `stream`, where what it returns is to be
+had.  What it reads has to be there on that stream, and to stay until it is read
+(Tensor.record_stream), as with any stream of torch's.
 ``rope`` alone rotates rows for the contiguous caches (``kv_append``,
 ``rswa_ring_write`` and ``rswa_record_prefill`` take rotated rows).
 
@@ -45,6 +48,20 @@ def _stream(index, stream):
     if stream is not None:
         return stream.cuda_stream
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _empty(sizes, dtype, device, index, stream):
+    """New tensors for a call on `stream`.  They come from that stream's memory (a
+    block that another stream has just let go of may still be read there) and stay
+    from reuse until what the caller's stream does with them is over."""
+    if stream.cuda_stream == _stream(index, None):
+        return [torch.empty(size, dtype=dtype, device=device) for size in sizes]
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        made = [torch.empty(size, dtype=dtype, device=device) for size in sizes]
+    for t in made:
+        t.record_stream(caller)
+    return made
 
 
 def _i32(t, name, numel, device):
@@ -125,9 +142,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor
         n_q = q.shape[1]
         qi = _rows(q, "q", (tokens, n_q, hd), dev)
         if q_out is None:
-            q_out = torch.empty_like(q)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = torch.empty_like(q) if stream is None else _empty([q.shape], dtype, dev, index, stream)[0]
         elif q_out.dtype is not dtype:
             raise ValueError("q_out must have q's dtype")
         qo = _rows(q_out, "q_out", (tokens, n_q, hd), dev)
@@ -139,9 +154,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor
         n_k = k.shape[1]
         ki = _rows(k, "k", (tokens, n_k, hd), dev)
         if k_out is None:
-            k_out = torch.empty_like(k)
-            if stream is not None:
-                k_out.record_stream(stream)
+            k_out = torch.empty_like(k) if stream is None else _empty([k.shape], dtype, dev, index, stream)[0]
         elif k_out.dtype is not dtype:
             raise ValueError("k_out must have k's dtype")
         ko = _rows(k_out, "k_out", (tokens, n_k, hd), dev)
@@ -270,13 +283,13 @@ def paged_plan(cache: PagedKvCache, new_len: torch.Tensor, n_tokens: int, keep_l
     if plan is None:
         if n_tokens < 0:
             raise ValueError("n_tokens must not be negative")
-        empty = torch.empty
-        plan = PagedPlan(empty(n + 1, dtype=_I32, device=dev), cache.seq_len if advance else empty(n, dtype=_I32, device=dev),
-                         cache.n_free if advance else empty(1, dtype=_I32, device=dev),
-                         empty(n_tokens, dtype=_I32, device=dev), empty(n_tokens, dtype=_I32, device=dev))
-        if stream is not None:
-            for t in (plan.cu_new, plan.seq_len, plan.n_free, plan.positions, plan.slots):
-                t.record_stream(stream)
+        sizes = (n + 1, n_tokens, n_tokens) if advance else (n + 1, n_tokens, n_tokens, n, 1)
+        made = [torch.empty(size, dtype=_I32, device=dev) for size in sizes] if stream is None else _empty(sizes, _I32, dev, index, stream)
+        lens, height = (cache.seq_len, cache.n_free) if advance else made[3:]
+        plan = PagedPlan(made[0], lens, height, made[1], made[2])
+        if stream is not None and advance:
+            lens.record_stream(stream)
+            height.record_stream(stream)
         cu, pos, slots = plan.cu_new.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr()
     else:
         cu = _i32(plan.cu_new, "plan.cu_new", n + 1, dev)
@@ -329,9 +342,7 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
         shape = (tokens, n_q, hd)
         qi = _rows(q, "q", shape, dev)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=cache.dtype, device=dev)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = torch.empty(shape, dtype=cache.dtype, device=dev) if stream is None else _empty([shape], cache.dtype, dev, index, stream)[0]
         elif q_out.dtype is not cache.dtype:
             raise ValueError("q_out must have the pages' dtype")
         qo = _rows(q_out, "q_out", shape, dev)
@@ -380,9 +391,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
         sinks = sinks.data_ptr()
     qi = _rows(q, "q", shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-        if stream is not None:
-            out.record_stream(stream)
+        out = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty([shape], dtype, dev, index, stream)[0]
     elif out.dtype is not dtype:
         raise ValueError("out must have q's dtype")
     oi = _rows(out, "out", shape, dev)
@@ -393,9 +402,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
         if _take is not None and _give is not None:
             ws = taken = _take(size, on)
         else:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if stream is None else _empty([size], torch.uint8, dev, index, stream)[0]
             ws = workspace.data_ptr()
     else:
         size = workspace.numel() * workspace.element_size()

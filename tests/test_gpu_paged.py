@@ -1042,3 +1042,53 @@ def test_a_launch_given_up_leaves_no_trace(env, lens, new):
     finally:
         _abi.lib().kvd_test_give_up(-1, 0)
     assert gave_up >= 4
+
+
+def test_outputs_made_for_another_stream_are_its_own(env):
+    """With stream= and no outputs given, a call's new outputs are not taken from memory that the current stream has just let go of and is
+    still reading; and what the current stream does with them holds them, though it has dropped them."""
+    torch, kvd = env
+    side, tokens = torch.cuda.Stream(), 1 << 15
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = kvd.PagedKvCache(tokens // 16, 16, 1, 64, 1, tokens // 16)
+    x = torch.randn(tokens, 2, 64, device="cuda", generator=g).bfloat16()
+    q, k, new = x, x[:, :1], _i32(torch, [tokens])
+    table, pos = kvd.RopeTable(64), torch.arange(tokens, device="cuda", dtype=torch.int32)
+    plan = kvd.paged_plan(cache, new, tokens)
+    kvd.paged_append(cache, plan, k, k)
+    empty = kvd.PagedPlan(plan.cu_new.zero_(), plan.seq_len)  # an attention of no rows writes nothing
+    other = kvd.PagedKvCache(tokens // 16, 16, 1, 64, 1, tokens // 16)
+    calls = [("rope", lambda: list(kvd.rope(q, k, pos, table, stream=side))),
+             ("plan", lambda: [getattr(kvd.paged_plan(other, new, tokens, advance=False, stream=side), n) for n in ("positions", "slots")]),
+             ("append", lambda: [kvd.paged_append(cache, plan, k, k, q=q, stream=side)]),
+             ("attention", lambda: [kvd.paged_attention(q, cache, empty, stream=side)])]
+    torch.cuda.synchronize()
+    for name, call in calls:
+        for _ in range(2):
+            outs = call()
+            torch.cuda.synchronize()
+            like = [torch.empty_like(o, memory_format=torch.contiguous_format).fill_(7) for o in outs]
+            shapes = [(o.shape, o.dtype) for o in like]
+            del outs
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)
+            copies = [t.clone() for t in like]
+            held = {t.data_ptr() for t in like}
+            del like
+            outs = call()
+            assert not held & {o.data_ptr() for o in outs}, name
+            again = [torch.empty(s, dtype=d, device="cuda") for s, d in shapes]
+            assert held & {o.data_ptr() for o in again}, name  # the test would see it
+            torch.cuda.synchronize()
+            assert all(bool((c == 7).all()) for c in copies), name
+            # the caller's work on them, queued behind a wait, outlives its hold on them
+            torch.cuda._sleep(20_000_000)
+            seen = [o.clone() for o in outs]
+            want = [o.data_ptr() for o in outs]
+            del outs
+            with torch.cuda.stream(side):
+                late = [torch.empty(s, dtype=d, device="cuda") for s, d in shapes]
+            assert not set(want) & {o.data_ptr() for o in late}, name
+            torch.cuda.synchronize()
+            del again, late, copies, seen
+    assert cache.device_error() == 0 and other.device_error() == 0
