@@ -38,6 +38,21 @@ def _stream(stream=None) -> C.c_void_p:
     return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _empty(sizes, dtype, device, stream) -> list:
+    """New tensors for a call on `stream` (None: the current one).  They come from
+    that stream's memory (a block that another stream has just let go of may still
+    be read there) and stay from reuse until what the caller's stream does with
+    them is over."""
+    if stream is None or stream.cuda_stream == _stream().value:
+        return [torch.empty(size, dtype=dtype, device=device) for size in sizes]
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        made = [torch.empty(size, dtype=dtype, device=device) for size in sizes]
+    for t in made:
+        t.record_stream(caller)
+    return made
+
+
 def _ptr(t: torch.Tensor | None) -> C.c_void_p | None:
     if t is None:
         return None
@@ -76,8 +91,8 @@ class LayerKvCache:
                   _np_ptr(cap), _np_ptr(self.alive), _np_ptr(sizes), C.byref(host_bytes))
         self.buf_bytes = sizes
         self.device = torch.device(device)
-        self.bufs = [torch.empty(int(n), dtype=torch.uint8, device=self.device) if n > 0 else None
-                     for n in sizes]
+        bufs = iter(_empty([int(n) for n in sizes if n > 0], torch.uint8, self.device, stream))
+        self.bufs = [next(bufs) if n > 0 else None for n in sizes]
         self._ptrs = (C.c_void_p * _abi.BUF_COUNT)(
             *[b.data_ptr() if b is not None else None for b in self.bufs])
         self._host = np.zeros(int(host_bytes.value) + 64, np.uint8)
@@ -131,7 +146,7 @@ class LayerKvCache:
         synchronising)."""
         n = C.c_int64(0)
         _abi.call("kvd_bounds_selftest_bytes", C.byref(self.L), C.byref(n))
-        scratch = torch.empty(int(n.value), dtype=torch.uint8, device=self.device)
+        scratch, = _empty([int(n.value)], torch.uint8, self.device, stream)
         _abi.call("kvd_bounds_selftest", C.byref(self.L), _ptr(scratch), int(scratch.numel()), _stream(stream))
         return scratch  # keep it alive until the launches have run
 
@@ -207,7 +222,7 @@ def decode_attention_verify(q: torch.Tensor, cache: LayerKvCache, K: int, out: t
     if n_q * cache.n_seq * K * cache.head_dim != q.numel():
         raise ValueError("q must be [n_seq, K, n_q, head_dim]")
     if out is None:
-        out = torch.empty(cache.n_seq, K, n_q, cache.head_dim, device=q.device)
+        out, = _empty([(cache.n_seq, K, n_q, cache.head_dim)], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
@@ -218,7 +233,7 @@ def decode_attention_verify(q: torch.Tensor, cache: LayerKvCache, K: int, out: t
     if workspace is None:
         n = C.c_int64(0)
         _abi.call("kvd_verify_workspace_bytes", C.byref(cache.L), int(n_q), int(K), C.byref(n))
-        workspace = torch.empty(max(int(n.value), 256), dtype=torch.uint8, device=q.device)
+        workspace, = _empty([max(int(n.value), 256)], torch.uint8, q.device, stream)
     _abi.call("decode_attention_verify", _ptr(q), C.byref(cache.L), int(n_q), int(K), C.c_float(scale),
               int(window), C.c_float(softcap), _ptr(sinks), _ptr(out), _ptr(workspace),
               int(workspace.numel()), _stream(stream))
@@ -251,7 +266,7 @@ def kv_evict_born(layer: LayerKvCache, imp: torch.Tensor, keep_last: int, sink: 
     n = C.c_int64(0)
     _abi.call("kv_evict_workspace_bytes", C.byref(layer.L), int(keep_last), C.byref(n))
     if workspace is None:
-        workspace = torch.empty(max(int(n.value), 256), dtype=torch.uint8, device=imp.device)
+        workspace, = _empty([max(int(n.value), 256)], torch.uint8, imp.device, stream)
     _abi.call("kv_evict_born", C.byref(layer.L), _ptr(imp), int(keep_last), int(sink), int(recent),
               _ptr(workspace), int(workspace.numel()), _stream(stream))
 
@@ -270,7 +285,7 @@ def decode_attention(q: torch.Tensor, cache: LayerKvCache, out: torch.Tensor | N
     if q.numel() != cache.n_seq * n_q * cache.head_dim:
         raise ValueError("q must be [n_seq, n_q, head_dim]")
     if out is None:
-        out = torch.empty_like(q)
+        out, = _empty([q.shape], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if imp is not None:
         _f32_cuda(imp, "imp")
@@ -278,7 +293,7 @@ def decode_attention(q: torch.Tensor, cache: LayerKvCache, out: torch.Tensor | N
             raise ValueError("imp must hold %d floats" % cache.imp_len)
     need = cache.workspace_bytes(n_q, imp is not None)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace, = _empty([need], torch.uint8, q.device, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
     if window or softcap or sinks is not None:
@@ -307,7 +322,7 @@ def decode_attention_static(q: torch.Tensor, cache: LayerKvCache, out: torch.Ten
     if q.numel() != cache.n_seq * n_q * cache.head_dim:
         raise ValueError("q must be [n_seq, n_q, head_dim]")
     if out is None:
-        out = torch.empty_like(q)
+        out, = _empty([q.shape], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
@@ -420,7 +435,7 @@ def rswa_decode(q: torch.Tensor, cache: RingCache, out: torch.Tensor | None = No
     if q.numel() != cache.B * cache.H * cache.head_dim:
         raise ValueError("q must be [B, H, head_dim]")
     if out is None:
-        out = torch.empty(cache.B, cache.H * cache.head_dim, device=q.device)
+        out, = _empty([(cache.B, cache.H * cache.head_dim)], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
@@ -442,7 +457,7 @@ def rswa_decode_i8(q: torch.Tensor, cache: RingCache, out: torch.Tensor | None =
     if q.numel() != cache.B * cache.H * cache.head_dim:
         raise ValueError("q must be [B, H, head_dim]")
     if out is None:
-        out = torch.empty(cache.B, cache.H * cache.head_dim, device=q.device)
+        out, = _empty([(cache.B, cache.H * cache.head_dim)], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
@@ -468,14 +483,14 @@ def rswa_verify(q: torch.Tensor, draft_k: torch.Tensor, draft_v: torch.Tensor, c
     if int8 and cache.mirror is None:
         raise ValueError("int8 verify needs a RingCache built with int8=True")
     if out is None:
-        out = torch.empty(cache.B, K, cache.H * cache.head_dim, device=q.device)
+        out, = _empty([(cache.B, K, cache.H * cache.head_dim)], torch.float32, q.device, stream)
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
     n = C.c_int64(0)
     _abi.call("rswa_verify_workspace_bytes", cache.B, cache.H, cache.head_dim, cache.ref_cap, cache.W, int(K),
               C.byref(n))
-    ws = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+    ws, = _empty([int(n.value)], torch.uint8, q.device, stream)
     tail = (_np_ptr(cache.prefill_len), _np_ptr(cache.ring_len), _np_ptr(cache.ring_pos), cache.B, cache.H,
             cache.head_dim, cache.ref_cap, cache.W, C.c_float(scale), _ptr(out), _ptr(ws), int(ws.numel()),
             _stream(stream))

@@ -24,6 +24,7 @@ import struct
 import torch
 
 from . import _abi
+from .api import _empty
 
 _I32, _F32 = torch.int32, torch.float32
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -48,20 +49,6 @@ def _stream(index, stream):
     if stream is not None:
         return stream.cuda_stream
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-
-
-def _empty(sizes, dtype, device, index, stream):
-    """New tensors for a call on `stream`.  They come from that stream's memory (a
-    block that another stream has just let go of may still be read there) and stay
-    from reuse until what the caller's stream does with them is over."""
-    if stream.cuda_stream == _stream(index, None):
-        return [torch.empty(size, dtype=dtype, device=device) for size in sizes]
-    caller = torch.cuda.current_stream(index)
-    with torch.cuda.stream(stream):
-        made = [torch.empty(size, dtype=dtype, device=device) for size in sizes]
-    for t in made:
-        t.record_stream(caller)
-    return made
 
 
 def _i32(t, name, numel, device):
@@ -142,7 +129,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor
         n_q = q.shape[1]
         qi = _rows(q, "q", (tokens, n_q, hd), dev)
         if q_out is None:
-            q_out = torch.empty_like(q) if stream is None else _empty([q.shape], dtype, dev, index, stream)[0]
+            q_out = torch.empty_like(q) if stream is None else _empty([q.shape], dtype, dev, stream)[0]
         elif q_out.dtype is not dtype:
             raise ValueError("q_out must have q's dtype")
         qo = _rows(q_out, "q_out", (tokens, n_q, hd), dev)
@@ -154,7 +141,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor
         n_k = k.shape[1]
         ki = _rows(k, "k", (tokens, n_k, hd), dev)
         if k_out is None:
-            k_out = torch.empty_like(k) if stream is None else _empty([k.shape], dtype, dev, index, stream)[0]
+            k_out = torch.empty_like(k) if stream is None else _empty([k.shape], dtype, dev, stream)[0]
         elif k_out.dtype is not dtype:
             raise ValueError("k_out must have k's dtype")
         ko = _rows(k_out, "k_out", (tokens, n_k, hd), dev)
@@ -284,7 +271,7 @@ def paged_plan(cache: PagedKvCache, new_len: torch.Tensor, n_tokens: int, keep_l
         if n_tokens < 0:
             raise ValueError("n_tokens must not be negative")
         sizes = (n + 1, n_tokens, n_tokens) if advance else (n + 1, n_tokens, n_tokens, n, 1)
-        made = [torch.empty(size, dtype=_I32, device=dev) for size in sizes] if stream is None else _empty(sizes, _I32, dev, index, stream)
+        made = [torch.empty(size, dtype=_I32, device=dev) for size in sizes] if stream is None else _empty(sizes, _I32, dev, stream)
         lens, height = (cache.seq_len, cache.n_free) if advance else made[3:]
         plan = PagedPlan(made[0], lens, height, made[1], made[2])
         if stream is not None and advance:
@@ -342,7 +329,7 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
         shape = (tokens, n_q, hd)
         qi = _rows(q, "q", shape, dev)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=cache.dtype, device=dev) if stream is None else _empty([shape], cache.dtype, dev, index, stream)[0]
+            q_out = torch.empty(shape, dtype=cache.dtype, device=dev) if stream is None else _empty([shape], cache.dtype, dev, stream)[0]
         elif q_out.dtype is not cache.dtype:
             raise ValueError("q_out must have the pages' dtype")
         qo = _rows(q_out, "q_out", shape, dev)
@@ -391,7 +378,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
         sinks = sinks.data_ptr()
     qi = _rows(q, "q", shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty([shape], dtype, dev, index, stream)[0]
+        out = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty([shape], dtype, dev, stream)[0]
     elif out.dtype is not dtype:
         raise ValueError("out must have q's dtype")
     oi = _rows(out, "out", shape, dev)
@@ -402,7 +389,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
         if _take is not None and _give is not None:
             ws = taken = _take(size, on)
         else:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if stream is None else _empty([size], torch.uint8, dev, index, stream)[0]
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if stream is None else _empty([size], torch.uint8, dev, stream)[0]
             ws = workspace.data_ptr()
     else:
         size = workspace.numel() * workspace.element_size()

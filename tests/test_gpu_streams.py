@@ -90,3 +90,59 @@ def test_two_streams_match_a_serial_replay(env):
     assert torch.equal(a_imp, ra_imp) and torch.equal(b_imp, rb_imp)
     assert [a_layer.seq_len(b) for b in range(4)] == [a2.seq_len(b) for b in range(4)]
     assert np.all(np.isfinite(torch.stack(a_outs).cpu().numpy()))
+
+
+def test_outputs_and_workspaces_made_for_another_stream_are_its_own(env):
+    """With stream= and no buffers given, a call takes its outputs, its workspace and a new cache's buffers from that stream's memory, not
+    from blocks that the current stream has just let go of and may still be reading."""
+    torch, kvd = env
+    side = torch.cuda.Stream()
+    n, L, n_kv, hd = 4, 700, 4, 128
+    ks, vs = seq_rows([L] * n, n_kv, hd, 7)
+    made = lambda: kvd.LayerKvCache(n, n_kv, hd, "f32", L + 8, stream=side)  # noqa: E731
+    layer = made()
+    torch.cuda.synchronize()
+    gpu_append_bulk(layer, ks, vs, torch)
+    ring = kvd.RingCache(8, 64, H=16, int8=True)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q, k, v = (torch.randn(n, 16, hd, generator=g, device="cuda") for _ in range(3))
+    rows = torch.randn(3, 8, 16, hd, generator=g, device="cuda")
+    drafts = torch.randn(3, 8, 5, 16, hd, generator=g, device="cuda")
+    for s in range(8):
+        kvd.rswa_record_prefill(ring, s, *(torch.randn(16, 64, hd, generator=g, device="cuda") for _ in range(2)))
+    kvd.rswa_ring_write(ring, rows[1], rows[2])
+    torch.cuda.synchronize()
+    verify_q = torch.randn(n, 3, 16, hd, generator=g, device="cuda")
+    calls = [lambda **kw: kvd.decode_attention(q, layer, **kw), lambda **kw: kvd.decode_attention(q, layer, window=300, **kw),
+             lambda **kw: kvd.decode_attention_static(q, layer, **kw), lambda **kw: kvd.decode_attention_verify(verify_q, layer, 3, **kw),
+             lambda **kw: kvd.rswa_decode(rows[0], ring, **kw), lambda **kw: kvd.rswa_decode_i8(rows[0], ring, **kw),
+             lambda **kw: kvd.rswa_verify(*drafts, ring, **kw)]
+    real, asked = torch.empty, []
+
+    def spy(*args, **kw):
+        t = real(*args, **kw)
+        asked.append((t.data_ptr(), torch.cuda.current_stream().cuda_stream))
+        return t
+
+    for i, call in enumerate(calls):
+        want = call()
+        torch.cuda.synchronize()
+        asked.clear()
+        torch.empty = spy
+        try:
+            got = call(stream=side)
+        finally:
+            torch.empty = real
+        assert asked and all(stream == side.cuda_stream for _, stream in asked), i
+        assert got.data_ptr() in [p for p, _ in asked], i
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), i
+    asked.clear()
+    torch.empty = spy
+    try:
+        made()
+    finally:
+        torch.empty = real
+    assert asked and all(stream == side.cuda_stream for _, stream in asked)
+    torch.cuda.synchronize()
+    assert layer.device_error() == 0 and ring.device_error() == 0
