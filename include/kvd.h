@@ -623,7 +623,9 @@ KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q
  * and attends rows [max(0, P - window + 1), P] (window 0: [0, P]); query head
  * h reads KV head h / (n_q / n_kv).  softcap and sinks as decode_attention_ex.
  *   q, out     [n_tokens][n_q][head_dim], dtype f16 or bf16 like the pages,
- *              16-byte aligned with strides of multiples of 8 elements;
+ *              16-byte aligned with strides of multiples of 8 elements; out
+ *              shares no memory with q or the pages, nor its rows with one
+ *              another (slices of one array are fine);
  *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0.
  * Scores, the softmax's maximum and sum and the output are accumulated in f32;
  * the weights are rounded once to dtype for the value product.  Capped scores

@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "kvd_paged_attn.cuh"
+#include "kvd_views.h"
 
 namespace kvd {
 
@@ -71,13 +72,13 @@ bool shape_ok(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t hd) {
 }
 
 // A [tokens][heads][hd] view whose rows a 16-byte access may touch (the stride of
-// an axis with one entry is never used); the rows of `out` may not lie on one another.
-bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads, bool out) {
+// an axis with one entry is never used).
+bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads) {
     const int64_t lim = int64_t(1) << 38;
     if (r == nullptr || (r->data == nullptr && tokens > 0) || (reinterpret_cast<uintptr_t>(r->data) & 15) != 0) return false;
     if (tokens == 0) return true;
     auto ok = [&](int64_t entries, int64_t stride) {
-        return entries <= 1 || (stride >= (out ? 8 : 0) && stride < lim && stride % 8 == 0);
+        return entries <= 1 || (stride >= 0 && stride < lim && stride % 8 == 0);
     };
     return ok(tokens, r->token_stride) && ok(heads, r->head_stride);
 }
@@ -123,7 +124,7 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
                                       int64_t workspace_bytes, uint32_t *err, void *stream) {
     KVD_NVTX_RANGE("paged_attention");
     if (!shape_ok(n_tokens, n_q, n_kv, head_dim) || (dtype != KVD_T_F16 && dtype != KVD_T_BF16)) return KVD_EINVAL;
-    if (!view_ok(q, n_tokens, n_q, false) || !view_ok(out, n_tokens, n_q, true) || (q->data == out->data && n_tokens > 0)) return KVD_EINVAL;
+    if (!view_ok(q, n_tokens, n_q) || !view_ok(out, n_tokens, n_q)) return KVD_EINVAL;
     if (k_pages == nullptr || v_pages == nullptr ||
         ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15) != 0)
         return KVD_EINVAL;
@@ -141,6 +142,13 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     const int32_t group = n_q / n_kv;
     const WsLayout ws = ws_layout(n_tokens, group, head_dim);
     if (n_tokens == 0) return KVD_OK;
+    {
+        const View o = make_view(out->data, out->token_stride, out->head_stride, n_tokens, n_q, head_dim, 2);
+        const int64_t pages = n_pages * page_size * n_kv * head_dim * 2;
+        if (!rows_apart(o) || !views_apart(o, make_view(q->data, q->token_stride, q->head_stride, n_tokens, n_q, head_dim, 2)) ||
+            !views_apart(o, make_range(k_pages, pages)) || !views_apart(o, make_range(v_pages, pages)))
+            return KVD_EINVAL;
+    }
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < ws.total)
         return KVD_EINVAL;
 

@@ -1092,3 +1092,24 @@ def test_outputs_made_for_another_stream_are_its_own(env):
             torch.cuda.synchronize()
             del again, late, copies, seen
     assert cache.device_error() == 0 and other.device_error() == 0
+
+
+def test_attention_refuses_outputs_that_share_memory(env):
+    """A slice of q's own array shifted by a head or a token, q itself, rows on one another, the pages; slices beside q are taken."""
+    torch, kvd = env
+    cache, _ = _poisoned(torch, kvd, [300, 40], 2, 64, 16, torch.bfloat16, 61)
+    x = torch.randn(31, 17, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).bfloat16()
+    old = x.clone()
+    q, plan = x[:30, :8, :64], kvd.PagedPlan(_i32(torch, [0, 20, 30]), cache.seq_len)
+    flat = torch.empty(30 * 8 * 64, device="cuda", dtype=torch.bfloat16)
+    for bad in (q, x[:30, 1:9, :64], x[1:, :8, :64], x[:30, 7:15, 32:96], torch.as_strided(flat, (30, 8, 64), (64, 64, 1)),
+                torch.as_strided(flat, (30, 8, 64), (256, 32, 1)), cache.k.view(-1)[: 30 * 512].view(30, 8, 64), cache.v.view(-1)[-30 * 512:].view(30, 8, 64)):
+        with pytest.raises(kvd.KvdError):
+            kvd.paged_attention(q, cache, plan, out=bad)
+    assert torch.equal(x, old)
+    want = kvd.paged_attention(q.contiguous(), cache, plan)
+    flipped = torch.empty(8, 30, 64, device="cuda", dtype=torch.bfloat16).transpose(0, 1)
+    for out in (x[:30, 8:16, :64], x[:30, :8, 64:], x[:30, 9:, 64:], flipped):
+        assert torch.equal(kvd.paged_attention(q, cache, plan, out=out), want)
+        assert torch.equal(q, old[:30, :8, :64])
+    assert cache.device_error() == 0

@@ -182,3 +182,101 @@ def test_give_up_refusals(abi):
     assert L.kvd_test_give_up(-1, 0) == abi.OK
     for bad in ((152, 0), (0, -1), (0, 10 ** 9 + 1)):
         assert L.kvd_test_give_up(*bad) == abi.EINVAL, bad
+
+
+VIEWS = r"""
+#include "kvd_views.h"
+using namespace kvd;
+static View view(const long long *v) { return {uintptr_t(v[0]), v[1], v[2], v[3], v[4], v[5]}; }
+extern "C" int apart(const long long *a, const long long *b) { return views_apart(view(a), view(b)); }
+extern "C" int rows(const long long *a) { return rows_apart(view(a)); }
+"""
+
+
+@pytest.fixture(scope="module")
+def views(tmp_path_factory):
+    """kvd_views.h as a library of its own."""
+    import subprocess
+
+    from kv_cache_decode_attention_gb300.build import CSRC
+
+    d = tmp_path_factory.mktemp("views")
+    (d / "v.cpp").write_text(VIEWS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(d / "v.cpp"), "-o", str(d / "v.so")], check=True)
+    lib = C.CDLL(str(d / "v.so"))
+    arr = lambda v: (C.c_longlong * 6)(*v)  # noqa: E731
+    return (lambda a, b: bool(lib.apart(arr(a), arr(b)))), (lambda a: bool(lib.rows(arr(a))))
+
+
+def _bytes(v):
+    at, t, h, nt, nh, row = v
+    return [at + i * t + j * h + c for i in range(nt) for j in range(nh) for c in range(row)]
+
+
+def test_views_that_share_bytes_are_never_taken_for_apart(views):
+    """Drawn views of any strides, byte by byte."""
+    import random
+
+    apart, rows = views
+    rng = random.Random(4)
+
+    def draw():
+        nt, nh, row = rng.randint(1, 4), rng.randint(1, 4), rng.randint(1, 5)
+        return [rng.randint(64, 110), rng.randint(0, 24) if nt > 1 else 0, rng.randint(0, 24) if nh > 1 else 0, nt, nh, row]
+
+    said = 0
+    for _ in range(30000):
+        a, b = draw(), draw()
+        shared = bool(set(_bytes(a)) & set(_bytes(b)))
+        assert not (shared and apart(a, b)), (a, b)
+        assert apart(a, b) == apart(b, a)
+        once = len(set(_bytes(a))) == len(_bytes(a))
+        assert not (rows(a) and not once), a
+        said += apart(a, b)
+    assert said > 5000
+
+
+def test_slices_of_one_array_are_known(views):
+    """Heads, channels, tokens and transpositions of one array: told apart exactly."""
+    import random
+
+    apart, rows = views
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(6000):
+        T, H, D = rng.randint(1, 5), rng.randint(1, 6), rng.randint(1, 6)
+        flip = rng.random() < 0.3  # heads outermost
+
+        def part():
+            t0, h0, d0 = rng.randrange(T), rng.randrange(H), rng.randrange(D)
+            nt, nh, nd = rng.randint(1, T - t0), rng.randint(1, H - h0), rng.randint(1, D - d0)
+            ts, hs = (D, T * D) if flip else (H * D, D)
+            return [1000 + t0 * ts + h0 * hs + d0, ts if nt > 1 else 0, hs if nh > 1 else 0, nt, nh, nd], (t0, t0 + nt, h0, h0 + nh, d0, d0 + nd)
+
+        (a, x), (b, y) = part(), part()
+        shared = bool(set(_bytes(a)) & set(_bytes(b)))
+        assert rows(a) and rows(b)
+        # boxes that differ in two axes or more are apart by any of them; the ranges or one modulus shows it unless an axis of one
+        # entry hides the array's stride
+        if shared:
+            assert not apart(a, b)
+        elif min(a[3], b[3]) > 1 and min(a[4], b[4]) > 1:
+            assert apart(a, b), (a, b, x, y)
+        seen.add((shared, apart(a, b)))
+    assert {(True, False), (False, True)} <= seen
+
+
+def test_attention_outputs_that_share_memory_are_refused(abi):
+    """Refused before anything is launched: out on q, on the pages, or on itself."""
+    L = abi.lib()
+    far = 1 << 32
+
+    def call(q, out, n=64, kp=far, vp=2 * far):
+        return L.paged_attention(q, out, n, 8, 8, 128, 2, kp, vp, 64, 16, FAKE, 8, FAKE, FAKE, 4, 0.1, 0, 0.0, None, FAKE, 1 << 40, FAKE, None)
+
+    rows = lambda at, tok=1024, head=128: _rows(abi, at, tok, head)  # noqa: E731
+    q = rows(FAKE, 4096)
+    for out in (rows(FAKE, 4096), rows(FAKE + 256, 4096), rows(FAKE + 7 * 256, 4096), rows(FAKE - 256, 4096), rows(FAKE + 8192, 4096), rows(FAKE + 128, 4096),
+                rows(FAKE, 2048), rows(far), rows(far + (64 * 16 * 8 * 256) - 16), rows(2 * far + 4096), rows(8 * FAKE, 1024, 64), rows(8 * FAKE, 64, 1024),
+                rows(8 * FAKE, 512), rows(8 * FAKE, 960)):
+        assert call(q, out) == abi.EINVAL
