@@ -562,7 +562,8 @@ KVD_API kvd_status kvd_rope_init(kvd_rope *R, const kvd_rope_config *config);
 
 /* Rotate the rows of q [n_tokens][n_q] and k [n_tokens][n_kv] (either may be
  * NULL with its output) into q_out and k_out, which may be the same rows (same
- * pointer and strides; outputs must not overlap inputs otherwise).  f32, f16
+ * pointer and strides; outputs that share memory otherwise, with an input, with
+ * one another or row on row, are refused; slices of one array are fine).  f32, f16
  * or bf16; the products are taken in f32 and rounded once.  The angle is held
  * as a 64-bit fraction of a turn, so it is as exact at position 2^31 - 1 as at
  * 1.  positions: device int32 [n_tokens]; a negative one leaves its output
@@ -605,7 +606,8 @@ KVD_API kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_len
  * pages alone, a negative position q_out's rows; a slot past the pool sets bit
  * 1 of the error word and is skipped.  Slots must differ: which of two rows
  * with one slot stays is not said.  n_pages * page_size < 2^31.  q_out may be
- * q (same strides and type); it must not overlap k or v. */
+ * q (same strides and type); else q_out, k_pages and v_pages share memory with
+ * no other argument nor with one another (refused). */
 KVD_API kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, const kvd_rows *q_out, int32_t n_q,
                                    const kvd_rows *k, const kvd_rows *v, int32_t n_kv, int32_t head_dim,
                                    int32_t in_dtype, int32_t page_dtype, const int32_t *positions,

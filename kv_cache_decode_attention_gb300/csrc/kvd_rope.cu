@@ -22,6 +22,7 @@
 #include <cstring>
 
 #include "kvd_internal.cuh"
+#include "kvd_views.h"
 
 namespace kvd {
 namespace {
@@ -390,11 +391,8 @@ Group group_of(const kvd_rows *in, const kvd_rows *out, int32_t heads) {
     return g;
 }
 
-// In place is fine row by row; any other way of sharing a buffer is not, nor are
-// output rows that lie on one another.
-bool out_ok(const kvd_rows *in, const kvd_rows *out, int64_t tokens, int32_t heads) {
-    if ((tokens > 1 && out->token_stride == 0) || (tokens > 0 && heads > 1 && out->head_stride == 0)) return false;
-    return in->data != out->data || in->data == nullptr || (in->token_stride == out->token_stride && in->head_stride == out->head_stride);
+View view_of(const kvd_rows *r, int64_t tokens, int32_t heads, int32_t hd, int bytes) {
+    return make_view(r->data, r->token_stride, r->head_stride, tokens, heads, hd, bytes);
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
@@ -479,11 +477,21 @@ extern "C" kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const
         if (in[i] == nullptr) continue;
         if (heads[i] < 1 || heads[i] > 1024) return KVD_EINVAL;
         if (!rows_ok(in[i], n_tokens, heads[i], bytes) || !rows_ok(out[i], n_tokens, heads[i], bytes)) return KVD_EINVAL;
-        if (!out_ok(in[i], out[i], n_tokens, heads[i])) return KVD_EINVAL;
         a.g[i] = group_of(in[i], out[i], heads[i]);
         aligned = aligned && aligned16(a.g[i], false, bytes, bytes);
     }
     if (n_tokens == 0) return KVD_OK;
+    // Rows turn in place, one by one; an output shares memory with nothing else.
+    View vi[2], vo[2];
+    for (int i = 0; i < 2; ++i) {
+        if (in[i] == nullptr) continue;
+        vi[i] = view_of(in[i], n_tokens, heads[i], head_dim, bytes);
+        vo[i] = view_of(out[i], n_tokens, heads[i], head_dim, bytes);
+        if (!rows_apart(vo[i]) || !(same_rows(vi[i], vo[i]) || views_apart(vi[i], vo[i]))) return KVD_EINVAL;
+    }
+    if (q != nullptr && k != nullptr &&
+        !(views_apart(vo[0], vo[1]) && views_apart(vo[0], vi[1]) && views_apart(vo[1], vi[0])))
+        return KVD_EINVAL;
     set_rope(&a, r, head_dim);
     a.positions = positions;
     a.n_tokens = n_tokens;
@@ -519,8 +527,6 @@ extern "C" kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, cons
     bool aligned = true;
     if (q != nullptr) {
         if (n_q < 1 || n_q > 1024 || !rows_ok(q, n_tokens, n_q, ib) || !rows_ok(q_out, n_tokens, n_q, ob)) return KVD_EINVAL;
-        if (q->data != nullptr && q->data == q_out->data && ib != ob) return KVD_EINVAL;
-        if (!out_ok(q, q_out, n_tokens, n_q)) return KVD_EINVAL;
         a.g[0] = group_of(q, q_out, n_q);
         aligned = aligned16(a.g[0], false, ib, ob);
     }
@@ -529,6 +535,19 @@ extern "C" kvd_status kv_paged_append(const kvd_rope *R, const kvd_rows *q, cons
     a.g[2] = group_of(v, &vp, n_kv);
     aligned = aligned && aligned16(a.g[1], true, ib, ob) && aligned16(a.g[2], true, ib, ob);
     if (n_tokens == 0) return KVD_OK;
+    {
+        // q turns in place; else what is written shares memory with nothing else
+        const int64_t pages = n_pages * page_size * n_kv * head_dim * ob;
+        const View vk = view_of(k, n_tokens, n_kv, head_dim, ib), vv = view_of(v, n_tokens, n_kv, head_dim, ib);
+        const View pk = make_range(k_pages, pages), pv = make_range(v_pages, pages);
+        bool ok = views_apart(pk, pv) && views_apart(vk, pk) && views_apart(vk, pv) && views_apart(vv, pk) && views_apart(vv, pv);
+        if (q != nullptr) {
+            const View vq = view_of(q, n_tokens, n_q, head_dim, ib), vo = view_of(q_out, n_tokens, n_q, head_dim, ob);
+            ok = ok && rows_apart(vo) && (same_rows(vq, vo) || views_apart(vq, vo)) && views_apart(vo, vk) && views_apart(vo, vv) &&
+                 views_apart(vo, pk) && views_apart(vo, pv) && views_apart(vq, pk) && views_apart(vq, pv);
+        }
+        if (!ok) return KVD_EINVAL;
+    }
     set_rope(&a, r, head_dim);
     a.paged = 1;
     a.n_kv = n_kv;

@@ -1113,3 +1113,33 @@ def test_attention_refuses_outputs_that_share_memory(env):
         assert torch.equal(kvd.paged_attention(q, cache, plan, out=out), want)
         assert torch.equal(q, old[:30, :8, :64])
     assert cache.device_error() == 0
+
+
+def test_rotated_outputs_beside_their_inputs(env):
+    """Slices of one projection that are taken as outputs, and those that are refused, with the arrays as they were."""
+    torch, kvd = env
+    x = torch.randn(40, 24, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9)).bfloat16()
+    old, pos, table = x.clone(), torch.arange(40, device="cuda", dtype=torch.int32), kvd.RopeTable(64)
+    q, k = x[:, :8], x[:, 8:12]
+    want = kvd.rope(q, k, pos, table)
+    got = kvd.rope(q, k, pos, table, q_out=x[:, 12:20], k_out=x[:, 20:])
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(x[:, :12], old[:, :12])
+    half = kvd.rope(q[..., :64], None, pos, table, q_out=q[..., 64:])[0]
+    assert torch.equal(half, want[0][..., :64])
+    x.copy_(old)
+    flat = torch.empty(40 * 8 * 128, device="cuda", dtype=torch.bfloat16)
+    for bad in (dict(q_out=x[:, 1:9]), dict(q_out=x[:, 8:16]), dict(k_out=x[:, 7:11]), dict(q_out=q, k_out=x[:, 4:8]),
+                dict(q_out=torch.as_strided(flat, (40, 8, 128), (64, 128, 1))), dict(q_out=x[:, 12:20], k_out=x[:, 16:20])):
+        with pytest.raises(kvd.KvdError):
+            kvd.rope(q, k, pos, table, **bad)
+    cache = kvd.PagedKvCache(8, 16, 4, 128, 1, 8)
+    plan = kvd.paged_plan(cache, _i32(torch, [40]), 40)
+    same = kvd.PagedKvCache.of(cache.k, cache.k, cache.block_table, cache.seq_len)
+    rows = cache.k.view(-1)[: 40 * 512].view(40, 4, 128)
+    for call in (lambda: kvd.paged_append(cache, plan, k, k, q=q, q_out=x[:, 4:12]), lambda: kvd.paged_append(same, plan, k, k),
+                 lambda: kvd.paged_append(cache, plan, k, rows), lambda: kvd.paged_append(cache, plan, rows, k)):
+        with pytest.raises(kvd.KvdError):
+            call()
+    assert torch.equal(x, old)
+    kvd.paged_append(cache, plan, k, k, q=q, q_out=x[:, 12:20])
+    assert torch.equal(x[:, 12:20], old[:, :8]) and cache.device_error() == 0

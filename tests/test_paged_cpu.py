@@ -280,3 +280,36 @@ def test_attention_outputs_that_share_memory_are_refused(abi):
                 rows(FAKE, 2048), rows(far), rows(far + (64 * 16 * 8 * 256) - 16), rows(2 * far + 4096), rows(8 * FAKE, 1024, 64), rows(8 * FAKE, 64, 1024),
                 rows(8 * FAKE, 512), rows(8 * FAKE, 960)):
         assert call(q, out) == abi.EINVAL
+
+
+def test_rotated_outputs_that_share_memory_are_refused(abi):
+    """Without a GPU a call that is taken fails at its launch (ECUDA), so a refusal is one of the arguments."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where nothing can be launched")
+    L = abi.lib()
+    R = C.byref(_init(abi)[1])
+    M = 1 << 24
+    r = lambda at, tok=1024, head=128: _rows(abi, at, tok, head)  # noqa: E731
+
+    def rope(q, qo, k=None, ko=None, dtype=2):
+        return L.kvd_rope_apply(R, q, qo, 8, k, ko, 8, 128, dtype, FAKE, 64, None)
+
+    def append(q, qo, k=None, v=None, kp=64 * M, vp=128 * M, it=2):
+        k, v = r(4 * M) if k is None else k, r(8 * M) if v is None else v
+        return L.kv_paged_append(R, q, qo, 8, k, v, 8, 128, it, 2, FAKE, FAKE, 64, kp, vp, 64, 16, FAKE, None)
+
+    W = 4096  # heads of 128 of one projection: q 0 .. 7, k 8 .. 15, v 16 .. 23
+    q, k, v = (r(M + i * 8 * 256, W) for i in range(3))
+    for call in (lambda: rope(r(M), r(M)), lambda: rope(r(M), r(2 * M)), lambda: rope(q, q, k, k), lambda: rope(q, v, k, r(2 * M)),
+                 lambda: rope(r(M, 128, 8192), r(M, 128, 8192)), lambda: rope(r(M, 0, 0), r(2 * M)), lambda: append(q, q, k, v), lambda: append(r(M), r(2 * M)),
+                 lambda: append(r(M), r(2 * M), q, q), lambda: append(None, None, k, k)):
+        assert call() == abi.ECUDA
+    for call in (lambda: rope(r(M), r(M + 256)), lambda: rope(r(M), r(M - 256)), lambda: rope(r(M), r(M + 2048)), lambda: rope(r(M), r(M, 2048)),
+                 lambda: rope(q, k, k, q), lambda: rope(q, q, q, q), lambda: rope(q, r(2 * M), k, r(2 * M)), lambda: rope(q, k, k, r(2 * M)),
+                 lambda: rope(r(M), r(2 * M, 1024, 64)), lambda: rope(r(M), r(2 * M, 512)), lambda: rope(r(M), r(2 * M, 64, 128)),
+                 lambda: append(q, k, k, v), lambda: append(q, v, k, v), lambda: append(r(M), r(M), it=0), lambda: append(r(M), r(M + 256)),
+                 lambda: append(r(64 * M), r(M)), lambda: append(r(M), r(128 * M + 4096)), lambda: append(None, None, r(64 * M + 65536)),
+                 lambda: append(None, None, None, r(128 * M)), lambda: append(None, None, kp=64 * M, vp=64 * M), lambda: append(None, None, kp=64 * M, vp=64 * M + 4096)):
+        assert call() == abi.EINVAL
