@@ -587,9 +587,12 @@ KVD_API kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const kv
  *           new rows, -1 in the places behind the last one.
  * n_tokens is the room for new rows.  A step that does not fit (pages, table
  * width, n_tokens) sets bit 2 of the error word, one with malformed numbers
- * (negative, keep_len > seq_len, n_free out of range) bit 1, and neither
+ * (negative, keep_len > seq_len, n_free out of range, a page outside the pool
+ * among those that would go back or be taken) bit 1, and neither
  * changes anything that counts: seq_len_out and n_free_out repeat the inputs,
- * cu_new is 0, positions and slots are -1, so the rest of the step does nothing.  Table
+ * cu_new is 0, positions and slots are -1, so the rest of the step does nothing.  (A
+ * page outside the pool that a request keeps sets bit 1 and leaves the new rows
+ * that would go there without a slot, -1; the step takes effect.)  Table
  * places past a request's pages and the stack above n_free_out hold nothing.
  * n_seq <= 8192. */
 KVD_API kvd_status kv_paged_plan(const int32_t *seq_len, const int32_t *keep_len, const int32_t *new_len,

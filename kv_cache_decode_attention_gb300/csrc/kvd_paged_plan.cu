@@ -12,9 +12,12 @@
 // fills crosses CTAs, and the cluster's hardware barrier carries those.  The
 // fills walk flat ranges of pages and rows with a binary search over the
 // prefix sums, so one long prompt spreads over all threads like many short ones.
+// Pages that are to change hands are looked at before the first barrier, which
+// carries the verdict too: one outside the pool stops the step while nothing that
+// counts is written (the stack above its old height is nobody's).
 //
-// Measured: one token for each of 256 requests 6.5 us, 500 requests with up to 256
-// new rows each 11.8 us, 8000 requests of one row 20 us.  An empty launch takes 2;
+// Measured: one token for each of 256 requests 6.8 us, 500 requests with up to 256
+// new rows each 12.1 us, 8000 requests of one row 20 us.  An empty launch takes 2;
 // the rest is a chain of dependent steps (lengths, three block scans, two cluster
 // barriers, table, slots).  Separate kernels would pay a launch for each barrier.
 
@@ -37,6 +40,14 @@ struct PlanArgs {
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A word of the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_word(const uint32_t *word, uint32_t rank) {
+    uint32_t at, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(word)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // Largest i in [0, n) with pre[i] <= x, for pre[0] = 0 <= x (the last of equal
@@ -82,8 +93,10 @@ template <int RUN>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int64_t warp_sums[32];
+    __shared__ uint32_t strange;  // this CTA has met a page outside the pool
     const int n = a.n_seq;
     int32_t *cu = sm, *keep = cu + n + 1, *held = keep + n, *gone = held + n, *take = gone + n + 1;
+    if (threadIdx.x == 0) strange = 0;
     pdl_wait();
 
     // Prefix sums.  A thread takes a run of consecutive requests.
@@ -110,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int64_t g0 = block_scan(given, warp_sums, &n_given);
     int64_t t0 = block_scan(taken, warp_sums, &n_taken);
     const int64_t free0 = a.n_free[0];
-    const bool malformed = any_bounds || free0 < 0 || free0 > a.n_pages || free0 + n_given > a.n_pages;
+    bool malformed = any_bounds || free0 < 0 || free0 > a.n_pages || free0 + n_given > a.n_pages;
     const bool full = any_full || n_taken > free0 + n_given || n_rows > a.n_tokens;
     const int tid = blockIdx.x * kPlanThreads + threadIdx.x, n_thr = gridDim.x * kPlanThreads;
     const int64_t top = free0 + n_given;  // height once everything given is pushed
@@ -132,20 +145,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             take[n] = int32_t(n_taken);
         }
         __syncthreads();
+        const auto in_pool = [&](int32_t page) { return page >= 0 && page < a.n_pages; };
         // push: j-th page given, counted over requests and then pages
         for (int j = tid; j < n_given; j += n_thr) {
             const int b = owner_of(gone, n, j);
             const int count = gone[b + 1] - gone[b];
             const int32_t page = a.block_table[int64_t(b) * a.max_pages + held[b] - count + (j - gone[b])];
-            if (page < 0 || page >= a.n_pages) set_error(a.err, kErrBounds);
+            if (!in_pool(page)) strange = 1;
             a.free_pages[free0 + j] = page;
+        }
+        // what lay on the stack and is taken; the thread's first is kept at hand
+        int32_t first = -1;
+        for (int64_t j = n_given + tid; j < n_taken; j += n_thr) {
+            const int32_t page = a.free_pages[top - 1 - j];
+            if (!in_pool(page)) strange = 1;
+            if (j == n_given + tid) first = page;
         }
         // every thread of every CTA has also read its inputs by now, so the
         // outputs that may alias them are written only after this barrier
         cluster_barrier();
-        for (int j = tid; j < n_taken; j += n_thr) {
-            const int b = owner_of(take, n, j);
-            a.block_table[int64_t(b) * a.max_pages + held[b] + (j - take[b])] = a.free_pages[top - 1 - j];
+        const uint32_t lane = threadIdx.x & 31;
+        malformed = __any_sync(0xffffffffu, lane < kPlanCtas && peer_word(&strange, lane) != 0);
+        if (!malformed) {
+            const auto pop = [&](int64_t j, int32_t page) {
+                const int b = owner_of(take, n, int32_t(j));
+                a.block_table[int64_t(b) * a.max_pages + held[b] + (j - take[b])] = page;
+            };
+            for (int64_t j = n_given + tid; j < n_taken; j += n_thr) pop(j, j == n_given + tid ? first : a.free_pages[top - 1 - j]);
+            for (int64_t j = tid; j < n_given && j < n_taken; j += n_thr) pop(j, a.free_pages[top - 1 - j]);
         }
         cluster_barrier();
     } else {

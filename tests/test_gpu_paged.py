@@ -1143,3 +1143,55 @@ def test_rotated_outputs_beside_their_inputs(env):
     assert torch.equal(x, old)
     kvd.paged_append(cache, plan, k, k, q=q, q_out=x[:, 12:20])
     assert torch.equal(x[:, 12:20], old[:, :8]) and cache.device_error() == 0
+
+
+@pytest.mark.parametrize("n_seq,rows", [(3, 40), (700, 60), (3000, 20)])
+@pytest.mark.parametrize("bad", [-1, "n_pages", 2 ** 31 - 1])
+def test_plan_refuses_pages_outside_the_pool(env, n_seq, rows, bad):
+    """Among those given back and among those taken: the step changes nothing, and goes through once the number is put right."""
+    torch, kvd = env
+    r = np.random.default_rng(n_seq)
+    width = -(-2 * rows // 16)
+    n_pages = n_seq * width
+    bad = n_pages if bad == "n_pages" else bad
+    cache = kvd.PagedKvCache(n_pages, 16, 1, 64, n_seq, width)
+    model = Model(n_seq, 16, width, n_pages)
+    first = r.integers(1, rows, n_seq).tolist()
+    assert model.step(first, None, sum(first)) is not None
+    kvd.paged_plan(cache, _i32(torch, first), sum(first))
+    _same_state(cache, model)
+    keep = [0 if b % 3 == 0 else n for b, n in enumerate(model.len)]
+    new = r.integers(0, rows, n_seq).tolist()
+    after = [-(-(k + n) // 16) for k, n in zip(keep, new)]
+    gives = [b for b in range(n_seq) if after[b] < len(model.pages[b])]
+    if not gives:  # a small batch: the first gives back what it has
+        new[0], gives = 0, [0]
+        after[0] = 0
+    room, takes, given = sum(new), sum(max(0, a - len(p)) for a, p in zip(after, model.pages)), sum(max(0, len(p) - a) for a, p in zip(after, model.pages))
+    places = [(cache.block_table, (b, int(r.integers(after[b], len(model.pages[b]))), )) for b in (gives[0], gives[-1])]
+    if takes > given:  # below the height that stands, as far as the step digs
+        places += [(cache.free_pages, (int(cache.n_free) - 1,)), (cache.free_pages, (int(cache.n_free) - (takes - given),))]
+    for tensor, at in places:
+        good = int(tensor[at])
+        tensor[at] = bad
+        state = [t.clone() for t in (cache.seq_len, cache.n_free, cache.block_table)]
+        height = int(cache.n_free)
+        stack = cache.free_pages[:height].clone()
+        for advance in (False, True):
+            plan = kvd.paged_plan(cache, _i32(torch, new), room, keep_len=_i32(torch, keep), advance=advance)
+            assert cache.device_error() == 2
+            assert not plan.cu_new.any() and bool((plan.slots == -1).all()) and bool((plan.positions == -1).all())
+            assert torch.equal(plan.seq_len, state[0]) and torch.equal(plan.n_free, state[1])
+            for a, b in zip(state, (cache.seq_len, cache.n_free, cache.block_table)):
+                assert torch.equal(a, b)
+            assert torch.equal(cache.free_pages[:height], stack)
+        tensor[at] = good
+    # a wrong page below those taken, or kept with room to spare, is no part of the step
+    if takes < given + int(cache.n_free):
+        cache.free_pages[0], spare = bad, int(cache.free_pages[0])
+    want = model.step(new, keep, room)
+    plan = kvd.paged_plan(cache, _i32(torch, new), room, keep_len=_i32(torch, keep))
+    assert cache.device_error() == 0 and plan.slots.tolist() == want[2] and plan.positions.tolist() == want[1]
+    if len(model.free) and model.free[0] != int(cache.free_pages[0]):
+        cache.free_pages[0] = spare
+    _same_state(cache, model)
