@@ -658,7 +658,9 @@ KVD_API kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64
  * exits normally.  cta < 0 disarms.  Process-wide. */
 KVD_API kvd_status kvd_test_give_up(int32_t cta, int64_t after_ns);
 
-/* The device error word of the paged calls (see kvd_layer_device_error). */
+/* The device error word of the paged calls (see kvd_layer_device_error), after the
+ * caller has synchronised the streams of the calls it asks about; clear != 0 resets
+ * it before this returns. */
 KVD_API kvd_status kv_paged_device_error(uint32_t *err, int32_t clear, uint32_t *word_out);
 
 /* Short English description of a status code (static storage). */

@@ -293,7 +293,8 @@ extern "C" kvd_status kv_paged_device_error(uint32_t *err, int32_t clear, uint32
     if (err == nullptr) return KVD_EINVAL;
     uint32_t w = 0;
     if (cudaMemcpy(&w, err, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return KVD_ECUDA;
-    if (clear && cudaMemset(err, 0, 4) != cudaSuccess) return KVD_ECUDA;
+    // (cleared when this returns: a call on another stream may follow at once)
+    if (clear && (cudaMemset(err, 0, 4) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)) return KVD_ECUDA;
     if (word_out) *word_out = w;
     return w ? KVD_EDEVICE : KVD_OK;
 }

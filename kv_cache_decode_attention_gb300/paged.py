@@ -226,10 +226,12 @@ class PagedKvCache:
         self.free_pages, self.n_free, self.error = free_pages, n_free, error
 
     def device_error(self, clear: bool = True) -> int:
-        """The error word (synchronises): bit 0 a bounded wait gave up, bit 1
-        metadata out of range, bit 2 a plan did not fit."""
+        """The error word, once every stream of the device has done what it was given:
+        bit 0 a bounded wait gave up, bit 1 metadata out of range, bit 2 a plan did
+        not fit."""
         w = C.c_uint32(0)
         with torch.cuda.device(self.device):
+            torch.cuda.synchronize()  # the copy below waits for no non-blocking stream
             st = _abi.lib().kv_paged_device_error(self.error.data_ptr(), int(clear), C.byref(w))
         if st not in (_abi.OK, _abi.EDEVICE):
             _abi.check("kv_paged_device_error", st)

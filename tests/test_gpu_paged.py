@@ -1195,3 +1195,19 @@ def test_plan_refuses_pages_outside_the_pool(env, n_seq, rows, bad):
     if len(model.free) and model.free[0] != int(cache.free_pages[0]):
         cache.free_pages[0] = spare
     _same_state(cache, model)
+
+
+def test_the_error_word_waits_for_every_stream(env):
+    """A call still under way on another stream is in the word, and the word is clear for the next one."""
+    torch, kvd = env
+    cache = kvd.PagedKvCache(2, 16, 2, 64, 1, 2)
+    x = torch.ones(1, 2, 64, device="cuda", dtype=torch.bfloat16)
+    bad = kvd.PagedPlan(None, None, positions=_i32(torch, [0]), slots=_i32(torch, [32]))
+    good = kvd.PagedPlan(None, None, positions=_i32(torch, [0]), slots=_i32(torch, [31]))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for plan, word in ((bad, 2), (good, 0), (bad, 2), (bad, 2), (good, 0)):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(30_000_000)
+            kvd.paged_append(cache, plan, x, x)
+        assert cache.device_error(clear=False) == word and cache.device_error() == word and cache.device_error() == 0
