@@ -631,7 +631,7 @@ KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q
  *              16-byte aligned with strides of multiples of 8 elements; out
  *              shares no memory with q or the pages, nor its rows with one
  *              another (slices of one array are fine);
- *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0.
+ *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0; n_seq <= 2^20.
  * Scores, the softmax's maximum and sum and the output are accumulated in f32;
  * the weights are rounded once to dtype for the value product.  Capped scores
  * are right to 2^-19 of themselves, or to 2^-20 of the cap where scores beside

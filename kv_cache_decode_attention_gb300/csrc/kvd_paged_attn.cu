@@ -131,7 +131,7 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     if (!pow2_page(page_size) || n_pages < 1 || n_pages * page_size >= (int64_t(1) << 31) ||
         n_pages >= (int64_t(1) << 31) || n_pages * page_size * n_kv >= (int64_t(1) << 31))
         return KVD_EINVAL;
-    if (block_table == nullptr || cu_new == nullptr || seq_len == nullptr || err == nullptr || n_seq < 1 || max_pages < 1 ||
+    if (block_table == nullptr || cu_new == nullptr || seq_len == nullptr || err == nullptr || n_seq < 1 || n_seq > kPaMaxSeq || max_pages < 1 ||
         int64_t(max_pages) * page_size > (int64_t(1) << 31) - 1024)
         return KVD_EINVAL;
     if (!std::isfinite(scale) || scale <= 0.0f || window < 0 || !std::isfinite(softcap) || softcap < 0.0f) return KVD_EINVAL;

@@ -83,6 +83,9 @@ constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
 static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
 constexpr int kPaMaxRows = 2 * kPaTile;
+// A CTA passes requests without new rows one after another, some 100 cycles each:
+// so many take well below the two seconds after which it would give up.
+constexpr int kPaMaxSeq = 1 << 20;
 // Joining 16 rows of 19 pieces takes one CTA some 3 us, as long as a second
 // launch; 256 rows of 2 pieces took it 20 us, and the kernel 3 to 4.
 constexpr int kPaJoinRows = 16;

@@ -1211,3 +1211,21 @@ def test_the_error_word_waits_for_every_stream(env):
             torch.cuda._sleep(30_000_000)
             kvd.paged_append(cache, plan, x, x)
         assert cache.device_error(clear=False) == word and cache.device_error() == word and cache.device_error() == 0
+
+
+def test_few_busy_places_among_many(env):
+    """The most places a call takes, all but three of them without new rows: at both ends and in the middle."""
+    torch, kvd = env
+    n = 1 << 20
+    lens, busy = [300, 40, 700], [0, n // 2 + 7, n - 1]
+    small, rows = _poisoned(torch, kvd, lens, 2, 64, 16, torch.bfloat16, 61)
+    table = torch.full((n, small.max_pages), -1, dtype=torch.int32, device="cuda")
+    table[busy] = small.block_table
+    seq, new = (torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2))
+    seq[busy], new[busy] = small.seq_len, _i32(torch, [1, 30, 2])
+    cu = torch.cat([new[:1] * 0, new.cumsum(0, dtype=torch.int32)])
+    cache = kvd.PagedKvCache.of(small.k, small.v, table, seq)
+    q = torch.randn(33, 8, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).bfloat16()
+    out = kvd.paged_attention(q, cache, kvd.PagedPlan(cu, seq))
+    assert torch.equal(out, kvd.paged_attention(q, small, kvd.PagedPlan(_i32(torch, [0, 1, 31, 33]), small.seq_len)))
+    assert cache.device_error() == 0 and small.device_error() == 0

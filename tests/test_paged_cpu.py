@@ -313,3 +313,12 @@ def test_rotated_outputs_that_share_memory_are_refused(abi):
                  lambda: append(r(64 * M), r(M)), lambda: append(r(M), r(128 * M + 4096)), lambda: append(None, None, r(64 * M + 65536)),
                  lambda: append(None, None, None, r(128 * M)), lambda: append(None, None, kp=64 * M, vp=64 * M), lambda: append(None, None, kp=64 * M, vp=64 * M + 4096)):
         assert call() == abi.EINVAL
+
+
+def test_attention_refuses_more_requests_than_it_can_walk(abi):
+    L = abi.lib()
+    call = lambda n_seq, n: L.paged_attention(_rows(abi), _rows(abi, 2 * FAKE), n, 8, 8, 128, 2, FAKE * 64, FAKE * 64, 64, 16, FAKE, 8, FAKE, FAKE, n_seq, 0.1,  # noqa: E731
+                                              0, 0.0, None, FAKE, 1 << 40, FAKE, None)
+    assert call(1 << 20, 0) == abi.OK  # nothing to do
+    for n_seq in ((1 << 20) + 1, 2 ** 31 - 1):
+        assert call(n_seq, 0) == abi.EINVAL and call(n_seq, 4) == abi.EINVAL
