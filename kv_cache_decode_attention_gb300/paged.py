@@ -286,9 +286,8 @@ def paged_plan(cache: PagedKvCache, new_len: torch.Tensor, n_tokens: int, keep_l
         slots = _i32(plan.slots, "plan.slots", n_tokens, dev)
         if advance:
             plan.seq_len, plan.n_free = cache.seq_len, cache.n_free
-        _i32(plan.seq_len, "plan.seq_len", n, dev)
-        _i32(plan.n_free, "plan.n_free", 1, dev)
-        if not advance and (plan.seq_len is cache.seq_len or plan.n_free is cache.n_free):
+        lens, height = _i32(plan.seq_len, "plan.seq_len", n, dev), _i32(plan.n_free, "plan.n_free", 1, dev)
+        if not advance and (lens == cache.seq_len.data_ptr() or height == cache.n_free.data_ptr()):
             raise ValueError("plan holds the cache's own state: pass advance=True, or a plan made with advance=False")
     st = _abi.lib().kv_paged_plan(
         cache.seq_len.data_ptr(), keep, new, n, cache.n_pages, cache.page_size, cache.block_table.data_ptr(),

@@ -1229,3 +1229,17 @@ def test_few_busy_places_among_many(env):
     out = kvd.paged_attention(q, cache, kvd.PagedPlan(cu, seq))
     assert torch.equal(out, kvd.paged_attention(q, small, kvd.PagedPlan(_i32(torch, [0, 1, 31, 33]), small.seq_len)))
     assert cache.device_error() == 0 and small.device_error() == 0
+
+
+def test_a_plan_apart_may_not_hold_a_view_of_the_state(env):
+    torch, kvd = env
+    cache = kvd.PagedKvCache(8, 16, 1, 64, 2, 4)
+    new = _i32(torch, [20, 3])
+    apart = kvd.paged_plan(cache, new, 23, advance=False)
+    for plan in (kvd.PagedPlan(apart.cu_new, cache.seq_len[:], apart.n_free, apart.positions, apart.slots),
+                 kvd.PagedPlan(apart.cu_new, apart.seq_len, cache.n_free.view(1, 1), apart.positions, apart.slots)):
+        with pytest.raises(ValueError):
+            kvd.paged_plan(cache, new, 23, advance=False, plan=plan)
+    assert cache.seq_len.tolist() == [0, 0] and int(cache.n_free) == 8
+    again = kvd.paged_plan(cache, new, 23, advance=False, plan=apart)
+    assert again is apart and apart.seq_len.tolist() == [20, 3] and cache.seq_len.tolist() == [0, 0] and cache.device_error() == 0
