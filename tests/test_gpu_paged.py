@@ -1243,3 +1243,32 @@ def test_a_plan_apart_may_not_hold_a_view_of_the_state(env):
     assert cache.seq_len.tolist() == [0, 0] and int(cache.n_free) == 8
     again = kvd.paged_plan(cache, new, 23, advance=False, plan=apart)
     assert again is apart and apart.seq_len.tolist() == [20, 3] and cache.seq_len.tolist() == [0, 0] and cache.device_error() == 0
+
+
+def test_a_replayed_plan_equals_an_eager_one(env):
+    """What the captured step's plan holds after each replay: slots, positions, row counts, tables, the stack, and -1 behind the last row."""
+    torch, kvd = env
+    room = 420
+    eager, graph = (kvd.PagedKvCache(60, 16, 2, 64, 4, 27) for _ in range(2))
+    new, keep = _i32(torch, [0] * 4), _i32(torch, [0] * 4)
+    plan = kvd.paged_plan(graph, new, room, keep_len=keep)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kvd.paged_plan(graph, new, room, keep_len=keep, plan=plan)
+    now, model = [0] * 4, Model(4, 16, 27, 60)
+    for n, k in STEPS + [([0, 0, 0, 0], [0, 0, 0, 0]), ([400, 0, 3, 17], None)]:
+        k = list(now) if k is None else k
+        new.copy_(_i32(torch, n))
+        keep.copy_(_i32(torch, k))
+        for t in (plan.slots, plan.positions, plan.cu_new):
+            t.fill_(77)
+        g.replay()
+        other = kvd.paged_plan(eager, _i32(torch, n), room, keep_len=_i32(torch, k))
+        cu, pos, slots = model.step(n, k, room)
+        for p in (plan, other):
+            assert p.cu_new.tolist() == cu and p.positions.tolist() == pos + [-1] * (room - cu[-1]) and p.slots.tolist() == slots + [-1] * (room - cu[-1])
+        for c in (graph, eager):
+            _same_state(c, model)
+            assert c.device_error() == 0
+        now = [a + b for a, b in zip(k, n)]
