@@ -564,9 +564,11 @@ KVD_API kvd_status kvd_rope_init(kvd_rope *R, const kvd_rope_config *config);
  * NULL with its output) into q_out and k_out, which may be the same rows (same
  * pointer and strides; outputs that share memory otherwise, with an input, with
  * one another or row on row, are refused; slices of one array are fine).  f32, f16
- * or bf16; the products are taken in f32 and rounded once.  The angle is held
- * as a 64-bit fraction of a turn, so it is as exact at position 2^31 - 1 as at
- * 1.  positions: device int32 [n_tokens]; a negative one leaves its output
+ * or bf16; the products are taken in f32 and rounded once.  Frequencies are held
+ * as 64-bit fractions of a turn, computed in f64 and right to 2^-54, and their
+ * products with the position are exact: an angle is off by 2^-54 of a turn a
+ * position (2^-34 at 2^20, 2^-23 at 2^31), and by 2^-26 for its f32 sine and
+ * cosine at any.  positions: device int32 [n_tokens]; a negative one leaves its output
  * rows as they were.  Any head_dim from rot_dim to 512. */
 KVD_API kvd_status kvd_rope_apply(const kvd_rope *R, const kvd_rows *q, const kvd_rows *q_out, int32_t n_q,
                                   const kvd_rows *k, const kvd_rows *k_out, int32_t n_kv, int32_t head_dim,

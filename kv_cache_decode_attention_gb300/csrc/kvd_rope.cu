@@ -3,8 +3,10 @@
 //
 // Pair i of a head turns by position * f_i.  The table holds f_i / 2 pi as a
 // 64-bit fraction of a turn, so position * table is the angle modulo one turn
-// in one wrapping integer product: exact to position * 2^-65 turns however far
-// the position (an f32 angle of 10^6 radians would be off by 0.03).
+// in one wrapping integer product.  The table is computed in f64 and right to 2^-54
+// turns, and the product adds nothing: position * 2^-54 turns (an f32 angle of 10^6
+// radians would be off by 0.03, this one by 4e-10).  Its top 32 bits, 2^-32 of a
+// turn, become an f32 between -1 and 1: 2^-26 turns.
 //
 // Bound by HBM: every row is read and written once.  A CTA computes the cos
 // and sin of its tokens once into shared memory and each thread keeps the

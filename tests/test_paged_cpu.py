@@ -322,3 +322,48 @@ def test_attention_refuses_more_requests_than_it_can_walk(abi):
     assert call(1 << 20, 0) == abi.OK  # nothing to do
     for n_seq in ((1 << 20) + 1, 2 ** 31 - 1):
         assert call(n_seq, 0) == abi.EINVAL and call(n_seq, 4) == abi.EINVAL
+
+
+def _turns_of(c, digits=60):
+    """f_i / 2 pi of a config by its formula, with so many digits."""
+    from decimal import Decimal as D, localcontext
+
+    with localcontext() as ctx:
+        ctx.prec = digits
+        two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+        rot, factor, length = c["rot_dim"], D(c["factor"]), D(c["original_len"])
+        log_base = D(c["base"]).ln()
+        if c["scaling"] == 2:
+            log_base += factor.ln() * rot / (rot - 2)
+        if c["scaling"] == 3:
+            pair = lambda turns: rot * (length / (D(turns) * two_pi)).ln() / (2 * log_base)  # noqa: E731
+            low = max(int(pair(c["beta_fast"]).to_integral_value("ROUND_FLOOR")), 0)
+            high = min(int(pair(c["beta_slow"]).to_integral_value("ROUND_CEILING")), rot - 1)
+        out = []
+        for i in range(rot // 2):
+            f = (log_base * (-2 * i) / rot).exp()
+            if c["scaling"] == 1:
+                f /= factor
+            elif c["scaling"] == 3:
+                r = min(max((i - low) / max(D(high - low), D("0.001")), D(0)), D(1))
+                f = f / factor * r + f * (1 - r)
+            elif c["scaling"] == 4:
+                lo, hi = D(c["low_freq_factor"]), D(c["high_freq_factor"])
+                m = min(max((length * f / two_pi - lo) / (hi - lo), D(0)), D(1))
+                f = f / factor * (1 - m) + f * m
+            out.append(f / two_pi)
+        return out
+
+
+@pytest.mark.parametrize("scaling", range(5))
+def test_rope_table_is_right_to_2_to_the_minus_54_turns(abi, scaling):
+    """Against 60 digits.  f <= 1, so f / 2 pi < 0.16: pow, the scaling's products and sums and the division by 2 pi are a few roundings of
+    2^-53 of that each."""
+    for rot in (4, 64, 70, 128, 512):
+        for base in (100.0, 10000.0, 500000.0, 1e7):
+            for factor, length in ((1.0, 8192.0), (3.7, 2048.0), (8.0, 4096.0), (32.0, 32768.0)):
+                kw = dict(rot_dim=rot, scaling=scaling, base=base, factor=factor, original_len=length)
+                st, R = _init(abi, **kw)
+                assert st == abi.OK
+                for got, want in zip(_fields(R)[1], _turns_of({**GOOD, **kw})):
+                    assert abs(got - want * 2 ** 64) <= 2 ** 10, kw
