@@ -396,3 +396,118 @@ def test_the_model_sees_what_an_end_forgets(mistake):
             run = Abandoned(_drawn_jobs(rng, 3), 10, rng)
             run.mistake = mistake
             run.run(int(2 ** rng.uniform(0, 10)))
+
+
+class Pieces:
+    """The joins of a small call: CTAs whose four warps each write their rows of a piece, one of which takes a ticket for it; the holder of an
+    item's last ticket has its warps join.  Some CTAs are given up at some moment and take the tickets they owe on their way out."""
+
+    owes = True
+
+    def __init__(self, items, rng):
+        # items: the CTAs that hold each one's pieces, in order; a CTA ends its items in that order
+        self.items, self.rng, self.words = items, rng, {}
+
+    def launch(self, nonce, give_up):
+        rng, items, words = self.rng, self.items, self.words
+        ctas = sorted({c for held in items for c in held})
+        written, joined, gone, open_ = set(), [], set(), {}
+
+        def ticket(i):
+            old, count = words.get(i, (None, 0))
+            count = count + 1 if old == nonce else 1
+            words[i] = (nonce, count) if count < len(items[i]) else (0, 0)
+            return count == len(items[i])
+
+        def cta(c):
+            """Yields (warp, condition) until the CTA is done: a scheduler of its own over its four warps."""
+            mine = [i for i, held in enumerate(items) if c in held]
+            piece_done, verdict, joins, taken = Bar("piece_done", 4), Bar("verdict", 1), {}, 0
+
+            def warp(w):
+                nonlocal taken
+                for cuts, i in enumerate(mine):
+                    yield None
+                    written.add((i, c, w))
+                    piece_done.arrive()
+                    if w == 0:
+                        yield piece_done, cuts
+                        joins[cuts] = ticket(i)
+                        taken += 1
+                        verdict.arrive()
+                    yield verdict, cuts
+                    if joins[cuts]:
+                        if not gone:
+                            assert {(i, x, y) for x in items[i] for y in range(4)} <= written, "joined before every piece was there"
+                        joined.append((i, w))
+
+            warps, waits = {w: warp(w) for w in range(4)}, dict.fromkeys(range(4))
+            left = rng.randrange(12) if c in give_up else 1 << 30
+            while warps:
+                able = [w for w in warps if waits[w] is None or waits[w][0].over(waits[w][1])]
+                if left <= 0:  # given up: whoever has to wait leaves
+                    able = [w for w in able if waits[w] is not None or rng.random() < 0.5]
+                    if not able:
+                        gone.add(c)
+                        break
+                w = rng.choice(able)
+                left -= 1
+                try:
+                    waits[w] = next(warps[w])
+                except StopIteration:
+                    del warps[w]
+                yield
+            if c in gone and self.owes:
+                for i in mine[taken:]:
+                    yield
+                    ticket(i)
+
+        open_ = {c: cta(c) for c in ctas}
+        while open_:
+            c = rng.choice(list(open_))
+            try:
+                next(open_[c])
+            except StopIteration:
+                del open_[c]
+        if not gone:
+            assert sorted(joined) == [(i, w) for i in range(len(items)) for w in range(4)], "an item joined twice or not at all"
+        return bool(gone)
+
+
+def _drawn_items(rng):
+    """Items cut over neighbouring CTAs: each begins where the last one ended."""
+    items, c = [], 0
+    for _ in range(rng.randint(1, 5)):
+        n = rng.randint(2, 5)
+        items.append(list(range(c, c + n)))
+        c += n - (rng.random() < 0.6)
+    return items
+
+
+def test_pieces_are_joined_once_and_after_launches_given_up():
+    """Replays of a graph (one nonce) and other calls on one workspace, some of them given up: the next one joins every item once."""
+    given_up = 0
+    for seed in range(400):
+        rng = random.Random(seed)
+        run = Pieces(_drawn_items(rng), rng)
+        run.words = {i: rng.choice([(None, 0), (7, 3), (8, 1)]) for i in range(len(run.items))}  # what the memory held
+        ctas = sorted({c for held in run.items for c in held})
+        for _ in range(5):
+            nonce = rng.choice([1, 1, 2])
+            give_up = set(rng.sample(ctas, rng.randint(1, 2))) if rng.random() < 0.5 else set()
+            given_up += run.launch(nonce, give_up)
+            assert all(count == 0 for _, count in run.words.values())
+    assert given_up > 100
+
+
+def test_the_model_sees_tickets_that_are_owed():
+    class Wrong(Pieces):
+        owes = False
+
+    with pytest.raises(AssertionError, match="joined"):
+        for seed in range(400):
+            rng = random.Random(seed)
+            run = Wrong(_drawn_items(rng), rng)
+            ctas = sorted({c for held in run.items for c in held})
+            for give_up in ({rng.choice(ctas)}, set(), set()):
+                run.launch(1, give_up)
