@@ -43,7 +43,7 @@ def _empty(sizes, dtype, device, stream) -> list:
     that stream's memory (a block that another stream has just let go of may still
     be read there) and stay from reuse until what the caller's stream does with
     them is over."""
-    if stream is None or stream.cuda_stream == _stream().value:
+    if stream is None or stream.cuda_stream == (_stream().value or 0):  # the default stream is 0
         return [torch.empty(size, dtype=dtype, device=device) for size in sizes]
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
@@ -285,7 +285,7 @@ def decode_attention(q: torch.Tensor, cache: LayerKvCache, out: torch.Tensor | N
     if q.numel() != cache.n_seq * n_q * cache.head_dim:
         raise ValueError("q must be [n_seq, n_q, head_dim]")
     if out is None:
-        out, = _empty([q.shape], torch.float32, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _empty([q.shape], q.dtype, q.device, stream)[0]
     _f32_cuda(out, "out")
     if imp is not None:
         _f32_cuda(imp, "imp")
@@ -293,7 +293,8 @@ def decode_attention(q: torch.Tensor, cache: LayerKvCache, out: torch.Tensor | N
             raise ValueError("imp must hold %d floats" % cache.imp_len)
     need = cache.workspace_bytes(n_q, imp is not None)
     if workspace is None:
-        workspace, = _empty([need], torch.uint8, q.device, stream)
+        workspace = (torch.empty(need, dtype=torch.uint8, device=q.device) if stream is None
+                     else _empty([need], torch.uint8, q.device, stream)[0])
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
     if window or softcap or sinks is not None:
@@ -322,7 +323,7 @@ def decode_attention_static(q: torch.Tensor, cache: LayerKvCache, out: torch.Ten
     if q.numel() != cache.n_seq * n_q * cache.head_dim:
         raise ValueError("q must be [n_seq, n_q, head_dim]")
     if out is None:
-        out, = _empty([q.shape], torch.float32, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _empty([q.shape], q.dtype, q.device, stream)[0]
     _f32_cuda(out, "out")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)

@@ -272,13 +272,18 @@ def paged_plan(cache: PagedKvCache, new_len: torch.Tensor, n_tokens: int, keep_l
     if plan is None:
         if n_tokens < 0:
             raise ValueError("n_tokens must not be negative")
-        sizes = (n + 1, n_tokens, n_tokens) if advance else (n + 1, n_tokens, n_tokens, n, 1)
-        made = [torch.empty(size, dtype=_I32, device=dev) for size in sizes] if stream is None else _empty(sizes, _I32, dev, stream)
-        lens, height = (cache.seq_len, cache.n_free) if advance else made[3:]
-        plan = PagedPlan(made[0], lens, height, made[1], made[2])
-        if stream is not None and advance:
-            lens.record_stream(stream)
-            height.record_stream(stream)
+        if stream is None:
+            empty = torch.empty
+            plan = PagedPlan(empty(n + 1, dtype=_I32, device=dev), cache.seq_len if advance else empty(n, dtype=_I32, device=dev),
+                             cache.n_free if advance else empty(1, dtype=_I32, device=dev),
+                             empty(n_tokens, dtype=_I32, device=dev), empty(n_tokens, dtype=_I32, device=dev))
+        else:
+            cu, lens, height, pos, slots = _empty((n + 1, n, 1, n_tokens, n_tokens), _I32, dev, stream)
+            if advance:
+                lens, height = cache.seq_len, cache.n_free
+                lens.record_stream(stream)
+                height.record_stream(stream)
+            plan = PagedPlan(cu, lens, height, pos, slots)
         cu, pos, slots = plan.cu_new.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr()
     else:
         cu = _i32(plan.cu_new, "plan.cu_new", n + 1, dev)
