@@ -54,15 +54,18 @@
 //     seconds).  A unit takes 1.8 us where its MMAs
 //     alone need 1.1: a warp's looks at barriers and the hand-over of P are what is
 //     left between them.  Head size 64 takes 1.6 us a unit for half the MMAs.
-//   short requests: an item costs some 3 us beside its copies (the chain of copy, S,
-//     softmax, P V, epilogue), a call some 8 before the first item and 4 more where
-//     a second kernel joins.  One row over 1023 rows takes 14 us, one for each of 256
-//     requests of 300 rows 73.
+//   short requests: an item costs some 3 us beside its copies (from its first S to
+//     its rows stored 2.6), and a CTA has its first scores some 4.5 us after it began:
+//     barriers and TMEM 0.5, lengths and the cut 1.1, the first item, its page numbers
+//     and the request for K 2, the copy and S 1.  A second kernel that joins takes 3
+//     to 4 us more, 9.6 where seven chunks of up to 700 rows are cut.  One row over
+//     1023 rows takes 14 us, one for each of 256 requests of 300 rows 96 (up to 300
+//     rows: 72), for 64 busy of 4096 places 9 more than for 64 alone.
 // Measured and not taken: two softmax groups for each stream, half a tile each
 // (prompts -5%, drafts +7%, windows +11%); P handed over in halves (prompts +6%); a
 // third buffer for S at head size 64 (long requests -1%, windows +4%); short items
 // each on one stream (one-tile items -24%, drafts +2%, windows and prompts of 2000
-// +2%); one warp for both streams' MMAs (300-row requests +16%, mixed prompts +3%,
+// +2%); one warp for both streams' MMAs (requests of up to 300 rows +16%, mixed prompts +3%,
 // windows -1%, 2000-row prompts at head size 64 -2%).
 #pragma once
 
@@ -83,8 +86,8 @@ constexpr int kPaRegs = 128, kPaSoftRegs = 184, kPaLoadRegs = 72;
 static_assert(2 * kPaSoftRegs + 2 * kPaLoadRegs <= 4 * kPaRegs, "setmaxnreg shares");
 constexpr int kPaTile = 128;       // query rows of a tile, and KV rows of a tile
 constexpr int kPaMaxRows = 2 * kPaTile;
-// A CTA passes requests without new rows one after another, some 100 cycles each:
-// so many take well below the two seconds after which it would give up.
+// A CTA passes requests without new rows one after another.  So many take 2.8 ms,
+// well below the two seconds without a step after which it would give up.
 constexpr int kPaMaxSeq = 1 << 20;
 // Joining 16 rows of 19 pieces takes one CTA some 3 us, as long as a second
 // launch; 256 rows of 2 pieces took it 20 us, and the kernel 3 to 4.

@@ -230,7 +230,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
 // A rot_dim that is no multiple of 16, in rows that allow 16-byte accesses: a
 // thread owns eight neighbouring channels.  Interleaved partners are its own;
 // the other layout's lie in other threads of the row, which is one warp's
-// (head_dim 64, 128 or 256), and come through shared memory.
+// (head_dim 64, 128 or 256), and come through shared memory.  Bound by issue, not by
+// memory (8192 tokens of 40 heads of 128, 70 rotated: 69 us, issue slots 69% busy,
+// DRAM 22%): eight angles from shared memory for every head and channel-wise
+// choices, half of the shared-memory wavefronts bank conflicts.
 template <typename TI, typename TO, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads) rope_part_kernel(const __grid_constant__ RopeArgs a, int tok_per_cta) {
     extern __shared__ __align__(16) float2 cs[];
@@ -288,7 +291,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_part_kernel(const __grid_co
 
 // Any other size, stride or alignment: one thread per pair or plain channel.
 // (8192 tokens of 40 heads of 128, 70 rotated channels: 120 us, rope_part_kernel 69;
-// 256 tokens: 8.7 and 4.8.)
+// 256 tokens: 8.7 and 4.8.  Issue slots 68% busy with index arithmetic and accesses
+// of one element.)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeArgs a, int interleaved) {
     extern __shared__ float2 cs[];
@@ -355,7 +359,9 @@ cudaError_t launch_rope(const RopeArgs &a, bool aligned, int layout, cudaStream_
     // Several tokens to a CTA amortise its prologue once there are CTAs enough
     // for every SM twice over; fewer tokens than that spread wider.  (8192 tokens of
     // 40 heads: four to a CTA 30.4 us, one 41.3; 1500: four 6.1, one 7.3; 64: four
-    // 4.0, one 2.5.)
+    // 4.0, one 2.5.  Two from four CTAs an SM on: 900 tokens 4.2, one 5.8, four 5.0;
+    // 608: 3.8, 3.8, 4.1; 1215: 4.9, 6.5, 5.1; appends alike.  rope_part_kernel takes
+    // the same: 900 tokens two 9.4, one 10.1, four 14.2; 608: 7.9, 6.6, 12.8.)
     const int lanes = kRopeThreads / a.n_tasks;
     int tok = a.n_tokens >= 152 * 2 * kMaxTok ? kMaxTok : a.n_tokens >= 152 * 4 ? 2 : 1;
     while (tok > lanes) tok >>= 1;
