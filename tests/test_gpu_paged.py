@@ -1272,3 +1272,48 @@ def test_a_replayed_plan_equals_an_eager_one(env):
             _same_state(c, model)
             assert c.device_error() == 0
         now = [a + b for a, b in zip(k, n)]
+
+
+def test_a_step_captured_onto_another_stream(env):
+    """Plan, append and attention captured with stream=, new outputs each, and two such graphs on one workspace, replayed in turn: small
+    calls, which join their pieces by tickets in it, and larger ones."""
+    torch, kvd = env
+    made = []
+    for lens, new, seed in (([9000, 5], [1, 1], 3), ([700, 3000], [40, 90], 4)):
+        cache, _ = _poisoned(torch, kvd, lens, 2, 128, 16, torch.bfloat16, seed)
+        plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+        q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)).bfloat16()
+        made.append((cache, plan, q))
+    small = kvd.PagedKvCache(40, 16, 2, 128, 2, 40)
+    new, pos = _i32(torch, [300, 20]), torch.arange(130, device="cuda", dtype=torch.int32)
+    rows = torch.randn(320, 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    table, ws = kvd.RopeTable(128), torch.empty(kvd.paged_attention_workspace(320, 8, 2, 128), dtype=torch.uint8, device="cuda")
+
+    def step(stream, shared):
+        outs = [kvd.paged_attention(q, c, p, workspace=ws if shared else None, stream=stream) for c, p, q in made]
+        outs += [kvd.rope(q[:130], None, pos[: q.shape[0]], table, stream=stream)[0] for _, _, q in made]
+        p = kvd.paged_plan(small, new, 330, keep_len=_zero, stream=stream)
+        qr = kvd.paged_append(small, p, rows_k, rows_k, q=rows_q, rope=table, stream=stream)
+        return outs + [p.slots, p.positions, p.cu_new, kvd.paged_attention(qr, small, p, workspace=ws_big if shared else None, stream=stream)[:320]]
+
+    _zero = _i32(torch, [0, 0])
+    rows = torch.cat([rows, rows[:10]])
+    rows_q, rows_k = rows, rows[:, :2]
+    ws_big = torch.empty(kvd.paged_attention_workspace(330, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    want = step(None, False)
+    torch.cuda.synchronize()
+    graphs = []
+    for shared in (True, True, False):
+        side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            side.wait_stream(torch.cuda.current_stream())
+            outs = step(side, shared)
+            torch.cuda.current_stream().wait_stream(side)
+        graphs.append((g, outs))
+    for _ in range(3):
+        for g, outs in graphs:
+            for t in outs:
+                t.fill_(9)
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert small.device_error() == 0 and all(c.device_error() == 0 for c, _, _ in made)
