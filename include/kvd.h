@@ -635,7 +635,8 @@ KVD_API kvd_status paged_attention_workspace_bytes(int64_t n_tokens, int32_t n_q
  *              another (slices of one array are fine);
  *   head_dim   64 or 128; n_q / n_kv <= 16; scale > 0; n_seq <= 2^20.
  * Scores, the softmax's maximum and sum and the output are accumulated in f32;
- * the weights are rounded once to dtype for the value product.  Capped scores
+ * the weights are rounded once to dtype for the value product, and one below
+ * 2^-126 of the row's largest, or of its sink, is zero.  Capped scores
  * are right to 2^-19 of themselves, or to 2^-20 of the cap where scores beside
  * them come to half of it; a cap that no score below 10^34 before scaling would
  * feel (scale / softcap below the normal f32 numbers) is none.  Rows of `out`
