@@ -948,14 +948,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attention_kernel(const __
                 volatile int *steps = &sh.steps;
                 int last = 0;
                 uint64_t since = global_ns();
-                const uint64_t end = a.give_up == int32_t(blockIdx.x) ? since + a.give_up_ns : ~0ull;
+                const bool early = a.give_up == int32_t(blockIdx.x);
+                const uint64_t limit = early ? a.give_up_ns : 2000000000ull;
                 while (!mbar_try_wait(&sh.all_done, 0)) {
                     const uint64_t now = global_ns();
                     if (*steps != last) {
                         last = *steps;
-                        since = now;
-                    }
-                    if (now - since > 2000000000ull || now >= end) {
+                        if (!early) since = now;
+                    } else if (now - since >= limit) {
                         *stop = 1;
                         break;
                     }
