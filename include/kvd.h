@@ -513,7 +513,7 @@ KVD_API kvd_status rswa_device_error(const void *workspace, int32_t clear, uint3
  * `err` is the device error word (uint32, caller-owned, zeroed once): bit 0 a
  * bounded wait gave up, bit 1 metadata out of range (the access is skipped),
  * bit 2 a plan did not fit.  kv_paged_device_error reads it. */
-typedef enum { KVD_T_F32 = 0, KVD_T_F16 = 1, KVD_T_BF16 = 2 } kvd_dtype;
+typedef enum { KVD_T_F32 = 0, KVD_T_F16 = 1, KVD_T_BF16 = 2, KVD_T_E4M3 = 3 } kvd_dtype;
 
 /* Rows [token][head][head_dim] inside a larger array: strides in elements,
  * head_dim contiguous.  q, k and v may so be slices of one projection. */
@@ -652,6 +652,71 @@ KVD_API kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64
                                    const int32_t *seq_len, int32_t n_seq, float scale, int64_t window,
                                    float softcap, const float *sinks, void *workspace,
                                    int64_t workspace_bytes, uint32_t *err, void *stream);
+
+/* ---- Pages of 8 bits: half the memory, and half the bytes of a decode step.
+ *
+ *   k_pages, v_pages   [n_pages][n_kv][page_size][head_dim] e4m3 codes (four bits of
+ *                      exponent, three of mantissa, largest 448), 16-byte aligned;
+ *   k_scale, v_scale   f32 [n_pages][n_kv]: one scale s for each block, a page of one
+ *                      KV head, so that a code c stands for c * s.
+ * Tables, lengths, slots, plans and the error word are those of the 16-bit pages, and
+ * kv_paged_plan plans both.  Readers take any scale in [2^-64, 2^64]; another one reads
+ * as 1 and sets bit 1 of the error word.  kv_paged_append_q8 writes powers of two. */
+
+/* kv_paged_append into pages of 8 bits.  x being a row of v, or of k once rotated
+ * (both in f32), a block's scale is the smallest power of two s in [2^-64, 2^64]
+ * with |x| <= 448 s for all finite x written to it since its row 0 was: a call that
+ * writes row 0 starts the block anew, and a later call that needs a larger s moves
+ * the codes standing before its rows to it, each rounded to nearest even (exact
+ * where the old scale was a power of two and the result is no subnormal of e4m3).  A
+ * scale in the block that is larger already stays.  Codes are x / s rounded to
+ * nearest even, +-448 at most (as infinities become); a NaN stays one.
+ *   in_dtype  of q, k and v: f32, f16 or bf16;
+ *   q_dtype   of q_out: f16 or bf16, and in_dtype's unless that is f32 (not read
+ *             without q);
+ *   slots     those of one page stand together in the batch and in order, as a plan
+ *             lays them; a page whose rows come in two runs holds any of the results.
+ * Scales and codes share memory with no other argument.  Rows of a block behind
+ * those written are left as they were.  All else as kv_paged_append. */
+KVD_API kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, const kvd_rows *q_out, int32_t n_q,
+                                      const kvd_rows *k, const kvd_rows *v, int32_t n_kv, int32_t head_dim,
+                                      int32_t in_dtype, int32_t q_dtype, const int32_t *positions,
+                                      const int32_t *slots, int64_t n_tokens, void *k_pages, void *v_pages,
+                                      float *k_scale, float *v_scale, int64_t n_pages, int32_t page_size,
+                                      uint32_t *err, void *stream);
+
+/* Rows of requests read back: rows start[b] + i, i < cu_rows[b + 1] - cu_rows[b], of
+ * every request b, packed in k_out and v_out [n_rows][n_kv][head_dim] as rows
+ * cu_rows[b] + i.  For a request that leaves the pages (another cache, another
+ * machine) or one whose rows are to be seen.  page_dtype f16, bf16 (k_scale and
+ * v_scale NULL) or e4m3; out_dtype f32, f16 or bf16: the value is rounded once.
+ * start: device int32 [n_seq] or NULL, zeros; cu_rows: device int32 [n_seq + 1].
+ * A row that the request does not hold, or whose page lies outside the pool, sets bit
+ * 1 of the error word and reads as zeros; output rows that no request has are left as
+ * they were.  Outputs are 16-byte aligned with strides of multiples of 16 bytes and
+ * share memory with nothing else.  n_seq <= 2^20. */
+KVD_API kvd_status kv_paged_read(const void *k_pages, const void *v_pages, const float *k_scale,
+                                 const float *v_scale, int32_t page_dtype, int64_t n_pages, int32_t page_size,
+                                 int32_t n_kv, int32_t head_dim, const int32_t *block_table, int32_t max_pages,
+                                 const int32_t *seq_len, const int32_t *start, const int32_t *cu_rows,
+                                 int32_t n_seq, const kvd_rows *k_out, const kvd_rows *v_out, int32_t out_dtype,
+                                 int64_t n_rows, uint32_t *err, void *stream);
+
+/* Workspace bytes paged_attention_q8 needs (as paged_attention_workspace_bytes). */
+KVD_API kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv,
+                                                      int32_t head_dim, int64_t *bytes_out);
+
+/* paged_attention over pages of 8 bits: the attention of q, f16 or bf16 (dtype), over
+ * the rows that codes and scales stand for.  Arguments, masks, options and what is
+ * skipped or left alone are those of paged_attention. */
+KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q,
+                                      int32_t n_kv, int32_t head_dim, int32_t dtype, const void *k_pages,
+                                      const void *v_pages, const float *k_scale, const float *v_scale,
+                                      int64_t n_pages, int32_t page_size, const int32_t *block_table,
+                                      int32_t max_pages, const int32_t *cu_new, const int32_t *seq_len,
+                                      int32_t n_seq, float scale, int64_t window, float softcap,
+                                      const float *sinks, void *workspace, int64_t workspace_bytes, uint32_t *err,
+                                      void *stream);
 
 /* The bounded waits of paged_attention, run on purpose (for tests).  While armed
  * with 0 <= cta < 152, that thread block of every launch gives up after_ns (0 ..

@@ -32,5 +32,6 @@ from .paged import (  # noqa: F401
     paged_attention,
     paged_attention_workspace,
     paged_plan,
+    paged_read,
     rope,
 )

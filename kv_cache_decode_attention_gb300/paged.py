@@ -3,7 +3,9 @@
 One step of a server is ``paged_plan`` (pages, slots and positions of the new
 rows, from request lengths on the device), then per layer ``paged_append``
 (rotate q and k, write k and v to their slots) and ``paged_attention``.  Nothing
-is read back, so a step can be captured into a CUDA graph and replayed.
+is read back, so a step can be captured into a CUDA graph and replayed.  Pages hold
+16-bit rows or, with half the memory, codes of 8 bits with a scale for each page of a
+KV head (``PagedKvCache(dtype=torch.float8_e4m3fn)``); ``paged_read`` gives rows back.
 A call goes to the current stream, or to `stream`, where what it returns is to be
 had.  What it reads has to be there on that stream, and to stay until it is read
 (Tensor.record_stream), as with any stream of torch's.
@@ -28,6 +30,8 @@ from .api import _empty
 
 _I32, _F32 = torch.int32, torch.float32
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_E4M3 = torch.float8_e4m3fn
+_PAGES = {torch.float16: 1, torch.bfloat16: 2, _E4M3: 3}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
@@ -159,39 +163,45 @@ class PagedKvCache:
     Requests 0 .. n_seq - 1 are the places of a batch; each holds seq_len[b] rows
     in the pages block_table[b].  Layers of one model share block_table, seq_len
     and the free pages: build the first layer's cache, then ``layer_like`` it.
-    dtype: torch.bfloat16 or torch.float16.
+    dtype: torch.bfloat16, torch.float16 or torch.float8_e4m3fn.  Pages of 8 bits
+    hold codes; k_scale and v_scale (float32 [n_pages, n_kv], else None) have one
+    scale for each page of a KV head, and a row is its codes times that.
     """
 
-    __slots__ = ("k", "v", "block_table", "seq_len", "free_pages", "n_free", "error", "page_size", "n_pages", "n_kv",
-                 "head_dim", "n_seq", "max_pages", "dtype", "device", "index")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "block_table", "seq_len", "free_pages", "n_free", "error", "page_size",
+                 "n_pages", "n_kv", "head_dim", "n_seq", "max_pages", "dtype", "device", "index")
 
     def __init__(self, n_pages: int, page_size: int, n_kv: int, head_dim: int, n_seq: int, max_pages: int,
                  dtype=torch.bfloat16, device="cuda"):
         dev = torch.device(device)
         shape = (int(n_pages), int(n_kv), int(page_size), int(head_dim))
+        scales = [torch.ones(shape[:2], dtype=_F32, device=dev) for _ in range(2)] if dtype is _E4M3 else (None, None)
         self._bind(torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev),
                    torch.full((int(n_seq), int(max_pages)), -1, dtype=torch.int32, device=dev),
                    torch.zeros(int(n_seq), dtype=torch.int32, device=dev),
                    # the stack's top is its last entry: page 0 is taken first
                    torch.arange(int(n_pages) - 1, -1, -1, dtype=torch.int32, device=dev),
                    torch.full((1,), int(n_pages), dtype=torch.int32, device=dev),
-                   torch.zeros(1, dtype=torch.int32, device=dev), None)
+                   torch.zeros(1, dtype=torch.int32, device=dev), None, *scales)
 
     @classmethod
-    def of(cls, k, v, block_table, seq_len, free_pages=None, n_free=None, error=None, page_size=None):
+    def of(cls, k, v, block_table, seq_len, free_pages=None, n_free=None, error=None, page_size=None, k_scale=None,
+           v_scale=None):
         """Bind to buffers that a program already has.  k and v may be None for a
         cache that is only planned on (page_size then says the pages' rows);
-        without free_pages and n_free it cannot be planned on."""
+        without free_pages and n_free it cannot be planned on.  Pages of 8 bits
+        come with their scales."""
         self = cls.__new__(cls)
-        self._bind(k, v, block_table, seq_len, free_pages, n_free, error, page_size)
+        self._bind(k, v, block_table, seq_len, free_pages, n_free, error, page_size, k_scale, v_scale)
         return self
 
     def layer_like(self) -> "PagedKvCache":
         """Another layer's pages with this one's tables, lengths and free pages."""
+        scales = [None if s is None else torch.ones_like(s) for s in (self.k_scale, self.v_scale)]
         return PagedKvCache.of(torch.empty_like(self.k), torch.empty_like(self.v), self.block_table, self.seq_len,
-                               self.free_pages, self.n_free, self.error)
+                               self.free_pages, self.n_free, self.error, None, *scales)
 
-    def _bind(self, k, v, block_table, seq_len, free_pages, n_free, error, page_size):
+    def _bind(self, k, v, block_table, seq_len, free_pages, n_free, error, page_size, k_scale, v_scale):
         dev = block_table.device
         self.index = _cuda(dev)
         if block_table.dim() != 2:
@@ -202,18 +212,24 @@ class PagedKvCache:
         _i32(seq_len, "seq_len", n, dev)
         if k is not None:
             dtype, shape = k.dtype, k.shape
-            if v is None or v.dtype is not dtype or v.shape != shape or (dtype is not torch.bfloat16 and dtype is not torch.float16):
-                raise ValueError("k and v must have one shape and be float16 or bfloat16")
+            if v is None or v.dtype is not dtype or v.shape != shape or dtype not in _PAGES:
+                raise ValueError("k and v must have one shape and be float16, bfloat16 or float8_e4m3fn")
             if not (len(shape) == 4 and k.device == dev and v.device == dev and k.is_contiguous() and v.is_contiguous()):
                 raise ValueError("k and v must be contiguous pages [n_pages, n_kv, page_size, head_dim] on %s" % dev)
             self.n_pages, self.n_kv, self.page_size, self.head_dim = shape
             if page_size is not None and page_size != self.page_size:
                 raise ValueError("page_size is not that of the pages")
             self.dtype = dtype
+            if dtype is _E4M3:
+                for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                    if s is None or not (s.dtype is _F32 and s.shape == shape[:2] and s.device == dev and s.is_contiguous()):
+                        raise ValueError("pages of 8 bits need %s, contiguous float32 [n_pages, n_kv] on %s" % (name, dev))
         else:
             if page_size is None or free_pages is None or v is not None:
                 raise ValueError("a cache without k and v needs page_size and free_pages")
             self.n_pages, self.n_kv, self.page_size, self.head_dim, self.dtype = free_pages.numel(), 0, int(page_size), 0, None
+        if (k_scale is not None or v_scale is not None) and self.dtype is not _E4M3:
+            raise ValueError("scales belong to pages of 8 bits")
         if free_pages is not None:
             if n_free is None:
                 raise ValueError("free_pages without n_free")
@@ -223,6 +239,7 @@ class PagedKvCache:
             error = torch.zeros(1, dtype=_I32, device=dev)
         _i32(error, "error", 1, dev)
         self.k, self.v, self.block_table, self.seq_len = k, v, block_table, seq_len
+        self.k_scale, self.v_scale = k_scale, v_scale
         self.free_pages, self.n_free, self.error = free_pages, n_free, error
 
     def device_error(self, clear: bool = True) -> int:
@@ -308,7 +325,12 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
     """Write the new rows k, v [tokens, n_kv, hd] to the plan's slots, k rotated by
     `rope` (None: as they are), and return q [tokens, n_q, hd] rotated in the
     pages' dtype (rows without a position are left as they were).
-    Inputs are float32 or the pages' dtype, all of one."""
+    Inputs are float32 or the pages' dtype, all of one.
+
+    Pages of 8 bits take float32, float16 or bfloat16: every block's scale grows to
+    what its rows need, and the codes before them move with it.  q comes in the
+    inputs' dtype, for float32 in q_out's (without one: bfloat16).  The rows of one
+    page have to stand together and in order, as a plan lays them."""
     if cache.k is None:
         raise ValueError("the cache has no pages")
     if plan.positions is None or plan.slots is None:
@@ -322,6 +344,10 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
     slots = _i32(plan.slots, "plan.slots", tokens, dev)
     if dtype not in _DTYPES or v.dtype is not dtype:
         raise ValueError("q, k and v must have one dtype: float32 or the pages'")
+    coded = cache.k_scale is not None
+    q_dtype = cache.dtype
+    if coded:
+        q_dtype = dtype if dtype is not _F32 else torch.bfloat16 if q_out is None else q_out.dtype
     shape = (tokens, n_kv, hd)
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError("k and v must be [tokens, n_kv, head_dim]")
@@ -335,12 +361,20 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
         shape = (tokens, n_q, hd)
         qi = _rows(q, "q", shape, dev)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=cache.dtype, device=dev) if stream is None else _empty([shape], cache.dtype, dev, stream)[0]
-        elif q_out.dtype is not cache.dtype:
-            raise ValueError("q_out must have the pages' dtype")
+            q_out = torch.empty(shape, dtype=q_dtype, device=dev) if stream is None else _empty([shape], q_dtype, dev, stream)[0]
+        elif q_out.dtype is not q_dtype or q_dtype is _F32:
+            raise ValueError("q_out must have the inputs' dtype, for float32 float16 or bfloat16" if coded else "q_out must have the pages' dtype")
         qo = _rows(q_out, "q_out", shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    if coded:
+        st = _abi.lib().kv_paged_append_q8(
+            None if rope is None else rope.R, qi, qo, n_q, ki, vi, n_kv, hd, _DTYPES[dtype], _DTYPES.get(q_dtype, -1), pos, slots,
+            tokens, cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.n_pages,
+            cache.page_size, cache.error.data_ptr(), _stream(index, stream))
+        if st:
+            _abi.check("kv_paged_append_q8", st)
+        return q_out
     st = _abi.lib().kv_paged_append(
         None if rope is None else rope.R, qi, qo, n_q, ki, vi, n_kv, hd, _DTYPES[dtype], _DTYPES[cache.dtype], pos, slots,
         tokens, cache.k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size, cache.error.data_ptr(),
@@ -350,11 +384,58 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
     return q_out
 
 
+def paged_read(cache: PagedKvCache, cu_rows: torch.Tensor, n_rows: int, start: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+               stream=None):
+    """Rows of requests read back from their pages: rows start[b] (int32 [n_seq];
+    None: 0) and on of every request b, as many as cu_rows (int32 [n_seq + 1]) says,
+    packed; returns (k, v) [n_rows, n_kv, hd] of `dtype` (float32, float16 or
+    bfloat16; k_out and v_out given: theirs).  Pages of any dtype.  Rows behind
+    cu_rows' last are left as they were; a row that its request does not hold reads
+    as zeros and sets the error word's bit 1."""
+    if cache.k is None:
+        raise ValueError("the cache has no pages")
+    dev, index = cache.device, cache.index
+    if _device() != index:
+        with torch.cuda.device(dev):
+            return paged_read(cache, cu_rows, n_rows, start, dtype, k_out, v_out, stream)
+    n_rows = int(n_rows)
+    if n_rows < 0:
+        raise ValueError("n_rows must not be negative")
+    cu = _i32(cu_rows, "cu_rows", cache.n_seq + 1, dev)
+    first = None if start is None else _i32(start, "start", cache.n_seq, dev)
+    shape = (n_rows, cache.n_kv, cache.head_dim)
+    given = k_out if k_out is not None else v_out
+    if given is not None:
+        dtype = given.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("paged_read gives float32, float16 or bfloat16")
+    outs = []
+    for o, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if o is None:
+            o = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty([shape], dtype, dev, stream)[0]
+        elif o.dim() != 3 or o.dtype is not dtype:
+            raise ValueError("k_out and v_out must have one dtype and be [n_rows, n_kv, head_dim]")
+        outs.append((o, _rows(o, name, shape, dev)))
+    (k_out, ko), (v_out, vo) = outs
+    ks, vs = cache.k_scale, cache.v_scale
+    st = _abi.lib().kv_paged_read(
+        cache.k.data_ptr(), cache.v.data_ptr(), None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(),
+        _PAGES[cache.dtype], cache.n_pages, cache.page_size, cache.n_kv, cache.head_dim, cache.block_table.data_ptr(),
+        cache.max_pages, cache.seq_len.data_ptr(), first, cu, cache.n_seq, ko, vo, _DTYPES[dtype], n_rows,
+        cache.error.data_ptr(), _stream(index, stream))
+    if st:
+        _abi.check("kv_paged_read", st)
+    return k_out, v_out
+
+
 @functools.lru_cache(maxsize=4096)
-def paged_attention_workspace(n_tokens: int, n_q: int, n_kv: int, head_dim: int) -> int:
-    """Bytes of workspace that paged_attention needs for up to n_tokens new rows."""
+def paged_attention_workspace(n_tokens: int, n_q: int, n_kv: int, head_dim: int, dtype: torch.dtype | None = None) -> int:
+    """Bytes of workspace that paged_attention needs for up to n_tokens new rows
+    (dtype: the pages', where they may be of 8 bits)."""
     n = C.c_int64(0)
-    _abi.call("paged_attention_workspace_bytes", int(n_tokens), int(n_q), int(n_kv), int(head_dim), C.byref(n))
+    _abi.call("paged_attention_q8_workspace_bytes" if dtype is _E4M3 else "paged_attention_workspace_bytes", int(n_tokens), int(n_q),
+              int(n_kv), int(head_dim), C.byref(n))
     return int(n.value)
 
 
@@ -363,7 +444,8 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention of the step's new rows q [tokens, n_q, hd] (appended already)
     over all rows their requests hold; out has q's shape and dtype (rows behind
-    the last new one are left as they were).
+    the last new one are left as they were).  q has the pages' dtype; over pages of
+    8 bits it is float16 or bfloat16.
     window, softcap and sinks as in decode_attention."""
     k = cache.k
     if k is None:
@@ -373,8 +455,11 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
         with torch.cuda.device(dev):
             return paged_attention(q, cache, plan, out, scale, window, softcap, sinks, workspace, stream)
     shape = q.shape
+    coded = dtype is _E4M3
+    if coded:
+        dtype = q.dtype if q.dtype is torch.bfloat16 or q.dtype is torch.float16 else None
     if len(shape) != 3 or shape[2] != hd or q.dtype is not dtype:
-        raise ValueError("q must be [tokens, n_q, head_dim] in the pages' dtype")
+        raise ValueError("q must be [tokens, n_q, head_dim] in the pages' dtype (over pages of 8 bits float16 or bfloat16)")
     tokens, n_q, _ = shape
     cu = _i32(plan.cu_new, "plan.cu_new", cache.n_seq + 1, dev)
     lens = _i32(plan.seq_len, "plan.seq_len", cache.n_seq, dev)
@@ -391,7 +476,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
     on = _stream(index, stream)
     taken = None
     if workspace is None:
-        size = paged_attention_workspace(tokens, n_q, n_kv, hd)
+        size = paged_attention_workspace(tokens, n_q, n_kv, hd, cache.dtype)
         if _take is not None and _give is not None:
             ws = taken = _take(size, on)
         else:
@@ -403,13 +488,20 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
         ws = workspace.data_ptr()
     try:
-        st = _abi.lib().paged_attention(
-            qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
-            cache.block_table.data_ptr(), cache.max_pages, cu, lens, cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale,
-            window, softcap, sinks, ws, size, cache.error.data_ptr(), on)
+        if coded:
+            st = _abi.lib().paged_attention_q8(
+                qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                cache.v_scale.data_ptr(), cache.n_pages, cache.page_size, cache.block_table.data_ptr(), cache.max_pages, cu, lens,
+                cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale, window, softcap, sinks, ws, size,
+                cache.error.data_ptr(), on)
+        else:
+            st = _abi.lib().paged_attention(
+                qi, oi, tokens, n_q, n_kv, hd, _DTYPES[dtype], k.data_ptr(), cache.v.data_ptr(), cache.n_pages, cache.page_size,
+                cache.block_table.data_ptr(), cache.max_pages, cu, lens, cache.n_seq, 1.0 / math.sqrt(hd) if scale is None else scale,
+                window, softcap, sinks, ws, size, cache.error.data_ptr(), on)
     finally:
         if taken is not None:
             _give(taken)
     if st:
-        _abi.check("paged_attention", st)
+        _abi.check("paged_attention_q8" if coded else "paged_attention", st)
     return out
