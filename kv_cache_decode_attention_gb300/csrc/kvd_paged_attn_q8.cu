@@ -1,90 +1,51 @@
 // kvd_paged_attn_q8.cu -- paged_attention over pages of 8-bit codes.
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
-#include "kvd_q8.cuh"
-#include "kvd_rope.cuh"
+#include "kvd_paged_attn_q8.cuh"
 
 namespace kvd {
 namespace {
 
-struct QaArgs {
-    const void *q;
-    void *out;
-    int64_t q_tok, q_head, out_tok, out_head;
-    const uint8_t *k, *v;
-    const float *k_scale, *v_scale;
-    const int32_t *block_table, *cu_new, *seq_len;
-    const float *sinks;
-    uint32_t *err;
-    int64_t window;
-    int32_t n_seq, n_tokens, n_q, n_kv, group, max_pages, n_pages, page_log2, hd;
-    float scale, softcap;
-};
+// The driver's encoder, looked up once; nullptr if it is missing.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
 
-// A warp for each new row and query head, a row of K and V at a time.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ QaArgs a) {
-    constexpr int kPer = HD / 32;
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0)  // requests that no row asks about are looked at too
-        for (int b = threadIdx.x; b < a.n_seq; b += blockDim.x) {
-            const int32_t q0 = a.cu_new[b], q1 = a.cu_new[b + 1], len = a.seq_len[b];
-            if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || len > (int64_t(a.max_pages) << a.page_log2)) set_error(a.err, kErrBounds);
-        }
-    const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int64_t tok = item / a.n_q;
-    const int head = int(item - tok * a.n_q), kv = head / a.group;
-    if (tok >= a.n_tokens || tok < a.cu_new[0] || tok >= a.cu_new[a.n_seq]) return;
-    int b = 0, above = a.n_seq;
-    while (above - b > 1) {
-        const int mid = (b + above) / 2;
-        if (a.cu_new[mid] <= tok) b = mid;
-        else above = mid;
-    }
-    const int32_t q0 = a.cu_new[b], q1 = a.cu_new[b + 1], len = a.seq_len[b];
-    if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || len > (int64_t(a.max_pages) << a.page_log2)) {
-        set_error(a.err, kErrBounds);
-        return;
-    }
-    const int64_t pos = int64_t(len) - (q1 - q0) + (tok - q0);
-    int64_t first = a.window > 0 ? pos - a.window + 1 : 0;
-    if (first < 0) first = 0;
-    float q[kPer], o[kPer] = {};
-    const T *qp = static_cast<const T *>(a.q) + tok * a.q_tok + head * a.q_head + lane * kPer;
-    for (int i = 0; i < kPer; ++i) q[i] = to_f32<T>(qp[i]) * a.scale;
-    float top = -INFINITY, sum = 0.0f;
-    for (int64_t p = first; p <= pos; ++p) {
-        const int32_t page = a.block_table[int64_t(b) * a.max_pages + (p >> a.page_log2)];
-        const bool there = page >= 0 && page < a.n_pages;
-        if (!there) set_error(a.err, kErrBounds);
-        const int64_t block = int64_t(there ? page : 0) * a.n_kv + kv;
-        const int64_t at = ((block << a.page_log2) + (p & ((1 << a.page_log2) - 1))) * HD + lane * kPer;
-        auto value = [&](const uint8_t *x) {
-            return there ? __half2float(__half(__nv_cvt_fp8_to_halfraw(*x, __NV_E4M3))) : 0.0f;
-        };
-        float s = 0.0f;
-        for (int i = 0; i < kPer; ++i) s += q[i] * value(a.k + at + i);
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-        s *= scale_of(a.k_scale[block], a.err);
-        if (a.softcap > 0.0f) s = a.softcap * tanhf(s / a.softcap);
-        const float now = fmaxf(top, s), f = expf(top - now), w = expf(s - now);
-        sum = sum * f + w;
-        const float wv = w * scale_of(a.v_scale[block], a.err);
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * f + wv * value(a.v + at + i);
-        top = now;
-    }
-    float g = 1.0f;
-    if (a.sinks != nullptr && top != -INFINITY) {
-        const float all = fmaxf(top, a.sinks[head]);
-        g = expf(top - all);
-        sum = sum * g + expf(a.sinks[head] - all);
-    }
-    g *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *op = static_cast<T *>(a.out) + tok * a.out_tok + head * a.out_head + lane * kPer;
-    for (int i = 0; i < kPer; ++i) op[i] = from_f32<T>(o[i] * g);
+// Codes as rows of head_dim bytes, a page of them to a box.
+bool encode(CUtensorMap *m, const void *base, int32_t hd, int64_t rows, int32_t page_size) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    const cuuint64_t dims[2] = {cuuint64_t(hd), cuuint64_t(rows)}, strides[1] = {cuuint64_t(hd)};
+    const cuuint32_t box[2] = {cuuint32_t(hd), cuuint32_t(page_size)}, ones[2] = {1, 1};
+    return fn != nullptr && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, ones,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct WsLayout {
+    int64_t cut, ml, o, total;
+};
+WsLayout ws_layout(int32_t hd) {
+    WsLayout w;
+    const int64_t rows = int64_t(2) * kQrMaxCtas * kQrRows;
+    w.cut = 0;
+    w.ml = round_up(int64_t(kQrMaxCtas) * int64_t(sizeof(QrCut)), 256);
+    w.o = w.ml + round_up(rows * 8, 256);
+    w.total = w.o + rows * hd * 4;
+    return w;
 }
 
 bool shape_ok(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t hd) {
@@ -112,7 +73,7 @@ using namespace kvd;
 extern "C" kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t head_dim,
                                                          int64_t *bytes_out) {
     if (bytes_out == nullptr || !shape_ok(n_tokens, n_q, n_kv, head_dim)) return KVD_EINVAL;
-    *bytes_out = 256;
+    *bytes_out = ws_layout(head_dim).total;
     return KVD_OK;
 }
 
@@ -152,19 +113,22 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
             !views_apart(o, make_range(v_scale, scales)))
             return KVD_EINVAL;
     }
-    int64_t need = 0;
-    paged_attention_q8_workspace_bytes(n_tokens, n_q, n_kv, head_dim, &need);
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < need) return KVD_EINVAL;
-    QaArgs a;
+    const WsLayout ws = ws_layout(head_dim);
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < ws.total) return KVD_EINVAL;
+    QrArgs a;
     std::memset(&a, 0, sizeof(a));
+    const int64_t pool_rows = n_pages * page_size * n_kv;
+    if (!encode(&a.k, k_pages, head_dim, pool_rows, page_size) || !encode(&a.v, v_pages, head_dim, pool_rows, page_size)) return KVD_EINVAL;
+    char *w = static_cast<char *>(workspace);
+    a.cut = reinterpret_cast<QrCut *>(w + ws.cut);
+    a.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
+    a.part_o = reinterpret_cast<float *>(w + ws.o);
     a.q = q->data;
     a.q_tok = q->token_stride;
     a.q_head = q->head_stride;
     a.out = out->data;
     a.out_tok = out->token_stride;
     a.out_head = out->head_stride;
-    a.k = static_cast<const uint8_t *>(k_pages);
-    a.v = static_cast<const uint8_t *>(v_pages);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.block_table = block_table;
@@ -172,20 +136,26 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
     a.seq_len = seq_len;
     a.sinks = sinks;
     a.err = err;
+    // every position is below 2^31, so a window from there on hides nothing
     a.window = window < (int64_t(1) << 31) ? window : 0;
     a.n_seq = n_seq;
     a.n_tokens = int32_t(n_tokens);
-    a.n_q = n_q;
     a.n_kv = n_kv;
     a.group = n_q / n_kv;
+    a.tile_tok = kQrRows / a.group;
     a.max_pages = max_pages;
     a.n_pages = int32_t(n_pages);
     a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
-    a.hd = head_dim;
-    a.scale = scale;
-    a.softcap = softcap;
-    const auto kern = dtype == KVD_T_F16 ? (head_dim == 64 ? rows_kernel<__half, 64> : rows_kernel<__half, 128>)
-                                         : (head_dim == 64 ? rows_kernel<__nv_bfloat16, 64> : rows_kernel<__nv_bfloat16, 128>);
-    const cudaError_t e = launch_pdl(kern, dim3(unsigned(ceil_div(n_tokens * n_q, 4))), dim3(128), 0, as_stream(stream), a);
+    a.pool_rows = int32_t(pool_rows);
+    a.give_up = -1;
+    // A cap so far above the scale that their quotient is no normal number (a raw
+    // score would have to pass 10^34 to feel it) is none.
+    const bool cap = softcap > 0.0f && scale / softcap >= FLT_MIN;
+    a.mul = cap ? float(2.0 * 1.4426950408889634 * double(scale) / softcap) : scale * log2e;
+    a.cap = cap ? softcap * log2e : 0.0f;
+    const bool bf16 = dtype == KVD_T_BF16;
+    cudaStream_t st = as_stream(stream);
+    const cudaError_t e = head_dim == 64 ? (bf16 ? launch_qr<64, true>(a, st) : launch_qr<64, false>(a, st))
+                                         : (bf16 ? launch_qr<128, true>(a, st) : launch_qr<128, false>(a, st));
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }

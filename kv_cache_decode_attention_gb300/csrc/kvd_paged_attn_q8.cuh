@@ -1,0 +1,835 @@
+// kvd_paged_attn_q8.cuh -- attention over pages of e4m3 codes, a few query rows at a
+// time, on the fifth-generation tensor cores.
+//
+// out_t = sum_p softmax_p(scale q_t . k_p) v_p with k_p = c_p s_K(p), v_p = d_p s_V(p):
+// codes c, d and one scale for each page of a KV head.  Decode steps and drafts are
+// bound by the bytes of K and V, so nothing is made of them but operands: the codes
+// go from the TMA's tile straight into the MMAs (kind::f8f6f4), as their M side,
+//   S^T [128 rows of K x N] = K Q^T,    O^T [head_dim x N] = V^T P^T,
+// and what is not of 8 bits becomes several e4m3 terms beside one another in N, each
+// with its own accumulator and so its own scale:
+//   q, scaled by a power of two so that its row's largest lies in [128, 256), is
+//   t0 + t1 / 16 (+ t2 / 256): eight significant bits for bf16, twelve for f16, down
+//   to 2^-21 (2^-25) of the largest;
+//   p, a weight with the scale of its V block, relative to the largest of its tile,
+//   likewise.
+// So S is exact but for its f32 sums, and the weights are rounded once, to about q's
+// type.  (Converting the codes to 16 bits instead costs 48 KB of shared-memory traffic
+// a tile of 16, which at the rate of HBM leaves no room for the MMAs' own.)
+//
+// An item is one (request, KV head, run of tokens): kQrRows query rows (token, head of
+// the group) at most.  Items are cut into tiles of 128 rows and every CTA gets the
+// same number of consecutive ones, however long the requests are; an item that is cut
+// leaves its pieces (unnormalised output, reference, sum) to qr_join_kernel.
+//
+// A CTA, of which an SM holds three (f16: two, with three stages each):
+//   warps 0-3  softmax, a thread per row of K: its scales are the thread's own, masks
+//              of single tokens a comparison; and the sum of the O^T over the tiles,
+//              a thread per channel, in f32 registers (fresh accumulators each tile:
+//              no rescaling in TMEM, a weight's range counts within its tile only);
+//   warp 4     walks the work, looks up pages and scales, TMA loads of K and V;
+//   warp 5     issues the MMAs: S^T of tile i + 1 before O^T of tile i.
+// Barriers, all of one phase a tile (K, V: a ring of kStages): s_full, s_free (S is in
+// registers), p_ready (P is in shared memory, O of the tile before in registers),
+// o_full.  No warp can be two phases ahead of one that waits: S(i + 1) waits for
+// s_free(i), P(i + 1) for o_full(i).
+#pragma once
+
+#include "kvd_paged_attn.cuh"
+#include "kvd_q8.cuh"
+#include "kvd_rope.cuh"
+
+namespace kvd {
+
+constexpr int kQrTile = 128;     // rows of K and V of a tile
+constexpr int kQrRows = 16;      // query rows of an item
+constexpr int kQrThreads = 192;
+constexpr int kQrMaxCtas = 152 * 3;
+constexpr int kQrJobs = 4;
+constexpr int kQrMaxSeq = 1 << 20;
+
+// A cut item as qr_join_kernel finds it; n = 0: none.
+struct QrCut {
+    int64_t unit0, total;
+    int32_t units, rows, q_row, kv_head, n, pad;
+};
+
+struct QrArgs {
+    CUtensorMap k, v;
+    const void *q;
+    void *out;
+    int64_t q_tok, q_head, out_tok, out_head;  // strides in elements
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *cu_new, *seq_len;
+    const float *sinks;
+    float *part_o;    // [2 * ctas][kQrRows][hd]
+    float2 *part_ml;  // [2 * ctas][kQrRows]: reference (log2 units), sum
+    QrCut *cut;       // [ctas]: the cut item that begins in each CTA
+    uint32_t *err;
+    int64_t window;   // below 2^31; 0 = none
+    int32_t ctas, n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2, pool_rows;
+    int32_t give_up;  // for tests: the CTA whose waits end so many ns after it began, or -1
+    uint32_t give_up_ns;
+    float mul;        // scale * log2 e; with a cap 2 * scale * log2 e / softcap
+    float cap;        // softcap * log2 e, or 0
+};
+
+// ---------------------------------------------------------------- tcgen05, 8 bits
+
+__device__ __forceinline__ void tc_ld16(uint32_t addr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Instruction descriptor of kind::f8f6f4, e4m3 both: f32 accumulator, M x N, operands MN-major or not.
+__host__ __device__ constexpr uint32_t tc_idesc8(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+// Shared-memory matrix descriptor; type 2: 128-byte swizzle, 4: 64-byte, 0: none.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t type) {
+    return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(lbo >> 4) << 16 | uint64_t(sbo >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(type) << 61;
+}
+
+// ---------------------------------------------------------------- the work
+
+struct QrItem {
+    int32_t count, first_pos, tile0, tiles;
+};
+__device__ __forceinline__ PaSeq qr_seq(const QrArgs &a, int b, bool report) {
+    PaSeq s = {0, 0, 0};
+    if (b >= a.n_seq) return s;
+    const int32_t q0 = a.cu_new[b], q1 = a.cu_new[b + 1], len = a.seq_len[b];
+    if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || len > (int64_t(a.max_pages) << a.page_log2)) {
+        if (report) set_error(a.err, kErrBounds);
+        return s;
+    }
+    s.q0 = q0;
+    s.fresh = q1 - q0;
+    s.len = len;
+    return s;
+}
+__device__ __forceinline__ QrItem qr_item(const QrArgs &a, const PaSeq &s, int32_t tok) {
+    QrItem it;
+    const int32_t left = s.fresh - tok;
+    it.count = left < a.tile_tok ? left : a.tile_tok;
+    it.first_pos = s.len - s.fresh + tok;
+    int64_t lo = a.window > 0 ? int64_t(it.first_pos) - a.window + 1 : 0;
+    if (lo < 0) lo = 0;
+    int32_t hi = it.first_pos + it.count;
+    if (hi < 0) hi = 0;
+    it.tile0 = int32_t(lo) / kQrTile;
+    const int32_t n = (hi + kQrTile - 1) / kQrTile - it.tile0;
+    it.tiles = n > 1 ? n : 1;
+    return it;
+}
+// The next item in the order (request, KV head, token run).
+__device__ __forceinline__ void qr_next(const QrArgs &a, PaWalk &w) {
+    w.tok += a.tile_tok;
+    if (w.tok < w.s.fresh) return;
+    w.tok = 0;
+    if (++w.h < a.n_kv) return;
+    w.h = 0;
+    do {
+        ++w.b;
+        w.s = qr_seq(a, w.b, false);
+    } while (w.s.fresh == 0 && w.b < a.n_seq);
+}
+
+// CTA c takes tiles [c W / ctas, (c + 1) W / ctas) of the W there are.  All
+// threads; the result is in shared memory.  (As pa_cut, in units of single tiles.)
+__device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *warp_sums) {
+    constexpr int kWarps = kQrThreads / 32;
+    const int per = (a.n_seq + kQrThreads - 1) / kQrThreads;
+    const int b0 = int(threadIdx.x) * per < a.n_seq ? int(threadIdx.x) * per : a.n_seq;
+    const int b1 = b0 + per < a.n_seq ? b0 + per : a.n_seq;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t mine = 0, off = 0, u = 0, from = 0, to = 0;
+    uint64_t total = 0;
+    PaSeq s = {0, 0, 0};
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+        int b = b0;
+        if (turn == 0 || per > 1) {  // a thread's only request is still at hand
+#pragma unroll 1
+            for (; b < b1; ++b) {
+                s = qr_seq(a, b, turn == 0 && blockIdx.x == 0);
+                u = 0;
+#pragma unroll 1
+                for (int32_t tok = 0; tok < s.fresh; tok += a.tile_tok) u += qr_item(a, s, tok).tiles;
+                if (turn == 0) mine += u * a.n_kv;
+                else if (off < u * a.n_kv) break;
+                else off -= u * a.n_kv;
+            }
+        }
+        if (turn == 1) {
+            int32_t h = 0, tok = 0;
+#pragma unroll 1
+            for (; off >= u; off -= u) ++h;
+#pragma unroll 1
+            for (;; tok += a.tile_tok) {
+                const int32_t n = qr_item(a, s, tok).tiles;
+                if (off < n) break;
+                off -= n;
+            }
+            *out = PaStart{b, h, tok, int32_t(off), s, to - from, from, int64_t(total)};
+            break;
+        }
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) warp_sums[w] = x;
+        if (threadIdx.x == 0) out->units = 0;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            before += i < w ? warp_sums[i] : 0;
+            total += uint64_t(warp_sums[i]);
+        }
+        before += x - mine;
+        from = total * blockIdx.x / gridDim.x;
+        to = total * (blockIdx.x + 1) / gridDim.x;
+        off = from - before;
+        if (from >= to || off < 0 || off >= mine) break;
+    }
+    __syncthreads();
+}
+
+// The CTAs that hold pieces of a cut item.  A piece of CTA c is kept in slot 2 c + 1 if
+// it begins its item, else in slot 2 c.
+static __device__ __forceinline__ int32_t qr_cta_of(int64_t u, int64_t total, int32_t ctas) {
+    return int32_t((uint64_t(u + 1) * ctas + total - 1) / uint64_t(total)) - 1;
+}
+struct QrPieces {
+    int32_t first, n, ctas;
+    int64_t unit0, sparse;  // sparse = units in all, if fewer than CTAs (each has one then), else 0
+    __device__ __forceinline__ QrPieces(int64_t unit0_, int32_t units, int64_t total, int32_t ctas_) {
+        ctas = ctas_;
+        first = qr_cta_of(unit0_, total, ctas);
+        sparse = total < ctas ? total : 0;
+        unit0 = unit0_;
+        n = sparse != 0 ? units : qr_cta_of(unit0_ + units - 1, total, ctas) - first + 1;
+    }
+    __device__ __forceinline__ int64_t slot(int32_t i) const {
+        if (i == 0) return 2 * first + 1;
+        return 2 * (sparse != 0 ? qr_cta_of(unit0 + i, sparse, ctas) : first + i);
+    }
+};
+
+// ---------------------------------------------------------------- the kernel
+
+template <int HD, bool BF16>
+struct QrShape {
+    static constexpr int kTerms = BF16 ? 2 : 3;
+    static constexpr int kN = kQrRows * kTerms;
+    // what fits: f16's third terms take the third CTA's room
+    static constexpr int kPerSm = BF16 ? 3 : 2, kCtas = 152 * kPerSm;
+    static constexpr int kStages = (BF16 ? 2 : 3) * (HD == 128 ? 1 : 2);
+    // Scales of tile t + kScales replace those of tile t once its K is asked for, for
+    // which S of tile t + 2 is over, and so tile t's softmax has read its own.
+    static constexpr int kScales = kStages + 2;
+    static constexpr int kTileBytes = kQrTile * HD;
+    static constexpr int kQBytes = kN * HD, kPBytes = kN * kQrTile;
+    static constexpr int kK = 0, kV = kStages * kTileBytes, kQ = 2 * kStages * kTileBytes, kP = kQ + kQBytes, kTotal = kP + kPBytes;
+    static constexpr int kColumns = 2 * kN <= 64 ? 64 : 128;  // of TMEM: S, then O
+    static constexpr uint32_t kSwizzle = HD == 128 ? 2 : 4, kAtom = HD * 8;
+};
+
+struct QrJob {
+    int32_t n, tile0, head, whole;  // tiles of this CTA's part of it, the first; begins here; begins and ends here
+    int32_t q_row, count, kv_head, first_pos, len;
+};
+
+template <typename S>
+struct QrShared {
+    uint64_t k_full[S::kStages], k_empty[S::kStages], v_full[S::kStages], v_empty[S::kStages], sc_full[S::kScales];
+    uint64_t s_full, s_free, p_ready, o_full, q_ready, job_full[kQrJobs], job_empty[kQrJobs], drain;
+    QrJob job[kQrJobs];
+    PaStart start;
+    int64_t warp_sums[kQrThreads / 32];
+    uint32_t tmem;
+    int stop;
+    uint64_t began;
+    float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's
+    float top[2][kQrRows][4];     // of a tile's columns, by warp
+    float ref[4][kQrRows];        // the tile's reference less 8, by warp
+    float2 fold[2][4][kQrRows];   // factors of old and new sums, by warp
+    float col[kQrRows];
+};
+
+// Waits end after two seconds, or once another wait of the CTA has (or at a test's
+// wish): nothing here waits for more than a tile's copies and MMAs.
+template <typename S>
+static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, QrShared<S> &sh, uint64_t *bar, uint32_t parity) {
+    volatile int *stop = &sh.stop;
+    const bool early = a.give_up == int32_t(blockIdx.x);
+    const uint64_t since = early ? sh.began : global_ns(), limit = early ? a.give_up_ns : 2000000000ull;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*stop != 0) return false;
+        if (global_ns() - since >= limit) {
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+template <typename S>
+__device__ __forceinline__ bool qr_wait(const QrArgs &a, QrShared<S> &sh, uint64_t *bar, uint32_t parity) {
+    const bool ok = mbar_try_wait(bar, parity) || qr_wait_long(a, sh, bar, parity);
+    return __all_sync(~0u, ok);
+}
+__device__ __forceinline__ void qr_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) pa_arrive(bar);
+}
+__device__ __forceinline__ void qr_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The largest of a warp's values.
+__device__ __forceinline__ float warp_top(float x) {
+    const int32_t b = __float_as_int(x);
+    const int32_t i = __reduce_max_sync(~0u, b ^ ((b >> 31) & 0x7fffffff));  // ordered as integers
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// x (two values) as e4m3 terms x = t0 + t1 / 16 (+ t2 / 256), packed in 16 bits each.
+template <int TERMS>
+__device__ __forceinline__ void split2(float x, float y, uint32_t *t) {
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        t[i] = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+        if (i + 1 == TERMS) break;
+        const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(t[i]), __NV_E4M3)));
+        x = (x - v.x) * 16.0f;
+        y = (y - v.y) * 16.0f;
+    }
+}
+template <int TERMS>
+__device__ __forceinline__ float joined(const float *x, int c) {
+    float v = fmaf(x[kQrRows + c], 1.0f / 16, x[c]);
+    if constexpr (TERMS == 3) v = fmaf(x[2 * kQrRows + c], 1.0f / 256, v);
+    return v;
+}
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_kernel(const __grid_constant__ QrArgs a) {
+    using S = QrShape<HD, BF16>;
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int kTerms = S::kTerms;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    QrShared<S> &sh = *reinterpret_cast<QrShared<S> *>(smem_raw + S::kTotal);
+    const uint32_t smem = smem_addr(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
+            mbar_init(&sh.v_full[i], 1);
+            mbar_init(&sh.v_empty[i], 1);
+        }
+        for (int i = 0; i < S::kScales; ++i) mbar_init(&sh.sc_full[i], 1);
+        for (int i = 0; i < kQrJobs; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], 5);  // softmax warps and the MMAs'
+        }
+        mbar_init(&sh.s_full, 1);
+        mbar_init(&sh.s_free, 4);
+        mbar_init(&sh.p_ready, 4);
+        mbar_init(&sh.o_full, 1);
+        mbar_init(&sh.q_ready, 4);
+        mbar_init(&sh.drain, 1);
+        fence_mbar_init();
+        sh.stop = 0;
+        sh.began = global_ns();
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(S::kColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_before();
+    }
+    if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.k : &a.v) : "memory");
+    pdl_wait();
+    qr_cut(a, &sh.start, sh.warp_sums);  // synchronises the CTA
+    tc_after();
+    const uint32_t tmem = sh.tmem;
+    const PaStart st = sh.start;
+    uint32_t k_loads = 0, v_loads = 0;  // tiles asked for
+    if (threadIdx.x == 128) a.cut[blockIdx.x].n = 0;  // whose thread writes a record, too
+
+    if (st.units > 0) {
+        if (warp == 4) {
+            // -------------------------------------------------------- work and loads
+            PaWalk w = {st.b, st.h, st.tok, st.s};
+            int32_t unit = st.unit;
+            int64_t left = st.units;
+            const int ppt = kQrTile >> a.page_log2;
+            const uint32_t box = uint32_t(HD) << a.page_log2;  // bytes of a page
+            bool ok = true;
+            for (uint32_t at = 0;; ++at) {
+                QrJob &job = sh.job[at % kQrJobs];
+                if (at >= kQrJobs) ok = qr_wait(a, sh, &sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1);
+                if (!ok) break;
+                if (left <= 0) {
+                    if (lane == 0) job.n = 0;
+                    qr_arrive(&sh.job_full[at % kQrJobs]);
+                    break;
+                }
+                const QrItem it = qr_item(a, w.s, w.tok);
+                const int32_t have = it.tiles - unit, n = left < have ? int32_t(left) : have, tile0 = it.tile0 + unit;
+                const bool whole = unit == 0 && n == it.tiles;
+                if (lane == 0) {
+                    job = QrJob{n, tile0, unit == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
+                    if (unit == 0 && !whole)
+                        a.cut[blockIdx.x] = QrCut{st.from + (st.units - left), st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
+                }
+                qr_arrive(&sh.job_full[at % kQrJobs]);
+                const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
+                const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
+                // lane's page of a tile, -1 = none
+                auto page_of = [&](int32_t t) {
+                    const int32_t p = (tile0 + t) * ppt + lane;
+                    int32_t page = -1;
+                    if (t < n && lane < ppt && p < held) {
+                        page = table[p];
+                        if (uint32_t(page) >= uint32_t(a.n_pages)) {
+                            set_error(a.err, kErrBounds);
+                            page = -1;
+                        }
+                    }
+                    return page;
+                };
+                const int32_t h = w.h;
+                auto scales = [&](int32_t page) {
+                    float2 s = make_float2(1.0f, 1.0f);
+                    if (page >= 0) s = make_float2(a.k_scale[int64_t(page) * a.n_kv + h], a.v_scale[int64_t(page) * a.n_kv + h]);
+                    return s;
+                };
+                auto load = [&](const CUtensorMap *map, uint32_t dst, int32_t page, uint64_t *bar) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
+                    __syncwarp();
+                    if (lane < ppt) tma_2d(dst + lane * box, map, 0, page < 0 ? a.pool_rows : (page * a.n_kv + h) << a.page_log2, bar);
+                };
+                auto load_k = [&](int32_t page, float2 s) {
+                    const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
+                    if (turn > 0) ok = qr_wait(a, sh, &sh.k_empty[slot], (turn & 1) ^ 1);
+                    if (!ok) return;
+                    if (lane < ppt) {
+                        const float vs = scale_of(s.y, a.err);
+                        sh.scale[sc][lane] = make_float4(scale_of(s.x, a.err), log2f(vs), 1.0f / vs, 0.0f);
+                    }
+                    qr_arrive(&sh.sc_full[sc]);
+                    load(&a.k, smem + S::kK + slot * S::kTileBytes, page, &sh.k_full[slot]);
+                    ++k_loads;
+                };
+                // K runs a tile ahead of V, page numbers two and scales one ahead of K
+                int32_t page = page_of(0), next = page_of(1);
+                float2 s = scales(next);
+                load_k(page, scales(page));
+                for (int32_t t = 0; ok && t < n; ++t) {
+                    const int32_t after = page_of(t + 2);
+                    if (t + 1 < n) load_k(next, s);
+                    if (!ok) break;
+                    const uint32_t slot = v_loads % S::kStages, turn = v_loads / S::kStages;
+                    if (turn > 0) ok = qr_wait(a, sh, &sh.v_empty[slot], (turn & 1) ^ 1);
+                    if (!ok) break;
+                    load(&a.v, smem + S::kV + slot * S::kTileBytes, page, &sh.v_full[slot]);
+                    ++v_loads;
+                    s = scales(after);
+                    page = next;
+                    next = after;
+                }
+                if (!ok) break;
+                left -= have;
+                unit = 0;
+                if (left > 0) qr_next(a, w);
+            }
+        } else if (warp == 5) {
+            // -------------------------------------------------------- MMAs
+            uint32_t g = 0;  // tiles so far
+            bool ok = true;
+            auto score = [&](uint32_t i) {
+                const uint32_t slot = i % S::kStages;
+                ok = qr_wait(a, sh, &sh.k_full[slot], i / S::kStages & 1);
+                if (ok && i > 0) ok = qr_wait(a, sh, &sh.s_free, (i - 1) & 1);
+                if (!ok) return;
+                tc_after();
+                if (elect_one()) {
+                    constexpr uint32_t id = tc_idesc8(128, S::kN, false, false);
+                    const uint64_t kd = tc_desc(smem + S::kK + slot * S::kTileBytes, 16, S::kAtom, S::kSwizzle);
+                    const uint64_t qd = tc_desc(smem + S::kQ, 16, S::kAtom, S::kSwizzle);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 32; ++kk) tc_mma8(tmem, kd + kk * 2, qd + kk * 2, id, kk != 0);
+                }
+                __syncwarp();
+                tc_commit(&sh.s_full);
+                tc_commit(&sh.k_empty[slot]);
+            };
+            for (uint32_t at = 0;; ++at) {
+                ok = qr_wait(a, sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
+                if (!ok) break;
+                const uint32_t n = uint32_t(sh.job[at % kQrJobs].n);
+                qr_arrive(&sh.job_empty[at % kQrJobs]);
+                if (n == 0) break;
+                ok = qr_wait(a, sh, &sh.q_ready, at & 1);
+                if (!ok) break;
+                score(g);
+                for (uint32_t i = g; ok && i < g + n; ++i) {
+                    if (i + 1 < g + n) score(i + 1);
+                    if (!ok) break;
+                    const uint32_t slot = i % S::kStages;
+                    ok = qr_wait(a, sh, &sh.v_full[slot], i / S::kStages & 1) && qr_wait(a, sh, &sh.p_ready, i & 1);
+                    if (!ok) break;
+                    tc_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = tc_idesc8(HD, S::kN, true, true);
+                        const uint64_t vd = tc_desc(smem + S::kV + slot * S::kTileBytes, kQrTile * 128, S::kAtom, S::kSwizzle);
+                        const uint64_t pd = tc_desc(smem + S::kP, 128, kQrTile * 16, 0);
+#pragma unroll
+                        for (int kk = 0; kk < kQrTile / 32; ++kk)
+                            tc_mma8(tmem + S::kN, vd + kk * (32 * HD >> 4), pd + kk * (512 >> 4), id, kk != 0);
+                    }
+                    __syncwarp();
+                    tc_commit(&sh.o_full);
+                    tc_commit(&sh.v_empty[slot]);
+                }
+                if (!ok) break;
+                g += n;
+            }
+        } else {
+            // -------------------------------------------------------- softmax and sums
+            const int row = threadIdx.x;                 // of the tile
+            const uint32_t t_row = tmem + (uint32_t(warp * 32) << 16);
+            // the channel whose sums this thread keeps: rows of 64 lie in the first 16 lanes of each warp
+            const int chan = HD == 128 ? row : warp * 16 + lane;
+            const bool has_chan = HD == 128 || lane < 16;
+            uint32_t g = 0;
+            bool ok = true;
+            for (uint32_t at = 0;; ++at) {
+                ok = qr_wait(a, sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
+                if (!ok) break;
+                const QrJob job = sh.job[at % kQrJobs];
+                qr_arrive(&sh.job_empty[at % kQrJobs]);
+                if (job.n == 0) break;
+                const int32_t live = job.count * a.group;  // query rows
+
+                // q as e4m3 terms; every MMA that read the last item's has been waited for
+                {
+                    constexpr int kPer = HD / 8;
+                    const int r = row / 8, part = row % 8;
+                    float x[kPer], top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
+                    if (r < live) {
+                        const int32_t tok = r / a.group;
+                        const T *p = static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok +
+                                     int64_t(job.kv_head * a.group + r - tok * a.group) * a.q_head + part * kPer;
+#pragma unroll
+                        for (int i = 0; i < kPer; i += 8) load8<T>(p + i, x + i);
+                    }
+                    bool fine = true;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        fine = fine && fabsf(x[i]) <= 3.4028234664e38f;
+                        top = fmaxf(top, fabsf(x[i]));
+                    }
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    const uint32_t odd = __ballot_sync(~0u, !fine) >> (lane & 24) & 0xffu;
+                    int e = 134 - int(__float_as_uint(top) >> 23);
+                    e = top == 0.0f ? 0 : e > 120 ? 120 : e < -120 ? -120 : e;
+                    const float up = __uint_as_float(uint32_t(e + 127) << 23);
+                    uint32_t t[kPer / 2][kTerms];
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i) split2<kTerms>(x[2 * i] * up, x[2 * i + 1] * up, t[i]);
+#pragma unroll
+                    for (int k = 0; k < kTerms; ++k) {
+                        const int n = k * kQrRows + r;
+                        if constexpr (HD == 128) {
+                            const uint32_t to = smem + S::kQ + n * 128 + ((part ^ (n & 7)) << 4);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(t[0][k] | t[1][k] << 16),
+                                         "r"(t[2][k] | t[3][k] << 16), "r"(t[4][k] | t[5][k] << 16), "r"(t[6][k] | t[7][k] << 16)
+                                         : "memory");
+                        } else {
+                            uint32_t to = n * 64 + part * 8;
+                            to ^= (to >> 7 & 3) << 4;
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(smem + S::kQ + to), "r"(t[0][k] | t[1][k] << 16),
+                                         "r"(t[2][k] | t[3][k] << 16)
+                                         : "memory");
+                        }
+                    }
+                    // a row that is not finite is none of numbers
+                    if (part == 0) sh.col[r] = odd != 0 ? __int_as_float(0x7fc00000) : a.mul * __uint_as_float(uint32_t(127 - e) << 23);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    qr_arrive(&sh.q_ready);
+                    qr_sync();
+                }
+
+                float acc[kQrRows], sum[kQrRows];
+#pragma unroll
+                for (int c = 0; c < kQrRows; ++c) acc[c] = sum[c] = 0.0f;
+                float m_run = -INFINITY;  // of column lane % 16
+                // the tile's part of the sums, once its O is there
+                auto take = [&](float *o) {
+                    tc_after();
+                    if constexpr (kTerms == 2) {
+                        tc_ld32(t_row + S::kN, o);
+                    } else {
+                        tc_ld32(t_row + S::kN, o);
+                        tc_ld16(t_row + S::kN + 32, o + 32);
+                    }
+                    tc_wait_ld();
+                    tc_before();
+                };
+                auto fold = [&](const float *o, uint32_t i) {
+#pragma unroll
+                    for (int c = 0; c < kQrRows; ++c) {
+                        const float2 f = sh.fold[i & 1][warp][c];
+                        acc[c] = fmaf(acc[c], f.x, joined<kTerms>(o, c) * f.y);
+                    }
+                };
+                for (int32_t i = 0; i < job.n; ++i, ++g) {
+                    ok = qr_wait(a, sh, &sh.sc_full[g % S::kScales], g / S::kScales & 1);
+                    if (!ok) break;
+                    const float4 sc = sh.scale[g % S::kScales][row >> a.page_log2];
+                    ok = qr_wait(a, sh, &sh.s_full, g & 1);
+                    if (!ok) break;
+                    float x[kQrRows];
+                    {
+                        float s[S::kN];
+                        tc_after();
+                        tc_ld32(t_row, s);
+                        if constexpr (kTerms == 3) tc_ld16(t_row + 32, s + 32);
+                        tc_wait_ld();
+                        tc_before();
+                        qr_arrive(&sh.s_free);
+#pragma unroll
+                        for (int c = 0; c < kQrRows; ++c) x[c] = joined<kTerms>(s, c) * sc.x * sh.col[c];
+                    }
+                    if (a.cap > 0.0f) {
+#pragma unroll
+                        for (int c = 0; c < kQrRows; ++c) x[c] = pa_tanh_of_any(x[c]) * a.cap;
+                    }
+                    // masks: rows behind a token, and before its window
+                    const int32_t key = (job.tile0 + i) * kQrTile + row;
+                    const int32_t key0 = key - row, last = job.first_pos + job.count - 1;
+                    const int64_t lo = a.window > 0 ? int64_t(job.first_pos) - a.window + 1 : 0;  // of the first token
+                    if (key0 + kQrTile - 1 > job.first_pos || (a.window > 0 && key0 < lo + job.count - 1)) {
+#pragma unroll
+                        for (int c = 0; c < kQrRows; ++c) {
+                            int32_t tok = a.group == 1 ? c : c / a.group;
+                            if (job.count == 1) tok = 0;
+                            const int32_t pos = job.first_pos + tok;
+                            const bool seen = key <= pos && pos <= last && (a.window == 0 || key > pos - a.window);
+                            x[c] = seen ? x[c] : -INFINITY;
+                        }
+                    }
+                    // the tile's reference: the largest weight with its block's scale
+#pragma unroll
+                    for (int c = 0; c < kQrRows; ++c) x[c] += sc.y;
+#pragma unroll
+                    for (int c = 0; c < kQrRows; ++c) {
+                        const float t = warp_top(x[c]);
+                        if (lane == c) sh.top[i & 1][c][warp] = t;
+                    }
+                    qr_sync();
+                    {
+                        const int c = lane % kQrRows;
+                        const float4 t = *reinterpret_cast<const float4 *>(sh.top[i & 1][c]);
+                        const float ref = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), now = fmaxf(m_run, ref);
+                        const float base = now == -INFINITY ? 0.0f : now;
+                        // weights are held 2^8 higher
+                        if (lane < kQrRows) {
+                            sh.ref[warp][c] = ref == -INFINITY ? 0.0f : ref - 8.0f;
+                            sh.fold[i & 1][warp][c] = make_float2(ex2(m_run - base), ex2(ref - base) * 0.00390625f);
+                        }
+                        m_run = now;
+                        __syncwarp();
+                    }
+                    uint32_t p[kQrRows / 2][kTerms];
+#pragma unroll
+                    for (int c = 0; c < kQrRows; c += 2) {
+                        const float2 ref = *reinterpret_cast<const float2 *>(&sh.ref[warp][c]);
+                        const float4 f = *reinterpret_cast<const float4 *>(&sh.fold[i & 1][warp][c]);
+                        const float w0 = ex2(x[c] - ref.x), w1 = ex2(x[c + 1] - ref.y);
+                        sum[c] = fmaf(sum[c], f.x, w0 * sc.z * f.y);
+                        sum[c + 1] = fmaf(sum[c + 1], f.z, w1 * sc.z * f.w);
+                        split2<kTerms>(w0, w1, p[c / 2]);
+                    }
+                    // rows of V that nobody holds: their weights are zero, but zero times NaN is not
+                    if (key0 + kQrTile > job.len) {
+                        ok = qr_wait(a, sh, &sh.v_full[g % S::kStages], g / S::kStages & 1);
+                        if (!ok) break;
+                        if (key >= job.len) {
+                            const uint32_t v = smem + S::kV + g % S::kStages * S::kTileBytes + row * HD;
+#pragma unroll
+                            for (int b = 0; b < HD; b += 16) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + b), "r"(0) : "memory");
+                        }
+                    }
+                    float o[S::kN];
+                    if (i > 0) {
+                        ok = qr_wait(a, sh, &sh.o_full, (g - 1) & 1);
+                        if (!ok) break;
+                        take(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kTerms; ++k)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem + S::kP + k * (kQrTile * 16) + row * 16),
+                                     "r"(p[0][k] | p[1][k] << 16), "r"(p[2][k] | p[3][k] << 16), "r"(p[4][k] | p[5][k] << 16), "r"(p[6][k] | p[7][k] << 16)
+                                     : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_before();
+                    qr_arrive(&sh.p_ready);
+                    if (i > 0) fold(o, uint32_t(i - 1));
+                }
+                if (!ok) break;
+                {
+                    float o[S::kN];
+                    ok = qr_wait(a, sh, &sh.o_full, (g - 1) & 1);
+                    if (!ok) break;
+                    take(o);
+                    fold(o, uint32_t(job.n - 1));
+                }
+                // the sums over the tile's rows, by way of the maxima's buffer that is not the last tile's
+                float(*const sums)[4] = sh.top[job.n & 1];
+#pragma unroll
+                for (int c = 0; c < kQrRows; ++c) {
+                    float s = sum[c];
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+                    if (lane == c) sums[c][warp] = s;
+                }
+                qr_sync();
+                const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
+#pragma unroll
+                for (int c = 0; c < kQrRows; ++c) {
+                    if (c >= live) break;
+                    const float4 s4 = *reinterpret_cast<const float4 *>(sums[c]);
+                    float s = (s4.x + s4.y) + (s4.z + s4.w);
+                    const float m = __shfl_sync(~0u, m_run, c);
+                    if (job.whole == 0) {
+                        if (row == 0) a.part_ml[slot * kQrRows + c] = make_float2(m, s);
+                        if (has_chan) a.part_o[(slot * kQrRows + c) * HD + chan] = acc[c];
+                        continue;
+                    }
+                    const int32_t tok = c / a.group, head = job.kv_head * a.group + c - tok * a.group;
+                    float f = 1.0f;
+                    if (a.sinks != nullptr && m != -INFINITY) {
+                        const float sink = a.sinks[head] * 1.4426950408889634f, all = fmaxf(m, sink);
+                        f = ex2(m - all);
+                        s = s * f + ex2(sink - all);
+                    }
+                    f *= s == 0.0f ? 0.0f : 1.0f / s;
+                    if (has_chan) static_cast<T *>(a.out)[(int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head + chan] = from_f32<T>(acc[c] * f);
+                }
+                // (the next item's sums are written behind qr_sync calls that every warp passes after this)
+            }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (*static_cast<volatile int *>(&sh.stop) != 0) {
+        // given up: nothing may be in flight into this CTA's memory
+        if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
+        if (warp == 5) {
+            tc_commit(&sh.drain);
+            mbar_wait_bounded(&sh.drain, 0, 500000000ull);
+        }
+        if (warp == 4)
+            for (uint32_t i = 0; i < uint32_t(S::kStages); ++i) {
+                if (k_loads > i) mbar_wait_bounded(&sh.k_full[(k_loads - 1 - i) % S::kStages], (k_loads - 1 - i) / S::kStages & 1, 500000000ull);
+                if (v_loads > i) mbar_wait_bounded(&sh.v_full[(v_loads - 1 - i) % S::kStages], (v_loads - 1 - i) / S::kStages & 1, 500000000ull);
+            }
+        tc_before();
+        __syncthreads();
+        tc_after();
+    }
+    pdl_trigger();
+    if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
+}
+
+// CTA c joins the rows of the cut item that begins in CTA c: a warp for each, whose
+// lanes stand for channels, four pieces under way at a time.
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ QrArgs a) {
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int kPer = HD / 32;
+    pdl_wait();
+    const QrCut cut = a.cut[blockIdx.x];
+    if (cut.n == 0) return;
+    const QrPieces pieces(cut.unit0, cut.units, cut.total, a.ctas);
+    const int32_t col = int32_t(threadIdx.x & 31) * kPer;
+    for (int32_t r = threadIdx.x >> 5; r < cut.rows; r += 8) {
+        float top = -INFINITY, sum = 0.0f, o[kPer] = {};
+#pragma unroll 1
+        for (int32_t i0 = 0; i0 < pieces.n; i0 += 4) {
+            float2 ml[4];
+            float v[4][kPer] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.0f);
+                if (i0 + i >= pieces.n) continue;
+                const int64_t at = pieces.slot(i0 + i) * kQrRows + r;
+                ml[i] = __ldcg(&a.part_ml[at]);
+                const float *p = a.part_o + at * HD + col;
+                if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[i]) = __ldcg(reinterpret_cast<const float4 *>(p));
+                else *reinterpret_cast<float2 *>(v[i]) = __ldcg(reinterpret_cast<const float2 *>(p));
+            }
+            const float now = fmaxf(max3(top, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), base = now == -INFINITY ? 0.0f : now;
+            const float f0 = ex2(top - base);
+            sum *= f0;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[c] *= f0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = ex2(ml[i].x - base);
+                sum += ml[i].y * f;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) o[c] += v[i][c] * f;
+            }
+            top = now;
+        }
+        const int32_t tok = r / a.group, head = cut.kv_head * a.group + r - tok * a.group;
+        float f = 1.0f;
+        if (a.sinks != nullptr && top != -INFINITY) {
+            const float sink = a.sinks[head] * 1.4426950408889634f, all = fmaxf(top, sink);
+            f = ex2(top - all);
+            sum = sum * f + ex2(sink - all);
+        }
+        f *= sum == 0.0f ? 0.0f : 1.0f / sum;
+        T *dst = static_cast<T *>(a.out) + (int64_t(cut.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head + col;
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2) *reinterpret_cast<uint32_t *>(dst + c) = pack2<BF16>(o[c] * f, o[c + 1] * f);
+    }
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_qr(QrArgs &a, cudaStream_t st) {
+    using S = QrShape<HD, BF16>;
+    constexpr int smem = QrShape<HD, BF16>::kTotal + int(sizeof(QrShared<S>));
+    static_assert(S::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    const auto kern = qr_kernel<HD, BF16>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    a.ctas = S::kCtas;
+    e = launch_pdl(kern, dim3(S::kCtas), dim3(kQrThreads), smem, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(S::kCtas), dim3(256), 0, st, a);
+}
+
+}  // namespace kvd
