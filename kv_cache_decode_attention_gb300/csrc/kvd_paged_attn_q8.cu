@@ -7,7 +7,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "kvd_paged_attn_q8.cuh"
+#include "kvd_paged_attn_q8p.cuh"
 
 namespace kvd {
 namespace {
@@ -35,16 +35,27 @@ bool encode(CUtensorMap *m, const void *base, int32_t hd, int64_t rows, int32_t 
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of one piece of a large item.
+int32_t piece_rows(int64_t n_tokens, int32_t group) {
+    const int64_t rows = round_up(n_tokens * group, 8);
+    return int32_t(rows < kQpMaxRows ? rows : kQpMaxRows);
+}
+
 struct WsLayout {
-    int64_t cut, ml, o, total;
+    int64_t cut[2], ml[2], o[2], total;  // of the launch for few rows, and of the one for many
 };
-WsLayout ws_layout(int32_t hd) {
+WsLayout ws_layout(int64_t n_tokens, int32_t group, int32_t hd) {
     WsLayout w;
-    const int64_t rows = int64_t(2) * kQrMaxCtas * kQrRows;
-    w.cut = 0;
-    w.ml = round_up(int64_t(kQrMaxCtas) * int64_t(sizeof(QrCut)), 256);
-    w.o = w.ml + round_up(rows * 8, 256);
-    w.total = w.o + rows * hd * 4;
+    const int64_t ctas[2] = {kQrMaxCtas, n_tokens * group > kQrRows ? kQpCtas : 0};
+    const int64_t rows[2] = {kQrRows, piece_rows(n_tokens, group)};
+    int64_t at = 0;
+    for (int i = 0; i < 2; ++i) {
+        w.cut[i] = at;
+        w.ml[i] = w.cut[i] + round_up(ctas[i] * int64_t(sizeof(QrCut)), 256);
+        w.o[i] = w.ml[i] + round_up(2 * ctas[i] * rows[i] * 8, 256);
+        at = w.o[i] + 2 * ctas[i] * rows[i] * hd * 4;
+    }
+    w.total = at;
     return w;
 }
 
@@ -65,6 +76,35 @@ bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads) {
     return ok(tokens, r->token_stride) && ok(heads, r->head_stride);
 }
 
+// Requests of up to kQrRows query rows a KV head and larger ones are taken by a kernel
+// each; how many of either there are is known on the device only, so a call that may
+// have both launches both.
+template <int HD, bool BF16>
+cudaError_t launch(const QrArgs &call, const WsLayout &ws, void *workspace, cudaStream_t st) {
+    char *w = static_cast<char *>(workspace);
+    QrJoin j;
+    std::memset(&j, 0, sizeof(j));
+    const bool many = int64_t(call.n_tokens) * call.group > kQrRows;
+    for (int i = 0; i < (many ? 2 : 1); ++i) {
+        QrArgs &a = i == 0 ? j.few : j.many;
+        a = call;
+        a.cut = reinterpret_cast<QrCut *>(w + ws.cut[i]);
+        a.part_ml = reinterpret_cast<float2 *>(w + ws.ml[i]);
+        a.part_o = reinterpret_cast<float *>(w + ws.o[i]);
+        a.part_rows = i == 0 ? kQrRows : piece_rows(call.n_tokens, call.group);
+        a.run = i == 0 ? kQrRows / call.group : 2 * (kQrTile / call.group);
+        a.more = i == 0 ? 0 : kQrRows;
+        a.most = i == 0 ? kQrRows : INT64_MAX;
+    }
+    cudaError_t e = cudaSuccess;
+    if (many) {
+        e = launch_qp<HD, BF16>(j.many, st);
+        j.wide = int32_t(ceil_div(j.many.part_rows, 32));
+    }
+    if (e == cudaSuccess) e = launch_qr<HD, BF16>(j.few, st);
+    return e == cudaSuccess ? launch_qr_join<HD, BF16>(j, st) : e;
+}
+
 }  // namespace
 }  // namespace kvd
 
@@ -73,7 +113,7 @@ using namespace kvd;
 extern "C" kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t n_q, int32_t n_kv, int32_t head_dim,
                                                          int64_t *bytes_out) {
     if (bytes_out == nullptr || !shape_ok(n_tokens, n_q, n_kv, head_dim)) return KVD_EINVAL;
-    *bytes_out = ws_layout(head_dim).total;
+    *bytes_out = ws_layout(n_tokens, n_q / n_kv, head_dim).total;
     return KVD_OK;
 }
 
@@ -113,16 +153,12 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
             !views_apart(o, make_range(v_scale, scales)))
             return KVD_EINVAL;
     }
-    const WsLayout ws = ws_layout(head_dim);
+    const WsLayout ws = ws_layout(n_tokens, n_q / n_kv, head_dim);
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < ws.total) return KVD_EINVAL;
     QrArgs a;
     std::memset(&a, 0, sizeof(a));
     const int64_t pool_rows = n_pages * page_size * n_kv;
     if (!encode(&a.k, k_pages, head_dim, pool_rows, page_size) || !encode(&a.v, v_pages, head_dim, pool_rows, page_size)) return KVD_EINVAL;
-    char *w = static_cast<char *>(workspace);
-    a.cut = reinterpret_cast<QrCut *>(w + ws.cut);
-    a.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
-    a.part_o = reinterpret_cast<float *>(w + ws.o);
     a.q = q->data;
     a.q_tok = q->token_stride;
     a.q_head = q->head_stride;
@@ -142,7 +178,6 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
     a.n_tokens = int32_t(n_tokens);
     a.n_kv = n_kv;
     a.group = n_q / n_kv;
-    a.tile_tok = kQrRows / a.group;
     a.max_pages = max_pages;
     a.n_pages = int32_t(n_pages);
     a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
@@ -155,7 +190,7 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
     a.cap = cap ? softcap * log2e : 0.0f;
     const bool bf16 = dtype == KVD_T_BF16;
     cudaStream_t st = as_stream(stream);
-    const cudaError_t e = head_dim == 64 ? (bf16 ? launch_qr<64, true>(a, st) : launch_qr<64, false>(a, st))
-                                         : (bf16 ? launch_qr<128, true>(a, st) : launch_qr<128, false>(a, st));
+    const cudaError_t e = head_dim == 64 ? (bf16 ? launch<64, true>(a, ws, workspace, st) : launch<64, false>(a, ws, workspace, st))
+                                         : (bf16 ? launch<128, true>(a, ws, workspace, st) : launch<128, false>(a, ws, workspace, st));
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }

@@ -35,6 +35,8 @@
 // s_free(i), P(i + 1) for o_full(i).
 #pragma once
 
+#include <cfloat>
+
 #include "kvd_paged_attn.cuh"
 #include "kvd_q8.cuh"
 #include "kvd_rope.cuh"
@@ -62,12 +64,14 @@ struct QrArgs {
     const float *k_scale, *v_scale;
     const int32_t *block_table, *cu_new, *seq_len;
     const float *sinks;
-    float *part_o;    // [2 * ctas][kQrRows][hd]
-    float2 *part_ml;  // [2 * ctas][kQrRows]: reference (log2 units), sum
+    float *part_o;    // [2 * ctas][part_rows][hd]
+    float2 *part_ml;  // [2 * ctas][part_rows]: reference (log2 units), sum
     QrCut *cut;       // [ctas]: the cut item that begins in each CTA
     uint32_t *err;
     int64_t window;   // below 2^31; 0 = none
-    int32_t ctas, n_seq, n_tokens, n_kv, group, tile_tok, max_pages, n_pages, page_log2, pool_rows;
+    int32_t ctas, n_seq, n_tokens, n_kv, group, run, max_pages, n_pages, page_log2, pool_rows;
+    int64_t more, most;  // requests with more than `more` and at most `most` query rows a KV head are this launch's
+    int32_t part_rows;
     int32_t give_up;  // for tests: the CTA whose waits end so many ns after it began, or -1
     uint32_t give_up_ns;
     float mul;        // scale * log2 e; with a cap 2 * scale * log2 e / softcap
@@ -113,6 +117,8 @@ __device__ __forceinline__ PaSeq qr_seq(const QrArgs &a, int b, bool report) {
         if (report) set_error(a.err, kErrBounds);
         return s;
     }
+    const int64_t rows = int64_t(q1 - q0) * a.group;
+    if (rows <= a.more || rows > a.most) return s;
     s.q0 = q0;
     s.fresh = q1 - q0;
     s.len = len;
@@ -121,7 +127,7 @@ __device__ __forceinline__ PaSeq qr_seq(const QrArgs &a, int b, bool report) {
 __device__ __forceinline__ QrItem qr_item(const QrArgs &a, const PaSeq &s, int32_t tok) {
     QrItem it;
     const int32_t left = s.fresh - tok;
-    it.count = left < a.tile_tok ? left : a.tile_tok;
+    it.count = left < a.run ? left : a.run;
     it.first_pos = s.len - s.fresh + tok;
     int64_t lo = a.window > 0 ? int64_t(it.first_pos) - a.window + 1 : 0;
     if (lo < 0) lo = 0;
@@ -134,7 +140,7 @@ __device__ __forceinline__ QrItem qr_item(const QrArgs &a, const PaSeq &s, int32
 }
 // The next item in the order (request, KV head, token run).
 __device__ __forceinline__ void qr_next(const QrArgs &a, PaWalk &w) {
-    w.tok += a.tile_tok;
+    w.tok += a.run;
     if (w.tok < w.s.fresh) return;
     w.tok = 0;
     if (++w.h < a.n_kv) return;
@@ -147,9 +153,10 @@ __device__ __forceinline__ void qr_next(const QrArgs &a, PaWalk &w) {
 
 // CTA c takes tiles [c W / ctas, (c + 1) W / ctas) of the W there are.  All
 // threads; the result is in shared memory.  (As pa_cut, in units of single tiles.)
+template <int THREADS>
 __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *warp_sums) {
-    constexpr int kWarps = kQrThreads / 32;
-    const int per = (a.n_seq + kQrThreads - 1) / kQrThreads;
+    constexpr int kWarps = THREADS / 32;
+    const int per = (a.n_seq + THREADS - 1) / THREADS;
     const int b0 = int(threadIdx.x) * per < a.n_seq ? int(threadIdx.x) * per : a.n_seq;
     const int b1 = b0 + per < a.n_seq ? b0 + per : a.n_seq;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -165,7 +172,7 @@ __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *w
                 s = qr_seq(a, b, turn == 0 && blockIdx.x == 0);
                 u = 0;
 #pragma unroll 1
-                for (int32_t tok = 0; tok < s.fresh; tok += a.tile_tok) u += qr_item(a, s, tok).tiles;
+                for (int32_t tok = 0; tok < s.fresh; tok += a.run) u += qr_item(a, s, tok).tiles;
                 if (turn == 0) mine += u * a.n_kv;
                 else if (off < u * a.n_kv) break;
                 else off -= u * a.n_kv;
@@ -176,7 +183,7 @@ __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *w
 #pragma unroll 1
             for (; off >= u; off -= u) ++h;
 #pragma unroll 1
-            for (;; tok += a.tile_tok) {
+            for (;; tok += a.run) {
                 const int32_t n = qr_item(a, s, tok).tiles;
                 if (off < n) break;
                 off -= n;
@@ -273,8 +280,8 @@ struct QrShared {
 
 // Waits end after two seconds, or once another wait of the CTA has (or at a test's
 // wish): nothing here waits for more than a tile's copies and MMAs.
-template <typename S>
-static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, QrShared<S> &sh, uint64_t *bar, uint32_t parity) {
+template <typename SH>
+static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, SH &sh, uint64_t *bar, uint32_t parity) {
     volatile int *stop = &sh.stop;
     const bool early = a.give_up == int32_t(blockIdx.x);
     const uint64_t since = early ? sh.began : global_ns(), limit = early ? a.give_up_ns : 2000000000ull;
@@ -287,8 +294,8 @@ static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, QrShared<S> &s
     }
     return true;
 }
-template <typename S>
-__device__ __forceinline__ bool qr_wait(const QrArgs &a, QrShared<S> &sh, uint64_t *bar, uint32_t parity) {
+template <typename SH>
+__device__ __forceinline__ bool qr_wait(const QrArgs &a, SH &sh, uint64_t *bar, uint32_t parity) {
     const bool ok = mbar_try_wait(bar, parity) || qr_wait_long(a, sh, bar, parity);
     return __all_sync(~0u, ok);
 }
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
     }
     if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.k : &a.v) : "memory");
     pdl_wait();
-    qr_cut(a, &sh.start, sh.warp_sums);  // synchronises the CTA
+    qr_cut<kQrThreads>(a, &sh.start, sh.warp_sums);  // synchronises the CTA
     tc_after();
     const uint32_t tmem = sh.tmem;
     const PaStart st = sh.start;
@@ -763,18 +770,38 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
     if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
 }
 
-// CTA c joins the rows of the cut item that begins in CTA c: a warp for each, whose
-// lanes stand for channels, four pieces under way at a time.
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ QrArgs a) {
+cudaError_t launch_qr(QrArgs &a, cudaStream_t st) {
+    using S = QrShape<HD, BF16>;
+    constexpr int smem = QrShape<HD, BF16>::kTotal + int(sizeof(QrShared<S>));
+    static_assert(S::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    const auto kern = qr_kernel<HD, BF16>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    a.ctas = S::kCtas;
+    return launch_pdl(kern, dim3(S::kCtas), dim3(kQrThreads), smem, st, a);
+}
+
+struct QrJoin {
+    QrArgs few, many;  // of the launches whose pieces these are; ctas 0 = none
+    int32_t wide;      // CTAs for each record of `many`
+};
+
+// Joins the rows of cut items, a warp for each, whose lanes stand for channels, four
+// pieces under way at a time: two CTAs for a record of `few`, `wide` for one of `many`.
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ QrJoin j) {
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr int kPer = HD / 32;
     pdl_wait();
-    const QrCut cut = a.cut[blockIdx.x];
+    const int32_t few = j.few.ctas * 2, at_cta = int32_t(blockIdx.x) - (int32_t(blockIdx.x) < few ? 0 : few);
+    const QrArgs &a = int32_t(blockIdx.x) < few ? j.few : j.many;
+    const int32_t share = int32_t(blockIdx.x) < few ? 2 : j.wide;
+    const QrCut cut = a.cut[at_cta / share];
     if (cut.n == 0) return;
     const QrPieces pieces(cut.unit0, cut.units, cut.total, a.ctas);
     const int32_t col = int32_t(threadIdx.x & 31) * kPer;
-    for (int32_t r = threadIdx.x >> 5; r < cut.rows; r += 8) {
+    for (int32_t r = at_cta % share * 8 + (threadIdx.x >> 5); r < cut.rows; r += share * 8) {
         float top = -INFINITY, sum = 0.0f, o[kPer] = {};
 #pragma unroll 1
         for (int32_t i0 = 0; i0 < pieces.n; i0 += 4) {
@@ -784,7 +811,7 @@ __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ Qr
             for (int i = 0; i < 4; ++i) {
                 ml[i] = make_float2(-INFINITY, 0.0f);
                 if (i0 + i >= pieces.n) continue;
-                const int64_t at = pieces.slot(i0 + i) * kQrRows + r;
+                const int64_t at = pieces.slot(i0 + i) * a.part_rows + r;
                 ml[i] = __ldcg(&a.part_ml[at]);
                 const float *p = a.part_o + at * HD + col;
                 if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[i]) = __ldcg(reinterpret_cast<const float4 *>(p));
@@ -819,17 +846,8 @@ __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ Qr
 }
 
 template <int HD, bool BF16>
-cudaError_t launch_qr(QrArgs &a, cudaStream_t st) {
-    using S = QrShape<HD, BF16>;
-    constexpr int smem = QrShape<HD, BF16>::kTotal + int(sizeof(QrShared<S>));
-    static_assert(S::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
-    const auto kern = qr_kernel<HD, BF16>;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
-    if (e != cudaSuccess) return e;
-    a.ctas = S::kCtas;
-    e = launch_pdl(kern, dim3(S::kCtas), dim3(kQrThreads), smem, st, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(S::kCtas), dim3(256), 0, st, a);
+cudaError_t launch_qr_join(const QrJoin &j, cudaStream_t st) {
+    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(unsigned(j.few.ctas * 2 + j.many.ctas * j.wide)), dim3(256), 0, st, j);
 }
 
 }  // namespace kvd

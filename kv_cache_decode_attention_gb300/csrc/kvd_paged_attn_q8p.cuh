@@ -1,0 +1,635 @@
+// kvd_paged_attn_q8p.cuh -- attention of many query rows over pages of e4m3 codes.
+//
+// The same sums as kvd_paged_attn_q8.cuh, for requests with more query rows a KV head
+// than its 16: prompts, whose bound is the tensor cores.  A tile of 128 rows is (token,
+// head of the group) pairs, and an item is one (request, KV head, run of up to two
+// tiles' tokens): both tiles ("streams") meet the same KV tile.
+//
+//   S = Q K^T   kind::f8f6f4.  q, scaled by a power of two so that its row's largest lies
+//               in [128, 256), is the sum of two e4m3 numbers (f16: three), each of which
+//               multiplies the codes of K as they lie in the pages: two products at
+//               twice the rate of 16 bits, from half the bytes.  Eight significant bits
+//               of bf16 are two times four; 2^-17 of the row's largest is left out.
+//   O += P V    kind::f16.  P in f16, whatever q's type, with the scale of V's block
+//               (relative to the row's largest such weight) in it; V's codes become f16,
+//               exactly, by four warps between the copy and the MMA.  P in e4m3 terms
+//               would do without, but a sum over a whole prompt meets weights far below
+//               2^-17 of the largest, and five instructions a weight cost the softmax
+//               warps more than the conversion, of which 256 rows share one.
+//
+// One CTA per SM:
+//   warps 0-3, 4-7   softmax of stream 0 and 1, a thread per query row; they make q's
+//                    terms, too;
+//   warp 8           walks the work, looks up pages and scales, TMA loads of K and V;
+//   warps 9, 14      issue the MMAs of stream 0 and 1;
+//   warps 10-13      V to f16, zeros for rows that nobody holds;
+//   warp 15          ends every wait if the CTA stops making steps.
+// TMEM: S0 S1 (128 columns each; P overwrites the first 64) O0 O1.  MMAs of one thread
+// run in order: S of a stream's next tile stands behind P V of its last one, and S being
+// complete says that P V before it is, so the softmax warps may then rescale O.  They do
+// so only where a row's reference grew by more than 2^kSlack.
+//
+// Barriers of a ring (k_full, k_empty; c_full, c_empty: codes of V; v_full, v_empty:
+// V in f16) turn once a slot; s_full, p_ready once a tile of a stream.  A stream
+// without rows lets go of what it does not use only once it is there, so it sees every
+// turn.
+#pragma once
+
+#include "kvd_paged_attn_q8.cuh"
+
+namespace kvd {
+
+constexpr int kQpThreads = 512;
+constexpr int kQpCtas = 152;
+constexpr int kQpRegs = 128, kQpSoftRegs = 184, kQpLoadRegs = 72;
+static_assert(2 * kQpSoftRegs + 2 * kQpLoadRegs <= 4 * kQpRegs, "setmaxnreg shares");
+constexpr int kQpMaxRows = 2 * kQrTile;
+
+template <int HD, bool BF16>
+struct QpShape {
+    static constexpr int kTerms = BF16 ? 2 : 3;
+    static constexpr int kCodeBytes = kQrTile * HD, kWideBytes = 2 * kCodeBytes;
+    static constexpr int kStages = BF16 ? 3 : 2;                  // of K's codes
+    static constexpr int kCodes = BF16 ? 2 : 1, kWide = 2;        // of V's codes, of V in f16
+    static constexpr int kScales = kStages + 2;
+    static constexpr int kQBytes = kTerms * kCodeBytes;           // of one stream: a term after another
+    static constexpr int kQ = 0, kK = 2 * kQBytes, kC = kK + kStages * kCodeBytes, kV = kC + kCodes * kCodeBytes,
+                         kTotal = kV + kWide * kWideBytes;
+    static constexpr uint32_t kSwizzle = HD == 128 ? 2 : 4, kAtom = HD * 8;
+};
+
+template <typename S>
+struct QpShared {
+    uint64_t k_full[S::kStages], k_empty[S::kStages], c_full[S::kCodes], c_empty[S::kCodes], v_full[S::kWide], v_empty[S::kWide], sc_full[S::kScales];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], job_full[kQrJobs], job_empty[kQrJobs], drain[2];
+    QrJob job[kQrJobs];
+    PaStart start;
+    int64_t warp_sums[kQpThreads / 32];
+    uint32_t tmem;
+    int stop, steps;  // the watch: give up; changes with every tile that is loaded
+    uint64_t all_done;
+    float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's
+};
+
+template <int HD, bool BF16, bool CAP>
+__global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant__ QrArgs a) {
+    using S = QpShape<HD, BF16>;
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int kTerms = S::kTerms;
+    constexpr uint32_t kO = 256;  // TMEM column of O0; O1 follows
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    QpShared<S> &sh = *reinterpret_cast<QpShared<S> *>(smem_raw + S::kTotal);
+    const uint32_t smem = smem_addr(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 2);
+        }
+        for (int i = 0; i < S::kCodes; ++i) {
+            mbar_init(&sh.c_full[i], 1);
+            mbar_init(&sh.c_empty[i], 4);
+        }
+        for (int i = 0; i < S::kWide; ++i) {
+            mbar_init(&sh.v_full[i], 4);
+            mbar_init(&sh.v_empty[i], 2);
+        }
+        for (int i = 0; i < S::kScales; ++i) mbar_init(&sh.sc_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_ready[i], 4);
+            mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.q_ready[i], 4);
+            mbar_init(&sh.drain[i], 1);
+        }
+        for (int i = 0; i < kQrJobs; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], 14);  // eight softmax warps, two of MMAs, four that convert
+        }
+        mbar_init(&sh.all_done, 15);  // every warp but 15
+        fence_mbar_init();
+        sh.stop = 0;
+        sh.steps = 0;
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_before();
+    }
+    if (warp == 8 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.k : &a.v) : "memory");
+    pdl_wait();
+    qr_cut<kQpThreads>(a, &sh.start, sh.warp_sums);  // synchronises the CTA
+    tc_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int *stop = &sh.stop;
+    const PaStart st = sh.start;
+    const int32_t tile_tok = a.run / 2;    // tokens of a stream
+    uint32_t k_loads = 0, v_loads = 0;     // tiles asked for
+    if (threadIdx.x == 256) a.cut[blockIdx.x].n = 0;  // whose thread writes a record, too
+
+    if (st.units > 0) {
+        bool ok = true;
+        if (warp >= 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQpLoadRegs));
+            if (warp == 8) {
+                // ---------------------------------------------------- work and loads
+                PaWalk w = {st.b, st.h, st.tok, st.s};
+                int32_t unit = st.unit;
+                int64_t left = st.units;
+                const int ppt = kQrTile >> a.page_log2;
+                const uint32_t box = uint32_t(HD) << a.page_log2;  // bytes of a page
+                for (uint32_t at = 0;; ++at) {
+                    QrJob &job = sh.job[at % kQrJobs];
+                    if (at >= kQrJobs) ok = pa_wait(&sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1, stop);
+                    if (!ok) break;
+                    if (left <= 0) {
+                        if (lane == 0) job.n = 0;
+                        qr_arrive(&sh.job_full[at % kQrJobs]);
+                        break;
+                    }
+                    const QrItem it = qr_item(a, w.s, w.tok);
+                    const int32_t have = it.tiles - unit, n = left < have ? int32_t(left) : have, tile0 = it.tile0 + unit;
+                    const bool whole = unit == 0 && n == it.tiles;
+                    if (lane == 0) {
+                        job = QrJob{n, tile0, unit == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
+                        if (unit == 0 && !whole)
+                            a.cut[blockIdx.x] = QrCut{st.from + (st.units - left), st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
+                    }
+                    qr_arrive(&sh.job_full[at % kQrJobs]);
+                    const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
+                    const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
+                    const int32_t h = w.h;
+                    // lane's page of a tile, -1 = none
+                    auto page_of = [&](int32_t t) {
+                        const int32_t p = (tile0 + t) * ppt + lane;
+                        int32_t page = -1;
+                        if (t < n && lane < ppt && p < held) {
+                            page = table[p];
+                            if (uint32_t(page) >= uint32_t(a.n_pages)) {
+                                set_error(a.err, kErrBounds);
+                                page = -1;
+                            }
+                        }
+                        return page;
+                    };
+                    auto scales = [&](int32_t page) {
+                        float2 s = make_float2(1.0f, 1.0f);
+                        if (page >= 0) s = make_float2(a.k_scale[int64_t(page) * a.n_kv + h], a.v_scale[int64_t(page) * a.n_kv + h]);
+                        return s;
+                    };
+                    auto load = [&](const CUtensorMap *map, uint32_t dst, int32_t page, uint64_t *bar) {
+                        if (lane == 0) mbar_arrive_expect_tx(bar, S::kCodeBytes);
+                        __syncwarp();
+                        if (lane < ppt) tma_2d(dst + lane * box, map, 0, page < 0 ? a.pool_rows : (page * a.n_kv + h) << a.page_log2, bar);
+                    };
+                    auto load_k = [&](int32_t page, float2 s) {
+                        const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
+                        if (turn > 0) ok = pa_wait(&sh.k_empty[slot], (turn & 1) ^ 1, stop);
+                        if (!ok) return;
+                        if (lane < ppt) {
+                            const float vs = scale_of(s.y, a.err);
+                            sh.scale[sc][lane] = make_float4(scale_of(s.x, a.err), log2f(vs), 1.0f / vs, 0.0f);
+                        }
+                        qr_arrive(&sh.sc_full[sc]);
+                        load(&a.k, smem + S::kK + slot * S::kCodeBytes, page, &sh.k_full[slot]);
+                        ++k_loads;
+                        if (lane == 0) *static_cast<volatile int *>(&sh.steps) = int(k_loads);
+                    };
+                    // K runs a tile ahead of V, page numbers two and scales one ahead of K
+                    int32_t page = page_of(0), next = page_of(1);
+                    float2 s = scales(next);
+                    load_k(page, scales(page));
+                    for (int32_t t = 0; ok && t < n; ++t) {
+                        const int32_t after = page_of(t + 2);
+                        if (t + 1 < n) load_k(next, s);
+                        if (!ok) break;
+                        const uint32_t slot = v_loads % S::kCodes, turn = v_loads / S::kCodes;
+                        if (turn > 0) ok = pa_wait(&sh.c_empty[slot], (turn & 1) ^ 1, stop);
+                        if (!ok) break;
+                        load(&a.v, smem + S::kC + slot * S::kCodeBytes, page, &sh.c_full[slot]);
+                        ++v_loads;
+                        s = scales(after);
+                        page = next;
+                        next = after;
+                    }
+                    if (!ok) break;
+                    left -= have;
+                    unit = 0;
+                    if (left > 0) qr_next(a, w);
+                }
+            } else if (warp == 9 || warp == 14) {
+                // ---------------------------------------------------- MMAs
+                const int d = warp == 14 ? 1 : 0;
+                uint32_t g = 0, mine = 0, items = 0;  // tiles, tiles and items of this stream
+                auto score = [&](uint32_t i) {
+                    const uint32_t slot = i % S::kStages;
+                    ok = pa_wait(&sh.k_full[slot], i / S::kStages & 1, stop);
+                    if (!ok) return;
+                    tc_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = tc_idesc8(128, 128, false, false);
+                        const uint64_t kd = tc_desc(smem + S::kK + slot * S::kCodeBytes, 16, S::kAtom, S::kSwizzle);
+                        const uint64_t qd = tc_desc(smem + S::kQ + d * S::kQBytes, 16, S::kAtom, S::kSwizzle);
+#pragma unroll
+                        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < HD / 32; ++kk)
+                                tc_mma8(tmem + d * 128, qd + t * (S::kCodeBytes >> 4) + kk * 2, kd + kk * 2, id, t != 0 || kk != 0);
+                    }
+                    __syncwarp();
+                    tc_commit(&sh.s_full[d]);
+                    tc_commit(&sh.k_empty[slot]);
+                };
+                for (uint32_t at = 0;; ++at) {
+                    ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
+                    if (!ok) break;
+                    const uint32_t n = uint32_t(sh.job[at % kQrJobs].n);
+                    const bool busy = d == 0 || sh.job[at % kQrJobs].count > tile_tok;
+                    qr_arrive(&sh.job_empty[at % kQrJobs]);
+                    if (n == 0) break;
+                    if (!busy) {
+                        for (uint32_t i = g; ok && i < g + n; ++i) {
+                            ok = pa_wait(&sh.k_full[i % S::kStages], i / S::kStages & 1, stop);
+                            if (!ok) break;
+                            qr_arrive(&sh.k_empty[i % S::kStages]);
+                            ok = pa_wait(&sh.v_full[i % S::kWide], i / S::kWide & 1, stop);
+                            if (!ok) break;
+                            qr_arrive(&sh.v_empty[i % S::kWide]);
+                        }
+                        if (!ok) break;
+                        g += n;
+                        continue;
+                    }
+                    // (q_ready says, too, that O of the item before has been read)
+                    ok = pa_wait(&sh.q_ready[d], items++ & 1, stop);
+                    if (!ok) break;
+                    score(g);
+                    for (uint32_t i = g; ok && i < g + n; ++i, ++mine) {
+                        const uint32_t slot = i % S::kWide;
+                        ok = pa_wait(&sh.v_full[slot], i / S::kWide & 1, stop) && pa_wait(&sh.p_ready[d], mine & 1, stop);
+                        if (!ok) break;
+                        tc_after();
+                        if (elect_one()) {
+                            constexpr uint32_t id = tc_idesc(false, 128, HD, true);
+                            const uint64_t vd = tc_desc(smem + S::kV + slot * S::kWideBytes, kQrTile * 128, 1024, 2);
+#pragma unroll
+                            for (int kk = 0; kk < kQrTile / 16; ++kk)
+                                tc_mma_ts(tmem + kO + d * HD, tmem + d * 128 + kk * 8, vd + kk * (2048 >> 4), id, i != g || kk != 0);
+                        }
+                        __syncwarp();
+                        if (i + 1 == g + n) tc_commit(&sh.o_full[d]);
+                        else score(i + 1);
+                        if (!ok) break;
+                        tc_commit(&sh.v_empty[slot]);
+                    }
+                    if (!ok) break;
+                    g += n;
+                }
+            } else if (warp >= 10 && warp < 14) {
+                // ---------------------------------------------------- V to f16
+                // A lane takes 16 codes of a row; lanes of the upper half of a row of 128
+                // store their two pieces in the other order, so that eight lanes' pieces
+                // fill all banks.
+                constexpr int kChunks = HD / 16, kRowsAtOnce = 32 / kChunks;
+                const int c = lane % kChunks, r0 = (warp - 10) * 32 + lane / kChunks;
+                uint32_t g = 0;
+                for (uint32_t at = 0;; ++at) {
+                    ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
+                    if (!ok) break;
+                    const int32_t n = sh.job[at % kQrJobs].n, tile0 = sh.job[at % kQrJobs].tile0, len = sh.job[at % kQrJobs].len;
+                    qr_arrive(&sh.job_empty[at % kQrJobs]);
+                    if (n == 0) break;
+                    for (int32_t i = 0; i < n; ++i, ++g) {
+                        const uint32_t from = g % S::kCodes, to = g % S::kWide;
+                        ok = pa_wait(&sh.c_full[from], g / S::kCodes & 1, stop);
+                        if (ok && g >= uint32_t(S::kWide)) ok = pa_wait(&sh.v_empty[to], (g / S::kWide & 1) ^ 1, stop);
+                        if (!ok) break;
+                        const uint32_t src = smem + S::kC + from * S::kCodeBytes, dst = smem + S::kV + to * S::kWideBytes;
+                        const int32_t held = len - (tile0 + i) * kQrTile;  // rows of the tile
+#pragma unroll 4
+                        for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
+                            const int r = r0 + k * kRowsAtOnce;
+                            uint32_t at8 = r * HD + c * 16;
+                            at8 ^= HD == 128 ? (r & 7) << 4 : (at8 >> 7 & 3) << 4;
+                            uint32_t w[4];
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + at8));
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[e / 2] >> (16 * (e % 2))), __NV_E4M3);
+                                x[e] = r < held ? uint32_t(v.x) | uint32_t(v.y) << 16 : 0u;
+                            }
+                            // channel 16 c of a row lies in half c / 4, 16-byte piece 2 (c % 4)
+                            const uint32_t row = dst + (c / 4) * (kQrTile * 128) + r * 128;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int p = j ^ (c / 4 & 1);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((2 * (c % 4) + p) ^ (r & 7)) << 4)), "r"(p ? x[4] : x[0]),
+                                             "r"(p ? x[5] : x[1]), "r"(p ? x[6] : x[2]), "r"(p ? x[7] : x[3])
+                                             : "memory");
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        qr_arrive(&sh.c_empty[from]);
+                        qr_arrive(&sh.v_full[to]);
+                    }
+                    if (!ok) break;
+                }
+            } else if (warp == 15 && lane == 0) {
+                // ---------------------------------------------------- watch
+                volatile int *steps = &sh.steps;
+                int last = 0;
+                uint64_t since = global_ns();
+                const bool early = a.give_up == int32_t(blockIdx.x);
+                const uint64_t limit = early ? a.give_up_ns : 2000000000ull;
+                while (!mbar_try_wait(&sh.all_done, 0)) {
+                    const uint64_t now = global_ns();
+                    if (*steps != last) {
+                        last = *steps;
+                        if (!early) since = now;
+                    } else if (now - since >= limit) {
+                        *stop = 1;
+                        break;
+                    }
+                }
+            }
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQpSoftRegs));
+            // -------------------------------------------------------- softmax
+            const int d = warp >> 2;                       // stream
+            const int row = (warp & 3) * 32 + lane;        // row of the tile
+            const uint32_t t_row = tmem + (uint32_t((warp & 3) * 32) << 16);
+            const uint32_t t_s = t_row + d * 128, t_o = t_row + kO + d * HD;
+            // weights are scaled up so that small ones stay normal numbers of f16; a row's then reach 2^(kLift + kSlack)
+            constexpr float kLift = 8.0f, kSlack = 4.0f;
+            const int32_t rtok = row / a.group, rhead = row - rtok * a.group;
+            uint32_t g = 0, mine = 0, items = 0;
+            for (uint32_t at = 0;; ++at) {
+                ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
+                if (!ok) break;
+                const QrJob job = sh.job[at % kQrJobs];
+                qr_arrive(&sh.job_empty[at % kQrJobs]);
+                if (job.n == 0) break;
+                if (d == 1 && job.count <= tile_tok) {
+                    g += job.n;
+                    continue;
+                }
+                const int32_t tok = d * tile_tok + rtok;  // of the item
+                const bool valid = rtok < tile_tok && tok < job.count;
+                const int32_t head = job.kv_head * a.group + rhead;
+                // q as e4m3 terms; every MMA that read the last item's has been waited for
+                float mul;
+                {
+                    uint4 x[HD / 8];
+#pragma unroll
+                    for (int i = 0; i < HD / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+                    if (valid) {
+                        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok + int64_t(head) * a.q_head);
+#pragma unroll
+                        for (int i = 0; i < HD / 8; ++i) x[i] = p[i];
+                    }
+                    auto two = [](uint32_t w) {
+                        float2 v;
+                        if constexpr (BF16) v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                        else v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                        return v;
+                    };
+                    float top = 0.0f;
+                    bool fine = true;
+#pragma unroll
+                    for (int i = 0; i < HD / 2; ++i) {
+                        const float2 v = two(reinterpret_cast<const uint32_t *>(x)[i]);
+                        const float m = fmaxf(fabsf(v.x), fabsf(v.y));
+                        fine = fine && fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX;
+                        top = fmaxf(top, m);
+                    }
+                    int e = 134 - int(__float_as_uint(top) >> 23);
+                    e = top == 0.0f ? 0 : e > 120 ? 120 : e < -120 ? -120 : e;
+                    const float up = __uint_as_float(uint32_t(e + 127) << 23);
+                    // a row that is not finite is none of numbers
+                    mul = fine ? a.mul * __uint_as_float(uint32_t(127 - e) << 23) : __int_as_float(0x7fc00000);
+#pragma unroll
+                    for (int c = 0; c < HD / 16; ++c) {
+                        uint32_t t[kTerms][4];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float2 v = two(reinterpret_cast<const uint32_t *>(x)[c * 8 + i]);
+                            v.x *= up;
+                            v.y *= up;
+#pragma unroll
+                            for (int k = 0; k < kTerms; ++k) {
+                                const uint32_t b = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                                t[k][i / 2] = i % 2 ? t[k][i / 2] | b << 16 : b;
+                                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(b), __NV_E4M3)));
+                                v.x -= y.x;
+                                v.y -= y.y;
+                            }
+                        }
+                        uint32_t to = row * HD + c * 16;
+                        to ^= HD == 128 ? (row & 7) << 4 : (to >> 7 & 3) << 4;
+#pragma unroll
+                        for (int k = 0; k < kTerms; ++k)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem + S::kQ + d * S::kQBytes + k * S::kCodeBytes + to), "r"(t[k][0]),
+                                         "r"(t[k][1]), "r"(t[k][2]), "r"(t[k][3])
+                                         : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_before();
+                    qr_arrive(&sh.q_ready[d]);
+                }
+                const int32_t pos = job.first_pos + tok;
+                const int64_t lo64 = a.window > 0 ? int64_t(pos) - a.window + 1 : 0;
+                const int32_t lo = lo64 > 0 ? int32_t(lo64) : 0;
+                const bool busy = __any_sync(~0u, valid);
+                int32_t key0 = job.tile0 * kQrTile;
+                float ref = -INFINITY;  // reference, log2 units, less kLift
+                float sum = 0.0f;
+                for (int32_t i = 0; i < job.n; ++i, ++g, ++mine, key0 += kQrTile) {
+                    ok = pa_wait(&sh.sc_full[g % S::kScales], g / S::kScales & 1, stop) && pa_wait(&sh.s_full[d], mine & 1, stop);
+                    if (!ok) break;
+                    if (busy) {
+                        const float4 *sc = sh.scale[g % S::kScales];
+                        tc_after();
+                        // first pass: the largest of the scores with their blocks' scales, from
+                        // that of each 16 columns; masked scores go back to TMEM as such
+                        const int32_t hi_c = pos - key0, lo_c = lo - key0;
+                        const bool edge = __any_sync(~0u, hi_c < kQrTile - 1 || lo_c > 0);
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kQrTile; c0 += 64) {
+                            float x[64];
+                            tc_ld32(t_s + c0, x);
+                            tc_ld32(t_s + c0 + 32, x + 32);
+                            tc_wait_ld();
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 64; e += 32) {
+                                    const uint32_t seen = pa_seen(lo_c - c0 - e, hi_c - c0 - e);
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
+                                }
+                                tc_st32(t_s + c0, x);
+                                tc_st32(t_s + c0 + 32, x + 32);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                float m0 = x[q * 16], m1 = x[q * 16 + 1];
+#pragma unroll
+                                for (int c = 2; c < 16; c += 4) {
+                                    m0 = max3(m0, x[q * 16 + c], c + 1 < 16 ? x[q * 16 + c + 1] : m0);
+                                    if (c + 2 < 16) m1 = max3(m1, x[q * 16 + c + 2], x[q * 16 + c + 3]);
+                                }
+                                const float4 f = sc[((c0 + q * 16) >> a.page_log2)];
+                                float m = fmaxf(m0, m1) * (f.x * mul);
+                                if (CAP) m = m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap;
+                                top = fmaxf(top, m + f.y);
+                            }
+                        }
+                        if (edge) tc_wait_st();
+                        top = valid ? top - kLift : -INFINITY;
+                        // move the reference when a row grew past the slack
+                        if (__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
+                            const float now = fmaxf(ref, top);
+                            if (i > 0) {
+                                const float f = now == -INFINITY ? 1.0f : ex2(ref - now);
+                                sum *= f;
+#pragma unroll 1
+                                for (int c = 0; c < HD; c += 32) {
+                                    float o[32];
+                                    tc_ld32(t_o + c, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                                    tc_st32(t_o + c, o);
+                                }
+                            }
+                            ref = now;
+                        }
+                        // second pass: the weights, 32 at a time, the next scores on their
+                        // way; P takes the place of scores already read
+                        const float base = ref == -INFINITY ? 0.0f : ref;
+                        float x[2][32];
+                        tc_ld32(t_s, x[0]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tc_wait_ld();
+                            if (q < 3) tc_ld32(t_s + (q + 1) * 32, x[(q + 1) & 1]);
+                            float p[16];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const float4 f = sc[((q * 32 + u * 16) >> a.page_log2)];
+                                const float k = f.x * mul, b = f.y - base;
+                                const float2 kk = make_float2(k, k), bb = make_float2(b, b);
+                                float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const float *y = &x[q & 1][u * 16 + 2 * c];
+                                    float2 v = make_float2(y[0], y[1]);
+                                    if constexpr (CAP) {
+                                        v = make_float2(v.x == -INFINITY ? v.x : fmaf(pa_tanh_of_any(v.x * k), a.cap, b),
+                                                        v.y == -INFINITY ? v.y : fmaf(pa_tanh_of_any(v.y * k), a.cap, b));
+                                    } else {
+                                        v = fma2(v, kk, bb);
+                                    }
+                                    v.x = ex2(v.x);
+                                    v.y = ex2(v.y);
+                                    acc = add2(acc, v);
+                                    p[u * 8 + c] = __uint_as_float(pack2<false>(v.x, v.y));
+                                }
+                                sum = fmaf(acc.x + acc.y, f.z, sum);
+                            }
+                            tc_st16(t_s + q * 16, p);
+                        }
+                        tc_wait_st();
+                        tc_before();
+                    }
+                    qr_arrive(&sh.p_ready[d]);
+                }
+                if (!ok) break;
+                // ---- the end of the item, or of this CTA's piece of it
+                ok = pa_wait(&sh.o_full[d], items++ & 1, stop);
+                if (!ok) break;
+                if (busy) {
+                    tc_after();
+                    const bool whole = job.whole != 0;
+                    float f = 1.0f;
+                    if (whole) {
+                        float s = sum;
+                        if (a.sinks != nullptr && valid && ref != -INFINITY) {
+                            // the sink joins the reference and the sum (a row without rows stays zero)
+                            const float sink = a.sinks[head] * 1.4426950408889634f, all = fmaxf(ref, sink);
+                            f = ex2(ref - all);
+                            s = s * f + ex2(sink - all);
+                        }
+                        f *= s == 0.0f ? 0.0f : 1.0f / s;
+                    }
+                    const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
+                    const int32_t prow = d * tile_tok * a.group + row;
+                    if (!whole && valid) a.part_ml[slot * a.part_rows + prow] = make_float2(ref, sum);
+                    uint8_t *dst = static_cast<uint8_t *>(a.out) + ((int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head) * 2;
+                    float *pdst = a.part_o + (slot * a.part_rows + prow) * HD;
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 32) {
+                        float y[32];
+                        __syncwarp();
+                        tc_ld32(t_o + c, y);
+                        tc_wait_ld();
+                        if (valid && whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4 *>(dst + (c + e) * 2) =
+                                    make_uint4(pack2<BF16>(y[e] * f, y[e + 1] * f), pack2<BF16>(y[e + 2] * f, y[e + 3] * f),
+                                               pack2<BF16>(y[e + 4] * f, y[e + 5] * f), pack2<BF16>(y[e + 6] * f, y[e + 7] * f));
+                        } else if (valid) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4 *>(pdst + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        }
+                    }
+                    __syncwarp();
+                    tc_before();
+                }
+            }
+        }
+        // (15 goes on watching until every warp is here)
+        if (warp != 15) qr_arrive(&sh.all_done);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (*stop != 0) {
+        // given up: nothing may be in flight into this CTA's memory
+        if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
+        if (warp == 9 || warp == 14) {
+            uint64_t *drain = &sh.drain[warp == 9 ? 0 : 1];
+            tc_commit(drain);
+            mbar_wait_bounded(drain, 0, 500000000ull);
+        }
+        if (warp == 8) {
+            for (uint32_t i = 0; i < uint32_t(S::kStages); ++i)
+                if (k_loads > i) mbar_wait_bounded(&sh.k_full[(k_loads - 1 - i) % S::kStages], (k_loads - 1 - i) / S::kStages & 1, 500000000ull);
+            for (uint32_t i = 0; i < uint32_t(S::kCodes); ++i)
+                if (v_loads > i) mbar_wait_bounded(&sh.c_full[(v_loads - 1 - i) % S::kCodes], (v_loads - 1 - i) / S::kCodes & 1, 500000000ull);
+        }
+        tc_before();
+        __syncthreads();
+        tc_after();
+    }
+    pdl_trigger();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_qp(QrArgs &a, cudaStream_t st) {
+    using S = QpShape<HD, BF16>;
+    constexpr int smem = S::kTotal + int(sizeof(QpShared<S>));
+    static_assert(smem <= 227 * 1024, "shared memory of an SM");
+    const auto kern = a.cap > 0.0f ? qp_kernel<HD, BF16, true> : qp_kernel<HD, BF16, false>;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    a.ctas = kQpCtas;
+    return launch_pdl(kern, dim3(kQpCtas), dim3(kQpThreads), smem, st, a);
+}
+
+}  // namespace kvd
