@@ -85,6 +85,9 @@ cudaError_t launch(const QrArgs &call, const WsLayout &ws, void *workspace, cuda
     QrJoin j;
     std::memset(&j, 0, sizeof(j));
     const bool many = int64_t(call.n_tokens) * call.group > kQrRows;
+    // Eight columns where one token for each request is what there is, as in a decode
+    // step; a request with more rows is then two items that read its K and V twice.
+    const bool eight = call.group <= 8 && call.n_tokens <= call.n_seq;
     for (int i = 0; i < (many ? 2 : 1); ++i) {
         QrArgs &a = i == 0 ? j.few : j.many;
         a = call;
@@ -92,16 +95,15 @@ cudaError_t launch(const QrArgs &call, const WsLayout &ws, void *workspace, cuda
         a.part_ml = reinterpret_cast<float2 *>(w + ws.ml[i]);
         a.part_o = reinterpret_cast<float *>(w + ws.o[i]);
         a.part_rows = i == 0 ? kQrRows : piece_rows(call.n_tokens, call.group);
-        a.run = i == 0 ? kQrRows / call.group : 2 * (kQrTile / call.group);
+        a.run = i == 0 ? (eight ? 8 : kQrRows) / call.group : 2 * (kQrTile / call.group);
         a.more = i == 0 ? 0 : kQrRows;
         a.most = i == 0 ? kQrRows : INT64_MAX;
     }
-    cudaError_t e = cudaSuccess;
-    if (many) {
+    cudaError_t e = eight ? launch_qr<HD, BF16, 8>(j.few, st) : launch_qr<HD, BF16, 16>(j.few, st);
+    if (e == cudaSuccess && many) {
         e = launch_qp<HD, BF16>(j.many, st);
         j.wide = int32_t(ceil_div(j.many.part_rows, 32));
     }
-    if (e == cudaSuccess) e = launch_qr<HD, BF16>(j.few, st);
     return e == cudaSuccess ? launch_qr_join<HD, BF16>(j, st) : e;
 }
 

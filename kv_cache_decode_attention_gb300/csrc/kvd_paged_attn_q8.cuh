@@ -239,21 +239,24 @@ struct QrPieces {
 
 // ---------------------------------------------------------------- the kernel
 
-template <int HD, bool BF16>
+// R: query rows of an item, 16 or 8 (half the columns, for half the work of the
+// softmax warps).
+template <int HD, bool BF16, int R>
 struct QrShape {
     static constexpr int kTerms = BF16 ? 2 : 3;
-    static constexpr int kN = kQrRows * kTerms;
-    // what fits: f16's third terms take the third CTA's room
-    static constexpr int kPerSm = BF16 ? 3 : 2, kCtas = 152 * kPerSm;
-    static constexpr int kStages = (BF16 ? 2 : 3) * (HD == 128 ? 1 : 2);
+    static constexpr int kN = (kTerms * R + 15) / 16 * 16;  // columns: a multiple of 16
+    // what fits: the third terms of 16 rows take the third CTA's room
+    static constexpr int kPerSm = kN <= 32 ? 3 : 2, kCtas = 152 * kPerSm;
+    static constexpr int kStages = (kN <= 32 ? 2 : 3) * (HD == 128 ? 1 : 2);
     // Scales of tile t + kScales replace those of tile t once its K is asked for, for
     // which S of tile t + 2 is over, and so tile t's softmax has read its own.
     static constexpr int kScales = kStages + 2;
     static constexpr int kTileBytes = kQrTile * HD;
-    static constexpr int kQBytes = kN * HD, kPBytes = kN * kQrTile;
+    static constexpr int kQBytes = (kN * HD + 1023) / 1024 * 1024, kPBytes = kN * kQrTile;
     static constexpr int kK = 0, kV = kStages * kTileBytes, kQ = 2 * kStages * kTileBytes, kP = kQ + kQBytes, kTotal = kP + kPBytes;
-    static constexpr int kColumns = 2 * kN <= 64 ? 64 : 128;  // of TMEM: S, then O
+    static constexpr int kColumns = 2 * kN <= 32 ? 32 : 2 * kN <= 64 ? 64 : 128;  // of TMEM: S, then O
     static constexpr uint32_t kSwizzle = HD == 128 ? 2 : 4, kAtom = HD * 8;
+    static constexpr int kRows = R;
 };
 
 struct QrJob {
@@ -272,10 +275,10 @@ struct QrShared {
     int stop;
     uint64_t began;
     float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's
-    float top[2][kQrRows][4];     // of a tile's columns, by warp
-    float ref[4][kQrRows];        // the tile's reference less 8, by warp
-    float2 fold[2][4][kQrRows];   // factors of old and new sums, by warp
-    float col[kQrRows];
+    float top[2][S::kRows][4];     // of a tile's columns, by warp
+    float ref[4][S::kRows];        // the tile's reference less 8, by warp
+    float2 fold[2][4][S::kRows];   // factors of old and new sums, by warp
+    float col[S::kRows];
 };
 
 // Waits end after two seconds, or once another wait of the CTA has (or at a test's
@@ -305,11 +308,27 @@ __device__ __forceinline__ void qr_arrive(uint64_t *bar) {
 }
 __device__ __forceinline__ void qr_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// The largest of a warp's values.
-__device__ __forceinline__ float warp_top(float x) {
-    const int32_t b = __float_as_int(x);
-    const int32_t i = __reduce_max_sync(~0u, b ^ ((b >> 31) & 0x7fffffff));  // ordered as integers
-    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+// The largest of a warp's values of each of R columns; lane l gets that of column
+// l % R.  Lanes pass on half of the columns that they still have, R - 1 exchanges in all,
+// and go on in groups.
+template <int R>
+__device__ __forceinline__ float warp_tops(const float *x) {
+    const int lane = threadIdx.x & 31;
+    float y[R];
+#pragma unroll
+    for (int c = 0; c < R; ++c) y[c] = x[c];
+#pragma unroll
+    for (int n = R / 2; n >= 1; n /= 2) {
+        const bool up = (lane & n) != 0;
+#pragma unroll
+        for (int c = 0; c < n; ++c) {
+            const float keep = up ? y[c + n] : y[c], pass = up ? y[c] : y[c + n];
+            y[c] = fmaxf(keep, __shfl_xor_sync(~0u, pass, n));
+        }
+    }
+#pragma unroll
+    for (int n = R; n < 32; n *= 2) y[0] = fmaxf(y[0], __shfl_xor_sync(~0u, y[0], n));
+    return y[0];
 }
 
 // x (two values) as e4m3 terms x = t0 + t1 / 16 (+ t2 / 256), packed in 16 bits each.
@@ -324,16 +343,22 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t *t) {
         y = (y - v.y) * 16.0f;
     }
 }
-template <int TERMS>
+template <int TERMS, int R>
 __device__ __forceinline__ float joined(const float *x, int c) {
-    float v = fmaf(x[kQrRows + c], 1.0f / 16, x[c]);
-    if constexpr (TERMS == 3) v = fmaf(x[2 * kQrRows + c], 1.0f / 256, v);
+    float v = fmaf(x[R + c], 1.0f / 16, x[c]);
+    if constexpr (TERMS == 3) v = fmaf(x[2 * R + c], 1.0f / 256, v);
     return v;
 }
+template <int N>
+__device__ __forceinline__ void tc_ld_columns(uint32_t addr, float *x) {
+    if constexpr (N == 16) tc_ld16(addr, x);
+    else tc_ld32(addr, x);
+    if constexpr (N == 48) tc_ld16(addr + 32, x + 32);
+}
 
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_kernel(const __grid_constant__ QrArgs a) {
-    using S = QrShape<HD, BF16>;
+template <int HD, bool BF16, int R>
+__global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr_kernel(const __grid_constant__ QrArgs a) {
+    using S = QrShape<HD, BF16, R>;
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr int kTerms = S::kTerms;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -371,6 +396,9 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
     }
     if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.k : &a.v) : "memory");
     pdl_wait();
+    // The next launch may come: it waits for this one before it writes, and finds its
+    // SM free when this one's CTAs leave.
+    pdl_trigger();
     qr_cut<kQrThreads>(a, &sh.start, sh.warp_sums);  // synchronises the CTA
     tc_after();
     const uint32_t tmem = sh.tmem;
@@ -536,8 +564,8 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
 
                 // q as e4m3 terms; every MMA that read the last item's has been waited for
                 {
-                    constexpr int kPer = HD / 8;
-                    const int r = row / 8, part = row % 8;
+                    constexpr int kLanes = 128 / R, kPer = HD / kLanes;  // lanes of a row, channels of a lane
+                    const int r = row / kLanes, part = row % kLanes;
                     float x[kPer], top = 0.0f;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
@@ -545,18 +573,25 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                         const int32_t tok = r / a.group;
                         const T *p = static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok +
                                      int64_t(job.kv_head * a.group + r - tok * a.group) * a.q_head + part * kPer;
+                        if constexpr (kPer >= 8) {
 #pragma unroll
-                        for (int i = 0; i < kPer; i += 8) load8<T>(p + i, x + i);
+                            for (int i = 0; i < kPer; i += 8) load8<T>(p + i, x + i);
+                        } else {
+                            T y[4];
+                            *reinterpret_cast<uint2 *>(y) = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[i] = to_f32<T>(y[i]);
+                        }
                     }
                     bool fine = true;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
-                        fine = fine && fabsf(x[i]) <= 3.4028234664e38f;
+                        fine = fine && fabsf(x[i]) <= FLT_MAX;
                         top = fmaxf(top, fabsf(x[i]));
                     }
 #pragma unroll
-                    for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                    const uint32_t odd = __ballot_sync(~0u, !fine) >> (lane & 24) & 0xffu;
+                    for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    const uint32_t odd = __ballot_sync(~0u, !fine) >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1);
                     int e = 134 - int(__float_as_uint(top) >> 23);
                     e = top == 0.0f ? 0 : e > 120 ? 120 : e < -120 ? -120 : e;
                     const float up = __uint_as_float(uint32_t(e + 127) << 23);
@@ -565,19 +600,17 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                     for (int i = 0; i < kPer / 2; ++i) split2<kTerms>(x[2 * i] * up, x[2 * i + 1] * up, t[i]);
 #pragma unroll
                     for (int k = 0; k < kTerms; ++k) {
-                        const int n = k * kQrRows + r;
-                        if constexpr (HD == 128) {
-                            const uint32_t to = smem + S::kQ + n * 128 + ((part ^ (n & 7)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(t[0][k] | t[1][k] << 16),
-                                         "r"(t[2][k] | t[3][k] << 16), "r"(t[4][k] | t[5][k] << 16), "r"(t[6][k] | t[7][k] << 16)
+                        uint32_t to = (k * R + r) * HD + part * kPer;
+                        to = smem + S::kQ + (to ^ (HD == 128 ? (to >> 7 & 7) << 4 : (to >> 7 & 3) << 4));
+                        const uint32_t w0 = t[0][k] | t[1][k] << 16;
+                        if constexpr (kPer == 16)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w0), "r"(t[2][k] | t[3][k] << 16),
+                                         "r"(t[4][k] | t[5][k] << 16), "r"(t[6][k] | t[7][k] << 16)
                                          : "memory");
-                        } else {
-                            uint32_t to = n * 64 + part * 8;
-                            to ^= (to >> 7 & 3) << 4;
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(smem + S::kQ + to), "r"(t[0][k] | t[1][k] << 16),
-                                         "r"(t[2][k] | t[3][k] << 16)
-                                         : "memory");
-                        }
+                        else if constexpr (kPer == 8)
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(w0), "r"(t[2][k] | t[3][k] << 16) : "memory");
+                        else
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(w0) : "memory");
                     }
                     // a row that is not finite is none of numbers
                     if (part == 0) sh.col[r] = odd != 0 ? __int_as_float(0x7fc00000) : a.mul * __uint_as_float(uint32_t(127 - e) << 23);
@@ -586,27 +619,23 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                     qr_sync();
                 }
 
-                float acc[kQrRows], sum[kQrRows];
+                float acc[R], sum[R];
 #pragma unroll
-                for (int c = 0; c < kQrRows; ++c) acc[c] = sum[c] = 0.0f;
-                float m_run = -INFINITY;  // of column lane % 16
+                for (int c = 0; c < R; ++c) acc[c] = sum[c] = 0.0f;
+                float m_run = -INFINITY;  // of column lane % R
                 // the tile's part of the sums, once its O is there
                 auto take = [&](float *o) {
                     tc_after();
-                    if constexpr (kTerms == 2) {
-                        tc_ld32(t_row + S::kN, o);
-                    } else {
-                        tc_ld32(t_row + S::kN, o);
-                        tc_ld16(t_row + S::kN + 32, o + 32);
-                    }
+                    tc_ld_columns<S::kN>(t_row + S::kN, o);
                     tc_wait_ld();
                     tc_before();
                 };
                 auto fold = [&](const float *o, uint32_t i) {
 #pragma unroll
-                    for (int c = 0; c < kQrRows; ++c) {
-                        const float2 f = sh.fold[i & 1][warp][c];
-                        acc[c] = fmaf(acc[c], f.x, joined<kTerms>(o, c) * f.y);
+                    for (int c = 0; c < R; c += 2) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sh.fold[i & 1][warp][c]);
+                        acc[c] = fmaf(acc[c], f.x, joined<kTerms, R>(o, c) * f.y);
+                        acc[c + 1] = fmaf(acc[c + 1], f.z, joined<kTerms, R>(o, c + 1) * f.w);
                     }
                 };
                 for (int32_t i = 0; i < job.n; ++i, ++g) {
@@ -615,21 +644,21 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                     const float4 sc = sh.scale[g % S::kScales][row >> a.page_log2];
                     ok = qr_wait(a, sh, &sh.s_full, g & 1);
                     if (!ok) break;
-                    float x[kQrRows];
+                    float x[R];
                     {
                         float s[S::kN];
                         tc_after();
-                        tc_ld32(t_row, s);
-                        if constexpr (kTerms == 3) tc_ld16(t_row + 32, s + 32);
+                        tc_ld_columns<S::kN>(t_row, s);
                         tc_wait_ld();
                         tc_before();
                         qr_arrive(&sh.s_free);
+                        // scores with the scale of V's block, log2 units
 #pragma unroll
-                        for (int c = 0; c < kQrRows; ++c) x[c] = joined<kTerms>(s, c) * sc.x * sh.col[c];
-                    }
-                    if (a.cap > 0.0f) {
-#pragma unroll
-                        for (int c = 0; c < kQrRows; ++c) x[c] = pa_tanh_of_any(x[c]) * a.cap;
+                        for (int c = 0; c < R; ++c) {
+                            const float k = sh.col[c] * sc.x, y = joined<kTerms, R>(s, c);
+                            if (a.cap > 0.0f) x[c] = fmaf(pa_tanh_of_any(y * k), a.cap, sc.y);
+                            else x[c] = fmaf(y, k, sc.y);
+                        }
                     }
                     // masks: rows behind a token, and before its window
                     const int32_t key = (job.tile0 + i) * kQrTile + row;
@@ -637,7 +666,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                     const int64_t lo = a.window > 0 ? int64_t(job.first_pos) - a.window + 1 : 0;  // of the first token
                     if (key0 + kQrTile - 1 > job.first_pos || (a.window > 0 && key0 < lo + job.count - 1)) {
 #pragma unroll
-                        for (int c = 0; c < kQrRows; ++c) {
+                        for (int c = 0; c < R; ++c) {
                             int32_t tok = a.group == 1 ? c : c / a.group;
                             if (job.count == 1) tok = 0;
                             const int32_t pos = job.first_pos + tok;
@@ -646,35 +675,32 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                         }
                     }
                     // the tile's reference: the largest weight with its block's scale
-#pragma unroll
-                    for (int c = 0; c < kQrRows; ++c) x[c] += sc.y;
-#pragma unroll
-                    for (int c = 0; c < kQrRows; ++c) {
-                        const float t = warp_top(x[c]);
-                        if (lane == c) sh.top[i & 1][c][warp] = t;
+                    {
+                        const float t = warp_tops<R>(x);
+                        if (lane < R) sh.top[i & 1][lane][warp] = t;
                     }
                     qr_sync();
                     {
-                        const int c = lane % kQrRows;
+                        const int c = lane % R;
                         const float4 t = *reinterpret_cast<const float4 *>(sh.top[i & 1][c]);
                         const float ref = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), now = fmaxf(m_run, ref);
                         const float base = now == -INFINITY ? 0.0f : now;
                         // weights are held 2^8 higher
-                        if (lane < kQrRows) {
+                        if (lane < R) {
                             sh.ref[warp][c] = ref == -INFINITY ? 0.0f : ref - 8.0f;
                             sh.fold[i & 1][warp][c] = make_float2(ex2(m_run - base), ex2(ref - base) * 0.00390625f);
                         }
                         m_run = now;
                         __syncwarp();
                     }
-                    uint32_t p[kQrRows / 2][kTerms];
+                    uint32_t p[R / 2][kTerms];
 #pragma unroll
-                    for (int c = 0; c < kQrRows; c += 2) {
+                    for (int c = 0; c < R; c += 2) {
                         const float2 ref = *reinterpret_cast<const float2 *>(&sh.ref[warp][c]);
                         const float4 f = *reinterpret_cast<const float4 *>(&sh.fold[i & 1][warp][c]);
                         const float w0 = ex2(x[c] - ref.x), w1 = ex2(x[c + 1] - ref.y);
-                        sum[c] = fmaf(sum[c], f.x, w0 * sc.z * f.y);
-                        sum[c + 1] = fmaf(sum[c + 1], f.z, w1 * sc.z * f.w);
+                        sum[c] = fmaf(sum[c], f.x, w0 * (sc.z * f.y));
+                        sum[c + 1] = fmaf(sum[c + 1], f.z, w1 * (sc.z * f.w));
                         split2<kTerms>(w0, w1, p[c / 2]);
                     }
                     // rows of V that nobody holds: their weights are zero, but zero times NaN is not
@@ -693,11 +719,19 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                         if (!ok) break;
                         take(o);
                     }
+                    // 16 columns of a row lie together
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem + S::kP + k * (kQrTile * 16) + row * 16),
-                                     "r"(p[0][k] | p[1][k] << 16), "r"(p[2][k] | p[3][k] << 16), "r"(p[4][k] | p[5][k] << 16), "r"(p[6][k] | p[7][k] << 16)
+                    for (int k = 0; k < (R == 16 ? kTerms : (kTerms + 1) / 2); ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int from = R == 16 ? k : k * 2 + e / 2, pair = R == 16 ? 2 * e : 2 * (e % 2);
+                            w[e] = from < kTerms ? p[pair][from] | p[pair + 1][from] << 16 : 0u;
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem + S::kP + k * (kQrTile * 16) + row * 16), "r"(w[0]), "r"(w[1]),
+                                     "r"(w[2]), "r"(w[3])
                                      : "memory");
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_before();
                     qr_arrive(&sh.p_ready);
@@ -714,7 +748,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                 // the sums over the tile's rows, by way of the maxima's buffer that is not the last tile's
                 float(*const sums)[4] = sh.top[job.n & 1];
 #pragma unroll
-                for (int c = 0; c < kQrRows; ++c) {
+                for (int c = 0; c < R; ++c) {
                     float s = sum[c];
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
@@ -723,14 +757,14 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
                 qr_sync();
                 const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
 #pragma unroll
-                for (int c = 0; c < kQrRows; ++c) {
+                for (int c = 0; c < R; ++c) {
                     if (c >= live) break;
                     const float4 s4 = *reinterpret_cast<const float4 *>(sums[c]);
                     float s = (s4.x + s4.y) + (s4.z + s4.w);
                     const float m = __shfl_sync(~0u, m_run, c);
                     if (job.whole == 0) {
-                        if (row == 0) a.part_ml[slot * kQrRows + c] = make_float2(m, s);
-                        if (has_chan) a.part_o[(slot * kQrRows + c) * HD + chan] = acc[c];
+                        if (row == 0) a.part_ml[slot * a.part_rows + c] = make_float2(m, s);
+                        if (has_chan) a.part_o[(slot * a.part_rows + c) * HD + chan] = acc[c];
                         continue;
                     }
                     const int32_t tok = c / a.group, head = job.kv_head * a.group + c - tok * a.group;
@@ -766,16 +800,15 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16>::kPerSm)) qr_ke
         __syncthreads();
         tc_after();
     }
-    pdl_trigger();
     if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
 }
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, int R>
 cudaError_t launch_qr(QrArgs &a, cudaStream_t st) {
-    using S = QrShape<HD, BF16>;
-    constexpr int smem = QrShape<HD, BF16>::kTotal + int(sizeof(QrShared<S>));
+    using S = QrShape<HD, BF16, R>;
+    constexpr int smem = S::kTotal + int(sizeof(QrShared<S>));
     static_assert(S::kPerSm * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
-    const auto kern = qr_kernel<HD, BF16>;
+    const auto kern = qr_kernel<HD, BF16, R>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
     a.ctas = S::kCtas;

@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
         tc_before();
     }
     if (warp == 8 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.k : &a.v) : "memory");
-    pdl_wait();
+    // The launch before has let this one come early: what it cuts is older than both.
     qr_cut<kQpThreads>(a, &sh.start, sh.warp_sums);  // synchronises the CTA
+    pdl_wait();
     tc_after();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
