@@ -61,7 +61,7 @@ struct QpShape {
 template <typename S>
 struct QpShared {
     uint64_t k_full[S::kStages], k_empty[S::kStages], c_full[S::kCodes], c_empty[S::kCodes], v_full[S::kWide], v_empty[S::kWide], sc_full[S::kScales];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], job_full[kQrJobs], job_empty[kQrJobs], drain[2];
+    uint64_t s_full[2][2], p_ready[2][2], o_step[2][2], q_ready[2], job_full[kQrJobs], job_empty[kQrJobs], drain[2];
     QrJob job[kQrJobs];
     PaStart start;
     int64_t warp_sums[kQpThreads / 32];
@@ -97,9 +97,11 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
         }
         for (int i = 0; i < S::kScales; ++i) mbar_init(&sh.sc_full[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_ready[i], 4);
-            mbar_init(&sh.o_full[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sh.s_full[i][b], 1);
+                mbar_init(&sh.p_ready[i][b], 4);
+                mbar_init(&sh.o_step[i][b], 1);
+            }
             mbar_init(&sh.q_ready[i], 4);
             mbar_init(&sh.drain[i], 1);
         }
@@ -223,24 +225,25 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 // ---------------------------------------------------- MMAs
                 const int d = warp == 14 ? 1 : 0;
                 uint32_t g = 0, mine = 0, items = 0;  // tiles, tiles and items of this stream
-                auto score = [&](uint32_t i) {
+                // S of half b of tile i: 64 rows of K
+                auto score = [&](uint32_t i, int b) {
                     const uint32_t slot = i % S::kStages;
-                    ok = pa_wait(&sh.k_full[slot], i / S::kStages & 1, stop);
+                    if (b == 0) ok = pa_wait(&sh.k_full[slot], i / S::kStages & 1, stop);
                     if (!ok) return;
                     tc_after();
                     if (elect_one()) {
-                        constexpr uint32_t id = tc_idesc8(128, 128, false, false);
-                        const uint64_t kd = tc_desc(smem + S::kK + slot * S::kCodeBytes, 16, S::kAtom, S::kSwizzle);
+                        constexpr uint32_t id = tc_idesc8(128, 64, false, false);
+                        const uint64_t kd = tc_desc(smem + S::kK + slot * S::kCodeBytes + b * (S::kCodeBytes / 2), 16, S::kAtom, S::kSwizzle);
                         const uint64_t qd = tc_desc(smem + S::kQ + d * S::kQBytes, 16, S::kAtom, S::kSwizzle);
 #pragma unroll
                         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
                             for (int kk = 0; kk < HD / 32; ++kk)
-                                tc_mma8(tmem + d * 128, qd + t * (S::kCodeBytes >> 4) + kk * 2, kd + kk * 2, id, t != 0 || kk != 0);
+                                tc_mma8(tmem + d * 128 + b * 64, qd + t * (S::kCodeBytes >> 4) + kk * 2, kd + kk * 2, id, t != 0 || kk != 0);
                     }
                     __syncwarp();
-                    tc_commit(&sh.s_full[d]);
-                    tc_commit(&sh.k_empty[slot]);
+                    tc_commit(&sh.s_full[d][b]);
+                    if (b == 1) tc_commit(&sh.k_empty[slot]);
                 };
                 for (uint32_t at = 0;; ++at) {
                     ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
@@ -265,35 +268,42 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     // (q_ready says, too, that O of the item before has been read)
                     ok = pa_wait(&sh.q_ready[d], items++ & 1, stop);
                     if (!ok) break;
-                    score(g);
+                    score(g, 0);
+                    if (ok) score(g, 1);
                     for (uint32_t i = g; ok && i < g + n; ++i, ++mine) {
                         const uint32_t slot = i % S::kWide;
-                        ok = pa_wait(&sh.v_full[slot], i / S::kWide & 1, stop) && pa_wait(&sh.p_ready[d], mine & 1, stop);
-                        if (!ok) break;
-                        tc_after();
-                        if (elect_one()) {
-                            constexpr uint32_t id = tc_idesc(false, 128, HD, true);
-                            const uint64_t vd = tc_desc(smem + S::kV + slot * S::kWideBytes, kQrTile * 128, 1024, 2);
+                        ok = pa_wait(&sh.v_full[slot], i / S::kWide & 1, stop);
+#pragma unroll 1
+                        for (int b = 0; ok && b < 2; ++b) {
+                            ok = pa_wait(&sh.p_ready[d][b], mine & 1, stop);
+                            if (!ok) break;
+                            tc_after();
+                            if (elect_one()) {
+                                constexpr uint32_t id = tc_idesc(false, 128, HD, true);
+                                const uint64_t vd = tc_desc(smem + S::kV + slot * S::kWideBytes + b * (64 * 128), kQrTile * 128, 1024, 2);
 #pragma unroll
-                            for (int kk = 0; kk < kQrTile / 16; ++kk)
-                                tc_mma_ts(tmem + kO + d * HD, tmem + d * 128 + kk * 8, vd + kk * (2048 >> 4), id, i != g || kk != 0);
+                                for (int kk = 0; kk < 64 / 16; ++kk)
+                                    tc_mma_ts(tmem + kO + d * HD, tmem + d * 128 + b * 64 + kk * 8, vd + kk * (2048 >> 4), id, i != g || b != 0 || kk != 0);
+                            }
+                            __syncwarp();
+                            tc_commit(&sh.o_step[d][b]);
+                            if (b == 1) tc_commit(&sh.v_empty[slot]);
+                            if (i + 1 < g + n) {
+                                // S takes the place of P once P V has read it
+                                ok = pa_wait(&sh.o_step[d][b], mine & 1, stop);
+                                if (ok) score(i + 1, b);
+                            }
                         }
-                        __syncwarp();
-                        if (i + 1 == g + n) tc_commit(&sh.o_full[d]);
-                        else score(i + 1);
-                        if (!ok) break;
-                        tc_commit(&sh.v_empty[slot]);
                     }
                     if (!ok) break;
                     g += n;
                 }
             } else if (warp >= 10 && warp < 14) {
                 // ---------------------------------------------------- V to f16
-                // A lane takes 16 codes of a row; lanes of the upper half of a row of 128
-                // store their two pieces in the other order, so that eight lanes' pieces
-                // fill all banks.
-                constexpr int kChunks = HD / 16, kRowsAtOnce = 32 / kChunks;
-                const int c = lane % kChunks, r0 = (warp - 10) * 32 + lane / kChunks;
+                // A lane takes 16 codes; eight neighbouring lanes those of eight rows, whose
+                // places the swizzle spreads over all banks, read and written.
+                constexpr int kChunks = HD / 16;
+                const int r0 = (warp - 10) * 32 + lane % 8, c0 = lane / 8;
                 uint32_t g = 0;
                 for (uint32_t at = 0;; ++at) {
                     ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
@@ -308,28 +318,27 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         if (!ok) break;
                         const uint32_t src = smem + S::kC + from * S::kCodeBytes, dst = smem + S::kV + to * S::kWideBytes;
                         const int32_t held = len - (tile0 + i) * kQrTile;  // rows of the tile
-#pragma unroll 4
-                        for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
-                            const int r = r0 + k * kRowsAtOnce;
+#pragma unroll
+                        for (int k = 0; k < kChunks; ++k) {
+                            const int r = r0 + k % 4 * 8, c = c0 + k / 4 * 4;
                             uint32_t at8 = r * HD + c * 16;
                             at8 ^= HD == 128 ? (r & 7) << 4 : (at8 >> 7 & 3) << 4;
                             uint32_t w[4];
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + at8));
+                            if (held < kQrTile && r >= held) w[0] = w[1] = w[2] = w[3] = 0;
                             uint32_t x[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[e / 2] >> (16 * (e % 2))), __NV_E4M3);
-                                x[e] = r < held ? uint32_t(v.x) | uint32_t(v.y) << 16 : 0u;
+                                x[e] = uint32_t(v.x) | uint32_t(v.y) << 16;
                             }
                             // channel 16 c of a row lies in half c / 4, 16-byte piece 2 (c % 4)
-                            const uint32_t row = dst + (c / 4) * (kQrTile * 128) + r * 128;
+                            const uint32_t to16 = dst + (c / 4) * (kQrTile * 128) + r * 128;
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int p = j ^ (c / 4 & 1);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((2 * (c % 4) + p) ^ (r & 7)) << 4)), "r"(p ? x[4] : x[0]),
-                                             "r"(p ? x[5] : x[1]), "r"(p ? x[6] : x[2]), "r"(p ? x[7] : x[3])
+                            for (int j = 0; j < 2; ++j)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to16 + (((2 * (c % 4) + j) ^ (r & 7)) << 4)), "r"(x[4 * j]),
+                                             "r"(x[4 * j + 1]), "r"(x[4 * j + 2]), "r"(x[4 * j + 3])
                                              : "memory");
-                            }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         qr_arrive(&sh.c_empty[from]);
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
             // weights are scaled up so that small ones stay normal numbers of f16; a row's then reach 2^(kLift + kSlack)
             constexpr float kLift = 8.0f, kSlack = 4.0f;
             const int32_t rtok = row / a.group, rhead = row - rtok * a.group;
-            uint32_t g = 0, mine = 0, items = 0;
+            uint32_t g = 0, mine = 0;  // tiles, and halves of this stream's
             for (uint32_t at = 0;; ++at) {
                 ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
                 if (!ok) break;
@@ -445,56 +454,94 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 const bool busy = __any_sync(~0u, valid);
                 int32_t key0 = job.tile0 * kQrTile;
                 float ref = -INFINITY;  // reference, log2 units, less kLift
-                float sum = 0.0f;
-                for (int32_t i = 0; i < job.n; ++i, ++g, ++mine, key0 += kQrTile) {
-                    ok = pa_wait(&sh.sc_full[g % S::kScales], g / S::kScales & 1, stop) && pa_wait(&sh.s_full[d], mine & 1, stop);
+                float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+                for (int32_t i = 0; i < 2 * job.n; ++i, ++mine, key0 += 64) {
+                    const int b = i & 1;  // the tile's first or second half, 64 rows of K
+                    const uint32_t tile = g + uint32_t(i / 2);
+                    if (b == 0) ok = pa_wait(&sh.sc_full[tile % S::kScales], tile / S::kScales & 1, stop);
+                    ok = ok && pa_wait(&sh.s_full[d][b], mine >> 1 & 1, stop);
                     if (!ok) break;
                     if (busy) {
-                        const float4 *sc = sh.scale[g % S::kScales];
+                        const float4 *sc = sh.scale[tile % S::kScales];
+                        const uint32_t t_h = t_s + b * 64;
+                        const int col0 = b * 64;
                         tc_after();
-                        // first pass: the largest of the scores with their blocks' scales, from
-                        // that of each 16 columns; masked scores go back to TMEM as such
                         const int32_t hi_c = pos - key0, lo_c = lo - key0;
-                        const bool edge = __any_sync(~0u, hi_c < kQrTile - 1 || lo_c > 0);
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int c0 = 0; c0 < kQrTile; c0 += 64) {
-                            float x[64];
-                            tc_ld32(t_s + c0, x);
-                            tc_ld32(t_s + c0 + 32, x + 32);
-                            tc_wait_ld();
-                            if (edge) {
+                        float x[64];
+                        tc_ld32(t_h, x);
+                        tc_ld32(t_h + 32, x + 32);
+                        tc_wait_ld();
+                        if (__any_sync(~0u, hi_c < 63 || lo_c > 0)) {
 #pragma unroll
-                                for (int e = 0; e < 64; e += 32) {
-                                    const uint32_t seen = pa_seen(lo_c - c0 - e, hi_c - c0 - e);
+                            for (int e = 0; e < 64; e += 32) {
+                                const uint32_t seen = pa_seen(lo_c - e, hi_c - e);
 #pragma unroll
-                                    for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
-                                }
-                                tc_st32(t_s + c0, x);
-                                tc_st32(t_s + c0 + 32, x + 32);
-                            }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                float m0 = x[q * 16], m1 = x[q * 16 + 1];
-#pragma unroll
-                                for (int c = 2; c < 16; c += 4) {
-                                    m0 = max3(m0, x[q * 16 + c], c + 1 < 16 ? x[q * 16 + c + 1] : m0);
-                                    if (c + 2 < 16) m1 = max3(m1, x[q * 16 + c + 2], x[q * 16 + c + 3]);
-                                }
-                                const float4 f = sc[((c0 + q * 16) >> a.page_log2)];
-                                float m = fmaxf(m0, m1) * (f.x * mul);
-                                if (CAP) m = m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap;
-                                top = fmaxf(top, m + f.y);
+                                for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
                             }
                         }
-                        if (edge) tc_wait_st();
-                        top = valid ? top - kLift : -INFINITY;
-                        // move the reference when a row grew past the slack
-                        if (__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
+                        // Weights relative to the reference as it stands, and the largest score
+                        // beside them: where a row grew past the slack they are taken once
+                        // more with a new one.
+#pragma unroll 1
+                        for (;;) {
+                            const float base = ref == -INFINITY ? 0.0f : ref;
+                            float top = -INFINITY;
+                            float2 sums = sum2;
+#pragma unroll
+                            for (int q = 0; q < 64; q += 32) {
+                                float p[16];
+#pragma unroll
+                                for (int u = q; u < q + 32; u += 16) {
+                                    const float4 f = sc[(col0 + u) >> a.page_log2];
+                                    float m0 = fmaxf(x[u], x[u + 1]), m1 = fmaxf(x[u + 2], x[u + 3]);
+#pragma unroll
+                                    for (int c = 4; c < 16; c += 4) {
+                                        m0 = max3(m0, x[u + c], x[u + c + 1]);
+                                        m1 = max3(m1, x[u + c + 2], x[u + c + 3]);
+                                    }
+                                    const float k = f.x * mul, b0 = f.y - base;
+                                    if constexpr (CAP) {
+                                        const float m = fmaxf(m0, m1) * k;
+                                        top = fmaxf(top, (m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap) + f.y);
+                                    } else {
+                                        top = fmaxf(top, fmaf(fmaxf(m0, m1), k, f.y));
+                                    }
+                                    const float2 kk = make_float2(k, k), bb = make_float2(b0, b0);
+                                    float2 acc[2];
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c) {
+                                        float2 v = make_float2(x[u + 2 * c], x[u + 2 * c + 1]);
+                                        if constexpr (CAP) {
+                                            v = make_float2(v.x == -INFINITY ? v.x : fmaf(pa_tanh_of_any(v.x * k), a.cap, b0),
+                                                            v.y == -INFINITY ? v.y : fmaf(pa_tanh_of_any(v.y * k), a.cap, b0));
+                                        } else {
+                                            v = fma2(v, kk, bb);
+                                        }
+                                        v.x = ex2(v.x);
+                                        v.y = ex2(v.y);
+                                        acc[c & 1] = c < 2 ? v : add2(acc[c & 1], v);
+                                        p[(u - q) / 2 + c] = __uint_as_float(pack2<false>(v.x, v.y));
+                                    }
+                                    sums = fma2(add2(acc[0], acc[1]), make_float2(f.z, f.z), sums);
+                                }
+                                tc_st16(t_h + q / 2, p);
+                            }
+                            top = valid ? top - kLift : -INFINITY;
+                            if (!__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
+                                sum2 = sums;
+                                break;
+                            }
+                            tc_wait_st();  // P is written once more
                             const float now = fmaxf(ref, top);
                             if (i > 0) {
+                                // O is the warps' own once P V of the half before is done
+                                ok = pa_wait(&sh.o_step[d][b ^ 1], (mine - 1) >> 1 & 1, stop);
+                                if (!ok) break;
+                                tc_after();
                                 const float f = now == -INFINITY ? 1.0f : ex2(ref - now);
-                                sum *= f;
+                                sum2.x *= f;
+                                sum2.y *= f;
 #pragma unroll 1
                                 for (int c = 0; c < HD; c += 32) {
                                     float o[32];
@@ -507,52 +554,20 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                             }
                             ref = now;
                         }
-                        // second pass: the weights, 32 at a time, the next scores on their
-                        // way; P takes the place of scores already read
-                        const float base = ref == -INFINITY ? 0.0f : ref;
-                        float x[2][32];
-                        tc_ld32(t_s, x[0]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tc_wait_ld();
-                            if (q < 3) tc_ld32(t_s + (q + 1) * 32, x[(q + 1) & 1]);
-                            float p[16];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const float4 f = sc[((q * 32 + u * 16) >> a.page_log2)];
-                                const float k = f.x * mul, b = f.y - base;
-                                const float2 kk = make_float2(k, k), bb = make_float2(b, b);
-                                float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const float *y = &x[q & 1][u * 16 + 2 * c];
-                                    float2 v = make_float2(y[0], y[1]);
-                                    if constexpr (CAP) {
-                                        v = make_float2(v.x == -INFINITY ? v.x : fmaf(pa_tanh_of_any(v.x * k), a.cap, b),
-                                                        v.y == -INFINITY ? v.y : fmaf(pa_tanh_of_any(v.y * k), a.cap, b));
-                                    } else {
-                                        v = fma2(v, kk, bb);
-                                    }
-                                    v.x = ex2(v.x);
-                                    v.y = ex2(v.y);
-                                    acc = add2(acc, v);
-                                    p[u * 8 + c] = __uint_as_float(pack2<false>(v.x, v.y));
-                                }
-                                sum = fmaf(acc.x + acc.y, f.z, sum);
-                            }
-                            tc_st16(t_s + q * 16, p);
-                        }
+                        if (!ok) break;
                         tc_wait_st();
                         tc_before();
                     }
-                    qr_arrive(&sh.p_ready[d]);
+                    qr_arrive(&sh.p_ready[d][b]);
                 }
+                g += uint32_t(job.n);
                 if (!ok) break;
                 // ---- the end of the item, or of this CTA's piece of it
-                ok = pa_wait(&sh.o_full[d], items++ & 1, stop);
+                ok = pa_wait(&sh.o_step[d][0], (mine - 2) >> 1 & 1, stop) && pa_wait(&sh.o_step[d][1], (mine - 1) >> 1 & 1, stop);
                 if (!ok) break;
                 if (busy) {
                     tc_after();
+                    const float sum = sum2.x + sum2.y;
                     const bool whole = job.whole != 0;
                     float f = 1.0f;
                     if (whole) {
