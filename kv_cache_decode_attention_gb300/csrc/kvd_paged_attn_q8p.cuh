@@ -163,12 +163,14 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
                     const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
                     const int32_t h = w.h;
-                    // lane's page of a tile, -1 = none
-                    auto page_of = [&](int32_t t) {
-                        const int32_t p = (tile0 + t) * ppt + lane;
+                    // Page numbers and scales of 32 pages at a time, lane by lane; the next 32 are
+                    // under way meanwhile.  (A tile's own, two and one ahead, held up pages of 16.)
+                    const int32_t page0 = tile0 * ppt, pages = n * ppt;
+                    auto lookup = [&](int32_t block) {
+                        const int32_t p = block * 32 + lane;
                         int32_t page = -1;
-                        if (t < n && lane < ppt && p < held) {
-                            page = table[p];
+                        if (p < pages && page0 + p < held) {
+                            page = table[page0 + p];
                             if (uint32_t(page) >= uint32_t(a.n_pages)) {
                                 set_error(a.err, kErrBounds);
                                 page = -1;
@@ -186,35 +188,43 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         __syncwarp();
                         if (lane < ppt) tma_2d(dst + lane * box, map, 0, page < 0 ? a.pool_rows : (page * a.n_kv + h) << a.page_log2, bar);
                     };
-                    auto load_k = [&](int32_t page, float2 s) {
-                        const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
-                        if (turn > 0) ok = pa_wait(&sh.k_empty[slot], (turn & 1) ^ 1, stop);
-                        if (!ok) return;
-                        if (lane < ppt) {
-                            const float vs = scale_of(s.y, a.err);
-                            sh.scale[sc][lane] = make_float4(scale_of(s.x, a.err), log2f(vs), 1.0f / vs, 0.0f);
+                    const int32_t per_block = 32 / ppt;  // tiles
+                    int32_t block_pages = lookup(0), next_pages = lookup(1), v_page = -1;
+                    float2 block_scales = scales(block_pages), next_scales = make_float2(1.0f, 1.0f);
+                    // K runs a tile ahead of V
+                    for (int32_t t = 0; ok && t <= n; ++t) {
+                        int32_t page = -1;
+                        if (t < n) {
+                            const int32_t in = t % per_block;
+                            if (t > 0 && in == 0) {
+                                block_pages = next_pages;
+                                block_scales = per_block > 1 ? next_scales : scales(block_pages);
+                                next_pages = lookup(t / per_block + 1);
+                            }
+                            if (in == 1) next_scales = scales(next_pages);
+                            const int from = in * ppt + lane % ppt;
+                            page = __shfl_sync(~0u, block_pages, from);
+                            const float ks = __shfl_sync(~0u, block_scales.x, from), vs = __shfl_sync(~0u, block_scales.y, from);
+                            const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
+                            if (turn > 0) ok = pa_wait(&sh.k_empty[slot], (turn & 1) ^ 1, stop);
+                            if (!ok) break;
+                            if (lane < ppt) {
+                                const float v = scale_of(vs, a.err);
+                                sh.scale[sc][lane] = make_float4(scale_of(ks, a.err), log2f(v), 1.0f / v, 0.0f);
+                            }
+                            qr_arrive(&sh.sc_full[sc]);
+                            load(&a.k, smem + S::kK + slot * S::kCodeBytes, page, &sh.k_full[slot]);
+                            ++k_loads;
+                            if (lane == 0) *static_cast<volatile int *>(&sh.steps) = int(k_loads);
+                    }
+                        if (t > 0) {
+                            const uint32_t slot = v_loads % S::kCodes, turn = v_loads / S::kCodes;
+                            if (turn > 0) ok = pa_wait(&sh.c_empty[slot], (turn & 1) ^ 1, stop);
+                            if (!ok) break;
+                            load(&a.v, smem + S::kC + slot * S::kCodeBytes, v_page, &sh.c_full[slot]);
+                            ++v_loads;
                         }
-                        qr_arrive(&sh.sc_full[sc]);
-                        load(&a.k, smem + S::kK + slot * S::kCodeBytes, page, &sh.k_full[slot]);
-                        ++k_loads;
-                        if (lane == 0) *static_cast<volatile int *>(&sh.steps) = int(k_loads);
-                    };
-                    // K runs a tile ahead of V, page numbers two and scales one ahead of K
-                    int32_t page = page_of(0), next = page_of(1);
-                    float2 s = scales(next);
-                    load_k(page, scales(page));
-                    for (int32_t t = 0; ok && t < n; ++t) {
-                        const int32_t after = page_of(t + 2);
-                        if (t + 1 < n) load_k(next, s);
-                        if (!ok) break;
-                        const uint32_t slot = v_loads % S::kCodes, turn = v_loads / S::kCodes;
-                        if (turn > 0) ok = pa_wait(&sh.c_empty[slot], (turn & 1) ^ 1, stop);
-                        if (!ok) break;
-                        load(&a.v, smem + S::kC + slot * S::kCodeBytes, page, &sh.c_full[slot]);
-                        ++v_loads;
-                        s = scales(after);
-                        page = next;
-                        next = after;
+                        v_page = page;
                     }
                     if (!ok) break;
                     left -= have;
@@ -290,8 +300,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                             if (b == 1) tc_commit(&sh.v_empty[slot]);
                             if (i + 1 < g + n) {
                                 // S takes the place of P once P V has read it
-                                ok = pa_wait(&sh.o_step[d][b], mine & 1, stop);
-                                if (ok) score(i + 1, b);
+                                score(i + 1, b);
                             }
                         }
                     }
