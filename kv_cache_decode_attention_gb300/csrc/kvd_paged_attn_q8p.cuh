@@ -380,9 +380,22 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
             const int row = (warp & 3) * 32 + lane;        // row of the tile
             const uint32_t t_row = tmem + (uint32_t((warp & 3) * 32) << 16);
             const uint32_t t_s = t_row + d * 128, t_o = t_row + kO + d * HD;
-            // weights are scaled up so that small ones stay normal numbers of f16; a row's then reach 2^(kLift + kSlack)
-            constexpr float kLift = 8.0f, kSlack = 4.0f;
+            // Weights reach 2^(kLift + kSlack), the most that f16 holds, before the reference
+            // moves, and keep 11 bits down to 2^-17 of it, some down to 2^-27.  (With a slack of
+            // 2^4 4096 rows over 4096 took 18 us longer: the maximum grows often while a
+            // row has seen little.)
+            constexpr float kLift = 3.0f, kSlack = 12.0f;
             const int32_t rtok = row / a.group, rhead = row - rtok * a.group;
+            // Rows travel between global memory and the threads by way of the first two
+            // terms' places of the warp's own rows, a row's 2 HD bytes by neighbouring
+            // lanes: a lane that read or wrote its own row in 16-byte pieces would take a
+            // sector of 32 rows each time, 2 us an item for q and again for O.
+            constexpr int kPieces = HD / 8, kRowsAtOnce = 32 / kPieces;
+            auto place = [&](int r, int piece) {  // of 16 bytes of tile row r
+                uint32_t at = r * HD + piece % (HD / 16) * 16;
+                at ^= HD == 128 ? (r & 7) << 4 : (at >> 7 & 3) << 4;
+                return smem + S::kQ + d * S::kQBytes + piece / (HD / 16) * S::kCodeBytes + at;
+            };
             uint32_t g = 0, mine = 0;  // tiles, and halves of this stream's
             for (uint32_t at = 0;; ++at) {
                 ok = pa_wait(&sh.job_full[at % kQrJobs], at / kQrJobs & 1, stop);
@@ -401,13 +414,24 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 float mul;
                 {
                     uint4 x[HD / 8];
+                    const T *mine_q = static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok + int64_t(head) * a.q_head;
+                    const uint64_t src = valid ? reinterpret_cast<uint64_t>(mine_q) : 0;
 #pragma unroll
-                    for (int i = 0; i < HD / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
-                    if (valid) {
-                        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok + int64_t(head) * a.q_head);
-#pragma unroll
-                        for (int i = 0; i < HD / 8; ++i) x[i] = p[i];
+                    for (int k = 0; k < kPieces; ++k) {
+                        const int r = k * kRowsAtOnce + lane / kPieces;
+                        const uint64_t from = __shfl_sync(~0u, src, r);
+                        x[k] = from != 0 ? reinterpret_cast<const uint4 *>(from)[lane % kPieces] : make_uint4(0, 0, 0, 0);
                     }
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place((warp & 3) * 32 + k * kRowsAtOnce + lane / kPieces, lane % kPieces)),
+                                     "r"(x[k].x), "r"(x[k].y), "r"(x[k].z), "r"(x[k].w)
+                                     : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(place(row, k)) : "memory");
+                    __syncwarp();
                     auto two = [](uint32_t w) {
                         float2 v;
                         if constexpr (BF16) v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -592,26 +616,44 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
                     const int32_t prow = d * tile_tok * a.group + row;
                     if (!whole && valid) a.part_ml[slot * a.part_rows + prow] = make_float2(ref, sum);
-                    uint8_t *dst = static_cast<uint8_t *>(a.out) + ((int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head) * 2;
-                    float *pdst = a.part_o + (slot * a.part_rows + prow) * HD;
-#pragma unroll 1
+                    const uint64_t dst = !valid ? 0
+                                         : whole ? reinterpret_cast<uint64_t>(static_cast<T *>(a.out) + (int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head)
+                                                 : reinterpret_cast<uint64_t>(a.part_o + (slot * a.part_rows + prow) * HD);
+                    // 2 HD bytes of each of the warp's rows to `skip` bytes behind their dst
+                    auto send = [&](int skip) {
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < kPieces; ++k) {
+                            const int r = k * kRowsAtOnce + lane / kPieces;
+                            const uint64_t to = __shfl_sync(~0u, dst, r);
+                            uint4 v;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place((warp & 3) * 32 + r, lane % kPieces)) : "memory");
+                            if (to != 0) *reinterpret_cast<uint4 *>(to + skip + lane % kPieces * 16) = v;
+                        }
+                        __syncwarp();
+                    };
+#pragma unroll
                     for (int c = 0; c < HD; c += 32) {
                         float y[32];
-                        __syncwarp();
                         tc_ld32(t_o + c, y);
                         tc_wait_ld();
-                        if (valid && whole) {
+                        if (whole) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4 *>(dst + (c + e) * 2) =
-                                    make_uint4(pack2<BF16>(y[e] * f, y[e + 1] * f), pack2<BF16>(y[e + 2] * f, y[e + 3] * f),
-                                               pack2<BF16>(y[e + 4] * f, y[e + 5] * f), pack2<BF16>(y[e + 6] * f, y[e + 7] * f));
-                        } else if (valid) {
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(row, (c + e) / 8)), "r"(pack2<BF16>(y[e] * f, y[e + 1] * f)),
+                                             "r"(pack2<BF16>(y[e + 2] * f, y[e + 3] * f)), "r"(pack2<BF16>(y[e + 4] * f, y[e + 5] * f)),
+                                             "r"(pack2<BF16>(y[e + 6] * f, y[e + 7] * f))
+                                             : "memory");
+                        } else {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(pdst + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(row, (c + e) % (HD / 2) / 4)), "f"(y[e]), "f"(y[e + 1]), "f"(y[e + 2]),
+                                             "f"(y[e + 3])
+                                             : "memory");
+                            if ((c + 32) % (HD / 2) == 0) send((c + 32 - HD / 2) * 4);
                         }
                     }
+                    if (whole) send(0);
                     __syncwarp();
                     tc_before();
                 }
