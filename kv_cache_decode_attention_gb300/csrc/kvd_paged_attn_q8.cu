@@ -76,6 +76,12 @@ bool view_ok(const kvd_rows *r, int64_t tokens, int32_t heads) {
     return ok(tokens, r->token_stride) && ok(heads, r->head_stride);
 }
 
+// What an item costs beside its tiles, in tiles: 10 us of 1.6 us (few rows), 8 of 1.2 to
+// 1.7.  (Drafts took 70 us without, 57 with 2, 49 with 4, 47 with 6, 45 to 46 with 8 and
+// 12, but a decode step 192 with 4, 194 with 6, 199 with 12; 4096 rows over 4096 took 218
+// us without, 151 with 4, 158 with 6, 169 with 12.)
+constexpr int kExtraFew = 6, kExtraMany = 5;
+
 // Requests of up to kQrRows query rows a KV head and larger ones are taken by a kernel
 // each; how many of either there are is known on the device only, so a call that may
 // have both launches both.
@@ -96,6 +102,7 @@ cudaError_t launch(const QrArgs &call, const WsLayout &ws, void *workspace, cuda
         a.part_o = reinterpret_cast<float *>(w + ws.o[i]);
         a.part_rows = i == 0 ? kQrRows : piece_rows(call.n_tokens, call.group);
         a.run = i == 0 ? (eight ? 8 : kQrRows) / call.group : 2 * (kQrTile / call.group);
+        a.extra = i == 0 ? kExtraFew : kExtraMany;
         a.more = i == 0 ? 0 : kQrRows;
         a.most = i == 0 ? kQrRows : INT64_MAX;
     }

@@ -53,7 +53,7 @@ constexpr int kQrMaxSeq = 1 << 20;
 // A cut item as qr_join_kernel finds it; n = 0: none.
 struct QrCut {
     int64_t unit0, total;
-    int32_t units, rows, q_row, kv_head, n, pad;
+    int32_t tiles, rows, q_row, kv_head, n, pad;  // unit0: of its first tile
 };
 
 struct QrArgs {
@@ -69,7 +69,7 @@ struct QrArgs {
     QrCut *cut;       // [ctas]: the cut item that begins in each CTA
     uint32_t *err;
     int64_t window;   // below 2^31; 0 = none
-    int32_t ctas, n_seq, n_tokens, n_kv, group, run, max_pages, n_pages, page_log2, pool_rows;
+    int32_t ctas, n_seq, n_tokens, n_kv, group, run, extra, max_pages, n_pages, page_log2, pool_rows;
     int64_t more, most;  // requests with more than `more` and at most `most` query rows a KV head are this launch's
     int32_t part_rows;
     int32_t give_up;  // for tests: the CTA whose waits end so many ns after it began, or -1
@@ -106,8 +106,11 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
 
 // ---------------------------------------------------------------- the work
 
+// An item costs its CTA more than its tiles do (q, the first scores, its end): as much
+// as `extra` tiles, which the cut counts before them.  A part without a tile of its own
+// is none.
 struct QrItem {
-    int32_t count, first_pos, tile0, tiles;
+    int32_t count, first_pos, tile0, tiles, units;
 };
 __device__ __forceinline__ PaSeq qr_seq(const QrArgs &a, int b, bool report) {
     PaSeq s = {0, 0, 0};
@@ -136,6 +139,7 @@ __device__ __forceinline__ QrItem qr_item(const QrArgs &a, const PaSeq &s, int32
     it.tile0 = int32_t(lo) / kQrTile;
     const int32_t n = (hi + kQrTile - 1) / kQrTile - it.tile0;
     it.tiles = n > 1 ? n : 1;
+    it.units = it.tiles + a.extra;
     return it;
 }
 // The next item in the order (request, KV head, token run).
@@ -151,8 +155,8 @@ __device__ __forceinline__ void qr_next(const QrArgs &a, PaWalk &w) {
     } while (w.s.fresh == 0 && w.b < a.n_seq);
 }
 
-// CTA c takes tiles [c W / ctas, (c + 1) W / ctas) of the W there are.  All
-// threads; the result is in shared memory.  (As pa_cut, in units of single tiles.)
+// CTA c takes units [c W / ctas, (c + 1) W / ctas) of the W there are.  All
+// threads; the result is in shared memory.  (As pa_cut.)
 template <int THREADS>
 __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *warp_sums) {
     constexpr int kWarps = THREADS / 32;
@@ -172,7 +176,7 @@ __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *w
                 s = qr_seq(a, b, turn == 0 && blockIdx.x == 0);
                 u = 0;
 #pragma unroll 1
-                for (int32_t tok = 0; tok < s.fresh; tok += a.run) u += qr_item(a, s, tok).tiles;
+                for (int32_t tok = 0; tok < s.fresh; tok += a.run) u += qr_item(a, s, tok).units;
                 if (turn == 0) mine += u * a.n_kv;
                 else if (off < u * a.n_kv) break;
                 else off -= u * a.n_kv;
@@ -184,7 +188,7 @@ __device__ __forceinline__ void qr_cut(const QrArgs &a, PaStart *out, int64_t *w
             for (; off >= u; off -= u) ++h;
 #pragma unroll 1
             for (;; tok += a.run) {
-                const int32_t n = qr_item(a, s, tok).tiles;
+                const int32_t n = qr_item(a, s, tok).units;
                 if (off < n) break;
                 off -= n;
             }
@@ -224,12 +228,12 @@ static __device__ __forceinline__ int32_t qr_cta_of(int64_t u, int64_t total, in
 struct QrPieces {
     int32_t first, n, ctas;
     int64_t unit0, sparse;  // sparse = units in all, if fewer than CTAs (each has one then), else 0
-    __device__ __forceinline__ QrPieces(int64_t unit0_, int32_t units, int64_t total, int32_t ctas_) {
+    __device__ __forceinline__ QrPieces(int64_t unit0_, int32_t tiles, int64_t total, int32_t ctas_) {
         ctas = ctas_;
         first = qr_cta_of(unit0_, total, ctas);
         sparse = total < ctas ? total : 0;
         unit0 = unit0_;
-        n = sparse != 0 ? units : qr_cta_of(unit0_ + units - 1, total, ctas) - first + 1;
+        n = sparse != 0 ? tiles : qr_cta_of(unit0_ + tiles - 1, total, ctas) - first + 1;
     }
     __device__ __forceinline__ int64_t slot(int32_t i) const {
         if (i == 0) return 2 * first + 1;
@@ -246,8 +250,8 @@ struct QrShape {
     static constexpr int kTerms = BF16 ? 2 : 3;
     static constexpr int kN = (kTerms * R + 15) / 16 * 16;  // columns: a multiple of 16
     // what fits: the third terms of 16 rows take the third CTA's room
-    static constexpr int kPerSm = kN <= 32 ? 3 : 2, kCtas = 152 * kPerSm;
-    static constexpr int kStages = (kN <= 32 ? 2 : 3) * (HD == 128 ? 1 : 2);
+    static constexpr int kPerSm = R == 8 ? 3 : 2, kCtas = 152 * kPerSm;
+    static constexpr int kStages = (R == 8 ? 2 : 3) * (HD == 128 ? 1 : 2);
     // Scales of tile t + kScales replace those of tile t once its K is asked for, for
     // which S of tile t + 2 is over, and so tile t's softmax has read its own.
     static constexpr int kScales = kStages + 2;
@@ -415,24 +419,32 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
             const int ppt = kQrTile >> a.page_log2;
             const uint32_t box = uint32_t(HD) << a.page_log2;  // bytes of a page
             bool ok = true;
-            for (uint32_t at = 0;; ++at) {
-                QrJob &job = sh.job[at % kQrJobs];
-                if (at >= kQrJobs) ok = qr_wait(a, sh, &sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1);
-                if (!ok) break;
-                if (left <= 0) {
-                    if (lane == 0) job.n = 0;
+            for (uint32_t at = 0;;) {
+                const bool over = left <= 0;
+                QrItem it = {};
+                int32_t have = 0, tile = 0, n = 0;
+                if (!over) {
+                    it = qr_item(a, w.s, w.tok);
+                    have = it.units - unit;
+                    const int32_t end = unit + (left < have ? int32_t(left) : have) - a.extra;
+                    tile = unit > a.extra ? unit - a.extra : 0;
+                    n = end > tile ? end - tile : 0;
+                }
+                const int32_t tile0 = it.tile0 + tile;
+                if (over || n > 0) {
+                    QrJob &job = sh.job[at % kQrJobs];
+                    if (at >= kQrJobs) ok = qr_wait(a, sh, &sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const bool whole = n == it.tiles;
+                        job = QrJob{n, tile0, tile == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
+                        if (!over && tile == 0 && !whole)
+                            a.cut[blockIdx.x] = QrCut{st.from + (st.units - left) - unit + a.extra, st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
+                    }
                     qr_arrive(&sh.job_full[at % kQrJobs]);
-                    break;
+                    ++at;
                 }
-                const QrItem it = qr_item(a, w.s, w.tok);
-                const int32_t have = it.tiles - unit, n = left < have ? int32_t(left) : have, tile0 = it.tile0 + unit;
-                const bool whole = unit == 0 && n == it.tiles;
-                if (lane == 0) {
-                    job = QrJob{n, tile0, unit == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
-                    if (unit == 0 && !whole)
-                        a.cut[blockIdx.x] = QrCut{st.from + (st.units - left), st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
-                }
-                qr_arrive(&sh.job_full[at % kQrJobs]);
+                if (over) break;
                 const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
                 const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
                 const int32_t h = w.h;
@@ -562,6 +574,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
             // the channel whose sums this thread keeps: rows of 64 lie in the first 16 lanes of each warp
             const int chan = HD == 128 ? row : warp * 16 + lane;
             const bool has_chan = HD == 128 || lane < 16;
+            const int32_t per_256 = (256 + a.group - 1) / a.group;  // exact for 16 columns
             uint32_t g = 0;
             bool ok = true;
             for (uint32_t at = 0;; ++at) {
@@ -677,9 +690,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     if (key0 + kQrTile - 1 > job.first_pos || (a.window > 0 && key0 < lo + job.count - 1)) {
 #pragma unroll
                         for (int c = 0; c < R; ++c) {
-                            int32_t tok = a.group == 1 ? c : c / a.group;
-                            if (job.count == 1) tok = 0;
-                            const int32_t pos = job.first_pos + tok;
+                            const int32_t pos = job.first_pos + (c * per_256 >> 8);  // its token is c / group
                             const bool seen = key <= pos && pos <= last && (a.window == 0 || key > pos - a.window);
                             x[c] = seen ? x[c] : -INFINITY;
                         }
@@ -842,7 +853,7 @@ __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ Qr
     const int32_t share = int32_t(blockIdx.x) < few ? 2 : j.wide;
     const QrCut cut = a.cut[at_cta / share];
     if (cut.n == 0) return;
-    const QrPieces pieces(cut.unit0, cut.units, cut.total, a.ctas);
+    const QrPieces pieces(cut.unit0, cut.tiles, cut.total, a.ctas);
     const int32_t col = int32_t(threadIdx.x & 31) * kPer;
     for (int32_t r = at_cta % share * 8 + (threadIdx.x >> 5); r < cut.rows; r += share * 8) {
         float top = -INFINITY, sum = 0.0f, o[kPer] = {};

@@ -44,6 +44,7 @@ constexpr int kQpCtas = 152;
 constexpr int kQpRegs = 128, kQpSoftRegs = 184, kQpLoadRegs = 72;
 static_assert(2 * kQpSoftRegs + 2 * kQpLoadRegs <= 4 * kQpRegs, "setmaxnreg shares");
 constexpr int kQpMaxRows = 2 * kQrTile;
+constexpr float kTanh1 = float(kPaTanh[0]), kTanh2 = float(kPaTanh[1]), kTanh3 = float(kPaTanh[2]), kTanh4 = float(kPaTanh[3]);
 
 template <int HD, bool BF16>
 struct QpShape {
@@ -142,24 +143,32 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 int64_t left = st.units;
                 const int ppt = kQrTile >> a.page_log2;
                 const uint32_t box = uint32_t(HD) << a.page_log2;  // bytes of a page
-                for (uint32_t at = 0;; ++at) {
-                    QrJob &job = sh.job[at % kQrJobs];
-                    if (at >= kQrJobs) ok = pa_wait(&sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1, stop);
-                    if (!ok) break;
-                    if (left <= 0) {
-                        if (lane == 0) job.n = 0;
+                for (uint32_t at = 0;;) {
+                    const bool over = left <= 0;
+                    QrItem it = {};
+                    int32_t have = 0, tile = 0, n = 0;
+                    if (!over) {
+                        it = qr_item(a, w.s, w.tok);
+                        have = it.units - unit;
+                        const int32_t end = unit + (left < have ? int32_t(left) : have) - a.extra;
+                        tile = unit > a.extra ? unit - a.extra : 0;
+                        n = end > tile ? end - tile : 0;
+                    }
+                    const int32_t tile0 = it.tile0 + tile;
+                    if (over || n > 0) {
+                        QrJob &job = sh.job[at % kQrJobs];
+                        if (at >= kQrJobs) ok = pa_wait(&sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1, stop);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            const bool whole = n == it.tiles;
+                            job = QrJob{n, tile0, tile == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
+                            if (!over && tile == 0 && !whole)
+                                a.cut[blockIdx.x] = QrCut{st.from + (st.units - left) - unit + a.extra, st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
+                        }
                         qr_arrive(&sh.job_full[at % kQrJobs]);
-                        break;
+                        ++at;
                     }
-                    const QrItem it = qr_item(a, w.s, w.tok);
-                    const int32_t have = it.tiles - unit, n = left < have ? int32_t(left) : have, tile0 = it.tile0 + unit;
-                    const bool whole = unit == 0 && n == it.tiles;
-                    if (lane == 0) {
-                        job = QrJob{n, tile0, unit == 0, whole, w.s.q0 + w.tok, it.count, w.h, it.first_pos, w.s.len};
-                        if (unit == 0 && !whole)
-                            a.cut[blockIdx.x] = QrCut{st.from + (st.units - left), st.total, it.tiles, it.count * a.group, w.s.q0 + w.tok, w.h, 1, 0};
-                    }
-                    qr_arrive(&sh.job_full[at % kQrJobs]);
+                    if (over) break;
                     const int32_t held = (w.s.len + (1 << a.page_log2) - 1) >> a.page_log2;
                     const int32_t *table = a.block_table + int64_t(w.b) * a.max_pages;
                     const int32_t h = w.h;
@@ -438,15 +447,13 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         else v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
                         return v;
                     };
-                    float top = 0.0f;
-                    bool fine = true;
+                    // the largest, by the bits of the type, which are ordered; what is not finite has all bits of the exponent
+                    uint32_t big = 0;
 #pragma unroll
-                    for (int i = 0; i < HD / 2; ++i) {
-                        const float2 v = two(reinterpret_cast<const uint32_t *>(x)[i]);
-                        const float m = fmaxf(fabsf(v.x), fabsf(v.y));
-                        fine = fine && fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX;
-                        top = fmaxf(top, m);
-                    }
+                    for (int i = 0; i < HD / 2; ++i) big = __vmaxu2(big, reinterpret_cast<const uint32_t *>(x)[i] & 0x7fff7fffu);
+                    big = max(big >> 16, big & 0xffffu);
+                    const bool fine = big < (BF16 ? 0x7f80u : 0x7c00u);
+                    const float top = BF16 ? __uint_as_float(big << 16) : __half2float(__ushort_as_half(uint16_t(big)));
                     int e = 134 - int(__float_as_uint(top) >> 23);
                     e = top == 0.0f ? 0 : e > 120 ? 120 : e < -120 ? -120 : e;
                     const float up = __uint_as_float(uint32_t(e + 127) << 23);
@@ -458,15 +465,13 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             float2 v = two(reinterpret_cast<const uint32_t *>(x)[c * 8 + i]);
-                            v.x *= up;
-                            v.y *= up;
+                            // f16 holds the scaled values and what the terms leave of them, but for 2^-25
+                            __half2 y = __floats2half2_rn(v.x * up, v.y * up);
 #pragma unroll
                             for (int k = 0; k < kTerms; ++k) {
-                                const uint32_t b = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                                const uint32_t b = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(y), __NV_SATFINITE, __NV_E4M3);
                                 t[k][i / 2] = i % 2 ? t[k][i / 2] | b << 16 : b;
-                                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(b), __NV_E4M3)));
-                                v.x -= y.x;
-                                v.y -= y.y;
+                                if (k + 1 < kTerms) y = __hsub2(y, __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(b), __NV_E4M3)));
                             }
                         }
                         uint32_t to = row * HD + c * 16;
@@ -505,14 +510,34 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         tc_ld32(t_h, x);
                         tc_ld32(t_h + 32, x + 32);
                         tc_wait_ld();
+                        float size = 0.0f;  // CAP: the largest score that is seen, by size
                         if (__any_sync(~0u, hi_c < 63 || lo_c > 0)) {
 #pragma unroll
-                            for (int e = 0; e < 64; e += 32) {
+                            for (int e = 0; e < 64; e += 16) {
                                 const uint32_t seen = pa_seen(lo_c - e, hi_c - e);
+                                float m = 0.0f;
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
+                                for (int c = 0; c < 16; ++c) {
+                                    if (CAP) m = fmaxf(m, (seen >> c & 1u) != 0 ? fabsf(x[e + c]) : 0.0f);
+                                    x[e + c] = (seen >> c & 1u) != 0 ? x[e + c] : -INFINITY;
+                                }
+                                if (CAP) size = fmaxf(size, m * sc[(col0 + e) >> a.page_log2].x);
+                            }
+                        } else if (CAP) {
+#pragma unroll
+                            for (int u = 0; u < 64; u += 16) {
+                                float m0 = fabsf(x[u]), m1 = fabsf(x[u + 1]);
+#pragma unroll
+                                for (int c = 2; c < 16; c += 2) {
+                                    m0 = fmaxf(m0, fabsf(x[u + c]));
+                                    m1 = fmaxf(m1, fabsf(x[u + c + 1]));
+                                }
+                                size = fmaxf(size, fmaxf(m0, m1) * sc[(col0 + u) >> a.page_log2].x);
                             }
                         }
+                        // 2 log2 e y = the score's tanh argument; the polynomial holds to y = 1/2.
+                        // (Rows that are no row of the request have no say in what its rows do.)
+                        const bool near = CAP && __all_sync(~0u, !valid || size * mul <= 1.4426950f);
                         // Weights relative to the reference as it stands, and the largest score
                         // beside them: where a row grew past the slack they are taken once
                         // more with a new one.
@@ -521,44 +546,59 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                             const float base = ref == -INFINITY ? 0.0f : ref;
                             float top = -INFINITY;
                             float2 sums = sum2;
+                            // `exponent` of two scores, their factor k and what is added to them
+                            auto weigh = [&](auto exponent) {
 #pragma unroll
-                            for (int q = 0; q < 64; q += 32) {
-                                float p[16];
+                                for (int q = 0; q < 64; q += 32) {
+                                    float p[16];
 #pragma unroll
-                                for (int u = q; u < q + 32; u += 16) {
-                                    const float4 f = sc[(col0 + u) >> a.page_log2];
-                                    float m0 = fmaxf(x[u], x[u + 1]), m1 = fmaxf(x[u + 2], x[u + 3]);
+                                    for (int u = q; u < q + 32; u += 16) {
+                                        const float4 f = sc[(col0 + u) >> a.page_log2];
+                                        float m0 = fmaxf(x[u], x[u + 1]), m1 = fmaxf(x[u + 2], x[u + 3]);
 #pragma unroll
-                                    for (int c = 4; c < 16; c += 4) {
-                                        m0 = max3(m0, x[u + c], x[u + c + 1]);
-                                        m1 = max3(m1, x[u + c + 2], x[u + c + 3]);
-                                    }
-                                    const float k = f.x * mul, b0 = f.y - base;
-                                    if constexpr (CAP) {
-                                        const float m = fmaxf(m0, m1) * k;
-                                        top = fmaxf(top, (m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap) + f.y);
-                                    } else {
-                                        top = fmaxf(top, fmaf(fmaxf(m0, m1), k, f.y));
-                                    }
-                                    const float2 kk = make_float2(k, k), bb = make_float2(b0, b0);
-                                    float2 acc[2];
-#pragma unroll
-                                    for (int c = 0; c < 8; ++c) {
-                                        float2 v = make_float2(x[u + 2 * c], x[u + 2 * c + 1]);
-                                        if constexpr (CAP) {
-                                            v = make_float2(v.x == -INFINITY ? v.x : fmaf(pa_tanh_of_any(v.x * k), a.cap, b0),
-                                                            v.y == -INFINITY ? v.y : fmaf(pa_tanh_of_any(v.y * k), a.cap, b0));
-                                        } else {
-                                            v = fma2(v, kk, bb);
+                                        for (int c = 4; c < 16; c += 4) {
+                                            m0 = max3(m0, x[u + c], x[u + c + 1]);
+                                            m1 = max3(m1, x[u + c + 2], x[u + c + 3]);
                                         }
-                                        v.x = ex2(v.x);
-                                        v.y = ex2(v.y);
-                                        acc[c & 1] = c < 2 ? v : add2(acc[c & 1], v);
-                                        p[(u - q) / 2 + c] = __uint_as_float(pack2<false>(v.x, v.y));
+                                        const float k = f.x * mul, b0 = f.y - base;
+                                        if constexpr (CAP) {
+                                            const float m = fmaxf(m0, m1) * k;
+                                            top = fmaxf(top, (m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap) + f.y);
+                                        } else {
+                                            top = fmaxf(top, fmaf(fmaxf(m0, m1), k, f.y));
+                                        }
+                                        float2 acc[2];
+#pragma unroll
+                                        for (int c = 0; c < 8; ++c) {
+                                            float2 v = exponent(make_float2(x[u + 2 * c], x[u + 2 * c + 1]), k, b0);
+                                            v.x = ex2(v.x);
+                                            v.y = ex2(v.y);
+                                            acc[c & 1] = c < 2 ? v : add2(acc[c & 1], v);
+                                            p[(u - q) / 2 + c] = __uint_as_float(pack2<false>(v.x, v.y));
+                                        }
+                                        sums = fma2(add2(acc[0], acc[1]), make_float2(f.z, f.z), sums);
                                     }
-                                    sums = fma2(add2(acc[0], acc[1]), make_float2(f.z, f.z), sums);
+                                    tc_st16(t_h + q / 2, p);
                                 }
-                                tc_st16(t_h + q / 2, p);
+                            };
+                            if constexpr (!CAP) {
+                                weigh([](float2 v, float k, float b0) { return fma2(v, make_float2(k, k), make_float2(b0, b0)); });
+                            } else if (near) {
+                                // cap tanh(y) = cap y (1 + c1 y^2 + .. + c4 y^8); what is masked stays -infinity
+                                weigh([&](float2 v, float k, float b0) {
+                                    const float ky = k * 0.34657359027997264f;  // y of a raw score
+                                    const float2 y = fma2(v, make_float2(ky, ky), make_float2(0.0f, 0.0f)), z = fma2(y, y, make_float2(0.0f, 0.0f));
+                                    float2 w = fma2(z, make_float2(kTanh4, kTanh4), make_float2(kTanh3, kTanh3));
+                                    w = fma2(w, z, make_float2(kTanh2, kTanh2));
+                                    w = fma2(w, z, make_float2(kTanh1, kTanh1));
+                                    w = fma2(w, z, make_float2(1.0f, 1.0f));
+                                    return fma2(fma2(y, make_float2(a.cap, a.cap), make_float2(0.0f, 0.0f)), w, make_float2(b0, b0));
+                                });
+                            } else {
+                                weigh([&](float2 v, float k, float b0) {
+                                    return make_float2(v.x == -INFINITY ? v.x : fmaf(pa_tanh_of_any(v.x * k), a.cap, b0),
+                                                       v.y == -INFINITY ? v.y : fmaf(pa_tanh_of_any(v.y * k), a.cap, b0));
+                                });
                             }
                             top = valid ? top - kLift : -INFINITY;
                             if (!__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
