@@ -12,11 +12,11 @@
 // precision.  (With s = max|x| / 448 every growth would round every code anew.)
 //
 // Writing.  The rows of one page stand together in the packed batch, so a CTA takes
-// the runs of rows that begin among its 16 tokens, for some heads of K or V: one
-// pass over the rows for the largest value of each run and head, then the scales and
-// the codes already there, then a second pass that writes the codes.  Nobody waits
-// for another CTA, because a block's rows all lie in one.  The second pass finds its
-// rows in L1 or L2.
+// the runs of rows in one page that begin among its tokens, for one head of K or V: it
+// holds up to 128 rows in registers, takes the largest value of each run, settles the
+// scales and the codes already there, and writes the codes.  Nobody waits for another
+// CTA, because a block's rows all lie in one, and every row is read once.  q turns in
+// CTAs of the same launch, whose place in it K and V share.
 
 #include <cfloat>
 #include <cmath>
@@ -27,14 +27,14 @@
 namespace kvd {
 namespace {
 
-constexpr int kStoreTok = 16;     // tokens whose runs a CTA takes
-constexpr int kMaxPage = 128;
-constexpr int kStoreHeads = 8;    // heads of one CTA at most
+constexpr int kStoreThreads = 256;
+constexpr int kWindow = 128;      // rows in registers: any run fits
 
 struct StoreArgs {
-    RopeArgs r;               // g[1], g[2]: k and v with their pages
+    RopeArgs r;               // g[0]: q; g[1], g[2]: k and v with their pages
     float *scale[2];          // of K and V: [n_pages][n_kv]
-    int32_t heads;            // of one CTA
+    int32_t tok;              // tokens whose runs a CTA takes: at most 128, and with a page's rows at most 256
+    int32_t q_heads, q_f16;   // heads of a CTA of q; q_out's type
 };
 
 // The smallest power of two s with top <= 448 s, within the limits: 448 = 1.75 * 2^8.
@@ -45,76 +45,77 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 __device__ __forceinline__ bool pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
 
-// Runs of rows in one page that begin among the CTA's tokens.
+// Runs of rows in one page that begin among the CTA's tokens; row i is token t0 + i.
 struct Runs {
-    int32_t slot[kStoreTok + kMaxPage];    // of token t0 + i, -1 = none
-    int8_t run[kStoreTok + kMaxPage];      // -1: no row of this CTA's
-    int32_t page[kStoreTok], row0[kStoreTok];
-    int32_t end, n;
-    uint32_t top[kStoreTok][kStoreHeads];  // largest finite |x|, as bits
-    float scale[kStoreTok][kStoreHeads], ratio[kStoreTok][kStoreHeads];
+    int32_t slot[kStoreThreads];
+    int16_t run[kStoreThreads];           // -1: no row of this CTA's
+    int32_t first[129], page[128];        // a run's first row, its page,
+    int32_t row0[128];                    // and the row of it in that page
+    int32_t end, leads[kStoreThreads / 32];
+    uint32_t top[128];                    // largest finite |x|, as bits
+    float scale[128], ratio[128];
 };
 
-__device__ __forceinline__ void find_runs(const RopeArgs &a, Runs &s, int64_t t0, bool report) {
-    const int size = 1 << a.page_log2, span = kStoreTok + size;
-    for (int i = threadIdx.x; i < span; i += blockDim.x) {
-        const int64_t t = t0 + i;
-        int32_t slot = t < a.n_tokens ? a.slots[t] : -1;
-        if (slot >= a.n_slots) {
-            if (report) set_error(a.err, kErrBounds);
-            slot = -1;
-        }
-        s.slot[i] = slot < 0 ? -1 : slot;
-        s.run[i] = -1;
+// How many there are.
+__device__ __forceinline__ int find_runs(const StoreArgs &args, Runs &s, int64_t t0, bool report) {
+    const RopeArgs &a = args.r;
+    const int size = 1 << a.page_log2, span = args.tok + size, i = threadIdx.x, warp = i >> 5;
+    const int64_t t = t0 + i;
+    int32_t slot = i < span && t < a.n_tokens ? a.slots[t] : -1, last = -1;
+    if (i == 0 && t0 > 0) last = a.slots[t0 - 1];
+    if (slot >= a.n_slots) {
+        if (report) set_error(a.err, kErrBounds);
+        slot = -1;
     }
-    for (int i = threadIdx.x; i < kStoreTok * kStoreHeads; i += blockDim.x) s.top[i / kStoreHeads][i % kStoreHeads] = 0;
-    if (threadIdx.x == 0) s.end = span;
+    if (slot < 0) slot = -1;
+    s.slot[i] = slot;
+    if (i < 128) s.top[i] = 0;
+    if (i == 0) s.end = span;
     __syncthreads();
+    if (i > 0) last = s.slot[i - 1];
     // a row that goes on where the one before it stands, in the same page
-    auto goes_on = [&](int i) {
-        const int32_t slot = s.slot[i];
-        const int32_t last = i > 0 ? s.slot[i - 1] : t0 > 0 ? a.slots[t0 - 1] : -1;
-        return slot >= 0 && last >= 0 && slot == last + 1 && (slot & (size - 1)) != 0;
-    };
-    for (int i = kStoreTok + int(threadIdx.x); i < span; i += blockDim.x)
-        if (!goes_on(i)) atomicMin(&s.end, i);
+    const bool on = slot >= 0 && last >= 0 && slot == last + 1 && (slot & (size - 1)) != 0;
+    const bool lead = i < args.tok && slot >= 0 && !on;
+    if (i >= args.tok && i < span && !on) atomicMin(&s.end, i);
+    const uint32_t leads = __ballot_sync(~0u, lead);
+    if ((i & 31) == 0) s.leads[warp] = __popc(leads);
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int i = threadIdx.x;
-        const bool there = i < kStoreTok && s.slot[i] >= 0, lead = there && !goes_on(i);
-        const uint32_t leads = __ballot_sync(~0u, lead), upto = leads & (~0u >> (31 - i));
-        const int run = __popc(upto) - 1;
-        if (there && run >= 0) s.run[i] = int8_t(run);
-        if (lead) {
-            s.page[run] = s.slot[i] >> a.page_log2;
-            s.row0[run] = s.slot[i] & (size - 1);
-        }
-        if (i == 0) s.n = __popc(leads);
+    int before = __popc(leads & (~0u >> (31 - (i & 31)))), n = 0;
+#pragma unroll
+    for (int w = 0; w < kStoreThreads / 32; ++w) {
+        before += w < warp ? s.leads[w] : 0;
+        n += s.leads[w];
     }
+    // rows past the CTA's tokens are those of a run that goes on
+    s.run[i] = int16_t(slot >= 0 && i < s.end ? before - 1 : -1);
+    if (lead) {
+        s.first[before - 1] = i;
+        s.page[before - 1] = slot >> a.page_log2;
+        s.row0[before - 1] = slot & (size - 1);
+    }
+    if (i == 0) s.first[n] = s.end;
     __syncthreads();
-    // rows past the sixteenth token belong to the run that its row is in
-    const int8_t last = s.run[kStoreTok - 1];
-    for (int i = kStoreTok + int(threadIdx.x); i < s.end; i += blockDim.x) s.run[i] = last;
-    __syncthreads();
+    return n;
 }
 
 // The 16 channels of a row that a thread owns, rotated.  HALF: eight and their
-// eight partners where they turn; else 16 neighbours.
+// eight partners where they turn; else 16 neighbours.  ANY: of any alignment and
+// rot_dim, element by element.
 template <typename TI, bool HALF, bool ANY>
 struct Row16 {
     float c[ANY ? 16 : 8], s[ANY ? 16 : 8];
     int at0, at1;
     bool turn;
 
-    __device__ __forceinline__ void place(const RopeArgs &a, int task) {
-        turn = ANY ? task * 16 < 2 * a.pairs : task < a.n_pairs_task;
+    __device__ __forceinline__ void place(const RopeArgs &a, int task, bool rotate) {
+        turn = rotate && (ANY ? task * 16 < 2 * a.pairs : task < a.n_pairs_task);
         at0 = !ANY && HALF && turn ? task * 8 : task * 16;
         at1 = !ANY && HALF && turn ? a.half + task * 8 : task * 16 + 8;
     }
     __device__ __forceinline__ void angles(const RopeArgs &a, int task, int64_t tok) {
         if (!turn) return;
         const uint64_t *turns = a.turns;
-        asm volatile("" : "+l"(turns));  // an ordinary load, as fill_angles explains
+        asm volatile("" : "+l"(turns));  // an ordinary load: of constant memory every lane's own would take a turn
         const int32_t pos = a.positions[tok];
 #pragma unroll
         for (int i = 0; i < (ANY ? 16 : 8); ++i) {
@@ -126,163 +127,231 @@ struct Row16 {
                 if (ch >= 2 * a.pairs) continue;
                 p = HALF ? (ch < a.pairs ? ch : ch - a.pairs) : ch / 2;
             }
-            if (pos >= 0) {
-                float sn, cs;
-                sincospif(float(int32_t((uint64_t(pos) * turns[p]) >> 32)) * 4.656612873077393e-10f, &sn, &cs);
-                c[i] = cs * a.factor;
-                s[i] = sn * a.factor;
+            if (pos < 0) continue;
+            // The angle, a fraction of a turn, in two parts: 24 bits that f32 holds, and the
+            // next ones by the first terms of sine and cosine.  (One f32 would move the
+            // result by 2^-23: more rows would fall on the other side of a code's border.)
+            const uint64_t frac = uint64_t(pos) * turns[p];
+            const int32_t hi = int32_t(uint32_t(frac >> 32) & 0xffffff00u);
+            const float rest = float(uint32_t(frac >> 8)) * 8.71967124502158e-17f;  // 2 pi 2^-56: radians
+            float sn, cs;
+            sincospif(float(hi) * 4.656612873077393e-10f, &sn, &cs);
+            c[i] = fmaf(-rest, sn, cs) * a.factor;
+            s[i] = fmaf(rest, cs, sn) * a.factor;
+        }
+    }
+    __device__ __forceinline__ void load(const TI *in, float *x) const {
+        load8<TI>(in + at0, x);
+        load8<TI>(in + at1, x + 8);
+    }
+    __device__ __forceinline__ void rotate(float *x) const {
+        if (!turn) return;
+        if (HALF) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = x[i] * c[i] - x[8 + i] * s[i], w = x[8 + i] * c[i] + x[i] * s[i];
+                x[i] = u;
+                x[8 + i] = w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
+                x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
+                x[2 * i] = u;
             }
         }
     }
-    __device__ __forceinline__ void load(const RopeArgs &a, const TI *in, int task, bool rotate, float *x) const {
-        if constexpr (ANY) {
+    __device__ __forceinline__ void load_any(const RopeArgs &a, const TI *in, int task, float *x) const {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int ch = task * 16 + i;
-                x[i] = to_f32<TI>(in[ch]);
-                if (!rotate || ch >= 2 * a.pairs) continue;
-                const bool low = HALF ? ch < a.pairs : ch % 2 == 0;
-                const float y = to_f32<TI>(in[HALF ? (low ? ch + a.pairs : ch - a.pairs) : ch ^ 1]);
-                x[i] = low ? x[i] * c[i] - y * s[i] : x[i] * c[i] + y * s[i];
-            }
-        } else {
-            load8<TI>(in + at0, x);
-            load8<TI>(in + at1, x + 8);
-            if (!rotate || !turn) return;
-            if (HALF) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = x[i] * c[i] - x[8 + i] * s[i], w = x[8 + i] * c[i] + x[i] * s[i];
-                    x[i] = u;
-                    x[8 + i] = w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-                    x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-                    x[2 * i] = u;
-                }
-            }
+        for (int i = 0; i < 16; ++i) {
+            const int ch = task * 16 + i;
+            x[i] = to_f32<TI>(in[ch]);
+            if (!turn || ch >= 2 * a.pairs) continue;
+            const bool low = HALF ? ch < a.pairs : ch % 2 == 0;
+            const float y = to_f32<TI>(in[HALF ? (low ? ch + a.pairs : ch - a.pairs) : ch ^ 1]);
+            x[i] = low ? x[i] * c[i] - y * s[i] : x[i] * c[i] + y * s[i];
         }
     }
 };
 
-template <typename TI, bool HALF, bool ANY>
-__global__ void __launch_bounds__(256) store_kernel(const __grid_constant__ StoreArgs args) {
+// q's rows of the CTA's tokens.
+template <typename TI, int HD, bool HALF, bool ANY>
+__device__ __forceinline__ void turn_rows(const StoreArgs &args, int64_t t0) {
+    constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;
+    const RopeArgs &a = args.r;
+    const Group &g = a.g[0];
+    const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks, h0 = blockIdx.y * args.q_heads;
+    const int heads = g.heads - h0 < args.q_heads ? g.heads - h0 : args.q_heads;
+    Row16<TI, HALF, ANY> row;
+    row.place(a, task, a.pairs > 0);
+    for (int i0 = 0; i0 < args.tok; i0 += kLanes) {
+        const int64_t t = t0 + i0 + lane;
+        const bool there = i0 + lane < args.tok && t < a.n_tokens && a.positions[t] >= 0;
+        if (there) row.angles(a, task, t);
+        for (int h = h0; h < h0 + heads; ++h) {
+            const TI *in = static_cast<const TI *>(g.in) + t * g.in_tok + h * g.in_head;
+            float x[16];
+            if (there) {
+                if constexpr (ANY) {
+                    row.load_any(a, in, task, x);
+                } else {
+                    row.load(in, x);
+                    row.rotate(x);
+                }
+            }
+            if (ANY) __syncwarp();  // in place, no channel is written before its partner's thread has it
+            if (!there) continue;
+            const int64_t at = t * g.out_tok + h * g.out_head;
+            auto put = [&](auto *out) {
+                using TO = std::remove_pointer_t<decltype(out)>;
+                if constexpr (ANY) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) out[at + task * 16 + e] = from_f32<TO>(x[e]);
+                } else {
+                    store8<TO>(out + at + row.at0, x);
+                    store8<TO>(out + at + row.at1, x + 8);
+                }
+            };
+            if (args.q_f16 != 0) put(static_cast<__half *>(g.out));
+            else put(static_cast<__nv_bfloat16 *>(g.out));
+        }
+    }
+}
+
+template <typename TI, int HD, bool HALF, bool ANY>
+__global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_constant__ StoreArgs args) {
+    constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;  // of a row; rows at once
+    constexpr int kTurns = kWindow / kLanes;
     __shared__ Runs sh;
     const RopeArgs &a = args.r;
     pdl_wait();
-    const int64_t t0 = int64_t(blockIdx.x) * kStoreTok;
-    const int kind = blockIdx.z, h0 = blockIdx.y * args.heads;
-    const int heads = a.n_kv - h0 < args.heads ? a.n_kv - h0 : args.heads;
+    const int64_t t0 = int64_t(blockIdx.x) * args.tok;
+    if (blockIdx.z == 2) {
+        turn_rows<TI, HD, HALF, ANY>(args, t0);
+        return;
+    }
+    const int kind = blockIdx.z, h = blockIdx.y;
     const Group &g = a.g[1 + kind];
-    const bool rotate = kind == 0 && a.pairs > 0;
-    find_runs(a, sh, t0, blockIdx.y == 0 && kind == 0);
-    if (sh.n == 0) return;
+    if (h >= g.heads) return;
+    const int n = find_runs(args, sh, t0, h == 0 && kind == 0);
+    if (n == 0) return;
     const int size = 1 << a.page_log2;
-    const int task = threadIdx.x % a.n_tasks, lane = threadIdx.x / a.n_tasks, lanes = blockDim.x / a.n_tasks;
+    const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks;
     Row16<TI, HALF, ANY> row;
-    row.place(a, task);
+    row.place(a, task, kind == 0 && a.pairs > 0);
+    uint8_t *pages = static_cast<uint8_t *>(g.out);
+    auto block_of = [&](int run) { return pages + ((int64_t(sh.page[run]) * a.n_kv + h) << a.page_log2) * HD; };
 
-    // the largest value of each run and head
-    for (int i0 = 0; i0 < sh.end; i0 += lanes) {
-        const int i = i0 + lane;
-        const int run = i < sh.end ? sh.run[i] : -1;
-        if (run >= 0 && rotate) row.angles(a, task, t0 + i);
-        for (int h = 0; h < heads; ++h) {
+    // as many runs at a time as the registers hold
+    for (int ra = 0, rb; ra < n; ra = rb) {
+        const int w0 = sh.first[ra];
+        rb = n;
+        if (sh.first[n] - w0 > kWindow)
+            for (rb = ra + 1; rb < n && sh.first[rb + 1] - w0 <= kWindow; ++rb) {
+            }
+        const int w1 = sh.first[rb];
+        // the scale that stands, for the thread that settles its run's
+        const int my = ra + int(threadIdx.x);
+        float *scale_at = nullptr, old = 0.0f;
+        if (my < rb) {
+            scale_at = args.scale[kind] + int64_t(sh.page[my]) * a.n_kv + h;
+            if (sh.row0[my] > 0) old = *scale_at;
+        }
+        float x[kTurns][16];
+        int run[kTurns];
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            const int i = w0 + k * kLanes + lane;
+            run[k] = i < w1 ? sh.run[i] : -1;
+            if (ANY || run[k] < 0) continue;
+            row.load(static_cast<const TI *>(g.in) + (t0 + i) * g.in_tok + h * g.in_head, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            if (w0 + k * kLanes >= w1) break;
             float top = 0.0f;
-            if (run >= 0) {
-                float x[16];
-                row.load(a, static_cast<const TI *>(g.in) + (t0 + i) * g.in_tok + (h0 + h) * g.in_head, task, rotate, x);
+            if (run[k] >= 0) {
+                const int64_t t = t0 + w0 + k * kLanes + lane;
+                row.angles(a, task, t);
+                if constexpr (ANY) row.load_any(a, static_cast<const TI *>(g.in) + t * g.in_tok + h * g.in_head, task, x[k]);
+                else row.rotate(x[k]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float v = fabsf(x[e]);
+                    const float v = fabsf(x[k][e]);
                     top = v <= FLT_MAX ? fmaxf(top, v) : top;
                 }
             }
-            for (int d = 1; d < a.n_tasks; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            if (run >= 0 && task == 0) atomicMax(&sh.top[run][h], __float_as_uint(top));
+#pragma unroll
+            for (int d = 1; d < kTasks; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            if (run[k] >= 0 && task == 0) atomicMax(&sh.top[run[k]], __float_as_uint(top));
         }
-    }
-    __syncthreads();
-
-    // the scales, which only grow while a block keeps rows
-    for (int i = threadIdx.x; i < sh.n * heads; i += blockDim.x) {
-        const int run = i / heads, h = i - run * heads;
-        float *at = args.scale[kind] + int64_t(sh.page[run]) * a.n_kv + h0 + h;
-        float s = scale_for(__uint_as_float(sh.top[run][h])), ratio = 1.0f;
-        if (sh.row0[run] > 0) {
-            const float old = *at;
-            if (!scale_ok(old)) set_error(a.err, kErrBounds);
-            else if (old >= s) s = old;
-            else ratio = old / s;
+        __syncthreads();
+        if (my < rb) {  // scales only grow while a block keeps rows
+            float s = scale_for(__uint_as_float(sh.top[my])), ratio = 1.0f;
+            if (sh.row0[my] > 0) {
+                if (!scale_ok(old)) set_error(a.err, kErrBounds);
+                else if (old >= s) s = old;
+                else ratio = old / s;
+            }
+            *scale_at = s;
+            sh.scale[my] = s;
+            sh.ratio[my] = ratio;
         }
-        *at = s;
-        sh.scale[run][h] = s;
-        sh.ratio[run][h] = ratio;
-    }
-    __syncthreads();
-
-    uint8_t *pages = static_cast<uint8_t *>(g.out);
-    auto block_of = [&](int run, int h) { return pages + ((int64_t(sh.page[run]) * a.n_kv + h0 + h) << a.page_log2) * a.hd; };
-    // codes that stand before a run move to the new scale
-    for (int run = 0; run < sh.n; ++run) {
-        if (sh.row0[run] == 0) continue;
-        for (int h = 0; h < heads; ++h) {
-            const float ratio = sh.ratio[run][h];
+        __syncthreads();
+        // codes that stand before a run move to the new scale: a warp for each run
+        for (int r = ra + int(threadIdx.x >> 5); r < rb; r += kStoreThreads / 32) {
+            const float ratio = sh.ratio[r];
             if (ratio == 1.0f) continue;
-            uint4 *p = reinterpret_cast<uint4 *>(block_of(run, h));
-            for (int i = threadIdx.x; i < sh.row0[run] * a.hd / 16; i += blockDim.x) {
+            uint4 *p = reinterpret_cast<uint4 *>(block_of(r));
+#pragma unroll 4
+            for (int i = threadIdx.x & 31; i < sh.row0[r] * HD / 16; i += 32) {
                 uint4 v = p[i];
                 uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x[4];
-                    values4(w[e], x);
+                    float y[4];
+                    values4(w[e], y);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] *= ratio;
-                    w[e] = codes4(x);
+                    for (int k = 0; k < 4; ++k) y[k] *= ratio;
+                    w[e] = codes4(y);
                 }
                 p[i] = v;
             }
         }
-    }
-
-    // the codes
-    for (int i0 = 0; i0 < sh.end; i0 += lanes) {
-        const int i = i0 + lane;
-        const int run = i < sh.end ? sh.run[i] : -1;
-        if (run < 0) continue;
-        if (rotate) row.angles(a, task, t0 + i);
-        for (int h = 0; h < heads; ++h) {
-            float x[16];
-            row.load(a, static_cast<const TI *>(g.in) + (t0 + i) * g.in_tok + (h0 + h) * g.in_head, task, rotate, x);
-            const float s = sh.scale[run][h], inv = 1.0f / s;  // exact for a power of two
-            const bool exact = pow2(s);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = exact ? x[e] * inv : x[e] / s;
-            uint8_t *out = block_of(run, h) + (sh.slot[i] & (size - 1)) * a.hd;
-            if (row.at1 == row.at0 + 8) {
-                *reinterpret_cast<uint4 *>(out + row.at0) = make_uint4(codes4(x), codes4(x + 4), codes4(x + 8), codes4(x + 12));
+        for (int k = 0; k < kTurns; ++k) {
+            if (run[k] < 0) continue;
+            const float s = sh.scale[run[k]], inv = 1.0f / s;  // exact for a power of two
+            if (pow2(s)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[k][e] *= inv;
             } else {
-                *reinterpret_cast<uint2 *>(out + row.at0) = make_uint2(codes4(x), codes4(x + 4));
-                *reinterpret_cast<uint2 *>(out + row.at1) = make_uint2(codes4(x + 8), codes4(x + 12));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[k][e] /= s;
+            }
+            uint8_t *out = block_of(run[k]) + (sh.slot[w0 + k * kLanes + lane] & (size - 1)) * HD;
+            if (row.at1 == row.at0 + 8) {
+                *reinterpret_cast<uint4 *>(out + row.at0) = make_uint4(codes4(x[k]), codes4(x[k] + 4), codes4(x[k] + 8), codes4(x[k] + 12));
+            } else {
+                *reinterpret_cast<uint2 *>(out + row.at0) = make_uint2(codes4(x[k]), codes4(x[k] + 4));
+                *reinterpret_cast<uint2 *>(out + row.at1) = make_uint2(codes4(x[k] + 8), codes4(x[k] + 12));
             }
         }
     }
 }
 
-template <typename TI>
+template <typename TI, int HD>
 cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, cudaStream_t st) {
     const bool any = !aligned || a.r.pairs % 8 != 0, half = layout == KVD_ROPE_HALF;
-    // One head to a CTA while that leaves no more CTAs than the SMs hold at once;
-    // two share the angles of a long prompt's rows.
-    a.heads = ceil_div(a.r.n_tokens, kStoreTok) * a.r.n_kv <= 152 * 8 ? 1 : 2;
-    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, kStoreTok)), unsigned(ceil_div(a.r.n_kv, a.heads)), 2);
-    const auto kern = any ? (half ? store_kernel<TI, true, true> : store_kernel<TI, false, true>)
-                          : (half ? store_kernel<TI, true, false> : store_kernel<TI, false, false>);
-    return launch_pdl(kern, grid, dim3(256), 0, st, a);
+    // Many tokens: as many to a CTA as a page has rows, so that most CTAs have one whole
+    // run; few: 16, for more CTAs.
+    a.tok = a.r.n_tokens >= 2048 ? 1 << a.r.page_log2 : 16;
+    a.q_heads = int32_t(ceil_div(a.r.g[0].heads, a.r.n_kv));
+    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.r.n_kv), a.r.g[0].heads > 0 ? 3 : 2);
+    const auto kern = any ? (half ? store_kernel<TI, HD, true, true> : store_kernel<TI, HD, false, true>)
+                          : (half ? store_kernel<TI, HD, true, false> : store_kernel<TI, HD, false, false>);
+    return launch_pdl(kern, grid, dim3(kStoreThreads), 0, st, a);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -295,20 +364,33 @@ struct ReadArgs {
     const int32_t *block_table, *seq_len, *start, *cu_rows;
     uint32_t *err;
     int64_t n_rows, n_pages;
-    int32_t n_seq, max_pages, page_log2, n_kv, hd;
+    int32_t n_seq, max_pages, page_log2, n_kv, hd, heads;
 };
 
 constexpr int kReadRows = 32;  // rows of one CTA
 
-// Where output row t comes from: its page and row there; page -1 = nothing stands
-// there (zeros), -2 = no request asked for it (left alone).
-__device__ __forceinline__ int2 read_place(const ReadArgs &a, int64_t t) {
-    if (t >= a.n_rows || t < a.cu_rows[0] || t >= a.cu_rows[a.n_seq]) return make_int2(-2, 0);
-    int lo = 0, hi = a.n_seq;  // cu_rows[lo] <= t < cu_rows[hi]
+// The last request b with cu_rows[b] <= t, by a warp: 32 places looked at at once.
+__device__ __forceinline__ int32_t request_of(const ReadArgs &a, int64_t t) {
+    int32_t lo = 0, hi = a.n_seq;  // cu_rows[lo] <= t, cu_rows[hi] > t
+    const int32_t lane = threadIdx.x & 31;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
+        const int32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool below = at < hi && (lane == 0 || a.cu_rows[at] <= t);
+        const int32_t k = 31 - __clz(__ballot_sync(~0u, below));
+        hi = lo + (k + 1) * step < hi ? lo + (k + 1) * step : hi;
+        lo += k * step;
+    }
+    return lo;
+}
+
+// Where output row t of a request between lo and hi comes from: its page and row there;
+// page -1 = nothing stands there (zeros), -2 = no request asked for it (left alone).
+__device__ __forceinline__ int2 read_place(const ReadArgs &a, int64_t t, int32_t lo, int32_t hi) {
+    if (t >= a.n_rows || t < a.cu_rows[0] || t >= a.cu_rows[a.n_seq]) return make_int2(-2, 0);
+    while (hi > lo) {
+        const int32_t mid = (lo + hi + 1) / 2;
         if (a.cu_rows[mid] <= t) lo = mid;
-        else hi = mid;
+        else hi = mid - 1;
     }
     const int64_t pos = (a.start != nullptr ? int64_t(a.start[lo]) : 0) + t - a.cu_rows[lo];
     const int64_t p = pos >> a.page_log2;
@@ -321,17 +403,24 @@ __device__ __forceinline__ int2 read_place(const ReadArgs &a, int64_t t) {
     return make_int2(page, int32_t(pos & ((1 << a.page_log2) - 1)));
 }
 
-template <typename TP, typename TO>  // TP uint8_t: e4m3 codes with scales
+// HD / 16 threads for a row of a head, 16 channels each; a warp's rows follow one
+// another in a page and in the output.
+template <typename TP, typename TO, int HD>  // TP uint8_t: e4m3 codes with scales
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
+    constexpr int kChunks = HD / 16;
     __shared__ int2 place[kReadRows];
     pdl_wait();
     const int64_t t0 = int64_t(blockIdx.x) * kReadRows;
-    if (threadIdx.x < kReadRows) place[threadIdx.x] = read_place(a, t0 + threadIdx.x);
+    if (threadIdx.x < kReadRows) {
+        const int64_t t1 = t0 + kReadRows - 1 < a.n_rows ? t0 + kReadRows - 1 : a.n_rows - 1;
+        const int32_t lo = request_of(a, t0), hi = request_of(a, t1);
+        place[threadIdx.x] = read_place(a, t0 + threadIdx.x, lo, hi);
+    }
     __syncthreads();
-    const int chunks = a.hd / 16, per_head = kReadRows * chunks, h0 = blockIdx.y;
-#pragma unroll 2
-    for (int i = threadIdx.x; i < per_head * 2; i += blockDim.x) {
-        const int kind = i / per_head, r = (i - kind * per_head) / chunks, at = (i % chunks) * 16;
+    const int h0 = blockIdx.y * a.heads, heads = a.n_kv - h0 < a.heads ? a.n_kv - h0 : a.heads;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kReadRows * kChunks * 2 * heads; i += 256) {
+        const int at = i % kChunks * 16, r = i / kChunks % kReadRows, kind = i / (kChunks * kReadRows) % 2, h = h0 + i / (kChunks * kReadRows * 2);
         const int2 from = place[r];
         if (from.x == -2) continue;
         float x[16];
@@ -339,8 +428,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = 0.0f;
         } else {
-            const int64_t block = int64_t(from.x) * a.n_kv + h0;
-            const TP *in = static_cast<const TP *>(a.pages[kind]) + ((block << a.page_log2) + from.y) * a.hd + at;
+            const int64_t block = int64_t(from.x) * a.n_kv + h;
+            const TP *in = static_cast<const TP *>(a.pages[kind]) + ((block << a.page_log2) + from.y) * HD + at;
             if constexpr (sizeof(TP) == 1) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(in);
                 const float s = scale_of(a.scale[kind][block], a.err);
@@ -355,19 +444,25 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
                 load8<TP>(in + 8, x + 8);
             }
         }
-        TO *out = static_cast<TO *>(a.out[kind]) + (t0 + r) * a.out_tok[kind] + int64_t(h0) * a.out_head[kind] + at;
+        TO *out = static_cast<TO *>(a.out[kind]) + (t0 + r) * a.out_tok[kind] + int64_t(h) * a.out_head[kind] + at;
         store8<TO>(out, x);
         store8<TO>(out + 8, x + 8);
     }
 }
 
-template <typename TP>
-cudaError_t launch_read(const ReadArgs &a, int32_t out_dtype, cudaStream_t st) {
-    const dim3 grid(unsigned(ceil_div(a.n_rows, kReadRows)), unsigned(a.n_kv));
-    const auto kern = out_dtype == KVD_T_F32   ? read_kernel<TP, float>
-                      : out_dtype == KVD_T_F16 ? read_kernel<TP, __half>
-                                               : read_kernel<TP, __nv_bfloat16>;
+template <typename TP, int HD>
+cudaError_t launch_read(ReadArgs &a, int32_t out_dtype, cudaStream_t st) {
+    // all heads to a CTA once that leaves CTAs enough for every SM several times
+    a.heads = ceil_div(a.n_rows, kReadRows) >= 152 * 8 ? a.n_kv : 1;
+    const dim3 grid(unsigned(ceil_div(a.n_rows, kReadRows)), unsigned(ceil_div(a.n_kv, a.heads)));
+    const auto kern = out_dtype == KVD_T_F32   ? read_kernel<TP, float, HD>
+                      : out_dtype == KVD_T_F16 ? read_kernel<TP, __half, HD>
+                                               : read_kernel<TP, __nv_bfloat16, HD>;
     return launch_pdl(kern, grid, dim3(256), 0, st, a);
+}
+template <typename TP>
+cudaError_t launch_read(ReadArgs &a, int32_t out_dtype, cudaStream_t st) {
+    return a.hd == 64 ? launch_read<TP, 64>(a, out_dtype, st) : launch_read<TP, 128>(a, out_dtype, st);
 }
 
 bool page_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
@@ -398,17 +493,18 @@ extern "C" kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, c
     if (!rows_ok(k, n_tokens, n_kv, ib) || !rows_ok(v, n_tokens, n_kv, ib)) return KVD_EINVAL;
     StoreArgs a;
     std::memset(&a, 0, sizeof(a));
-    RopeArgs turn;
-    std::memset(&turn, 0, sizeof(turn));
+    bool aligned = true;
     if (q != nullptr) {
         if (qb != 2 || (in_dtype != KVD_T_F32 && in_dtype != q_dtype)) return KVD_EINVAL;
         if (n_q < 1 || n_q > 1024 || !rows_ok(q, n_tokens, n_q, ib) || !rows_ok(q_out, n_tokens, n_q, qb)) return KVD_EINVAL;
-        turn.g[0] = group_of(q, q_out, n_q);
+        a.r.g[0] = group_of(q, q_out, n_q);
+        aligned = aligned16(a.r.g[0], false, ib, qb);
+        a.q_f16 = q_dtype == KVD_T_F16 ? 1 : 0;
     }
     const kvd_rows kp = {k_pages, 0, 0}, vp = {v_pages, 0, 0};
     a.r.g[1] = group_of(k, &kp, n_kv);
     a.r.g[2] = group_of(v, &vp, n_kv);
-    const bool aligned = aligned16(a.r.g[1], true, ib, 1) && aligned16(a.r.g[2], true, ib, 1);
+    aligned = aligned && aligned16(a.r.g[1], true, ib, 1) && aligned16(a.r.g[2], true, ib, 1);
     if (n_tokens == 0) return KVD_OK;
     {
         // q turns in place; else what is written shares memory with nothing else
@@ -429,14 +525,6 @@ extern "C" kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, c
     }
     const int layout = r != nullptr ? r->layout : KVD_ROPE_HALF;
     cudaStream_t st = as_stream(stream);
-    cudaError_t e = cudaSuccess;
-    if (q != nullptr) {
-        set_rope(&turn, r, head_dim);
-        turn.positions = positions;
-        turn.n_tokens = n_tokens;
-        e = rotate_rows(turn, layout, in_dtype, q_dtype, st);
-        if (e != cudaSuccess) return KVD_ECUDA;
-    }
     set_rope(&a.r, r, head_dim);
     a.r.paged = 1;
     a.r.n_kv = n_kv;
@@ -448,9 +536,11 @@ extern "C" kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, c
     a.r.err = err;
     a.scale[0] = k_scale;
     a.scale[1] = v_scale;
-    e = in_dtype == KVD_T_F32   ? launch_store<float>(a, aligned, layout, st)
-        : in_dtype == KVD_T_F16 ? launch_store<__half>(a, aligned, layout, st)
-                                : launch_store<__nv_bfloat16>(a, aligned, layout, st);
+    const auto go = [&](auto type) {
+        using TI = decltype(type);
+        return head_dim == 64 ? launch_store<TI, 64>(a, aligned, layout, st) : launch_store<TI, 128>(a, aligned, layout, st);
+    };
+    const cudaError_t e = in_dtype == KVD_T_F32 ? go(float()) : in_dtype == KVD_T_F16 ? go(__half()) : go(__nv_bfloat16());
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
 }
 
