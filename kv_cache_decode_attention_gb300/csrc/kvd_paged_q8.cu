@@ -12,11 +12,10 @@
 // precision.  (With s = max|x| / 448 every growth would round every code anew.)
 //
 // Writing.  The rows of one page stand together in the packed batch, so a CTA takes
-// the runs of rows in one page that begin among its tokens, for one head of K or V: it
-// holds up to 128 rows in registers, takes the largest value of each run, settles the
-// scales and the codes already there, and writes the codes.  Nobody waits for another
-// CTA, because a block's rows all lie in one, and every row is read once.  q turns in
-// CTAs of the same launch, whose place in it K and V share.
+// the runs of rows in one page that begin among its tokens, for some heads of K or one of
+// V: it holds up to 128 rows of a head in registers, takes the largest value of each run,
+// settles the scales and the codes already there, and writes the codes.  Nobody waits for
+// another CTA, because a block's rows all lie in one, and every row is read once.
 
 #include <cfloat>
 #include <cmath>
@@ -34,7 +33,8 @@ struct StoreArgs {
     RopeArgs r;               // g[0]: q; g[1], g[2]: k and v with their pages
     float *scale[2];          // of K and V: [n_pages][n_kv]
     int32_t tok;              // tokens whose runs a CTA takes: at most 128, and with a page's rows at most 256
-    int32_t q_heads, q_f16;   // heads of a CTA of q; q_out's type
+    int32_t k_heads, k_ctas;  // heads of a CTA of K; CTAs of K's heads, before V's and q's in the grid
+    int32_t q_tok, q_f16;     // tokens of a CTA of q; q_out's type
 };
 
 // The smallest power of two s with top <= 448 s, within the limits: 448 = 1.75 * 2^8.
@@ -98,12 +98,35 @@ __device__ __forceinline__ int find_runs(const StoreArgs &args, Runs &s, int64_t
     return n;
 }
 
+// cos and sin of rows t0 .. t0 + n - 1 into cs[row][pair]; a row without a position stays.
+__device__ __forceinline__ void find_angles(const RopeArgs &a, float2 *cs, int64_t t0, int n) {
+    const uint64_t *turns = a.turns;
+    asm volatile("" : "+l"(turns));  // an ordinary load: of constant memory every lane's own would take a turn
+    for (int i = threadIdx.x; i < n * a.pairs; i += kStoreThreads) {
+        const int r = i / a.pairs, p = i - r * a.pairs;
+        const int32_t pos = a.positions[t0 + r];
+        float sn = 0.0f, c = 1.0f;
+        if (pos >= 0) {
+            // The angle, a fraction of a turn, in two parts: 24 bits that f32 holds, and the
+            // next ones by the first terms of sine and cosine.  (One f32 would move the
+            // result by 2^-23: more rows would fall on the other side of a code's border.)
+            const uint64_t frac = uint64_t(pos) * turns[p];
+            const int32_t hi = int32_t(uint32_t(frac >> 32) & 0xffffff00u);
+            const float rest = float(uint32_t(frac >> 8)) * 8.71967124502158e-17f;  // 2 pi 2^-56: radians
+            float s0, c0;
+            sincospif(float(hi) * 4.656612873077393e-10f, &s0, &c0);
+            c = fmaf(-rest, s0, c0);
+            sn = fmaf(rest, c0, s0);
+        }
+        cs[i] = make_float2(c * a.factor, sn * a.factor);
+    }
+}
+
 // The 16 channels of a row that a thread owns, rotated.  HALF: eight and their
 // eight partners where they turn; else 16 neighbours.  ANY: of any alignment and
 // rot_dim, element by element.
 template <typename TI, bool HALF, bool ANY>
 struct Row16 {
-    float c[ANY ? 16 : 8], s[ANY ? 16 : 8];
     int at0, at1;
     bool turn;
 
@@ -112,57 +135,27 @@ struct Row16 {
         at0 = !ANY && HALF && turn ? task * 8 : task * 16;
         at1 = !ANY && HALF && turn ? a.half + task * 8 : task * 16 + 8;
     }
-    __device__ __forceinline__ void angles(const RopeArgs &a, int task, int64_t tok) {
-        if (!turn) return;
-        const uint64_t *turns = a.turns;
-        asm volatile("" : "+l"(turns));  // an ordinary load: of constant memory every lane's own would take a turn
-        const int32_t pos = a.positions[tok];
-#pragma unroll
-        for (int i = 0; i < (ANY ? 16 : 8); ++i) {
-            c[i] = a.factor;
-            s[i] = 0.0f;
-            int p = task * 8 + i;
-            if (ANY) {
-                const int ch = task * 16 + i;
-                if (ch >= 2 * a.pairs) continue;
-                p = HALF ? (ch < a.pairs ? ch : ch - a.pairs) : ch / 2;
-            }
-            if (pos < 0) continue;
-            // The angle, a fraction of a turn, in two parts: 24 bits that f32 holds, and the
-            // next ones by the first terms of sine and cosine.  (One f32 would move the
-            // result by 2^-23: more rows would fall on the other side of a code's border.)
-            const uint64_t frac = uint64_t(pos) * turns[p];
-            const int32_t hi = int32_t(uint32_t(frac >> 32) & 0xffffff00u);
-            const float rest = float(uint32_t(frac >> 8)) * 8.71967124502158e-17f;  // 2 pi 2^-56: radians
-            float sn, cs;
-            sincospif(float(hi) * 4.656612873077393e-10f, &sn, &cs);
-            c[i] = fmaf(-rest, sn, cs) * a.factor;
-            s[i] = fmaf(rest, cs, sn) * a.factor;
-        }
-    }
     __device__ __forceinline__ void load(const TI *in, float *x) const {
         load8<TI>(in + at0, x);
         load8<TI>(in + at1, x + 8);
     }
-    __device__ __forceinline__ void rotate(float *x) const {
+    // cs: the row's pairs
+    __device__ __forceinline__ void rotate(const float2 *cs, int task, float *x) const {
         if (!turn) return;
-        if (HALF) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[i] * c[i] - x[8 + i] * s[i], w = x[8 + i] * c[i] + x[i] * s[i];
-                x[i] = u;
-                x[8 + i] = w;
-            }
-        } else {
+        for (int i = 0; i < 8; i += 2) {
+            const float4 v = reinterpret_cast<const float4 *>(cs + task * 8)[i / 2];
+            const float c[2] = {v.x, v.z}, s[2] = {v.y, v.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-                x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-                x[2 * i] = u;
+            for (int k = 0; k < 2; ++k) {
+                const int p = HALF ? i + k : 2 * (i + k), q = HALF ? 8 + i + k : 2 * (i + k) + 1;
+                const float u = x[p] * c[k] - x[q] * s[k], w = x[q] * c[k] + x[p] * s[k];
+                x[p] = u;
+                x[q] = w;
             }
         }
     }
-    __device__ __forceinline__ void load_any(const RopeArgs &a, const TI *in, int task, float *x) const {
+    __device__ __forceinline__ void load_any(const RopeArgs &a, const float2 *cs, const TI *in, int task, float *x) const {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int ch = task * 16 + i;
@@ -170,52 +163,54 @@ struct Row16 {
             if (!turn || ch >= 2 * a.pairs) continue;
             const bool low = HALF ? ch < a.pairs : ch % 2 == 0;
             const float y = to_f32<TI>(in[HALF ? (low ? ch + a.pairs : ch - a.pairs) : ch ^ 1]);
-            x[i] = low ? x[i] * c[i] - y * s[i] : x[i] * c[i] + y * s[i];
+            const float2 v = cs[HALF ? (low ? ch : ch - a.pairs) : ch / 2];
+            x[i] = low ? x[i] * v.x - y * v.y : x[i] * v.x + y * v.y;
         }
     }
 };
 
-// q's rows of the CTA's tokens.
+// q's rows t0 .. t0 + n - 1, all heads; n at most kLanes.
 template <typename TI, int HD, bool HALF, bool ANY>
-__device__ __forceinline__ void turn_rows(const StoreArgs &args, int64_t t0) {
+__device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int64_t t0, int n) {
     constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;
     const RopeArgs &a = args.r;
     const Group &g = a.g[0];
-    const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks, h0 = blockIdx.y * args.q_heads;
-    const int heads = g.heads - h0 < args.q_heads ? g.heads - h0 : args.q_heads;
+    const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks;
+    const int at_once = kLanes / n, r = lane % n, first = lane / n;  // heads at once
     Row16<TI, HALF, ANY> row;
     row.place(a, task, a.pairs > 0);
-    for (int i0 = 0; i0 < args.tok; i0 += kLanes) {
-        const int64_t t = t0 + i0 + lane;
-        const bool there = i0 + lane < args.tok && t < a.n_tokens && a.positions[t] >= 0;
-        if (there) row.angles(a, task, t);
-        for (int h = h0; h < h0 + heads; ++h) {
+    find_angles(a, cs, t0, n);
+    __syncthreads();
+    const int64_t t = t0 + r;
+    const bool there = first < at_once && a.positions[t] >= 0;
+    for (int h0 = 0; h0 < g.heads; h0 += at_once) {
+        const int h = h0 + first;
+        const bool mine = there && h < g.heads;
+        float x[16];
+        if (mine) {
             const TI *in = static_cast<const TI *>(g.in) + t * g.in_tok + h * g.in_head;
-            float x[16];
-            if (there) {
-                if constexpr (ANY) {
-                    row.load_any(a, in, task, x);
-                } else {
-                    row.load(in, x);
-                    row.rotate(x);
-                }
+            if constexpr (ANY) {
+                row.load_any(a, cs + r * a.pairs, in, task, x);
+            } else {
+                row.load(in, x);
+                row.rotate(cs + r * a.pairs, task, x);
             }
-            if (ANY) __syncwarp();  // in place, no channel is written before its partner's thread has it
-            if (!there) continue;
-            const int64_t at = t * g.out_tok + h * g.out_head;
-            auto put = [&](auto *out) {
-                using TO = std::remove_pointer_t<decltype(out)>;
-                if constexpr (ANY) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) out[at + task * 16 + e] = from_f32<TO>(x[e]);
-                } else {
-                    store8<TO>(out + at + row.at0, x);
-                    store8<TO>(out + at + row.at1, x + 8);
-                }
-            };
-            if (args.q_f16 != 0) put(static_cast<__half *>(g.out));
-            else put(static_cast<__nv_bfloat16 *>(g.out));
         }
+        if (ANY) __syncwarp();  // in place, no channel is written before its partner's thread has it
+        if (!mine) continue;
+        const int64_t at = t * g.out_tok + h * g.out_head;
+        auto put = [&](auto *out) {
+            using TO = std::remove_pointer_t<decltype(out)>;
+            if constexpr (ANY) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) out[at + task * 16 + e] = from_f32<TO>(x[e]);
+            } else {
+                store8<TO>(out + at + row.at0, x);
+                store8<TO>(out + at + row.at1, x + 8);
+            }
+        };
+        if (args.q_f16 != 0) put(static_cast<__half *>(g.out));
+        else put(static_cast<__nv_bfloat16 *>(g.out));
     }
 }
 
@@ -223,25 +218,29 @@ template <typename TI, int HD, bool HALF, bool ANY>
 __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_constant__ StoreArgs args) {
     constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;  // of a row; rows at once
     constexpr int kTurns = kWindow / kLanes;
+    extern __shared__ __align__(16) float2 cs[];  // of the rows at hand
     __shared__ Runs sh;
     const RopeArgs &a = args.r;
     pdl_wait();
-    const int64_t t0 = int64_t(blockIdx.x) * args.tok;
-    if (blockIdx.z == 2) {
-        turn_rows<TI, HD, HALF, ANY>(args, t0);
+    int64_t t0 = int64_t(blockIdx.x) * args.tok;
+    const int part = int(blockIdx.y) - args.k_ctas;  // below 0: of K; below n_kv: V; then q
+    if (part >= a.n_kv) {
+        t0 += int64_t(part - a.n_kv) * args.q_tok;
+        const int64_t end = int64_t(blockIdx.x + 1) * args.tok < a.n_tokens ? int64_t(blockIdx.x + 1) * args.tok : a.n_tokens;
+        const int n = int(end - t0 < args.q_tok ? end - t0 : args.q_tok);
+        if (n > 0) turn_rows<TI, HD, HALF, ANY>(args, cs, t0, n);
         return;
     }
-    const int kind = blockIdx.z, h = blockIdx.y;
+    const int kind = part < 0 ? 0 : 1, h0 = kind == 0 ? int(blockIdx.y) * args.k_heads : part;
+    const int heads = kind == 1 ? 1 : a.n_kv - h0 < args.k_heads ? a.n_kv - h0 : args.k_heads;
     const Group &g = a.g[1 + kind];
-    if (h >= g.heads) return;
-    const int n = find_runs(args, sh, t0, h == 0 && kind == 0);
+    const int n = find_runs(args, sh, t0, blockIdx.y == 0);
     if (n == 0) return;
     const int size = 1 << a.page_log2;
     const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks;
     Row16<TI, HALF, ANY> row;
     row.place(a, task, kind == 0 && a.pairs > 0);
     uint8_t *pages = static_cast<uint8_t *>(g.out);
-    auto block_of = [&](int run) { return pages + ((int64_t(sh.page[run]) * a.n_kv + h) << a.page_log2) * HD; };
 
     // as many runs at a time as the registers hold
     for (int ra = 0, rb; ra < n; ra = rb) {
@@ -251,107 +250,135 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_co
             for (rb = ra + 1; rb < n && sh.first[rb + 1] - w0 <= kWindow; ++rb) {
             }
         const int w1 = sh.first[rb];
-        // the scale that stands, for the thread that settles its run's
-        const int my = ra + int(threadIdx.x);
-        float *scale_at = nullptr, old = 0.0f;
-        if (my < rb) {
-            scale_at = args.scale[kind] + int64_t(sh.page[my]) * a.n_kv + h;
-            if (sh.row0[my] > 0) old = *scale_at;
+        if (kind == 0 && a.pairs > 0) {
+            if (ra > 0) __syncthreads();
+            find_angles(a, cs, t0 + w0, w1 - w0);
+            __syncthreads();
         }
-        float x[kTurns][16];
         int run[kTurns];
 #pragma unroll
         for (int k = 0; k < kTurns; ++k) {
             const int i = w0 + k * kLanes + lane;
             run[k] = i < w1 ? sh.run[i] : -1;
-            if (ANY || run[k] < 0) continue;
-            row.load(static_cast<const TI *>(g.in) + (t0 + i) * g.in_tok + h * g.in_head, x[k]);
         }
+        for (int h = h0; h < h0 + heads; ++h) {
+            auto block_of = [&](int r) { return pages + ((int64_t(sh.page[r]) * a.n_kv + h) << a.page_log2) * HD; };
+            // the scale that stands, for the thread that settles its run's
+            const int my = ra + int(threadIdx.x);
+            float *scale_at = nullptr, old = 0.0f;
+            if (my < rb) {
+                scale_at = args.scale[kind] + int64_t(sh.page[my]) * a.n_kv + h;
+                if (sh.row0[my] > 0) old = *scale_at;
+            }
+            float x[kTurns][16];
 #pragma unroll
-        for (int k = 0; k < kTurns; ++k) {
-            if (w0 + k * kLanes >= w1) break;
-            float top = 0.0f;
-            if (run[k] >= 0) {
-                const int64_t t = t0 + w0 + k * kLanes + lane;
-                row.angles(a, task, t);
-                if constexpr (ANY) row.load_any(a, static_cast<const TI *>(g.in) + t * g.in_tok + h * g.in_head, task, x[k]);
-                else row.rotate(x[k]);
+            for (int k = 0; k < kTurns; ++k) {
+                if (ANY || run[k] < 0) continue;
+                row.load(static_cast<const TI *>(g.in) + (t0 + w0 + k * kLanes + lane) * g.in_tok + h * g.in_head, x[k]);
+            }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float v = fabsf(x[k][e]);
-                    top = v <= FLT_MAX ? fmaxf(top, v) : top;
+            for (int k = 0; k < kTurns; ++k) {
+                if (w0 + k * kLanes >= w1) break;
+                const int i = k * kLanes + lane;  // row of the window
+                float top = 0.0f;
+                if (run[k] >= 0) {
+                    if constexpr (ANY) row.load_any(a, cs + i * a.pairs, static_cast<const TI *>(g.in) + (t0 + w0 + i) * g.in_tok + h * g.in_head, task, x[k]);
+                    else row.rotate(cs + i * a.pairs, task, x[k]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = fabsf(x[k][e]);
+                        top = v <= FLT_MAX ? fmaxf(top, v) : top;
+                    }
                 }
-            }
 #pragma unroll
-            for (int d = 1; d < kTasks; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            if (run[k] >= 0 && task == 0) atomicMax(&sh.top[run[k]], __float_as_uint(top));
-        }
-        __syncthreads();
-        if (my < rb) {  // scales only grow while a block keeps rows
-            float s = scale_for(__uint_as_float(sh.top[my])), ratio = 1.0f;
-            if (sh.row0[my] > 0) {
-                if (!scale_ok(old)) set_error(a.err, kErrBounds);
-                else if (old >= s) s = old;
-                else ratio = old / s;
+                for (int d = 1; d < kTasks; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                if (run[k] >= 0 && task == 0) atomicMax(&sh.top[run[k]], __float_as_uint(top));
             }
-            *scale_at = s;
-            sh.scale[my] = s;
-            sh.ratio[my] = ratio;
-        }
-        __syncthreads();
-        // codes that stand before a run move to the new scale: a warp for each run
-        for (int r = ra + int(threadIdx.x >> 5); r < rb; r += kStoreThreads / 32) {
-            const float ratio = sh.ratio[r];
-            if (ratio == 1.0f) continue;
-            uint4 *p = reinterpret_cast<uint4 *>(block_of(r));
+            __syncthreads();
+            if (my < rb) {  // scales only grow while a block keeps rows
+                float s = scale_for(__uint_as_float(sh.top[my])), ratio = 1.0f;
+                sh.top[my] = 0;  // for the next head
+                if (sh.row0[my] > 0) {
+                    if (!scale_ok(old)) set_error(a.err, kErrBounds);
+                    else if (old >= s) s = old;
+                    else ratio = old / s;
+                }
+                *scale_at = s;
+                sh.scale[my] = s;
+                sh.ratio[my] = ratio;
+            }
+            __syncthreads();
+            // codes that stand before a run move to the new scale: a warp for each run
+            for (int r = ra + int(threadIdx.x >> 5); r < rb; r += kStoreThreads / 32) {
+                const float ratio = sh.ratio[r];
+                if (ratio == 1.0f) continue;
+                uint4 *p = reinterpret_cast<uint4 *>(block_of(r));
 #pragma unroll 4
-            for (int i = threadIdx.x & 31; i < sh.row0[r] * HD / 16; i += 32) {
-                uint4 v = p[i];
-                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                for (int i = threadIdx.x & 31; i < sh.row0[r] * HD / 16; i += 32) {
+                    uint4 v = p[i];
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y[4];
-                    values4(w[e], y);
+                    for (int e = 0; e < 4; ++e) {
+                        float y[4];
+                        values4(w[e], y);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] *= ratio;
-                    w[e] = codes4(y);
+                        for (int k = 0; k < 4; ++k) y[k] *= ratio;
+                        w[e] = codes4(y);
+                    }
+                    p[i] = v;
                 }
-                p[i] = v;
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kTurns; ++k) {
-            if (run[k] < 0) continue;
-            const float s = sh.scale[run[k]], inv = 1.0f / s;  // exact for a power of two
-            if (pow2(s)) {
+            for (int k = 0; k < kTurns; ++k) {
+                if (run[k] < 0) continue;
+                const float s = sh.scale[run[k]], inv = 1.0f / s;  // exact for a power of two
+                if (pow2(s)) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[k][e] *= inv;
-            } else {
+                    for (int e = 0; e < 16; ++e) x[k][e] *= inv;
+                } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[k][e] /= s;
-            }
-            uint8_t *out = block_of(run[k]) + (sh.slot[w0 + k * kLanes + lane] & (size - 1)) * HD;
-            if (row.at1 == row.at0 + 8) {
-                *reinterpret_cast<uint4 *>(out + row.at0) = make_uint4(codes4(x[k]), codes4(x[k] + 4), codes4(x[k] + 8), codes4(x[k] + 12));
-            } else {
-                *reinterpret_cast<uint2 *>(out + row.at0) = make_uint2(codes4(x[k]), codes4(x[k] + 4));
-                *reinterpret_cast<uint2 *>(out + row.at1) = make_uint2(codes4(x[k] + 8), codes4(x[k] + 12));
+                    for (int e = 0; e < 16; ++e) x[k][e] /= s;
+                }
+                uint8_t *out = block_of(run[k]) + (sh.slot[w0 + k * kLanes + lane] & (size - 1)) * HD;
+                if (row.at1 == row.at0 + 8) {
+                    *reinterpret_cast<uint4 *>(out + row.at0) = make_uint4(codes4(x[k]), codes4(x[k] + 4), codes4(x[k] + 8), codes4(x[k] + 12));
+                } else {
+                    *reinterpret_cast<uint2 *>(out + row.at0) = make_uint2(codes4(x[k]), codes4(x[k] + 4));
+                    *reinterpret_cast<uint2 *>(out + row.at1) = make_uint2(codes4(x[k] + 8), codes4(x[k] + 12));
+                }
             }
         }
     }
 }
 
 template <typename TI, int HD>
-cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, cudaStream_t st) {
+cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, int32_t in_dtype, cudaStream_t st) {
     const bool any = !aligned || a.r.pairs % 8 != 0, half = layout == KVD_ROPE_HALF;
     // Many tokens: as many to a CTA as a page has rows, so that most CTAs have one whole
-    // run; few: 16, for more CTAs.
-    a.tok = a.r.n_tokens >= 2048 ? 1 << a.r.page_log2 : 16;
-    a.q_heads = int32_t(ceil_div(a.r.g[0].heads, a.r.n_kv));
-    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.r.n_kv), a.r.g[0].heads > 0 ? 3 : 2);
+    // run, four heads of K for the angles of its rows, and q in a launch of its own, whose
+    // CTAs are more to an SM.  Few: 16 tokens, one head and q beside them, for more CTAs
+    // and one launch.
+    const bool many = a.r.n_tokens >= 2048;
+    const int32_t size = 1 << a.r.page_log2;
+    a.tok = many ? size : 16;
+    a.k_heads = many ? 4 : 1;
+    a.k_ctas = int32_t(ceil_div(a.r.n_kv, a.k_heads));
+    int32_t q_ctas = 0;
+    if (a.r.g[0].heads > 0 && many) {
+        const cudaError_t e = rotate_rows(a.r, layout, in_dtype, a.q_f16 != 0 ? KVD_T_F16 : KVD_T_BF16, st);
+        if (e != cudaSuccess) return e;
+    } else if (a.r.g[0].heads > 0) {
+        a.q_tok = 4;
+        q_ctas = a.tok / a.q_tok;
+    }
+    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.k_ctas + a.r.n_kv + q_ctas));
+    const int32_t rows = a.tok + size < kWindow ? a.tok + size : kWindow;
+    const int smem = int(sizeof(float2)) * a.r.pairs * rows;
     const auto kern = any ? (half ? store_kernel<TI, HD, true, true> : store_kernel<TI, HD, false, true>)
                           : (half ? store_kernel<TI, HD, true, false> : store_kernel<TI, HD, false, false>);
-    return launch_pdl(kern, grid, dim3(kStoreThreads), 0, st, a);
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, dim3(kStoreThreads), size_t(smem), st, a);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -538,7 +565,7 @@ extern "C" kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, c
     a.scale[1] = v_scale;
     const auto go = [&](auto type) {
         using TI = decltype(type);
-        return head_dim == 64 ? launch_store<TI, 64>(a, aligned, layout, st) : launch_store<TI, 128>(a, aligned, layout, st);
+        return head_dim == 64 ? launch_store<TI, 64>(a, aligned, layout, in_dtype, st) : launch_store<TI, 128>(a, aligned, layout, in_dtype, st);
     };
     const cudaError_t e = in_dtype == KVD_T_F32 ? go(float()) : in_dtype == KVD_T_F16 ? go(__half()) : go(__nv_bfloat16());
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;
