@@ -26,7 +26,6 @@
 namespace kvd {
 namespace {
 
-constexpr int kStoreThreads = 256;
 constexpr int kWindow = 128;      // rows in registers: any run fits
 
 struct StoreArgs {
@@ -47,11 +46,11 @@ __device__ __forceinline__ bool pow2(float s) { return (__float_as_uint(s) & 0x7
 
 // Runs of rows in one page that begin among the CTA's tokens; row i is token t0 + i.
 struct Runs {
-    int32_t slot[kStoreThreads];
-    int16_t run[kStoreThreads];           // -1: no row of this CTA's
+    int32_t slot[256];
+    int16_t run[256];           // -1: no row of this CTA's
     int32_t first[129], page[128];        // a run's first row, its page,
     int32_t row0[128];                    // and the row of it in that page
-    int32_t end, leads[kStoreThreads / 32];
+    int32_t end, leads[8];
     uint32_t top[128];                    // largest finite |x|, as bits
     float scale[128], ratio[128];
 };
@@ -60,6 +59,7 @@ struct Runs {
 __device__ __forceinline__ int find_runs(const StoreArgs &args, Runs &s, int64_t t0, bool report) {
     const RopeArgs &a = args.r;
     const int size = 1 << a.page_log2, span = args.tok + size, i = threadIdx.x, warp = i >> 5;
+    const bool in = i < 256;  // a thread for each row
     const int64_t t = t0 + i;
     int32_t slot = i < span && t < a.n_tokens ? a.slots[t] : -1, last = -1;
     if (i == 0 && t0 > 0) last = a.slots[t0 - 1];
@@ -68,26 +68,26 @@ __device__ __forceinline__ int find_runs(const StoreArgs &args, Runs &s, int64_t
         slot = -1;
     }
     if (slot < 0) slot = -1;
-    s.slot[i] = slot;
+    if (in) s.slot[i] = slot;
     if (i < 128) s.top[i] = 0;
     if (i == 0) s.end = span;
     __syncthreads();
-    if (i > 0) last = s.slot[i - 1];
+    if (in && i > 0) last = s.slot[i - 1];
     // a row that goes on where the one before it stands, in the same page
     const bool on = slot >= 0 && last >= 0 && slot == last + 1 && (slot & (size - 1)) != 0;
     const bool lead = i < args.tok && slot >= 0 && !on;
     if (i >= args.tok && i < span && !on) atomicMin(&s.end, i);
     const uint32_t leads = __ballot_sync(~0u, lead);
-    if ((i & 31) == 0) s.leads[warp] = __popc(leads);
+    if (in && (i & 31) == 0) s.leads[warp] = __popc(leads);
     __syncthreads();
     int before = __popc(leads & (~0u >> (31 - (i & 31)))), n = 0;
 #pragma unroll
-    for (int w = 0; w < kStoreThreads / 32; ++w) {
+    for (int w = 0; w < 8; ++w) {
         before += w < warp ? s.leads[w] : 0;
         n += s.leads[w];
     }
     // rows past the CTA's tokens are those of a run that goes on
-    s.run[i] = int16_t(slot >= 0 && i < s.end ? before - 1 : -1);
+    if (in) s.run[i] = int16_t(slot >= 0 && i < s.end ? before - 1 : -1);
     if (lead) {
         s.first[before - 1] = i;
         s.page[before - 1] = slot >> a.page_log2;
@@ -99,18 +99,23 @@ __device__ __forceinline__ int find_runs(const StoreArgs &args, Runs &s, int64_t
 }
 
 // cos and sin of rows t0 .. t0 + n - 1 into cs[row][pair]; a row without a position stays.
+template <int THREADS>
 __device__ __forceinline__ void find_angles(const RopeArgs &a, float2 *cs, int64_t t0, int n) {
     const uint64_t *turns = a.turns;
     asm volatile("" : "+l"(turns));  // an ordinary load: of constant memory every lane's own would take a turn
-    for (int i = threadIdx.x; i < n * a.pairs; i += kStoreThreads) {
-        const int r = i / a.pairs, p = i - r * a.pairs;
+    // a thread has one pair; no pairs, no angles, and rot_dim is at most 128
+    const int at_once = a.pairs > 0 ? THREADS / a.pairs : 0;  // rows
+    const int r0 = at_once > 0 ? threadIdx.x / a.pairs : 0, p = at_once > 0 ? threadIdx.x % a.pairs : 0;
+    if (r0 >= at_once) return;
+    const uint64_t step = turns[p];
+    for (int r = r0; r < n; r += at_once) {
         const int32_t pos = a.positions[t0 + r];
         float sn = 0.0f, c = 1.0f;
         if (pos >= 0) {
             // The angle, a fraction of a turn, in two parts: 24 bits that f32 holds, and the
             // next ones by the first terms of sine and cosine.  (One f32 would move the
             // result by 2^-23: more rows would fall on the other side of a code's border.)
-            const uint64_t frac = uint64_t(pos) * turns[p];
+            const uint64_t frac = uint64_t(pos) * step;
             const int32_t hi = int32_t(uint32_t(frac >> 32) & 0xffffff00u);
             const float rest = float(uint32_t(frac >> 8)) * 8.71967124502158e-17f;  // 2 pi 2^-56: radians
             float s0, c0;
@@ -118,7 +123,7 @@ __device__ __forceinline__ void find_angles(const RopeArgs &a, float2 *cs, int64
             c = fmaf(-rest, s0, c0);
             sn = fmaf(rest, c0, s0);
         }
-        cs[i] = make_float2(c * a.factor, sn * a.factor);
+        cs[r * a.pairs + p] = make_float2(c * a.factor, sn * a.factor);
     }
 }
 
@@ -169,17 +174,17 @@ struct Row16 {
     }
 };
 
-// q's rows t0 .. t0 + n - 1, all heads; n at most kLanes.
-template <typename TI, int HD, bool HALF, bool ANY>
+// q's rows t0 .. t0 + n - 1, all heads; n at most 16.
+template <typename TI, int HD, bool HALF, bool ANY, int THREADS>
 __device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int64_t t0, int n) {
-    constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;
+    constexpr int kTasks = HD / 16, kLanes = THREADS / kTasks;
     const RopeArgs &a = args.r;
     const Group &g = a.g[0];
     const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks;
     const int at_once = kLanes / n, r = lane % n, first = lane / n;  // heads at once
     Row16<TI, HALF, ANY> row;
     row.place(a, task, a.pairs > 0);
-    find_angles(a, cs, t0, n);
+    find_angles<THREADS>(a, cs, t0, n);
     __syncthreads();
     const int64_t t = t0 + r;
     const bool there = first < at_once && a.positions[t] >= 0;
@@ -214,9 +219,9 @@ __device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int
     }
 }
 
-template <typename TI, int HD, bool HALF, bool ANY>
-__global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_constant__ StoreArgs args) {
-    constexpr int kTasks = HD / 16, kLanes = kStoreThreads / kTasks;  // of a row; rows at once
+template <typename TI, int HD, bool HALF, bool ANY, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2) store_kernel(const __grid_constant__ StoreArgs args) {
+    constexpr int kTasks = HD / 16, kLanes = THREADS / kTasks;  // of a row; rows at once
     constexpr int kTurns = kWindow / kLanes;
     extern __shared__ __align__(16) float2 cs[];  // of the rows at hand
     __shared__ Runs sh;
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_co
         t0 += int64_t(part - a.n_kv) * args.q_tok;
         const int64_t end = int64_t(blockIdx.x + 1) * args.tok < a.n_tokens ? int64_t(blockIdx.x + 1) * args.tok : a.n_tokens;
         const int n = int(end - t0 < args.q_tok ? end - t0 : args.q_tok);
-        if (n > 0) turn_rows<TI, HD, HALF, ANY>(args, cs, t0, n);
+        if (n > 0) turn_rows<TI, HD, HALF, ANY, THREADS>(args, cs, t0, n);
         return;
     }
     const int kind = part < 0 ? 0 : 1, h0 = kind == 0 ? int(blockIdx.y) * args.k_heads : part;
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_co
         const int w1 = sh.first[rb];
         if (kind == 0 && a.pairs > 0) {
             if (ra > 0) __syncthreads();
-            find_angles(a, cs, t0 + w0, w1 - w0);
+            find_angles<THREADS>(a, cs, t0 + w0, w1 - w0);
             __syncthreads();
         }
         int run[kTurns];
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_co
             }
             __syncthreads();
             // codes that stand before a run move to the new scale: a warp for each run
-            for (int r = ra + int(threadIdx.x >> 5); r < rb; r += kStoreThreads / 32) {
+            for (int r = ra + int(threadIdx.x >> 5); r < rb; r += THREADS / 32) {
                 const float ratio = sh.ratio[r];
                 if (ratio == 1.0f) continue;
                 uint4 *p = reinterpret_cast<uint4 *>(block_of(r));
@@ -351,34 +356,31 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_kernel(const __grid_co
     }
 }
 
+template <typename TI, int HD, int THREADS>
+cudaError_t launch_store(const StoreArgs &a, dim3 grid, bool any, bool half, int smem, cudaStream_t st) {
+    const auto kern = any ? (half ? store_kernel<TI, HD, true, true, THREADS> : store_kernel<TI, HD, false, true, THREADS>)
+                          : (half ? store_kernel<TI, HD, true, false, THREADS> : store_kernel<TI, HD, false, false, THREADS>);
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
+    return e != cudaSuccess ? e : launch_pdl(kern, grid, dim3(THREADS), size_t(smem), st, a);
+}
+
 template <typename TI, int HD>
-cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, int32_t in_dtype, cudaStream_t st) {
+cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, cudaStream_t st) {
     const bool any = !aligned || a.r.pairs % 8 != 0, half = layout == KVD_ROPE_HALF;
-    // Many tokens: as many to a CTA as a page has rows, so that most CTAs have one whole
-    // run, four heads of K for the angles of its rows, and q in a launch of its own, whose
-    // CTAs are more to an SM.  Few: 16 tokens, one head and q beside them, for more CTAs
-    // and one launch.
+    // Many tokens: 128 to a CTA of 512 threads, which hold their rows, and two heads of K
+    // for the angles.  Few: 16 tokens, one head, 256 threads, for more CTAs.  (8192 tokens
+    // into pages of 128, with q and the reading back: XXX.)
     const bool many = a.r.n_tokens >= 2048;
     const int32_t size = 1 << a.r.page_log2;
-    a.tok = many ? size : 16;
-    a.k_heads = many ? 4 : 1;
+    a.tok = many ? 128 : 16;
+    a.k_heads = many ? 2 : 1;
     a.k_ctas = int32_t(ceil_div(a.r.n_kv, a.k_heads));
-    int32_t q_ctas = 0;
-    if (a.r.g[0].heads > 0 && many) {
-        const cudaError_t e = rotate_rows(a.r, layout, in_dtype, a.q_f16 != 0 ? KVD_T_F16 : KVD_T_BF16, st);
-        if (e != cudaSuccess) return e;
-    } else if (a.r.g[0].heads > 0) {
-        a.q_tok = 4;
-        q_ctas = a.tok / a.q_tok;
-    }
+    a.q_tok = many ? 16 : 4;
+    const int32_t q_ctas = a.r.g[0].heads > 0 ? a.tok / a.q_tok : 0;
     const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.k_ctas + a.r.n_kv + q_ctas));
     const int32_t rows = a.tok + size < kWindow ? a.tok + size : kWindow;
     const int smem = int(sizeof(float2)) * a.r.pairs * rows;
-    const auto kern = any ? (half ? store_kernel<TI, HD, true, true> : store_kernel<TI, HD, false, true>)
-                          : (half ? store_kernel<TI, HD, true, false> : store_kernel<TI, HD, false, false>);
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, dim3(kStoreThreads), size_t(smem), st, a);
+    return many ? launch_store<TI, HD, 512>(a, grid, any, half, smem, st) : launch_store<TI, HD, 256>(a, grid, any, half, smem, st);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -565,7 +567,7 @@ extern "C" kvd_status kv_paged_append_q8(const kvd_rope *R, const kvd_rows *q, c
     a.scale[1] = v_scale;
     const auto go = [&](auto type) {
         using TI = decltype(type);
-        return head_dim == 64 ? launch_store<TI, 64>(a, aligned, layout, in_dtype, st) : launch_store<TI, 128>(a, aligned, layout, in_dtype, st);
+        return head_dim == 64 ? launch_store<TI, 64>(a, aligned, layout, st) : launch_store<TI, 128>(a, aligned, layout, st);
     };
     const cudaError_t e = in_dtype == KVD_T_F32 ? go(float()) : in_dtype == KVD_T_F16 ? go(__half()) : go(__nv_bfloat16());
     return e == cudaSuccess ? KVD_OK : KVD_ECUDA;

@@ -272,20 +272,6 @@ cudaError_t launch_rope(const RopeArgs &a, bool aligned, int layout, cudaStream_
 }
 
 }  // namespace
-
-cudaError_t rotate_rows(const RopeArgs &call, int layout, int32_t in_dtype, int32_t out_dtype, cudaStream_t st) {
-    RopeArgs a = call;
-    a.paged = 0;
-    a.g[1].heads = a.g[2].heads = 0;
-    const int ib = dtype_bytes(in_dtype), ob = dtype_bytes(out_dtype);
-    const bool aligned = aligned16(a.g[0], false, ib, ob);
-    if (out_dtype == KVD_T_F16)
-        return in_dtype == KVD_T_F32 ? launch_rope<float, __half>(a, aligned, layout, st)
-                                     : launch_rope<__half, __half>(a, aligned, layout, st);
-    return in_dtype == KVD_T_F32 ? launch_rope<float, __nv_bfloat16>(a, aligned, layout, st)
-                                 : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, aligned, layout, st);
-}
-
 }  // namespace kvd
 
 using namespace kvd;

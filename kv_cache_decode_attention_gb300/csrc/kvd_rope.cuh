@@ -142,7 +142,4 @@ inline View view_of(const kvd_rows *r, int64_t tokens, int32_t heads, int32_t hd
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
-// The rows of a.g[0] (q) rotated into their outputs, f16 or bf16 (kvd_rope.cu).
-cudaError_t rotate_rows(const RopeArgs &a, int layout, int32_t in_dtype, int32_t out_dtype, cudaStream_t st);
-
 }  // namespace kvd
