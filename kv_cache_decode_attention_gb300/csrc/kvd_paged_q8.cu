@@ -32,8 +32,9 @@ struct StoreArgs {
     RopeArgs r;               // g[0]: q; g[1], g[2]: k and v with their pages
     float *scale[2];          // of K and V: [n_pages][n_kv]
     int32_t tok;              // tokens whose runs a CTA takes: at most 128, and with a page's rows at most 256
-    int32_t k_heads, k_ctas;  // heads of a CTA of K; CTAs of K's heads, before V's and q's in the grid
-    int32_t q_tok, q_f16;     // tokens of a CTA of q; q_out's type
+    int32_t k_heads, k_ctas;  // heads of a CTA of K; CTAs of K's heads
+    int32_t q_tok, q_ctas;    // tokens of a CTA of q; CTAs of q
+    int32_t q_f16;            // q_out's type
 };
 
 // The smallest power of two s with top <= 448 s, within the limits: 448 = 1.75 * 2^8.
@@ -174,7 +175,7 @@ struct Row16 {
     }
 };
 
-// q's rows t0 .. t0 + n - 1, all heads; n at most 16.
+// q's rows t0 .. t0 + n - 1, all heads; n at most 32.
 template <typename TI, int HD, bool HALF, bool ANY, int THREADS>
 __device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int64_t t0, int n) {
     constexpr int kTasks = HD / 16, kLanes = THREADS / kTasks;
@@ -188,30 +189,31 @@ __device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int
     __syncthreads();
     const int64_t t = t0 + r;
     const bool there = first < at_once && a.positions[t] >= 0;
-    for (int h0 = 0; h0 < g.heads; h0 += at_once) {
-        const int h = h0 + first;
+    const TI *in = static_cast<const TI *>(g.in) + t * g.in_tok;
+    float x[2][16];  // rows of this turn and of the next
+    if (!ANY && there && first < g.heads) row.load(in + first * g.in_head, x[0]);
+#pragma unroll 2
+    for (int k = 0; k * at_once < g.heads; ++k) {
+        const int h = k * at_once + first;
         const bool mine = there && h < g.heads;
-        float x[16];
-        if (mine) {
-            const TI *in = static_cast<const TI *>(g.in) + t * g.in_tok + h * g.in_head;
-            if constexpr (ANY) {
-                row.load_any(a, cs + r * a.pairs, in, task, x);
-            } else {
-                row.load(in, x);
-                row.rotate(cs + r * a.pairs, task, x);
-            }
+        float *y = x[k & 1];
+        if constexpr (ANY) {
+            if (mine) row.load_any(a, cs + r * a.pairs, in + h * g.in_head, task, y);
+            __syncwarp();  // in place, no channel is written before its partner's thread has it
+        } else {
+            if (there && h + at_once < g.heads) row.load(in + (h + at_once) * g.in_head, x[(k + 1) & 1]);
+            if (mine) row.rotate(cs + r * a.pairs, task, y);
         }
-        if (ANY) __syncwarp();  // in place, no channel is written before its partner's thread has it
         if (!mine) continue;
         const int64_t at = t * g.out_tok + h * g.out_head;
         auto put = [&](auto *out) {
             using TO = std::remove_pointer_t<decltype(out)>;
             if constexpr (ANY) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) out[at + task * 16 + e] = from_f32<TO>(x[e]);
+                for (int e = 0; e < 16; ++e) out[at + task * 16 + e] = from_f32<TO>(y[e]);
             } else {
-                store8<TO>(out + at + row.at0, x);
-                store8<TO>(out + at + row.at1, x + 8);
+                store8<TO>(out + at + row.at0, y);
+                store8<TO>(out + at + row.at1, y + 8);
             }
         };
         if (args.q_f16 != 0) put(static_cast<__half *>(g.out));
@@ -228,18 +230,21 @@ __global__ void __launch_bounds__(THREADS, 2) store_kernel(const __grid_constant
     const RopeArgs &a = args.r;
     pdl_wait();
     int64_t t0 = int64_t(blockIdx.x) * args.tok;
-    const int part = int(blockIdx.y) - args.k_ctas;  // below 0: of K; below n_kv: V; then q
-    if (part >= a.n_kv) {
-        t0 += int64_t(part - a.n_kv) * args.q_tok;
+    // q's CTAs, which only copy, between those of K and V, which mostly wait
+    const int y = int(blockIdx.y), kv = args.k_ctas + a.n_kv, both = args.q_ctas < kv ? args.q_ctas : kv;
+    const bool is_q = y < 2 * both ? y % 2 == 0 : args.q_ctas > kv;
+    const int place = y < 2 * both ? y / 2 : y - both;
+    if (is_q) {
+        t0 += int64_t(place) * args.q_tok;
         const int64_t end = int64_t(blockIdx.x + 1) * args.tok < a.n_tokens ? int64_t(blockIdx.x + 1) * args.tok : a.n_tokens;
         const int n = int(end - t0 < args.q_tok ? end - t0 : args.q_tok);
         if (n > 0) turn_rows<TI, HD, HALF, ANY, THREADS>(args, cs, t0, n);
         return;
     }
-    const int kind = part < 0 ? 0 : 1, h0 = kind == 0 ? int(blockIdx.y) * args.k_heads : part;
+    const int kind = place < args.k_ctas ? 0 : 1, h0 = kind == 0 ? place * args.k_heads : place - args.k_ctas;
     const int heads = kind == 1 ? 1 : a.n_kv - h0 < args.k_heads ? a.n_kv - h0 : args.k_heads;
     const Group &g = a.g[1 + kind];
-    const int n = find_runs(args, sh, t0, blockIdx.y == 0);
+    const int n = find_runs(args, sh, t0, place == 0);
     if (n == 0) return;
     const int size = 1 << a.page_log2;
     const int task = threadIdx.x % kTasks, lane = threadIdx.x / kTasks;
@@ -367,17 +372,19 @@ cudaError_t launch_store(const StoreArgs &a, dim3 grid, bool any, bool half, int
 template <typename TI, int HD>
 cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, cudaStream_t st) {
     const bool any = !aligned || a.r.pairs % 8 != 0, half = layout == KVD_ROPE_HALF;
-    // Many tokens: 128 to a CTA of 512 threads, which hold their rows, and two heads of K
+    // Many tokens: 128 to a CTA of 512 threads, which hold their rows, and four heads of K
     // for the angles.  Few: 16 tokens, one head, 256 threads, for more CTAs.  (8192 tokens
-    // into pages of 128, with q and the reading back: XXX.)
+    // of 32 + 8 + 8 heads into pages of 128: 47 us, in the small form 91; 256 tokens: 5.3,
+    // in the large form 13 to 20.  K and V alone take 24, q alone 30: it copies at 4.5 TB/s,
+    // held back by the registers of the others.)
     const bool many = a.r.n_tokens >= 2048;
     const int32_t size = 1 << a.r.page_log2;
     a.tok = many ? 128 : 16;
-    a.k_heads = many ? 2 : 1;
+    a.k_heads = many ? 4 : 1;
     a.k_ctas = int32_t(ceil_div(a.r.n_kv, a.k_heads));
-    a.q_tok = many ? 16 : 4;
-    const int32_t q_ctas = a.r.g[0].heads > 0 ? a.tok / a.q_tok : 0;
-    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.k_ctas + a.r.n_kv + q_ctas));
+    a.q_tok = many ? 32 : 4;
+    a.q_ctas = a.r.g[0].heads > 0 ? a.tok / a.q_tok : 0;
+    const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.k_ctas + a.r.n_kv + a.q_ctas));
     const int32_t rows = a.tok + size < kWindow ? a.tok + size : kWindow;
     const int smem = int(sizeof(float2)) * a.r.pairs * rows;
     return many ? launch_store<TI, HD, 512>(a, grid, any, half, smem, st) : launch_store<TI, HD, 256>(a, grid, any, half, smem, st);
