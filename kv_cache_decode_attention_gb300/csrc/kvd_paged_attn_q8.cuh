@@ -842,15 +842,15 @@ struct QrJoin {
 };
 
 // Joins the rows of cut items, a warp for each, whose lanes stand for channels, four
-// pieces under way at a time: two CTAs for a record of `few`, `wide` for one of `many`.
+// pieces under way at a time: one CTA for a record of `few`, `wide` for one of `many`.
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ QrJoin j) {
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr int kPer = HD / 32;
     pdl_wait();
-    const int32_t few = j.few.ctas * 2, at_cta = int32_t(blockIdx.x) - (int32_t(blockIdx.x) < few ? 0 : few);
+    const int32_t few = j.few.ctas, at_cta = int32_t(blockIdx.x) - (int32_t(blockIdx.x) < few ? 0 : few);
     const QrArgs &a = int32_t(blockIdx.x) < few ? j.few : j.many;
-    const int32_t share = int32_t(blockIdx.x) < few ? 2 : j.wide;
+    const int32_t share = int32_t(blockIdx.x) < few ? 1 : j.wide;
     const QrCut cut = a.cut[at_cta / share];
     if (cut.n == 0) return;
     const QrPieces pieces(cut.unit0, cut.tiles, cut.total, a.ctas);
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ Qr
 
 template <int HD, bool BF16>
 cudaError_t launch_qr_join(const QrJoin &j, cudaStream_t st) {
-    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(unsigned(j.few.ctas * 2 + j.many.ctas * j.wide)), dim3(256), 0, st, j);
+    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(unsigned(j.few.ctas + j.many.ctas * j.wide)), dim3(256), 0, st, j);
 }
 
 }  // namespace kvd
