@@ -841,49 +841,77 @@ struct QrJoin {
     int32_t wide;      // CTAs for each record of `many`
 };
 
-// Joins the rows of cut items, a warp for each, whose lanes stand for channels, four
-// pieces under way at a time: one CTA for a record of `few`, `wide` for one of `many`.
+// Joins the rows of cut items, by warps whose lanes stand for channels, four pieces
+// under way at a time: one CTA for a record of `few`, whose warps share the pieces of its
+// rows, `wide` for one of `many`.  (A token over 131072 rows leaves 57 pieces of a row.)
+constexpr int kJoinThreads = 256;
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ QrJoin j) {
+__global__ void __launch_bounds__(kJoinThreads) qr_join_kernel(const __grid_constant__ QrJoin j) {
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
-    constexpr int kPer = HD / 32;
+    constexpr int kPer = HD / 32, kWarps = kJoinThreads / 32, kDeep = 4;
+    __shared__ float parts[kWarps][HD + 2];
     pdl_wait();
-    const int32_t few = j.few.ctas, at_cta = int32_t(blockIdx.x) - (int32_t(blockIdx.x) < few ? 0 : few);
-    const QrArgs &a = int32_t(blockIdx.x) < few ? j.few : j.many;
-    const int32_t share = int32_t(blockIdx.x) < few ? 1 : j.wide;
+    const bool is_few = int32_t(blockIdx.x) < j.few.ctas;
+    const int32_t at_cta = int32_t(blockIdx.x) - (is_few ? 0 : j.few.ctas);
+    const QrArgs &a = is_few ? j.few : j.many;
+    const int32_t share = is_few ? 1 : j.wide;
     const QrCut cut = a.cut[at_cta / share];
     if (cut.n == 0) return;
     const QrPieces pieces(cut.unit0, cut.tiles, cut.total, a.ctas);
-    const int32_t col = int32_t(threadIdx.x & 31) * kPer;
-    for (int32_t r = at_cta % share * 8 + (threadIdx.x >> 5); r < cut.rows; r += share * 8) {
+    const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane * kPer;
+    int32_t at_once = kWarps;  // rows
+    if (is_few)
+        while (at_once / 2 >= cut.rows) at_once /= 2;
+    const int32_t split = kWarps / at_once, part = warp / at_once;  // warps of a row
+    for (int32_t r = at_cta % share * at_once + warp % at_once; r < cut.rows || split > 1; r += share * at_once) {
         float top = -INFINITY, sum = 0.0f, o[kPer] = {};
 #pragma unroll 1
-        for (int32_t i0 = 0; i0 < pieces.n; i0 += 4) {
-            float2 ml[4];
-            float v[4][kPer] = {};
+        for (int32_t i0 = part; i0 < pieces.n && r < cut.rows; i0 += kDeep * split) {
+            float2 ml[kDeep];
+            float v[kDeep][kPer] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kDeep; ++i) {
                 ml[i] = make_float2(-INFINITY, 0.0f);
-                if (i0 + i >= pieces.n) continue;
-                const int64_t at = pieces.slot(i0 + i) * a.part_rows + r;
+                if (i0 + i * split >= pieces.n) continue;
+                const int64_t at = pieces.slot(i0 + i * split) * a.part_rows + r;
                 ml[i] = __ldcg(&a.part_ml[at]);
                 const float *p = a.part_o + at * HD + col;
                 if constexpr (kPer == 4) *reinterpret_cast<float4 *>(v[i]) = __ldcg(reinterpret_cast<const float4 *>(p));
                 else *reinterpret_cast<float2 *>(v[i]) = __ldcg(reinterpret_cast<const float2 *>(p));
             }
-            const float now = fmaxf(max3(top, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), base = now == -INFINITY ? 0.0f : now;
-            const float f0 = ex2(top - base);
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) now = fmaxf(now, ml[i].x);
+            const float base = now == -INFINITY ? 0.0f : now, f0 = ex2(top - base);
             sum *= f0;
 #pragma unroll
             for (int c = 0; c < kPer; ++c) o[c] *= f0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kDeep; ++i) {
                 const float f = ex2(ml[i].x - base);
                 sum += ml[i].y * f;
 #pragma unroll
                 for (int c = 0; c < kPer; ++c) o[c] += v[i][c] * f;
             }
             top = now;
+        }
+        if (split > 1) {  // the warps' parts of a row, in their order
+            if (lane == 0) parts[warp][HD] = top, parts[warp][HD + 1] = sum;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) parts[warp][col + c] = o[c];
+            __syncthreads();
+            if (part > 0 || r >= cut.rows) return;
+            for (int32_t w = warp; w < kWarps; w += at_once) top = fmaxf(top, parts[w][HD]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[c] = 0.0f;
+            for (int32_t w = warp; w < kWarps; w += at_once) {
+                const float f = ex2(parts[w][HD] - base);
+                sum += parts[w][HD + 1] * f;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) o[c] += parts[w][col + c] * f;
+            }
         }
         const int32_t tok = r / a.group, head = cut.kv_head * a.group + r - tok * a.group;
         float f = 1.0f;
@@ -896,12 +924,13 @@ __global__ void __launch_bounds__(256) qr_join_kernel(const __grid_constant__ Qr
         T *dst = static_cast<T *>(a.out) + (int64_t(cut.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head + col;
 #pragma unroll
         for (int c = 0; c < kPer; c += 2) *reinterpret_cast<uint32_t *>(dst + c) = pack2<BF16>(o[c] * f, o[c + 1] * f);
+        if (split > 1) return;  // all rows were at once
     }
 }
 
 template <int HD, bool BF16>
 cudaError_t launch_qr_join(const QrJoin &j, cudaStream_t st) {
-    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(unsigned(j.few.ctas + j.many.ctas * j.wide)), dim3(256), 0, st, j);
+    return launch_pdl(qr_join_kernel<HD, BF16>, dim3(unsigned(j.few.ctas + j.many.ctas * j.wide)), dim3(kJoinThreads), 0, st, j);
 }
 
 }  // namespace kvd
