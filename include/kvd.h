@@ -707,8 +707,13 @@ KVD_API kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t 
                                                       int32_t head_dim, int64_t *bytes_out);
 
 /* paged_attention over pages of 8 bits: the attention of q, f16 or bf16 (dtype), over
- * the rows that codes and scales stand for.  Arguments, masks, options and what is
- * skipped or left alone are those of paged_attention. */
+ * the rows that codes and scales stand for.  Arguments, masks, options, what is skipped
+ * or left alone, and the sums in f32 are those of paged_attention.  q is taken to 2^-17
+ * of its row's largest value (exactly, if that is within 2^9 of every other: f16 2^6), and
+ * the weights, with the scale of V's block, are rounded once, to eight significant bits for
+ * bf16 and twelve for f16 (eleven in chunks of more than 16 query rows a KV head) and to
+ * 2^-22 of the largest of a tile's 128 rows (2^-27 of the row's in such chunks).
+ * A row of q that is not finite gives NaN, in that row alone.  n_seq <= 2^20. */
 KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q,
                                       int32_t n_kv, int32_t head_dim, int32_t dtype, const void *k_pages,
                                       const void *v_pages, const float *k_scale, const float *v_scale,
@@ -718,8 +723,8 @@ KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, in
                                       const float *sinks, void *workspace, int64_t workspace_bytes, uint32_t *err,
                                       void *stream);
 
-/* The bounded waits of paged_attention, run on purpose (for tests).  While armed
- * with 0 <= cta < 152, that thread block of every launch gives up after_ns (0 ..
+/* The bounded waits of paged_attention and paged_attention_q8, run on purpose (for
+ * tests).  While armed with 0 <= cta < 152, that thread block of every launch gives up after_ns (0 ..
  * 10^9) nanoseconds after it began, if it is not done by then: as after the two
  * seconds without a step that it has otherwise, every wait of the block ends, bit 0
  * of the error word is set, the rows it had to do are undefined, and the kernel

@@ -105,6 +105,9 @@ void set_cap(PaArgs *a, float scale, float softcap) {
 }
 
 }  // namespace
+
+int64_t paged_give_up() { return g_give_up.load(std::memory_order_relaxed); }
+
 }  // namespace kvd
 
 using namespace kvd;
@@ -172,7 +175,7 @@ extern "C" kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, in
     char *w = static_cast<char *>(workspace);
     a.cut = reinterpret_cast<PaPiecesOf *>(w + ws.cut);
     a.join_here = n_tokens * group <= kPaJoinRows ? 1 : 0;
-    const int64_t armed = g_give_up.load(std::memory_order_relaxed);
+    const int64_t armed = paged_give_up();
     a.give_up = armed < 0 ? -1 : int32_t(armed >> 32);
     a.give_up_ns = uint32_t(armed);
     a.tickets = reinterpret_cast<uint64_t *>(w + ws.tickets);

@@ -125,6 +125,9 @@ struct PaArgs {
     float cap_c[4];    // its other coefficients, in powers of the score
 };
 
+// What kvd_test_give_up armed: CTA << 32 | ns, or below zero.
+int64_t paged_give_up();
+
 // A ticket that carries another nonce counts as zero, so the workspace needs no
 // initialisation; whoever joins the pieces sets it to 0 for a graph's next
 // replay, which comes with the same nonce.  (So every piece has its ticket taken,

@@ -191,7 +191,9 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
     a.n_pages = int32_t(n_pages);
     a.page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     a.pool_rows = int32_t(pool_rows);
-    a.give_up = -1;
+    const int64_t armed = paged_give_up();
+    a.give_up = armed < 0 ? -1 : int32_t(armed >> 32);
+    a.give_up_ns = uint32_t(armed);
     // A cap so far above the scale that their quotient is no normal number (a raw
     // score would have to pass 10^34 to feel it) is none.
     const bool cap = softcap > 0.0f && scale / softcap >= FLT_MIN;

@@ -838,3 +838,132 @@ def test_a_pool_past_31_bits_of_bytes(env):
     out = kvd.paged_attention(x[:2, :n_kv], cache, plan)
     assert cache.device_error() == 0
     _check8(torch, out, _attend8(torch, x[:2, :n_kv], k.double(), v.double(), 300, hd ** -0.5), float(cache.v_scale.max()))
+
+
+@pytest.mark.parametrize("lens,new", [([30000], [1]), ([5000, 30, 900, 3000], [1, 1, 4, 1]), ([4000, 1500, 700], [300, 1, 90])])
+def test_a_launch_given_up_leaves_no_trace(env, lens, new):
+    """One block's waits end early, at one moment or another: the error bit, and the next calls and replays right."""
+    torch, kvd = env
+    from kv_cache_decode_attention_gb300 import _abi
+
+    cache, _ = _poisoned8(torch, kvd, lens, 2, 128, 16, 3)
+    q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).bfloat16()
+    plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+    ws = torch.zeros(kvd.paged_attention_workspace(sum(new), 8, 2, 128, torch.float8_e4m3fn), dtype=torch.uint8, device="cuda")
+    want, out = kvd.paged_attention(q, cache, plan, workspace=ws), torch.empty_like(q)
+    assert cache.device_error() == 0
+    gave_up = 0
+    try:
+        for cta in (0, 37, 76, 151):
+            for after in (0, 2000, 5000, 9000):
+                assert _abi.lib().kvd_test_give_up(cta, after) == 0
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    kvd.paged_attention(q, cache, plan, out=out, workspace=ws)
+                _abi.lib().kvd_test_give_up(-1, 0)
+                for _ in range(3):
+                    out.fill_(float("nan"))
+                    graph.replay()
+                    error = cache.device_error()
+                    assert error in (0, 1)
+                    gave_up += error
+                    assert error == 1 or torch.equal(out, want)
+                assert torch.equal(kvd.paged_attention(q, cache, plan, out=out, workspace=ws), want) and cache.device_error() == 0
+    finally:
+        _abi.lib().kvd_test_give_up(-1, 0)
+    assert gave_up >= 3
+
+
+def _banded(torch, shape, dtype, fill):
+    """A contiguous tensor between two bands of 4 KB, and what tells whether they stand."""
+    size = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    room = -(-size // 256) * 256
+    box = torch.full((8192 + room,), 0x5a, dtype=torch.uint8, device="cuda")
+    inner = box[4096:4096 + size].view(dtype).view(shape)
+    inner.fill_(fill)
+    return inner, lambda: bool((box[:4096] == 0x5a).all()) and bool((box[4096 + size:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("hd,group,dtype", [(128, 4, "bf16"), (64, 16, "f16"), (128, 1, "f16")])
+def test_nothing_is_written_beside_the_outputs(env, hd, group, dtype):
+    """Workspace of exactly the size that is asked for, outputs, codes and scales between guard bands."""
+    torch, kvd = env
+    n_kv, page, dt = 2, 16, _dt(torch, dtype)
+    for lens, new in (([9000, 40], [1, 1]), ([600, 3000, 20], [130, 7, 20])):
+        src, rows = _poisoned8(torch, kvd, lens, n_kv, hd, page, 7)
+        t = sum(new)
+        q = torch.randn(t, n_kv * group, hd, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(dt)
+        plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), src.seq_len)
+        out, ok_out = _banded(torch, q.shape, dt, 0)
+        ws, ok_ws = _banded(torch, (kvd.paged_attention_workspace(t, n_kv * group, n_kv, hd, torch.float8_e4m3fn),), torch.uint8, 0xff)
+        kvd.paged_attention(q, src, plan, out=out, workspace=ws)
+        assert torch.equal(out, kvd.paged_attention(q, src, plan)) and ok_out() and ok_ws()
+        k_out, ok_k = _banded(torch, (sum(lens), n_kv, hd), torch.float32, 0)
+        v_out, ok_v = _banded(torch, (sum(lens), n_kv, hd), torch.float32, 0)
+        kvd.paged_read(src, _i32(torch, [0] + np.cumsum(lens).tolist()), sum(lens), k_out=k_out, v_out=v_out)
+        assert ok_k() and ok_v() and torch.equal(k_out, torch.cat([r[0] for r in rows]).float())
+        parts = [_banded(torch, (5, n_kv, page, hd), torch.uint8, 0) for _ in range(2)] + [_banded(torch, (5, n_kv), torch.float32, 1) for _ in range(2)]
+        cache = kvd.PagedKvCache.of(parts[0][0].view(torch.float8_e4m3fn), parts[1][0].view(torch.float8_e4m3fn), _i32(torch, [[0, 1, 2, 3, 4]]), _i32(torch, [80]),
+                                    k_scale=parts[2][0], v_scale=parts[3][0])
+        x = torch.randn(80, 2 * n_kv, hd, device="cuda")
+        q_out, ok_q = _banded(torch, (80, n_kv, hd), torch.bfloat16, 0)
+        kvd.paged_append(cache, _plan(torch, kvd, range(80), range(80)), x[:, :n_kv], x[:, n_kv:], q=x[:, :n_kv], q_out=q_out, rope=kvd.RopeTable(hd))
+        torch.cuda.synchronize()
+        assert ok_q() and all(ok() for _, ok in parts)
+
+
+@pytest.mark.parametrize("dtype,hd,softcap", [("bf16", 128, 0.0), ("f16", 64, 0.0), ("bf16", 64, 20.0), ("f16", 128, 20.0)])
+def test_what_nobody_holds_leaves_no_trace(env, dtype, hd, softcap):
+    """The same bits whatever lies behind the requests' rows: zeros, the largest code, NaN; and in free pages, their scales too."""
+    torch, kvd = env
+    lens, new, page = [300, 17, 1000, 5], [1, 17, 300, 4], 64
+    outs = []
+    for byte, scale in ((0x00, 1.0), (0x7e, 2.0 ** 60), (0x7f, float("nan"))):
+        cache, _ = _poisoned8(torch, kvd, lens, 2, hd, page, 5)
+        for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            raw = c.view(torch.uint8)
+            raw.copy_(torch.where(raw == 0x7f, torch.full_like(raw, byte), raw))
+            s.nan_to_num_(scale) if scale == scale else None
+        q = (torch.randn(sum(new), 8, hd, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)) * 4).to(_dt(torch, dtype))
+        plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+        outs.append(kvd.paged_attention(q, cache, plan, softcap=softcap))
+        assert cache.device_error() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and not bool(torch.isnan(outs[0]).any())
+
+
+def test_a_query_that_is_no_number_is_its_own(env):
+    """Infinities and NaN in one row of q: that row's output is NaN, all others as they were."""
+    torch, kvd = env
+    for lens, new in (([700], [3]), ([700], [200])):
+        cache, _ = _poisoned8(torch, kvd, lens, 2, 128, 16, 9)
+        for dt in (torch.bfloat16, torch.float16):
+            q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).to(dt)
+            plan = kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+            want = kvd.paged_attention(q, cache, plan)
+            for bad in (math.nan, math.inf, -math.inf):
+                y = q.clone()
+                y[1, 2, 77] = bad
+                got = kvd.paged_attention(y, cache, plan)
+                assert bool(torch.isnan(got[1, 2]).all())
+                got[1, 2] = want[1, 2]
+                assert torch.equal(got, want)
+
+
+def test_pages_may_be_shared_and_queries_broadcast(env):
+    """Two requests with one beginning, and one query row for all heads."""
+    torch, kvd = env
+    cache, rows = _poisoned8(torch, kvd, [128, 200], 2, 64, 64, 15)
+    table = cache.block_table.clone()
+    table[1, 0] = table[0, 0]
+    shared = kvd.PagedKvCache.of(cache.k, cache.v, table, cache.seq_len, k_scale=cache.k_scale, v_scale=cache.v_scale)
+    k = torch.cat([rows[0][0][:64], rows[1][0][64:]])
+    v = torch.cat([rows[0][1][:64], rows[1][1][64:]])
+    row = torch.randn(2, 1, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).bfloat16()
+    q = row.expand(2, 8, 64)
+    out = kvd.paged_attention(q, shared, kvd.PagedPlan(_i32(torch, [0, 1, 2]), cache.seq_len))
+    v_top = float(cache.v_scale.nan_to_num(0).max())
+    _check8(torch, out[:1], _attend8(torch, q[:1], *rows[0], 128, 1 / 8), v_top)
+    _check8(torch, out[1:], _attend8(torch, q[1:], k, v, 200, 1 / 8), v_top)
+    got = kvd.paged_read(shared, _i32(torch, [0, 0, 200]), 200, dtype=torch.float32)
+    assert torch.equal(got[0], k.float()) and torch.equal(got[1], v.float())
