@@ -285,16 +285,15 @@ struct QrShared {
     float col[S::kRows];
 };
 
-// Waits end after two seconds, or once another wait of the CTA has (or at a test's
-// wish): nothing here waits for more than a tile's copies and MMAs.
+// Waits end after two seconds, or once another wait of the CTA has, or the loading warp
+// at a test's wish: nothing here waits for more than a tile's copies and MMAs.
 template <typename SH>
-static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, SH &sh, uint64_t *bar, uint32_t parity) {
+static __device__ __noinline__ bool qr_wait_long(SH &sh, uint64_t *bar, uint32_t parity) {
     volatile int *stop = &sh.stop;
-    const bool early = a.give_up == int32_t(blockIdx.x);
-    const uint64_t since = early ? sh.began : global_ns(), limit = early ? a.give_up_ns : 2000000000ull;
+    const uint64_t since = global_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (*stop != 0) return false;
-        if (global_ns() - since >= limit) {
+        if (global_ns() - since >= 2000000000ull) {
             *stop = 1;
             return false;
         }
@@ -302,8 +301,8 @@ static __device__ __noinline__ bool qr_wait_long(const QrArgs &a, SH &sh, uint64
     return true;
 }
 template <typename SH>
-__device__ __forceinline__ bool qr_wait(const QrArgs &a, SH &sh, uint64_t *bar, uint32_t parity) {
-    const bool ok = mbar_try_wait(bar, parity) || qr_wait_long(a, sh, bar, parity);
+__device__ __forceinline__ bool qr_wait(SH &sh, uint64_t *bar, uint32_t parity) {
+    const bool ok = mbar_try_wait(bar, parity) || qr_wait_long(sh, bar, parity);
     return __all_sync(~0u, ok);
 }
 __device__ __forceinline__ void qr_arrive(uint64_t *bar) {
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 const int32_t tile0 = it.tile0 + tile;
                 if (over || n > 0) {
                     QrJob &job = sh.job[at % kQrJobs];
-                    if (at >= kQrJobs) ok = qr_wait(a, sh, &sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1);
+                    if (at >= kQrJobs) ok = qr_wait(sh, &sh.job_empty[at % kQrJobs], (at / kQrJobs & 1) ^ 1);
                     if (!ok) break;
                     if (lane == 0) {
                         const bool whole = n == it.tiles;
@@ -479,6 +478,11 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 // K runs a tile ahead of V
                 for (int32_t t = 0; ok && t <= n; ++t) {
                     int32_t page = -1;
+                    if (a.give_up == int32_t(blockIdx.x) && global_ns() - sh.began >= a.give_up_ns) {
+                        *static_cast<volatile int *>(&sh.stop) = 1;
+                        ok = false;
+                        break;
+                    }
                     if (t < n) {
                         const int32_t in = t % per_block;
                         if (t > 0 && in == 0) {
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         page = __shfl_sync(~0u, block_pages, from);
                         const float ks = __shfl_sync(~0u, block_scales.x, from), vs = __shfl_sync(~0u, block_scales.y, from);
                         const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
-                        if (turn > 0) ok = qr_wait(a, sh, &sh.k_empty[slot], (turn & 1) ^ 1);
+                        if (turn > 0) ok = qr_wait(sh, &sh.k_empty[slot], (turn & 1) ^ 1);
                         if (!ok) break;
                         if (lane < ppt) {
                             const float v = scale_of(vs, a.err);
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     }
                     if (t > 0) {
                         const uint32_t slot = v_loads % S::kStages, turn = v_loads / S::kStages;
-                        if (turn > 0) ok = qr_wait(a, sh, &sh.v_empty[slot], (turn & 1) ^ 1);
+                        if (turn > 0) ok = qr_wait(sh, &sh.v_empty[slot], (turn & 1) ^ 1);
                         if (!ok) break;
                         load(&a.v, smem + S::kV + slot * S::kTileBytes, v_page, &sh.v_full[slot]);
                         ++v_loads;
@@ -521,8 +525,8 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
             bool ok = true;
             auto score = [&](uint32_t i) {
                 const uint32_t slot = i % S::kStages;
-                ok = qr_wait(a, sh, &sh.k_full[slot], i / S::kStages & 1);
-                if (ok && i > 0) ok = qr_wait(a, sh, &sh.s_free, (i - 1) & 1);
+                ok = qr_wait(sh, &sh.k_full[slot], i / S::kStages & 1);
+                if (ok && i > 0) ok = qr_wait(sh, &sh.s_free, (i - 1) & 1);
                 if (!ok) return;
                 tc_after();
                 if (elect_one()) {
@@ -537,19 +541,19 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 tc_commit(&sh.k_empty[slot]);
             };
             for (uint32_t at = 0;; ++at) {
-                ok = qr_wait(a, sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
+                ok = qr_wait(sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
                 if (!ok) break;
                 const uint32_t n = uint32_t(sh.job[at % kQrJobs].n);
                 qr_arrive(&sh.job_empty[at % kQrJobs]);
                 if (n == 0) break;
-                ok = qr_wait(a, sh, &sh.q_ready, at & 1);
+                ok = qr_wait(sh, &sh.q_ready, at & 1);
                 if (!ok) break;
                 score(g);
                 for (uint32_t i = g; ok && i < g + n; ++i) {
                     if (i + 1 < g + n) score(i + 1);
                     if (!ok) break;
                     const uint32_t slot = i % S::kStages;
-                    ok = qr_wait(a, sh, &sh.v_full[slot], i / S::kStages & 1) && qr_wait(a, sh, &sh.p_ready, i & 1);
+                    ok = qr_wait(sh, &sh.v_full[slot], i / S::kStages & 1) && qr_wait(sh, &sh.p_ready, i & 1);
                     if (!ok) break;
                     tc_after();
                     if (elect_one()) {
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
             uint32_t g = 0;
             bool ok = true;
             for (uint32_t at = 0;; ++at) {
-                ok = qr_wait(a, sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
+                ok = qr_wait(sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
                 if (!ok) break;
                 const QrJob job = sh.job[at % kQrJobs];
                 qr_arrive(&sh.job_empty[at % kQrJobs]);
@@ -662,10 +666,10 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     }
                 };
                 for (int32_t i = 0; i < job.n; ++i, ++g) {
-                    ok = qr_wait(a, sh, &sh.sc_full[g % S::kScales], g / S::kScales & 1);
+                    ok = qr_wait(sh, &sh.sc_full[g % S::kScales], g / S::kScales & 1);
                     if (!ok) break;
                     const float4 sc = sh.scale[g % S::kScales][row >> a.page_log2];
-                    ok = qr_wait(a, sh, &sh.s_full, g & 1);
+                    ok = qr_wait(sh, &sh.s_full, g & 1);
                     if (!ok) break;
                     float x[R];
                     {
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     }
                     // rows of V that nobody holds: their weights are zero, but zero times NaN is not
                     if (key0 + kQrTile > job.len) {
-                        ok = qr_wait(a, sh, &sh.v_full[g % S::kStages], g / S::kStages & 1);
+                        ok = qr_wait(sh, &sh.v_full[g % S::kStages], g / S::kStages & 1);
                         if (!ok) break;
                         if (key >= job.len) {
                             const uint32_t v = smem + S::kV + g % S::kStages * S::kTileBytes + row * HD;
@@ -736,7 +740,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     }
                     float o[S::kN];
                     if (i > 0) {
-                        ok = qr_wait(a, sh, &sh.o_full, (g - 1) & 1);
+                        ok = qr_wait(sh, &sh.o_full, (g - 1) & 1);
                         if (!ok) break;
                         take(o);
                     }
@@ -761,7 +765,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 if (!ok) break;
                 {
                     float o[S::kN];
-                    ok = qr_wait(a, sh, &sh.o_full, (g - 1) & 1);
+                    ok = qr_wait(sh, &sh.o_full, (g - 1) & 1);
                     if (!ok) break;
                     take(o);
                     fold(o, uint32_t(job.n - 1));
