@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
     // The launch before has let this one come early: what it cuts is older than both.
     qr_cut<kQpThreads>(a, &sh.start, sh.warp_sums);  // synchronises the CTA
     pdl_wait();
+    pdl_trigger();
     tc_after();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
@@ -736,7 +737,6 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
         __syncthreads();
         tc_after();
     }
-    pdl_trigger();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
