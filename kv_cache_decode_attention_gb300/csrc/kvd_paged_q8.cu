@@ -175,7 +175,7 @@ struct Row16 {
     }
 };
 
-// q's rows t0 .. t0 + n - 1, all heads; n at most 32.
+// q's rows t0 .. t0 + n - 1, all heads; n at most 16.
 template <typename TI, int HD, bool HALF, bool ANY, int THREADS>
 __device__ __forceinline__ void turn_rows(const StoreArgs &args, float2 *cs, int64_t t0, int n) {
     constexpr int kTasks = HD / 16, kLanes = THREADS / kTasks;
@@ -382,7 +382,7 @@ cudaError_t launch_store(StoreArgs &a, bool aligned, int layout, cudaStream_t st
     a.tok = many ? 128 : 16;
     a.k_heads = many ? 4 : 1;
     a.k_ctas = int32_t(ceil_div(a.r.n_kv, a.k_heads));
-    a.q_tok = many ? 32 : 4;
+    a.q_tok = many ? 16 : 4;
     a.q_ctas = a.r.g[0].heads > 0 ? a.tok / a.q_tok : 0;
     const dim3 grid(unsigned(ceil_div(a.r.n_tokens, a.tok)), unsigned(a.k_ctas + a.r.n_kv + a.q_ctas));
     const int32_t rows = a.tok + size < kWindow ? a.tok + size : kWindow;
