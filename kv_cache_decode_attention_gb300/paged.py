@@ -362,7 +362,7 @@ def paged_append(cache: PagedKvCache, plan: PagedPlan, k: torch.Tensor, v: torch
         qi = _rows(q, "q", shape, dev)
         if q_out is None:
             q_out = torch.empty(shape, dtype=q_dtype, device=dev) if stream is None else _empty([shape], q_dtype, dev, stream)[0]
-        elif q_out.dtype is not q_dtype or q_dtype is _F32:
+        elif q_out.dtype is not q_dtype or (coded and q_dtype is not torch.bfloat16 and q_dtype is not torch.float16):
             raise ValueError("q_out must have the inputs' dtype, for float32 float16 or bfloat16" if coded else "q_out must have the pages' dtype")
         qo = _rows(q_out, "q_out", shape, dev)
     elif q_out is not None:

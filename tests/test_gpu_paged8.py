@@ -802,6 +802,7 @@ def test_python_checks_of_8_bits(env):
                 lambda: kvd.paged_attention(q, cache, plan, out=q.half()), lambda: kvd.paged_attention(q[..., :32], cache, plan),
                 lambda: kvd.paged_append(cache, plan, q[:, :2], q[:, 2:].half()), lambda: kvd.paged_append(cache, plan, q[:, :2], q[:, 2:], q=q, q_out=q.half()),
                 lambda: kvd.paged_append(cache, plan, q[:, :2].float(), q[:, 2:].float(), q=q.float(), q_out=q.float()),
+                lambda: kvd.paged_append(cache, plan, q[:, :2].float(), q[:, 2:].float(), q=q.float(), q_out=q.to(torch.float8_e4m3fn)),
                 lambda: kvd.paged_append(cache, plan, q[:, :2].double(), q[:, 2:].double()),
                 lambda: kvd.paged_read(cache, _i32(torch, [0, 1, 2]), 1), lambda: kvd.paged_read(cache, _i32(torch, [0, 1]), -1),
                 lambda: kvd.paged_read(cache, _i32(torch, [0, 1]), 1, dtype=torch.float64), lambda: kvd.paged_read(cache, _i32(torch, [0, 1]).long(), 1),
