@@ -710,9 +710,9 @@ KVD_API kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t 
  * the rows that codes and scales stand for.  Arguments, masks, options, what is skipped
  * or left alone, and the sums in f32 are those of paged_attention.  q is taken to 2^-17
  * of its row's largest value (exactly, if that is within 2^9 of every other: f16 2^6), and
- * the weights, with the scale of V's block, are rounded once, to eight significant bits for
- * bf16 and twelve for f16 (eleven in chunks of more than 16 query rows a KV head) and to
- * 2^-22 of the largest of a tile's 128 rows (2^-27 of the row's in such chunks).
+ * the weights, with the scale of V's block, are rounded to eight significant bits for bf16
+ * and eleven for f16, and to 2^-22 of the largest of a tile's 128 rows (2^-27 of the row's
+ * in chunks of more than 16 query rows a KV head).
  * A row of q that is not finite gives NaN, in that row alone.  n_seq <= 2^20. */
 KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q,
                                       int32_t n_kv, int32_t head_dim, int32_t dtype, const void *k_pages,
