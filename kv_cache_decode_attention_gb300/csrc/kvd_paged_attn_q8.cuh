@@ -12,10 +12,10 @@
 //   t0 + t1 / 16 (+ t2 / 256): eight significant bits for bf16, twelve for f16, down
 //   to 2^-21 (2^-25) of the largest;
 //   p, a weight with the scale of its V block, relative to the largest of its tile,
-//   likewise.
-// So S is exact but for its f32 sums, and the weights are rounded once, to about q's
-// type.  (Converting the codes to 16 bits instead costs 48 KB of shared-memory traffic
-// a tile of 16, which at the rate of HBM leaves no room for the MMAs' own.)
+//   likewise, by way of f16: rounded by 2^-9 + 2^-11 of it at most for bf16, 2^-11 for f16.
+// So S is exact but for its f32 sums, and the weights are rounded to about q's type.
+// (Converting the codes to 16 bits instead costs 48 KB of shared-memory traffic a tile of
+// 16, which at the rate of HBM leaves no room for the MMAs' own.)
 //
 // An item is one (request, KV head, run of tokens): kQrRows query rows (token, head of
 // the group) at most.  Items are cut into tiles of 128 rows and every CTA gets the
@@ -46,7 +46,9 @@
 // Measured and not taken: 16 columns for single tokens (decode 253 us when eight took
 // 211); three CTAs of two stages for 16 bf16 columns (drafts 80 us against 70: registers
 // spill); a reduction by instruction for each column's maximum (five instructions more a
-// column); joining CTAs of 512 threads (decode 203 against 194).
+// column); joining CTAs of 512 threads (decode 203 against 194); zeros for V's rows before
+// a window, as for those behind the last (decode 203 against 193, without any window): rows
+// that a request holds have to be finite.
 #pragma once
 
 #include <cfloat>
@@ -360,9 +362,9 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t *t) {
         y = (y - v.y) * 16.0f;
     }
 }
-// The same of two weights up to 256, by way of f16: its eleven bits hold what the terms
-// keep, and what they leave of one another is exact in it.  Six instructions for two
-// terms, ten for three, where f32 takes nine and seventeen.
+// The same of two weights up to 256, by way of f16: three terms hold its eleven bits, two
+// round them to nine, and what a term leaves to the next is exact in it.  Six instructions
+// for two terms, ten for three, where f32 takes nine and seventeen.
 template <int TERMS>
 __device__ __forceinline__ void split2_weights(float x, float y, uint32_t *t) {
     __half2 v = __floats2half2_rn(x, y);
