@@ -32,7 +32,13 @@
 // Barriers, all of one phase a tile (K, V: a ring of kStages): s_full, s_free (S is in
 // registers), p_ready (P is in shared memory, O of the tile before in registers),
 // o_full.  No warp can be two phases ahead of one that waits: S(i + 1) waits for
-// s_free(i), P(i + 1) for o_full(i).
+// s_free(i), P(i + 1) for o_full(i).  The softmax warps meet once an item, a tile and an
+// item's end, and at their end, at a named barrier, whose wait knows no limit.  So all four
+// come to every meeting, one whose wait was given up to the rest of its item's without doing
+// anything else; it says so at the next item's first, where all leave.
+// (tests/test_paged8_protocol_cpu.py has warps and barriers as a model.  Meetings at an
+// mbarrier with a bounded wait cost a decode step 2%, 256 requests of 300 rows 10%; a reduction at
+// every one of them 0 and 4%.)
 //
 // Measured (GPU time on one GB300; a copy runs at 6.77 TB/s): one new row for each of 64
 // requests of up to 16384 rows, 32 heads over 8, 193 us, 6.1 TB/s, f16 214; 4 of 131072
@@ -326,6 +332,17 @@ __device__ __forceinline__ void qr_arrive(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) pa_arrive(bar);
 }
 __device__ __forceinline__ void qr_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same; whether all four had what they waited for.
+__device__ __forceinline__ bool qr_meet(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(uint32_t(ok))
+        : "memory");
+    return all != 0;
+}
 
 // The largest of a warp's values of each of R columns; lane l gets that of column
 // l % R.  Lanes pass on half of the columns that they still have, R - 1 exchanges in all,
@@ -609,7 +626,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
             const bool has_chan = HD == 128 || lane < 16;
             const int32_t per_256 = (256 + a.group - 1) / a.group;  // exact for 16 columns
             uint32_t g = 0;
-            bool ok = true;
+            bool ok = true, met = true;
             for (uint32_t at = 0;; ++at) {
                 ok = qr_wait(sh, &sh.job_full[at % kQrJobs], at / kQrJobs & 1);
                 if (!ok) break;
@@ -672,7 +689,8 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     if (part == 0) sh.col[r] = odd != 0 ? __int_as_float(0x7fc00000) : a.mul * __uint_as_float(uint32_t(127 - e) << 23);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     qr_arrive(&sh.q_ready);
-                    qr_sync();
+                    met = qr_meet(true);
+                    if (!met) break;
                 }
 
                 float acc[R], sum[R];
@@ -694,7 +712,9 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         acc[c + 1] = fmaf(acc[c + 1], f.z, joined<kTerms, R>(o, c + 1) * f.w);
                     }
                 };
+                int32_t owed = 0;  // meetings to come of this item, before a wait
                 for (int32_t i = 0; i < job.n; ++i, ++g) {
+                    owed = job.n - i + 1;
                     ok = qr_wait(sh, &sh.sc_full[g % S::kScales], g / S::kScales & 1);
                     if (!ok) break;
                     const float4 sc = sh.scale[g % S::kScales][row >> a.page_log2];
@@ -734,6 +754,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         if (lane < R) sh.top[i & 1][lane][warp] = t;
                     }
                     qr_sync();
+                    owed = job.n - i;
                     {
                         const int c = lane % R;
                         const float4 t = *reinterpret_cast<const float4 *>(sh.top[i & 1][c]);
@@ -791,13 +812,18 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                     qr_arrive(&sh.p_ready);
                     if (i > 0) fold(o, uint32_t(i - 1));
                 }
-                if (!ok) break;
-                {
+                if (ok) {
                     float o[S::kN];
+                    owed = 1;
                     ok = qr_wait(sh, &sh.o_full, (g - 1) & 1);
-                    if (!ok) break;
-                    take(o);
-                    fold(o, uint32_t(job.n - 1));
+                    if (ok) {
+                        take(o);
+                        fold(o, uint32_t(job.n - 1));
+                    }
+                }
+                if (!ok) {
+                    for (; owed > 0; --owed) qr_sync();
+                    break;
                 }
                 // the sums over the tile's rows, by way of the maxima's buffer that is not the last tile's
                 float(*const sums)[4] = sh.top[job.n & 1];
@@ -833,6 +859,8 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 }
                 // (the next item's sums are written behind qr_sync calls that every warp passes after this)
             }
+            // behind the last item, or with a wait given up: the others are on their way to this meeting
+            if (met) qr_meet(ok);
         }
     }
     tc_before();
