@@ -617,6 +617,9 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 if (!ok) break;
                 g += n;
             }
+            // nobody waits for the last v_empty, but the block must not end before it has come
+            tc_commit(&sh.drain);
+            if (!mbar_wait_bounded(&sh.drain, 0, 500000000ull)) *static_cast<volatile int *>(&sh.stop) = 1;
         } else {
             // -------------------------------------------------------- softmax and sums
             const int row = threadIdx.x;                 // of the tile
@@ -867,12 +870,8 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
     __syncthreads();
     tc_after();
     if (*static_cast<volatile int *>(&sh.stop) != 0) {
-        // given up: nothing may be in flight into this CTA's memory
+        // given up: no copy may be in flight into this CTA's memory
         if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
-        if (warp == 5) {
-            tc_commit(&sh.drain);
-            mbar_wait_bounded(&sh.drain, 0, 500000000ull);
-        }
         if (warp == 4)
             for (uint32_t i = 0; i < uint32_t(S::kStages); ++i) {
                 if (k_loads > i) mbar_wait_bounded(&sh.k_full[(k_loads - 1 - i) % S::kStages], (k_loads - 1 - i) / S::kStages & 1, 500000000ull);

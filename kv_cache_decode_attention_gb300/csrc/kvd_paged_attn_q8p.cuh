@@ -330,6 +330,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     if (!ok) break;
                     g += n;
                 }
+                // nobody waits for the last v_empty, but the block must not end before it has come
+                tc_commit(&sh.drain[d]);
+                if (!mbar_wait_bounded(&sh.drain[d], 0, 500000000ull)) *stop = 1;
             } else if (warp >= 10 && warp < 14) {
                 // ---------------------------------------------------- V to f16
                 // A lane takes 16 codes; eight neighbouring lanes those of eight rows, whose
@@ -720,13 +723,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
     __syncthreads();
     tc_after();
     if (*stop != 0) {
-        // given up: nothing may be in flight into this CTA's memory
+        // given up: no copy may be in flight into this CTA's memory
         if (threadIdx.x == 0) set_error(a.err, kErrTimeout);
-        if (warp == 9 || warp == 14) {
-            uint64_t *drain = &sh.drain[warp == 9 ? 0 : 1];
-            tc_commit(drain);
-            mbar_wait_bounded(drain, 0, 500000000ull);
-        }
         if (warp == 8) {
             for (uint32_t i = 0; i < uint32_t(S::kStages); ++i)
                 if (k_loads > i) mbar_wait_bounded(&sh.k_full[(k_loads - 1 - i) % S::kStages], (k_loads - 1 - i) / S::kStages & 1, 500000000ull);

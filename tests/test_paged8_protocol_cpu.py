@@ -15,6 +15,8 @@ from test_paged_protocol_cpu import JOBS, Bar
 
 
 class Base:
+    drains = True  # warps that issue MMAs wait for their last commits
+
     def __init__(self, jobs, rng):
         self.jobs, self.rng, self.slot, self.up = jobs, rng, [None] * JOBS, False
         self.job_full = self.bars("job_full", JOBS, 1)
@@ -92,9 +94,8 @@ class Base:
                 go(k[5:], True)
             else:
                 go(k)
-        if moves is None:
-            return
-        self.drain()
+        if moves is not None:
+            self.drain()
         assert not any(self.later.values()), "still under way at the end: %s" % {k: len(v) for k, v in self.later.items() if v}
 
     def drain(self):
@@ -123,6 +124,7 @@ class Few(Base):
         self.sc_full = self.bars("sc_full", self.scales, 1)
         self.s_full, self.s_free, self.p_ready, self.o_full, self.q_ready, self.meet = (
             Bar(n, c) for n, c in (("s_full", 1), ("s_free", 4), ("p_ready", 4), ("o_full", 1), ("q_ready", 4), ("meet", 4)))
+        self.drained = Bar("drained", 1)
         self.later = {"K": [], "V": [], "MMA": []}
         self.k, self.v, self.sc = [None] * stages, [None] * stages, [None] * self.scales
         self.q, self.p, self.top, self.s, self.o = [None] * 4, [None] * 4, [[None] * 4, [None] * 4], None, None
@@ -214,7 +216,10 @@ class Few(Base):
                 commit(self.v_empty[slot].arrive)
             g += n
 
-        return self.over_jobs(body)
+        yield from self.over_jobs(body)
+        if self.drains:
+            commit(self.drained.arrive)
+            yield self.drained, 0
 
     def softmax(self, w):
         g = met = 0  # tiles, meetings
@@ -311,6 +316,7 @@ class Many(Base):
         self.sc_full = self.bars("sc_full", self.scales, 1)
         self.s_full, self.p_ready, self.o_step = ([self.bars("%s%d" % (n, d), 2, c) for d in range(2)] for n, c in (("s_full", 1), ("p_ready", 4), ("o_step", 1)))
         self.q_ready = self.bars("q_ready", 2, 4)
+        self.drained = self.bars("drained", 2, 1)
         self.later = {"K": [], "C": [], "MMA0": [], "MMA1": []}
         self.k, self.c, self.sc = [None] * self.stages, [None] * self.codes, [None] * self.scales
         self.v = [[None] * 4 for _ in range(self.wide)]
@@ -413,7 +419,10 @@ class Many(Base):
                 mine += 1
             g += n
 
-        return self.over_jobs(body)
+        yield from self.over_jobs(body)
+        if self.drains:
+            commit(self.drained[d].arrive)
+            yield self.drained[d], 0
 
     def convert(self, c):
         g = 0
@@ -526,6 +535,15 @@ def test_the_model_sees_what_a_softmax_warp_owes(mistake):
         for seed in range(1000):
             rng = random.Random(seed)
             Wrong(_jobs(rng, 8), rng.choice([2, 3, 4, 6]), rng).run(int(2 ** rng.uniform(0, 9)))
+
+
+@pytest.mark.parametrize("kind", ["few", "many"])
+def test_the_model_sees_a_last_commit_that_nobody_waits_for(kind):
+    with pytest.raises(AssertionError, match="still under way"):
+        for seed in range(300):
+            run, _ = _make(kind, seed, 5)
+            run.drains = False
+            run.run()
 
 
 @pytest.mark.parametrize("mistake", ["scales too few", "S not let go of", "P before O", "one barrier for both halves"])
