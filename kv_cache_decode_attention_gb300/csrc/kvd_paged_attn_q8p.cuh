@@ -577,7 +577,11 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                                             m0 = max3(m0, x[u + c], x[u + c + 1]);
                                             m1 = max3(m1, x[u + c + 2], x[u + c + 3]);
                                         }
-                                        const float k = f.x * mul, b0 = f.y - base;
+                                        // Never zero, for which what is hidden, -infinity, would be no
+                                        // number: scores are below 2^-100 where this is not their factor.
+                                        float k = f.x * mul;
+                                        k = k < FLT_MIN ? FLT_MIN : k;  // (no number stays none)
+                                        const float b0 = f.y - base;
                                         if constexpr (CAP) {
                                             const float m = fmaxf(m0, m1) * k;
                                             top = fmaxf(top, (m == -INFINITY ? m : pa_tanh_of_any(m) * a.cap) + f.y);

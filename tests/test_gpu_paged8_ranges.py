@@ -1,0 +1,46 @@
+"""Pages of 8-bit codes on the GPU at the ends of what is allowed.  References and tolerances are those of test_gpu_paged8.py; what a test adds to
+them stands beside it.
+"""
+
+import math
+
+import numpy as np
+import pytest
+from test_gpu_paged import _dt, _i32
+from test_gpu_paged8 import LOW, _attend8, _check8, _poisoned8, env  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _plan_of(torch, kvd, cache, new):
+    return kvd.PagedPlan(_i32(torch, [0] + np.cumsum(new).tolist()), cache.seq_len)
+
+
+def _zero_keys(torch, cache, rows, b, page, places):
+    """Pages of request b whose keys are all zero, as the writer leaves them: codes 0, the smallest scale."""
+    for j in places:
+        p, n = int(cache.block_table[b, j]), rows[b][0].shape[0]
+        cache.k.view(torch.uint8)[p, :, : max(0, min(page, n - j * page))] = 0
+        cache.k_scale[p] = LOW
+        rows[b][0][j * page:(j + 1) * page] = 0
+
+
+@pytest.mark.parametrize("size,scale,softcap", [(2.0 ** -100, None, 0.0), (2.0 ** -100, None, 20.0), (1.0, 1e-30, 0.0), (1.0, None, 1e25), (2.0 ** -60, 1e-20, 3.0)])
+@pytest.mark.parametrize("hd,window", [(128, 0), (64, 0), (128, 100)])
+def test_small_scores_over_pages_of_zeros(env, size, scale, softcap, hd, window):  # noqa: F811
+    """Scores times a page's smallest scale leave f32: what is hidden stays hidden, what is seen weighs the same."""
+    torch, kvd = env
+    scale = hd ** -0.5 if scale is None else scale
+    for lens, new in (([70], [3]), ([300], [200]), ([260], [1])):
+        cache, rows = _poisoned8(torch, kvd, lens, 2, hd, 16, 17)
+        last = (lens[0] - 1) // 16
+        _zero_keys(torch, cache, rows, 0, 16, {last, last - 1, last // 2, 1, 10 % (last + 1)})
+        for dt in (torch.bfloat16, torch.float16):
+            if size < 2.0 ** -20 and dt is torch.float16:
+                continue
+            q = (torch.randn(sum(new), 8, hd, device="cuda", generator=torch.Generator(device="cuda").manual_seed(18)) * size).to(dt)
+            out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, new), scale=scale, window=window, softcap=softcap)
+            assert cache.device_error() == 0
+            # (a cap of 1e25 is no cap to scores of this size: its tolerance, 2^-20 of it, would say nothing)
+            want = _attend8(torch, q, *rows[0], lens[0], scale, window, softcap if softcap < 1e10 else 0.0)
+            _check8(torch, out, want, float(cache.v_scale.nan_to_num(0).max()))
