@@ -367,6 +367,11 @@ __device__ __forceinline__ float warp_tops(const float *x) {
     return y[0];
 }
 
+// The factor of raw scores under a cap.  A raw score that is not zero is 2^-26 at least,
+// with which a factor of 2^100 is past every cap's end; infinity would make a number of
+// zero that is none.
+__device__ __forceinline__ float qr_cap_factor(float k) { return k > 1.2676506e30f ? 1.2676506e30f : k; }
+
 // x (two values) as e4m3 terms x = t0 + t1 / 16 (+ t2 / 256), packed in 16 bits each.
 template <int TERMS>
 __device__ __forceinline__ void split2(float x, float y, uint32_t *t) {
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
 #pragma unroll
                         for (int c = 0; c < R; ++c) {
                             const float k = sh.col[c] * sc.x, y = joined<kTerms, R>(s, c);
-                            if (a.cap > 0.0f) x[c] = fmaf(pa_tanh_of_any(y * k), a.cap, sc.y);
+                            if (a.cap > 0.0f) x[c] = fmaf(pa_tanh_of_any(y * qr_cap_factor(k)), a.cap, sc.y);
                             else x[c] = fmaf(y, k, sc.y);
                         }
                     }

@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                                         // number: scores are below 2^-100 where this is not their factor.
                                         float k = f.x * mul;
                                         k = k < FLT_MIN ? FLT_MIN : k;  // (no number stays none)
+                                        if constexpr (CAP) k = qr_cap_factor(k);
                                         const float b0 = f.y - base;
                                         if constexpr (CAP) {
                                             const float m = fmaxf(m0, m1) * k;

@@ -44,3 +44,22 @@ def test_small_scores_over_pages_of_zeros(env, size, scale, softcap, hd, window)
             # (a cap of 1e25 is no cap to scores of this size: its tolerance, 2^-20 of it, would say nothing)
             want = _attend8(torch, q, *rows[0], lens[0], scale, window, softcap if softcap < 1e10 else 0.0)
             _check8(torch, out, want, float(cache.v_scale.nan_to_num(0).max()))
+
+
+def test_caps_below_every_score(env):  # noqa: F811
+    """A cap so small that score / cap leaves f32: weights are all alike, keys of zeros among them."""
+    torch, kvd = env
+    for lens, new in (([400], [3]), ([500], [150])):
+        cache, rows = _poisoned8(torch, kvd, lens, 2, 128, 32, 31)
+        cache.k_scale *= 2.0 ** 30
+        pair = rows[0][0] * 2.0 ** 30, rows[0][1]
+        raw = cache.k.view(torch.uint8)
+        for i in range(3, lens[0], 7):
+            raw[int(cache.block_table[0, i // 32]), :, i % 32] = 0
+            pair[0][i] = 0
+        for dt in (torch.bfloat16, torch.float16):
+            q = torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(32)).to(dt)
+            out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, new), softcap=1e-36)
+            want, size, slack = _attend8(torch, q, *pair, lens[0], 128 ** -0.5, 0, 1e-36)
+            # (a score's own error is that of its tanh, of which 1e-36 is left)
+            _check8(torch, out, (want, size, torch.full_like(slack, 2.0 ** -20)), float(cache.v_scale.nan_to_num(0).max()))
