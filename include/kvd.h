@@ -713,7 +713,9 @@ KVD_API kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t 
  * the weights, with the scale of V's block, are rounded to eight significant bits for bf16
  * and eleven for f16, and to 2^-22 of the largest of a tile's 128 rows (2^-27 of the row's
  * in chunks of more than 16 query rows a KV head).
- * A row of q that is not finite gives NaN, in that row alone.  n_seq <= 2^20. */
+ * A cap that no score below 10^15 before scaling would feel (scale / softcap below
+ * 2^-64) is none.  A row of q that is not finite gives NaN, in that row alone.
+ * n_seq <= 2^20. */
 KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, int64_t n_tokens, int32_t n_q,
                                       int32_t n_kv, int32_t head_dim, int32_t dtype, const void *k_pages,
                                       const void *v_pages, const float *k_scale, const float *v_scale,

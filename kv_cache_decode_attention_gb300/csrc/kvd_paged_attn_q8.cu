@@ -3,7 +3,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -194,9 +193,10 @@ extern "C" kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out,
     const int64_t armed = paged_give_up();
     a.give_up = armed < 0 ? -1 : int32_t(armed >> 32);
     a.give_up_ns = uint32_t(armed);
-    // A cap so far above the scale that their quotient is no normal number (a raw
-    // score would have to pass 10^34 to feel it) is none.
-    const bool cap = softcap > 0.0f && scale / softcap >= FLT_MIN;
+    // A cap that q.k would have to pass 10^15 to feel is none.  The kernels' factor holds
+    // the page's and the row's powers of two, too: with caps up to 16-bit pages' limit (10^34)
+    // it fell below the normal numbers of f32 and took the scores' last bits with it.
+    const bool cap = softcap > 0.0f && scale / softcap >= 5.421010862427522e-20f;  // 2^-64
     a.mul = cap ? float(2.0 * 1.4426950408889634 * double(scale) / softcap) : scale * log2e;
     a.cap = cap ? softcap * log2e : 0.0f;
     const bool bf16 = dtype == KVD_T_BF16;

@@ -46,6 +46,25 @@ def test_small_scores_over_pages_of_zeros(env, size, scale, softcap, hd, window)
             _check8(torch, out, want, float(cache.v_scale.nan_to_num(0).max()))
 
 
+@pytest.mark.parametrize("softcap", [1e15, 1e20, 1e25, 1e33, 1e36, 7e36, 3e38])
+def test_caps_out_of_reach_change_nothing(env, softcap):  # noqa: F811
+    """Scores of some hundreds under caps of any size: right to 2^-19 of themselves, as capped scores are."""
+    torch, kvd = env
+    for lens, new in (([400], [3]), ([500], [150])):
+        for dt in (torch.bfloat16, torch.float16):
+            cache, rows = _poisoned8(torch, kvd, lens, 2, 128, 32, 29)
+            q = (torch.randn(sum(new), 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(30)) * 40).to(dt)
+            scale = 128 ** -0.5 if softcap < 1e38 else 1.0
+            if softcap >= 1e38:
+                q = (q.float() * 128 ** -0.5).to(dt)
+                softcap = 2.3e38  # log2 e times it is still a number
+            out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, new), scale=scale, softcap=softcap)
+            assert cache.device_error() == 0
+            ref, size, slack = _attend8(torch, q, *rows[0], lens[0], scale)
+            top = max(float((q[:, h].double() @ rows[0][0][:, h // 4].T).abs().max()) * scale for h in range(8))
+            _check8(torch, out, (ref, size, slack + 2 * 2.0 ** -19 * top), float(cache.v_scale.nan_to_num(0).max()))
+
+
 def test_caps_below_every_score(env):  # noqa: F811
     """A cap so small that score / cap leaves f32: weights are all alike, keys of zeros among them."""
     torch, kvd = env
