@@ -435,13 +435,14 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 }
                 const int32_t tok = d * tile_tok + rtok;  // of the item
                 const bool valid = rtok < tile_tok && tok < job.count;
-                const int32_t head = job.kv_head * a.group + rhead;
+                const int32_t head = job.kv_head * a.group + rhead, pos = job.first_pos + tok;
                 // q as e4m3 terms; every MMA that read the last item's has been waited for
                 float mul;
                 {
                     uint4 x[HD / 8];
                     const T *mine_q = static_cast<const T *>(a.q) + (int64_t(job.q_row) + tok) * a.q_tok + int64_t(head) * a.q_head;
-                    const uint64_t src = valid ? reinterpret_cast<uint64_t>(mine_q) : 0;
+                    // (a row before its request's start sees nothing, whatever q is there)
+                    const uint64_t src = valid && pos >= 0 ? reinterpret_cast<uint64_t>(mine_q) : 0;
 #pragma unroll
                     for (int k = 0; k < kPieces; ++k) {
                         const int r = k * kRowsAtOnce + lane / kPieces;
@@ -503,7 +504,6 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     tc_before();
                     qr_arrive(&sh.q_ready[d]);
                 }
-                const int32_t pos = job.first_pos + tok;
                 const int64_t lo64 = a.window > 0 ? int64_t(pos) - a.window + 1 : 0;
                 const int32_t lo = lo64 > 0 ? int32_t(lo64) : 0;
                 const bool busy = __any_sync(~0u, valid);

@@ -82,3 +82,21 @@ def test_caps_below_every_score(env):  # noqa: F811
             want, size, slack = _attend8(torch, q, *pair, lens[0], 128 ** -0.5, 0, 1e-36)
             # (a score's own error is that of its tanh, of which 1e-36 is left)
             _check8(torch, out, (want, size, torch.full_like(slack, 2.0 ** -20)), float(cache.v_scale.nan_to_num(0).max()))
+
+
+def test_rows_that_see_nothing_are_zero_whatever_q_is(env):  # noqa: F811
+    """New rows that stand before the start of their request, with infinities and NaN in q."""
+    torch, kvd = env
+    for lens, new in (([3], [5]), ([130], [400]), ([0], [40])):
+        for dt, sinks, softcap in ((torch.bfloat16, False, 0.0), (torch.float16, True, 0.0), (torch.bfloat16, True, 20.0)):
+            cache, rows = _poisoned8(torch, kvd, lens, 2, 128, 16, 37)
+            q = torch.randn(new[0], 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(38)).to(dt)
+            hidden = new[0] - lens[0]
+            q[0, :, 3] = math.nan
+            q[hidden - 1, 2, 77] = math.inf
+            sink = torch.randn(8, device="cuda", generator=torch.Generator(device="cuda").manual_seed(39)) if sinks else None
+            out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, new), sinks=sink, softcap=softcap)
+            assert cache.device_error() == 0 and not out[:hidden].any()
+            if lens[0]:
+                want = _attend8(torch, q[hidden:], *rows[0], lens[0], 128 ** -0.5, 0, softcap, sink)
+                _check8(torch, out[hidden:], want, float(cache.v_scale.nan_to_num(0).max()))
