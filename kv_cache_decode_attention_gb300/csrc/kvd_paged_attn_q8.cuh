@@ -13,6 +13,10 @@
 //   to 2^-21 (2^-25) of the largest;
 //   p, a weight with the scale of its V block, relative to the largest of its tile,
 //   likewise, by way of f16: rounded by 2^-9 + 2^-11 of it at most for bf16, 2^-11 for f16.
+// References are those of weights with their scales, the sum that of weights alone, and a
+// weight that is nothing beside another's scale still counts there.  So once a part has met
+// a scale of V past kScaleFar its weights are summed from the scores once more, and the
+// factor between two references reaches the sum as two halves.
 // So S is exact but for its f32 sums, and the weights are rounded to about q's type.
 // (Converting the codes to 16 bits instead costs 48 KB of shared-memory traffic a tile of
 // 16, which at the rate of HBM leaves no room for the MMAs' own.)
@@ -70,6 +74,9 @@ constexpr int kQrRows = 16;      // query rows of an item
 constexpr int kQrThreads = 192;
 constexpr int kQrMaxCtas = 152 * 3;
 constexpr int kQrJobs = 4;
+// With scales of V up to here (2^8; f16 needs no larger ones) a weight that is lost beside
+// another's scale is below 2^-54 of that one's.
+constexpr float kScaleFar = 256.0f;
 constexpr int kQrMaxSeq = 1 << 20;
 
 // A cut item as qr_join_kernel finds it; n = 0: none.
@@ -300,7 +307,7 @@ struct QrShared {
     uint32_t tmem;
     int stop;
     uint64_t began;
-    float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's
+    float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's; in all alike: far ones since the part began
     float top[2][S::kRows][4];     // of a tile's columns, by warp
     float ref[4][S::kRows];        // the tile's reference less 8, by warp
     float2 fold[2][4][S::kRows];   // factors of old and new sums, by warp
@@ -526,6 +533,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 const int32_t per_block = 32 / ppt;  // tiles
                 int32_t block_pages = lookup(0), next_pages = lookup(1), v_page = -1;
                 float2 block_scales = scales(block_pages), next_scales = make_float2(1.0f, 1.0f);
+                bool far = false;
                 // K runs a tile ahead of V
                 for (int32_t t = 0; ok && t <= n; ++t) {
                     int32_t page = -1;
@@ -548,12 +556,14 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
                         if (turn > 0) ok = qr_wait(sh, &sh.k_empty[slot], (turn & 1) ^ 1);
                         if (!ok) break;
+                        // (K first: the scales may still be on their way)
+                        load(&a.k, smem + S::kK + slot * S::kTileBytes, page, &sh.k_full[slot]);
+                        far = far || __any_sync(~0u, vs > kScaleFar && vs <= kScaleHigh);
                         if (lane < ppt) {
                             const float v = scale_of(vs, a.err);
-                            sh.scale[sc][lane] = make_float4(scale_of(ks, a.err), log2f(v), 1.0f / v, 0.0f);
+                            sh.scale[sc][lane] = make_float4(scale_of(ks, a.err), log2f(v), 1.0f / v, far ? 1.0f : 0.0f);
                         }
                         qr_arrive(&sh.sc_full[sc]);
-                        load(&a.k, smem + S::kK + slot * S::kTileBytes, page, &sh.k_full[slot]);
                         ++k_loads;
                     }
                     if (t > 0) {
@@ -769,6 +779,14 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         const float ref = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), now = fmaxf(m_run, ref);
                         const float base = now == -INFINITY ? 0.0f : now;
                         // weights are held 2^8 higher
+                        if (sc.w != 0.0f) {
+                            const float half = ex2(0.5f * (m_run - base));
+#pragma unroll
+                            for (int e = 0; e < R; ++e) {
+                                const float f = __shfl_sync(~0u, half, e);
+                                sum[e] = fmaf(sum[e] * f, f, ex2(x[e] - sc.y - __shfl_sync(~0u, base, e)));
+                            }
+                        }
                         if (lane < R) {
                             sh.ref[warp][c] = ref == -INFINITY ? 0.0f : ref - 8.0f;
                             sh.fold[i & 1][warp][c] = make_float2(ex2(m_run - base), ex2(ref - base) * 0.00390625f);
@@ -782,8 +800,10 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                         const float2 ref = *reinterpret_cast<const float2 *>(&sh.ref[warp][c]);
                         const float4 f = *reinterpret_cast<const float4 *>(&sh.fold[i & 1][warp][c]);
                         const float w0 = ex2(x[c] - ref.x), w1 = ex2(x[c + 1] - ref.y);
-                        sum[c] = fmaf(sum[c], f.x, w0 * (sc.z * f.y));
-                        sum[c + 1] = fmaf(sum[c + 1], f.z, w1 * (sc.z * f.w));
+                        if (sc.w == 0.0f) {
+                            sum[c] = fmaf(sum[c], f.x, w0 * (sc.z * f.y));
+                            sum[c + 1] = fmaf(sum[c + 1], f.z, w1 * (sc.z * f.w));
+                        }
                         split2_weights<kTerms>(w0, w1, p[c / 2]);
                     }
                     // rows of V that nobody holds: their weights are zero, but zero times NaN is not
@@ -844,26 +864,31 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 }
                 qr_sync();
                 const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
+                // what column lane % R is multiplied by
+                float f;
+                {
+                    const int c = lane % R;
+                    const float4 s4 = *reinterpret_cast<const float4 *>(sums[c]);
+                    float s = (s4.x + s4.y) + (s4.z + s4.w);
+                    f = 1.0f;
+                    if (job.whole != 0 && a.sinks != nullptr && c < live && m_run != -INFINITY) {
+                        const float sink = a.sinks[job.kv_head * a.group + c % a.group] * 1.4426950408889634f, all = fmaxf(m_run, sink);
+                        f = ex2(m_run - all);
+                        s = s * f + ex2(sink - all);
+                    }
+                    f *= s == 0.0f ? 0.0f : rcp(s);
+                    // Of a piece the outputs over the sum, whose logarithm joins the reference: pieces meet as weights, without V's
+                    // scales.  (By approximate instructions, whose errors are 2^-22 of a weight: what rcp is off by stays in s * f.)
+                    if (job.whole == 0 && row < live) a.part_ml[slot * a.part_rows + c] = make_float2(s == 0.0f ? -INFINITY : m_run + __log2f(s), s * f);
+                }
 #pragma unroll
                 for (int c = 0; c < R; ++c) {
                     if (c >= live) break;
-                    const float4 s4 = *reinterpret_cast<const float4 *>(sums[c]);
-                    float s = (s4.x + s4.y) + (s4.z + s4.w);
-                    const float m = __shfl_sync(~0u, m_run, c);
-                    if (job.whole == 0) {
-                        if (row == 0) a.part_ml[slot * a.part_rows + c] = make_float2(m, s);
-                        if (has_chan) a.part_o[(slot * a.part_rows + c) * HD + chan] = acc[c];
-                        continue;
-                    }
+                    const float y = acc[c] * __shfl_sync(~0u, f, c);
+                    if (!has_chan) continue;
                     const int32_t tok = c / a.group, head = job.kv_head * a.group + c - tok * a.group;
-                    float f = 1.0f;
-                    if (a.sinks != nullptr && m != -INFINITY) {
-                        const float sink = a.sinks[head] * 1.4426950408889634f, all = fmaxf(m, sink);
-                        f = ex2(m - all);
-                        s = s * f + ex2(sink - all);
-                    }
-                    f *= s == 0.0f ? 0.0f : 1.0f / s;
-                    if (has_chan) static_cast<T *>(a.out)[(int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head + chan] = from_f32<T>(acc[c] * f);
+                    if (job.whole == 0) a.part_o[(slot * a.part_rows + c) * HD + chan] = y;
+                    else static_cast<T *>(a.out)[(int64_t(job.q_row) + tok) * a.out_tok + int64_t(head) * a.out_head + chan] = from_f32<T>(y);
                 }
                 // (the next item's sums are written behind qr_sync calls that every warp passes after this)
             }

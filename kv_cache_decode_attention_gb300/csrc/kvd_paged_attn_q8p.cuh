@@ -10,9 +10,13 @@
 //               multiplies the codes of K as they lie in the pages: two products at
 //               twice the rate of 16 bits, from half the bytes.  Eight significant bits
 //               of bf16 are two times four; 2^-17 of the row's largest is left out.
-//   O += P V    kind::f16.  P in f16, whatever q's type, with the scale of V's block
-//               (relative to the row's largest such weight) in it; V's codes become f16,
-//               exactly, by four warps between the copy and the MMA.  P in e4m3 terms
+//   O += P V    kind::f16.  V's codes become f16 by four warps between the copy and the
+//               MMA, times their block's power of two over the largest that the part of the
+//               item has met: exactly, down to 2^-31 of that one's codes (to within 2^-24 of
+//               one below).  P in f16, whatever q's type, with what is left of the block's
+//               scale, a number in [1, 2), in it.  So the softmax's references and sums know
+//               of V's scales only that; a part that meets a larger one rescales O, as
+//               for a reference that grew.  P in e4m3 terms
 //               would do without, but a sum over a whole prompt meets weights far below
 //               2^-17 of the largest, and five instructions a weight cost the softmax
 //               warps more than the conversion, of which 256 rows share one.
@@ -57,6 +61,7 @@ constexpr int kQpCtas = 152;
 constexpr int kQpRegs = 128, kQpSoftRegs = 184, kQpLoadRegs = 72;
 static_assert(2 * kQpSoftRegs + 2 * kQpLoadRegs <= 4 * kQpRegs, "setmaxnreg shares");
 constexpr int kQpMaxRows = 2 * kQrTile;
+constexpr int kVUp = 7;  // codes, 448 at most, times 2^kVUp are numbers of f16
 constexpr float kTanh1 = float(kPaTanh[0]), kTanh2 = float(kPaTanh[1]), kTanh3 = float(kPaTanh[2]), kTanh4 = float(kPaTanh[3]);
 
 template <int HD, bool BF16>
@@ -82,7 +87,8 @@ struct QpShared {
     uint32_t tmem;
     int stop, steps;  // the watch: give up; changes with every tile that is loaded
     uint64_t all_done;
-    float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's
+    float4 scale[S::kScales][8];  // of a tile's pages: K's scale; V's over its power of two, m: log2 m, 1 / m; the largest power's exponent
+    uint32_t v_up[S::kScales][8];  // what V's codes are multiplied by, f16 twice
 };
 
 template <int HD, bool BF16, bool CAP>
@@ -214,6 +220,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     const int32_t per_block = 32 / ppt;  // tiles
                     int32_t block_pages = lookup(0), next_pages = lookup(1), v_page = -1;
                     float2 block_scales = scales(block_pages), next_scales = make_float2(1.0f, 1.0f);
+                    int32_t most = -64;  // exponent of V's largest scale so far
                     // K runs a tile ahead of V
                     for (int32_t t = 0; ok && t <= n; ++t) {
                         int32_t page = -1;
@@ -231,12 +238,18 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                             const uint32_t slot = k_loads % S::kStages, turn = k_loads / S::kStages, sc = k_loads % S::kScales;
                             if (turn > 0) ok = pa_wait(&sh.k_empty[slot], (turn & 1) ^ 1, stop);
                             if (!ok) break;
+                            // (K first: the scales may still be on their way)
+                            load(&a.k, smem + S::kK + slot * S::kCodeBytes, page, &sh.k_full[slot]);
+                            const uint32_t v = __float_as_uint(scale_ok(vs) ? vs : scale_of(vs, lane < ppt ? a.err : nullptr));
+                            const int32_t e = page >= 0 ? int32_t(v >> 23) - 127 : -64;
+                            most = max(most, __reduce_max_sync(~0u, e));
                             if (lane < ppt) {
-                                const float v = scale_of(vs, a.err);
-                                sh.scale[sc][lane] = make_float4(scale_of(ks, a.err), log2f(v), 1.0f / v, 0.0f);
+                                const float m = __uint_as_float((v & 0x7fffffu) | 0x3f800000u);
+                                sh.scale[sc][lane] = make_float4(scale_of(ks, a.err), log2f(m), 1.0f / m, float(most));
+                                const int32_t up = e - most + kVUp;  // f16's normal numbers begin at 2^-14, its others at 2^-24
+                                sh.v_up[sc][lane] = 0x10001u * (up >= -14 ? uint32_t(up + 15) << 10 : up >= -24 ? 1u << (up + 24) : 0u);
                             }
                             qr_arrive(&sh.sc_full[sc]);
-                            load(&a.k, smem + S::kK + slot * S::kCodeBytes, page, &sh.k_full[slot]);
                             ++k_loads;
                             if (lane == 0) *static_cast<volatile int *>(&sh.steps) = int(k_loads);
                     }
@@ -349,6 +362,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     for (int32_t i = 0; i < n; ++i, ++g) {
                         const uint32_t from = g % S::kCodes, to = g % S::kWide;
                         ok = pa_wait(&sh.c_full[from], g / S::kCodes & 1, stop);
+                        uint32_t up[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) up[k] = sh.v_up[g % S::kScales][(r0 + k * 8) >> a.page_log2];
                         if (ok && g >= uint32_t(S::kWide)) ok = pa_wait(&sh.v_empty[to], (g / S::kWide & 1) ^ 1, stop);
                         if (!ok) break;
                         const uint32_t src = smem + S::kC + from * S::kCodeBytes, dst = smem + S::kV + to * S::kWideBytes;
@@ -364,8 +380,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                             uint32_t x[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[e / 2] >> (16 * (e % 2))), __NV_E4M3);
-                                x[e] = uint32_t(v.x) | uint32_t(v.y) << 16;
+                                const __half2 v = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[e / 2] >> (16 * (e % 2))), __NV_E4M3));
+                                const __half2 y = __hmul2(v, *reinterpret_cast<const __half2 *>(&up[k % 4]));
+                                x[e] = *reinterpret_cast<const uint32_t *>(&y);
                             }
                             // channel 16 c of a row lies in half c / 4, 16-byte piece 2 (c % 4)
                             const uint32_t to16 = dst + (c / 4) * (kQrTile * 128) + r * 128;
@@ -509,6 +526,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                 const bool busy = __any_sync(~0u, valid);
                 int32_t key0 = job.tile0 * kQrTile;
                 float ref = -INFINITY;  // reference, log2 units, less kLift
+                float unit = 0.0f;      // O's: 2^(unit - kVUp)
                 float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll 1
                 for (int32_t i = 0; i < 2 * job.n; ++i, ++mine, key0 += 64) {
@@ -519,6 +537,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     if (!ok) break;
                     if (busy) {
                         const float4 *sc = sh.scale[tile % S::kScales];
+                        const float most = sc[0].w;
+                        if (i == 0) unit = most;
                         const uint32_t t_h = t_s + b * 64;
                         const int col0 = b * 64;
                         tc_after();
@@ -623,7 +643,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                                 });
                             }
                             top = valid ? top - kLift : -INFINITY;
-                            if (!__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY))) {
+                            if (!__any_sync(~0u, top > ref + kSlack || (ref == -INFINITY && top > -INFINITY) || unit != most)) {
                                 sum2 = sums;
                                 break;
                             }
@@ -634,9 +654,10 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                                 ok = pa_wait(&sh.o_step[d][b ^ 1], (mine - 1) >> 1 & 1, stop);
                                 if (!ok) break;
                                 tc_after();
-                                const float f = now == -INFINITY ? 1.0f : ex2(ref - now);
+                                float f = now == -INFINITY ? 1.0f : ex2(ref - now);
                                 sum2.x *= f;
                                 sum2.y *= f;
+                                f *= ex2(unit - most);
 #pragma unroll 1
                                 for (int c = 0; c < HD; c += 32) {
                                     float o[32];
@@ -648,6 +669,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                                 }
                             }
                             ref = now;
+                            unit = most;
                         }
                         if (!ok) break;
                         tc_wait_st();
@@ -665,6 +687,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                     const float sum = sum2.x + sum2.y;
                     const bool whole = job.whole != 0;
                     float f = 1.0f;
+                    const float to_v = __uint_as_float(uint32_t(127 - kVUp + int32_t(unit)) << 23);
                     if (whole) {
                         float s = sum;
                         if (a.sinks != nullptr && valid && ref != -INFINITY) {
@@ -675,6 +698,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         }
                         f *= s == 0.0f ? 0.0f : 1.0f / s;
                     }
+                    f *= to_v;
                     const int64_t slot = int64_t(blockIdx.x) * 2 + job.head;
                     const int32_t prow = d * tile_tok * a.group + row;
                     if (!whole && valid) a.part_ml[slot * a.part_rows + prow] = make_float2(ref, sum);
@@ -709,8 +733,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qp_kernel(const __grid_constant
                         } else {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(row, (c + e) % (HD / 2) / 4)), "f"(y[e]), "f"(y[e + 1]), "f"(y[e + 2]),
-                                             "f"(y[e + 3])
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(row, (c + e) % (HD / 2) / 4)), "f"(y[e] * f), "f"(y[e + 1] * f),
+                                             "f"(y[e + 2] * f), "f"(y[e + 3] * f)
                                              : "memory");
                             if ((c + 32) % (HD / 2) == 0) send((c + 32 - HD / 2) * 4);
                         }

@@ -46,6 +46,37 @@ def test_small_scores_over_pages_of_zeros(env, size, scale, softcap, hd, window)
             _check8(torch, out, want, float(cache.v_scale.nan_to_num(0).max()))
 
 
+PATTERNS = {
+    "small first": lambda i, n: -64 if 2 * i < n else 64,
+    "large first": lambda i, n: 64 if 2 * i < n else -64,
+    "in turn": lambda i, n: 64 if i % 2 else -64,
+    "steps": lambda i, n: (-64, 0, 64, 0, -30, 33)[i % 6],
+    "one large": lambda i, n: 64 if i == n // 3 else -64,
+}
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("pattern", list(PATTERNS))
+@pytest.mark.parametrize("hd,lens,new", [(128, 300, 1), (64, 300, 3), (128, 9000, 1), (64, 20011, 2), (128, 700, 200), (64, 9000, 300), (128, 3000, 64)])
+def test_scales_of_v_at_both_ends_of_their_range(env, hd, lens, new, pattern, sinks):  # noqa: F811
+    """A weight counts in the sum whatever scale its row of V has: scales 2^-64 and 2^64, in tiles, inside tiles and in pieces of one request."""
+    torch, kvd = env
+    page, pages = 16, -(-lens // 16)
+    cache, rows = _poisoned8(torch, kvd, [lens], 2, hd, page, 23)
+    for i in range(pages):
+        p = int(cache.block_table[0, i])
+        to = 2.0 ** PATTERNS[pattern](i, pages)
+        rows[0][1][i * page:(i + 1) * page] *= (to / cache.v_scale[p].double())[None, :, None]
+        cache.v_scale[p] = to
+    g = torch.Generator(device="cuda").manual_seed(24)
+    sink = torch.randn(8, generator=g, device="cuda") * 3 + math.log(lens) if sinks else None
+    for size, softcap in ((0.0, 0.0), (1.5, 0.0), (4.0, 6.0)):
+        q = (torch.randn(new, 8, hd, generator=g, device="cuda") * size).bfloat16()
+        out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, [new]), softcap=softcap, sinks=sink)
+        assert cache.device_error() == 0
+        _check8(torch, out, _attend8(torch, q, *rows[0], lens, hd ** -0.5, 0, softcap, sink), 2.0 ** 64)
+
+
 @pytest.mark.parametrize("softcap", [1e15, 1e20, 1e25, 1e33, 1e36, 7e36, 3e38])
 def test_caps_out_of_reach_change_nothing(env, softcap):  # noqa: F811
     """Scores of some hundreds under caps of any size: right to 2^-19 of themselves, as capped scores are."""

@@ -434,9 +434,9 @@ class Many(Base):
                 yield self.c_full[a], g // self.codes
                 if g >= self.wide:
                     yield self.v_empty[to], g // self.wide - 1
-                self.expect(self.c[a] == g)
+                self.expect(self.c[a] == g and self.sc[g % self.scales] == g)
                 yield None
-                self.expect(self.c[a] == g)
+                self.expect(self.c[a] == g and self.sc[g % self.scales] == g)
                 self.v[to][c] = g
                 self.c_empty[a].arrive()
                 self.v_full[to].arrive()
