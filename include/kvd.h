@@ -670,7 +670,9 @@ KVD_API kvd_status paged_attention(const kvd_rows *q, const kvd_rows *out, int64
  * the codes standing before its rows to it, each rounded to nearest even (exact
  * where the old scale was a power of two and the result is no subnormal of e4m3).  A
  * scale in the block that is larger already stays.  Codes are x / s rounded to
- * nearest even, +-448 at most (as infinities become); a NaN stays one.
+ * nearest even, +-448 at most (as infinities become); a NaN stays one.  (Beside a
+ * standing scale that is no power of two, quotients and products are rounded to f32
+ * before they become codes.)
  *   in_dtype  of q, k and v: f32, f16 or bf16;
  *   q_dtype   of q_out: f16 or bf16, and in_dtype's unless that is f32 (not read
  *             without q);

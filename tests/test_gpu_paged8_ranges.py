@@ -131,3 +131,39 @@ def test_rows_that_see_nothing_are_zero_whatever_q_is(env):  # noqa: F811
             if lens[0]:
                 want = _attend8(torch, q[hidden:], *rows[0], lens[0], 128 ** -0.5, 0, softcap, sink)
                 _check8(torch, out[hidden:], want, float(cache.v_scale.nan_to_num(0).max()))
+
+
+def _rounded(x, bits):
+    """f64 rounded to so many significant bits, to nearest even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
+
+
+@pytest.mark.parametrize("to,bits", [("bf16", 8), ("f16", 11), ("f32", 24)])
+def test_odd_scales_are_read_with_one_rounding(env, to, bits):  # noqa: F811
+    """code * scale just beside the middle of two numbers of the type, where f32 already rounds to the middle: a second rounding would go to the even one."""
+    torch, kvd = env
+    scales, b = [], min(bits, 11)
+    for c in (9, 11, 13, 15):  # significands of codes
+        for k in range(1 << (b - 1), 1 << b, 1 if b == 8 else 11):
+            middle = (2 * k + 1) << (27 - b)  # 28 bits, of which f32 keeps 24
+            m = round(middle / c)
+            off = c * m - middle
+            if (1 << 23) <= m < (1 << 24) and off != 0 and (off > 0) == (k % 2 == 0):
+                scales.append(m * 2.0 ** -24)
+    assert len(scales) >= 20
+    scales = np.array(scales[:200])
+    n = len(scales)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(4, 64).repeat(n, 4, 1).view(n, 1, 16, 64)
+    codes[(codes & 127) == 127] = 0
+    one = torch.from_numpy(scales).float().cuda().view(n, 1)
+    cache = kvd.PagedKvCache.of(codes.view(torch.float8_e4m3fn), codes.clone().view(torch.float8_e4m3fn), torch.arange(n, dtype=torch.int32, device="cuda").view(1, n),
+                                _i32(torch, [16 * n]), k_scale=one, v_scale=one.clone())
+    got = kvd.paged_read(cache, _i32(torch, [0, 16 * n]), 16 * n, dtype=_dt(torch, to))
+    values = codes.view(torch.float8_e4m3fn).double().cpu().numpy().reshape(n, 16, 64)
+    exact = values * scales[:, None, None]
+    twice = _rounded(exact.astype(np.float32).astype(np.float64), bits)
+    want = _rounded(exact, bits)
+    assert to == "f32" or (twice != want).sum() >= n // 2  # what is tested happens
+    for x in got:
+        assert np.array_equal(x.double().cpu().numpy().reshape(n, 16, 64), want)
