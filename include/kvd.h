@@ -735,7 +735,10 @@ KVD_API kvd_status paged_attention_q8(const kvd_rows *q, const kvd_rows *out, in
  * 10^9) nanoseconds after it began, if it is not done by then: as after the two
  * seconds without a step that it has otherwise, every wait of the block ends, bit 0
  * of the error word is set, the rows it had to do are undefined, and the kernel
- * exits normally.  cta < 0 disarms.  Process-wide. */
+ * exits normally.  (A block that has loaded its last rows and waits for nothing more
+ * ends its work instead.  Launches of paged_attention_q8 for requests of few rows have
+ * more than 152 blocks: blocks cta, cta + 152 and cta + 304 give up.)  cta < 0
+ * disarms.  Process-wide. */
 KVD_API kvd_status kvd_test_give_up(int32_t cta, int64_t after_ns);
 
 /* The device error word of the paged calls (see kvd_layer_device_error), after the

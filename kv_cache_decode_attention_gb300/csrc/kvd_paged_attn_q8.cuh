@@ -101,7 +101,7 @@ struct QrArgs {
     int32_t ctas, n_seq, n_tokens, n_kv, group, run, extra, max_pages, n_pages, page_log2, pool_rows;
     int64_t more, most;  // requests with more than `more` and at most `most` query rows a KV head are this launch's
     int32_t part_rows;
-    int32_t give_up;  // for tests: the CTA whose waits end so many ns after it began, or -1
+    int32_t give_up;  // for tests: the CTA (of qr_kernel every 152nd) whose waits end so many ns after it began, or -1
     uint32_t give_up_ns;
     float mul;        // scale * log2 e; with a cap 2 * scale * log2 e / softcap
     float cap;        // softcap * log2 e, or 0
@@ -306,7 +306,7 @@ struct QrShared {
     int64_t warp_sums[kQrThreads / 32];
     uint32_t tmem;
     int stop;
-    uint64_t began;
+    uint64_t deadline;  // for tests: when every wait ends
     float4 scale[S::kScales][8];  // of a tile's pages: K's scale, log2 of V's, 1 / V's; in all alike: far ones since the part began
     float top[2][S::kRows][4];     // of a tile's columns, by warp
     float ref[4][S::kRows];        // the tile's reference less 8, by warp
@@ -314,15 +314,20 @@ struct QrShared {
     float col[S::kRows];
 };
 
-// Waits end after two seconds, or once another wait of the CTA has, or the loading warp
-// at a test's wish: nothing here waits for more than a tile's copies and MMAs.
+// Whether a test wants this CTA given up: one in 152 has the number that it names.
+__device__ __forceinline__ bool qr_gives_up(const QrArgs &a) { return a.give_up == int32_t(blockIdx.x) % 152; }
+
+// Waits end after two seconds, or once another wait of the CTA has, or at a test's wish,
+// which the loading warp sees with every tile, too: nothing here waits for more than a
+// tile's copies and MMAs.
 template <typename SH>
 static __device__ __noinline__ bool qr_wait_long(SH &sh, uint64_t *bar, uint32_t parity) {
     volatile int *stop = &sh.stop;
     const uint64_t since = global_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (*stop != 0) return false;
-        if (global_ns() - since >= 2000000000ull) {
+        const uint64_t now = global_ns();
+        if (now - since >= 2000000000ull || now >= sh.deadline) {
             *stop = 1;
             return false;
         }
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.stop = 0;
-        sh.began = global_ns();
+        sh.deadline = qr_gives_up(a) ? global_ns() + a.give_up_ns : ~0ull;
     }
     if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(S::kColumns)
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kQrThreads, (QrShape<HD, BF16, R>::kPerSm)) qr
                 // K runs a tile ahead of V
                 for (int32_t t = 0; ok && t <= n; ++t) {
                     int32_t page = -1;
-                    if (a.give_up == int32_t(blockIdx.x) && global_ns() - sh.began >= a.give_up_ns) {
+                    if (qr_gives_up(a) && global_ns() >= sh.deadline) {
                         *static_cast<volatile int *>(&sh.stop) = 1;
                         ok = false;
                         break;

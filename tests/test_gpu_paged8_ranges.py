@@ -167,3 +167,54 @@ def test_odd_scales_are_read_with_one_rounding(env, to, bits):  # noqa: F811
     assert to == "f32" or (twice != want).sum() >= n // 2  # what is tested happens
     for x in got:
         assert np.array_equal(x.double().cpu().numpy().reshape(n, 16, 64), want)
+
+
+@pytest.mark.parametrize("total,new,group,dtype", [(200000, 1, 4, "bf16"), (200000, 1, 8, "f16"), (200000, 1, 16, "f16"), (200000, 3, 4, "bf16"), (30000, 600, 4, "bf16"),
+                                                   (30000, 600, 2, "f16")])
+def test_launches_given_up_within_a_run_of_tiles(env, total, new, group, dtype):  # noqa: F811
+    """Blocks with tens of tiles, given up long after their first and long before their last: the launch ends and says so, and the next call is right."""
+    torch, kvd = env
+    from kv_cache_decode_attention_gb300 import _abi
+
+    n_kv, hd, page = 8, 128, 128
+    pages = -(-total // page)
+    cache = kvd.PagedKvCache(pages, page, n_kv, hd, 1, pages, dtype=torch.float8_e4m3fn)
+    g = torch.Generator(device="cuda").manual_seed(43)
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).copy_(torch.randint(0, 0x7f, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    cache.k_scale.fill_(2.0 ** -10)
+    cache.block_table.copy_(torch.randperm(pages, generator=g, device="cuda").int()[None])
+    cache.seq_len.fill_(total)
+    q = torch.randn(new, n_kv * group, hd, generator=g, device="cuda").to(_dt(torch, dtype))
+    plan = _plan_of(torch, kvd, cache, [new])
+    want = kvd.paged_attention(q, cache, plan)
+    assert cache.device_error() == 0
+    graph, times = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        for _ in range(8):
+            kvd.paged_attention(q, cache, plan)
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / 8 * 1e6)
+    whole = sorted(times)[2]  # ns of a call's launches: a block is at its tiles for most of it
+    try:
+        for cta in (0, 37, 95, 151):
+            for share in (0.15, 0.25, 0.35):
+                assert _abi.lib().kvd_test_give_up(cta, int(share * whole)) == 0
+                kvd.paged_attention(q, cache, plan)
+                _abi.lib().kvd_test_give_up(-1, 0)
+                assert cache.device_error() == 1, (cta, share)
+                assert torch.equal(kvd.paged_attention(q, cache, plan), want) and cache.device_error() == 0
+            for share in (0.7, 0.8, 0.9, 1.0, 1.5):  # about its end
+                assert _abi.lib().kvd_test_give_up(cta, int(share * whole)) == 0
+                out = kvd.paged_attention(q, cache, plan)
+                _abi.lib().kvd_test_give_up(-1, 0)
+                assert cache.device_error() == 1 or torch.equal(out, want)
+            assert _abi.lib().kvd_test_give_up(cta, 10 ** 9) == 0
+            assert torch.equal(kvd.paged_attention(q, cache, plan), want) and cache.device_error() == 0
+    finally:
+        _abi.lib().kvd_test_give_up(-1, 0)
