@@ -710,14 +710,17 @@ KVD_API kvd_status paged_attention_q8_workspace_bytes(int64_t n_tokens, int32_t 
 
 /* paged_attention over pages of 8 bits: the attention of q, f16 or bf16 (dtype), over
  * the rows that codes and scales stand for.  Arguments, masks, options, what is skipped
- * or left alone, and the sums in f32 are those of paged_attention.  q is taken to 2^-17
- * of its row's largest value (exactly, if that is within 2^9 of every other: f16 2^6), and
- * the weights, with the scale of V's block, are rounded to eight significant bits for bf16
- * and eleven for f16, and to 2^-22 of the largest of a tile's 128 rows.  In chunks of more
- * than 16 query rows a KV head they are rounded to eleven bits and to 2^-27 of the row's
- * largest, and V to 2^-32 of 448 times the largest scale that the chunk meets (exactly, if
- * its block's is within 2^22 of that).  The softmax's sum has every weight, however far
- * apart the scales of V are.
+ * or left alone, and the sums in f32 are those of paged_attention; so rows that a request
+ * holds have to be finite here, too.  A NaN in V (kv_paged_append_q8 keeps one that it is
+ * given) may reach every new row of its request, those before it and those whose window
+ * has left it behind among them.  Scores have to be numbers of f32.  q is taken to 2^-17
+ * of its row's largest value (exactly, if that is within 2^9 of every other: f16 2^6), or to
+ * 2^-130 where that is more, and the weights, with the scale of V's block, are rounded to
+ * eight significant bits for bf16 and eleven for f16, and to 2^-22 of the largest of a
+ * tile's 128 rows.  In chunks of more than 16 query rows a KV head they are rounded to
+ * eleven bits and to 2^-27 of the row's largest, and V to 2^-32 of 448 times the largest
+ * scale that the chunk meets (exactly, if its block's is within 2^22 of that).  The
+ * softmax's sum has every weight, however far apart the scales of V are.
  * A cap that no score below 10^15 before scaling would feel (scale / softcap below
  * 2^-64) is none.  A row of q that is not finite gives NaN, in that row alone.
  * n_seq <= 2^20. */

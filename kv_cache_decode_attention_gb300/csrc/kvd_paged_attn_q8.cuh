@@ -24,7 +24,7 @@
 // An item is one (request, KV head, run of tokens): kQrRows query rows (token, head of
 // the group) at most.  Items are cut into tiles of 128 rows and every CTA gets the
 // same number of consecutive ones, however long the requests are; an item that is cut
-// leaves its pieces (unnormalised output, reference, sum) to qr_join_kernel.
+// leaves its pieces (output, reference, sum) to qr_join_kernel.
 //
 // A CTA, of which an SM holds three (f16: two, with three stages each):
 //   warps 0-3  softmax, a thread per row of K: its scales are the thread's own, masks
@@ -45,9 +45,9 @@
 // every one of them 0 and 4%.)
 //
 // Measured (GPU time on one GB300; a copy runs at 6.77 TB/s): one new row for each of 64
-// requests of up to 16384 rows, 32 heads over 8, 193 us, 6.1 TB/s, f16 214; 4 of 131072
-// rows, 128 heads over 8, 184 us, 5.8 TB/s; four drafts for each of 32 requests 47 us; one
-// row for each of 256 requests of 300 rows 56; one over 1023 rows 10.9.  With eight
+// requests of up to 16384 rows, 32 heads over 8, 193 us, 6.1 TB/s, f16 217; 4 of 131072
+// rows, 128 heads over 8, 184 to 186 us, 5.8 TB/s; four drafts for each of 32 requests 47 us;
+// one row for each of 256 requests of 300 rows 52; one over 1023 rows 11.  With eight
 // columns and bf16 a CTA waits for HBM (a tile in 4300 cycles, 2400 of them busy: 6.8 TB/s
 // while all CTAs are at it; the rest is the first scores, some 5 us after the launch, the
 // ends and the joining launch); with 16 columns in three terms, two CTAs to an SM, it is
@@ -55,7 +55,7 @@
 // 5 us beside its tiles with eight columns and 10 with 16.
 // Measured and not taken: 16 columns for single tokens (decode 253 us when eight took
 // 211); three CTAs of two stages for 16 bf16 columns (drafts 80 us against 70: registers
-// spill); a reduction by instruction for each column's maximum (five instructions more a
+// spill; eight columns spill 24 bytes in bf16 and some 145 in f16 for their third CTA); a reduction by instruction for each column's maximum (five instructions more a
 // column); joining CTAs of 512 threads (decode 203 against 194); zeros for V's rows before
 // a window, as for those behind the last (decode 203 against 193, without any window): rows
 // that a request holds have to be finite.
@@ -77,7 +77,6 @@ constexpr int kQrJobs = 4;
 // With scales of V up to here (2^8; f16 needs no larger ones) a weight that is lost beside
 // another's scale is below 2^-54 of that one's.
 constexpr float kScaleFar = 256.0f;
-constexpr int kQrMaxSeq = 1 << 20;
 
 // A cut item as qr_join_kernel finds it; n = 0: none.
 struct QrCut {

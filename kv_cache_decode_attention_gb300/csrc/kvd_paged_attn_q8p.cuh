@@ -12,14 +12,13 @@
 //               of bf16 are two times four; 2^-17 of the row's largest is left out.
 //   O += P V    kind::f16.  V's codes become f16 by four warps between the copy and the
 //               MMA, times their block's power of two over the largest that the part of the
-//               item has met: exactly, down to 2^-31 of that one's codes (to within 2^-24 of
-//               one below).  P in f16, whatever q's type, with what is left of the block's
-//               scale, a number in [1, 2), in it.  So the softmax's references and sums know
-//               of V's scales only that; a part that meets a larger one rescales O, as
-//               for a reference that grew.  P in e4m3 terms
-//               would do without, but a sum over a whole prompt meets weights far below
-//               2^-17 of the largest, and five instructions a weight cost the softmax
-//               warps more than the conversion, of which 256 rows share one.
+//               item has met: exactly, if that is within 2^22 of it, else to 2^-32 of the
+//               largest number there.  P in f16, whatever q's type, with what is left of the
+//               block's scale, a number in [1, 2), in it.  So references and sums know no more
+//               of V's scales; a part that meets a larger one rescales O, as for a reference
+//               that grew.  P in e4m3 terms would do without the conversion, but a sum over a
+//               whole prompt meets weights far below 2^-17 of the largest, and five instructions
+//               a weight cost the softmax warps more than it, of which 256 rows share one.
 //
 // One CTA per SM:
 //   warps 0-3, 4-7   softmax of stream 0 and 1, a thread per query row; they make q's
@@ -42,14 +41,17 @@
 // warps know of it (their last s_full of that half stands behind the one before).
 //
 // Measured (GPU time on one GB300): 4096 new rows of a prompt over 32768, 32 heads over
-// 8, 1417 to 1465 us, 1410 to 1450 TFLOP/s at the power limit; 4096 over 4096 155; seven
-// chunks of up to 700 rows with a window, 58 with capped scores, 40 without.  A unit (a KV tile of both streams) takes some 1.15 us, 1.7 at the power
-// limit, and its MMAs alone 1.1; an item 8 us beside its units (q, the first scores, the
-// last P V, its rows).
+// 8, 1480 to 1515 us, 1360 to 1390 TFLOP/s at the power limit, in f16 1.77 ms; 4096 over 4096
+// 158, in f16 178; seven chunks of up to 700 rows with a window, 60 with capped scores, 40
+// without.  A unit (a KV tile of both streams) takes some 1.15 us, 1.7 at the power limit,
+// and its MMAs alone 1.1; an item 8 us beside its units (q, the first scores, the last P V,
+// its rows).  (Some 50 to 90 bytes of registers spill.)
 // Measured and not taken: S in one piece of 128 columns, as wide as the tile (prompt 1.99
 // ms: a stream's softmax, 2500 cycles, and its MMAs with their barriers, 2100, one after
 // the other); S only once P V has been seen done (1.61 ms against 1.48); the maximum
-// before the weights (no difference beside that); a slack of 2^4 (below).
+// before the weights (no difference beside that); a slack of 2^4 (below); all of V's scale
+// in P, and the weights summed once more from the scores where scales lie far apart (prompt
+// 1.57 to 1.71 ms, from the larger code alone).
 #pragma once
 
 #include "kvd_paged_attn_q8.cuh"

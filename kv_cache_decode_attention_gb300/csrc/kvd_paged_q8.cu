@@ -20,7 +20,7 @@
 // Measured (GPU time on one GB300; a copy runs at 6.77 TB/s): 8192 tokens of a prompt, 32
 // + 8 + 8 heads, bf16, written in 47 us (184 MB; 3.9 TB/s), 9000 of chunks in f32 in 25.5,
 // one token for each of 256 requests in 5.4; 373000 rows of 48 requests read back to bf16
-// in 367 us, 6.25 TB/s (32 rows and one head to a CTA, a binary search each: 470).  Writing
+// in 368 us, 6.23 TB/s (32 rows and one head to a CTA, a binary search each: 470).  Writing
 // is bound by latency: a run's rows, their largest value, the scale, the codes, one after
 // another, with some 30 warps to an SM.
 

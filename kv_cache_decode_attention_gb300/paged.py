@@ -445,7 +445,9 @@ def paged_attention(q: torch.Tensor, cache: PagedKvCache, plan: PagedPlan, out: 
     """Causal attention of the step's new rows q [tokens, n_q, hd] (appended already)
     over all rows their requests hold; out has q's shape and dtype (rows behind
     the last new one are left as they were).  q has the pages' dtype; over pages of
-    8 bits it is float16 or bfloat16.
+    8 bits it is float16 or bfloat16.  Rows that a request holds have to be finite: a NaN
+    in one may reach all new rows of its request, those that do not see it too (pages of
+    8 bits keep a NaN that is appended).
     window, softcap and sinks as in decode_attention."""
     k = cache.k
     if k is None:
