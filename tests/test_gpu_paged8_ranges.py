@@ -218,3 +218,40 @@ def test_launches_given_up_within_a_run_of_tiles(env, total, new, group, dtype):
             assert torch.equal(kvd.paged_attention(q, cache, plan), want) and cache.device_error() == 0
     finally:
         _abi.lib().kvd_test_give_up(-1, 0)
+
+
+@pytest.mark.parametrize("value,low", [(1.0, -8), (2.0 ** 15, 9)])
+@pytest.mark.parametrize("dtype,hd,group", [("bf16", 128, 4), ("f16", 64, 16), ("f16", 128, 5), ("bf16", 64, 1)])
+def test_one_number_everywhere_comes_out_as_itself(env, value, low, dtype, hd, group):  # noqa: F811
+    """V is one number, held at scales 2^low .. 2^(low + 5), and zero in some pages: what comes out is the number times the weight of the others.
+    A weight times its scale is held to 2^-22 of the largest of its 128 rows, so at scales 2^5 apart the output is off by 128 * 2^-22 * 2^5 of
+    the number at most for that."""
+    torch, kvd = env
+    lens, new, page = [900, 5000, 3, 700, 2000], [1, 2, 3, 300, 33], 32
+    r = np.random.default_rng(hd + group)
+    for window, softcap, sinks, size in ((0, 0.0, False, 1.5), (600, 0.0, True, 1.5), (0, 20.0, True, 4.0), (0, 0.0, False, 0.0)):
+        cache, rows = _poisoned8(torch, kvd, lens, 2, hd, page, 47)
+        raw, shares = cache.v.view(torch.uint8), []
+        for b, n in enumerate(lens):
+            v = torch.full((n,), value, dtype=torch.float64, device="cuda")
+            for j in range(-(-n // page)):
+                p, held = int(cache.block_table[b, j]), min(page, n - j * page)
+                e = int(r.integers(low, low + 6))
+                zero = r.random() < 0.15
+                cache.v_scale[p] = LOW if zero else 2.0 ** e
+                raw[p, :, :held] = 0 if zero else int(torch.tensor(value * 2.0 ** -e).to(torch.float8_e4m3fn).view(torch.uint8))
+                if zero:
+                    v[j * page:j * page + held] = 0
+            shares.append(v)
+        g = torch.Generator(device="cuda").manual_seed(48)
+        q = (torch.randn(sum(new), 2 * group, hd, generator=g, device="cuda") * size).to(_dt(torch, dtype))
+        sink = torch.randn(2 * group, generator=g, device="cuda") if sinks else None
+        out = kvd.paged_attention(q, cache, _plan_of(torch, kvd, cache, new), window=window, softcap=softcap, sinks=sink)
+        assert cache.device_error() == 0
+        at, half = 0, float(torch.finfo(out.dtype).eps) / 2
+        for b, n in enumerate(new):
+            v = shares[b][:, None, None].expand(lens[b], 2, hd)
+            want, size_of, slack = _attend8(torch, q[at:at + n], rows[b][0], v, lens[b], hd ** -0.5, window, softcap, sink)
+            tol = (half + slack * (1 + half)) * size_of * (1 + half) + half * want.abs() + value * 2.0 ** -10
+            assert bool(((out[at:at + n].double() - want).abs() <= tol).all())
+            at += n
